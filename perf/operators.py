@@ -1,0 +1,592 @@
+"""The tree round's operators and the cases they are measured on.
+
+Four operators of one speculative round over a tree of drafted tokens: the
+attention of the tree's nodes over a paged cache, the verification of the tree
+against the target's probabilities from given random numbers, the commit of
+the accepted path into the cache, and the fork of a cache's pages by the
+ancestors of a particle step.
+
+`run` computes them in plain torch operations where `own` is false and calls
+the library where it is true; `exact` computes the same outputs in 64 bits,
+sequence by sequence.
+"""
+
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+# --------------------------------------------------------------- cases
+
+def _attn(name, **kw):
+    c = dict(name=name, op="attention", B=1, N=1, Hq=32, Hkv=8, D=128, len=1000, page=16, dtype="bf16", branch=1,
+             window=0, sinks=0, ragged=False, head_major=False)
+    c.update(kw)
+    return c
+
+
+def _verify(name, **kw):
+    c = dict(name=name, op="verify", B=1, N=8, V=128256, dtype="fp32", branch=1, draft=True, ragged=False)
+    c.update(kw)
+    return c
+
+
+def _cache(name, op, **kw):
+    c = dict(name=name, op=op, B=1, N=8, layers=4, Hkv=8, D=128, len=500, page=16, dtype="bf16", head_major=False)
+    c.update(kw)
+    return c
+
+
+def listed():
+    return [
+        # one sequence's next token over a short context: latency
+        _attn("attention_single_token", len=1111),
+        # a serving batch with five drafted tokens in a chain each
+        _attn("attention_chain_batch", B=64, N=6, len=4096, ragged=True),
+        # wide trees over long contexts: the largest call
+        _attn("attention_tree_long", B=64, N=32, len=16384, branch=3, page=64, ragged=True, head_major=True),
+        # odd sizes: five query heads per key head, 23 nodes, 80-wide heads, lengths that end inside a page
+        _attn("attention_tree_odd", B=7, N=23, Hq=30, Hkv=6, D=80, len=5003, branch=2, page=32, dtype="fp16",
+              ragged=True),
+        # long documents under a sliding window with the first tokens kept
+        _attn("attention_window_sinks", B=32, N=16, len=32768, branch=2, window=4096, sinks=4, page=64),
+        # one sequence's chain under a window
+        _attn("attention_window_chain", N=6, len=20001, window=1024, sinks=16),
+        # one sequence, a small tree of draft samples
+        _verify("verify_tree_one", N=8, branch=2),
+        # a batch of trees drawn from the draft model
+        _verify("verify_tree_batch", B=64, N=16, branch=3, ragged=True),
+        # chosen (not drawn) candidates: no draft distribution
+        _verify("verify_tree_chosen", B=96, N=21, branch=4, draft=False, dtype="bf16"),
+        # one sequence's accepted tokens into the cache
+        _cache("commit_one", "commit", N=6, len=777),
+        # a batch's accepted paths into every layer's cache
+        _cache("commit_batch", "commit", B=64, N=16, layers=16, len=600),
+        # a particle population continued by its ancestors, every layer's cache
+        _cache("fork_particles", "fork", B=64, layers=16, len=600, page=32),
+    ]
+
+
+def _log_uniform(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    kind = rng.choice(("attention", "attention", "verify", "commit", "fork"))
+    if kind == "attention":
+        Hkv = rng.choice((1, 2, 4, 6, 8))
+        c = dict(op="attention", B=_log_uniform(rng, 1, 64), N=_log_uniform(rng, 1, 64), Hkv=Hkv,
+                 Hq=Hkv * rng.choice((1, 2, 4, 5, 8)), D=rng.choice((64, 80, 96, 128)),
+                 len=_log_uniform(rng, 1, 32768), page=rng.choice((16, 32, 64, 128)),
+                 dtype=rng.choice(("bf16", "bf16", "fp16")), branch=rng.randint(1, 4), window=0, sinks=0,
+                 ragged=rng.random() < 0.6, head_major=rng.random() < 0.5)
+        if rng.random() < 0.35:
+            c["window"] = _log_uniform(rng, 64, 4096)
+            c["sinks"] = rng.choice((0, 4, 16, 64))
+        while c["B"] > 1 and (c["B"] * c["len"] * c["Hkv"] > 64 * 16384 * 8 * 0.7
+                              or c["B"] * c["N"] * c["Hq"] * c["len"] > 64 * 32 * 32 * 16384 * 0.7):
+            c["B"] = (c["B"] + 1) // 2
+        return c
+    if kind == "verify":
+        c = dict(op="verify", B=_log_uniform(rng, 1, 256), N=_log_uniform(rng, 2, 32), V=_log_uniform(rng, 500, 150000),
+                 dtype=rng.choice(("fp32", "bf16")), branch=rng.randint(1, 4), draft=rng.random() < 0.6,
+                 ragged=rng.random() < 0.5)
+        while c["B"] > 1 and c["B"] * c["N"] * c["V"] > 64 * 16 * 128256:
+            c["B"] = (c["B"] + 1) // 2
+        return c
+    c = dict(op=kind, B=_log_uniform(rng, 1, 128), N=_log_uniform(rng, 1, 32), layers=rng.randint(1, 16),
+             Hkv=rng.choice((1, 2, 4, 8)), D=rng.choice((64, 80, 128)), len=_log_uniform(rng, 1, 2000),
+             page=rng.choice((8, 16, 32, 64)), dtype=rng.choice(("bf16", "fp16", "fp32")),
+             head_major=rng.random() < 0.5)
+    while c["B"] > 1 and c["B"] * (c["len"] + c["N"] + c["page"]) * c["layers"] * c["Hkv"] * c["D"] > 64 * 600 * 16 * 1024:
+        c["B"] = (c["B"] + 1) // 2
+    return c
+
+
+# --------------------------------------------------------------- inputs
+
+def _spread(n, lo, hi):
+    """n whole numbers evenly spread over [lo, hi], the same for every seed."""
+    if n == 1:
+        return [hi]
+    return [lo + (hi - lo) * i // (n - 1) for i in range(n)]
+
+
+def _lengths(c):
+    """The sequences' lengths in the cache, in no particular order."""
+    L = c["len"]
+    if c["op"] == "attention":
+        return _spread(c["B"], max(1, L // 4), L) if c["ragged"] else [L] * c["B"]
+    return _spread(c["B"], max(0, L // 2), L)
+
+
+def _nodes(c):
+    return _spread(c["B"], max(1, c["N"] // 2), c["N"]) if c.get("ragged") else [c["N"]] * c["B"]
+
+
+def _shuffled(values, g):
+    t = torch.tensor(values, dtype=torch.int32, device="cuda")
+    return t[torch.randperm(len(values), generator=g, device="cuda")].contiguous()
+
+
+def _parents(B, N, branch, g):
+    """Trees in level order: sequence b gives every node w_b children, w_b in
+    [1, branch]; node 0 is the root (its parent -1)."""
+    w = torch.randint(1, branch + 1, (B, 1), generator=g, device="cuda")
+    i = torch.arange(N, device="cuda").view(1, N)
+    par = torch.div(i - 1, w, rounding_mode="floor")
+    return torch.where(i == 0, -1, par).to(torch.int32).contiguous()
+
+
+def _randn(shape, dtype, g, scale=1.0):
+    out = torch.empty(shape, dtype=dtype, device="cuda")
+    out.normal_(0.0, scale, generator=g)
+    return out
+
+
+def _pages(c, lens, g, spare):
+    """A pool's page count and the sequences' tables: every sequence's blocks
+    at random places of the pool, -1 after them."""
+    ps, B = c["page"], c["B"]
+    host = _lengths(c)
+    width = (max(host) + c["N"] + ps) // ps + 1
+    pages = sum((n + ps - 1) // ps for n in host) + spare
+    perm = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    blocks = torch.div(lens.long() + ps - 1, ps, rounding_mode="floor")
+    start = torch.cumsum(blocks, 0) - blocks
+    col = torch.arange(width, device="cuda").view(1, width)
+    live = col < blocks.view(B, 1)
+    at = torch.where(live, start.view(B, 1) + col, 0)
+    return pages, torch.where(live, perm[at], -1).to(torch.int32).contiguous()
+
+
+def _pool(shape, dtype, head_major, g):
+    """[..., pages, page, Hkv, D], stored so or with the heads before the page's rows."""
+    if head_major:
+        s = list(shape)
+        s[-3], s[-2] = s[-2], s[-3]
+        return _randn(s, dtype, g).transpose(-3, -2)
+    return _randn(shape, dtype, g)
+
+
+def prepare(case, seed):
+    c = case
+    g = torch.Generator(device="cuda")
+    g.manual_seed(int(seed) * 1000003 + 17)
+    s = {"case": dict(c)}
+    B, N = c["B"], c["N"]
+    if c["op"] == "verify":
+        V, dt = c["V"], DTYPES[c["dtype"]]
+        parent = _parents(B, N, c["branch"], g)
+        # the target's logits, a draft model near them (about two in three of its samples pass), temperature 0.7
+        logits = _randn((B, N, V), torch.float32, g, 2.0)
+        s["target"] = torch.softmax(logits / 0.7, -1).to(dt)
+        at = parent.clamp(min=0).long()
+        if c["draft"]:
+            P = max(1, N - 1)
+            noisy = logits[:, :P] + _randn((B, P, V), torch.float32, g, 0.6)
+            del logits
+            s["draft"] = torch.softmax(noisy / 0.7, -1).to(dt)
+            del noisy
+            tokens = torch.empty((B, N), dtype=torch.int64, device="cuda")
+            rows = torch.arange(B, device="cuda")
+            for i in range(N):  # node i's id is a sample of its parent's draft distribution
+                race = torch.empty((B, V), dtype=torch.float32, device="cuda").exponential_(generator=g)
+                tokens[:, i] = (s["draft"][rows, at[:, i]].float() / race).argmax(-1)
+        else:
+            del logits
+            s["draft"] = None
+            # the children of a node are its most probable ids in order
+            top = s["target"].float().topk(min(V, c["branch"]), -1).indices
+            i = torch.arange(N, device="cuda").view(1, N)
+            first = (parent.view(B, 1, N) == parent.view(B, N, 1)).to(torch.int8).argmax(-1)
+            rank = (i - first) % top.shape[-1]
+            tokens = torch.gather(torch.gather(top, 1, at.unsqueeze(-1).expand(B, N, top.shape[-1])), 2,
+                                  rank.unsqueeze(-1)).squeeze(-1)
+        s["tokens"] = tokens.to(torch.int32).contiguous()
+        s["parent"] = parent
+        s["n_nodes"] = _shuffled(_nodes(c), g) if c["ragged"] else None
+        s["u_accept"] = torch.rand((B, N), generator=g, device="cuda")
+        s["u_final"] = torch.rand((B,), generator=g, device="cuda")
+        return s
+    dt = DTYPES[c["dtype"]]
+    lens = _shuffled(_lengths(c), g)
+    ps, Hkv, D = c["page"], c["Hkv"], c["D"]
+    if c["op"] == "attention":
+        pages, table = _pages(c, lens, g, 1)
+        s["k"] = _pool((pages, ps, Hkv, D), dt, c["head_major"], g)
+        s["v"] = _pool((pages, ps, Hkv, D), dt, c["head_major"], g)
+        s["q"] = _randn((B, N, c["Hq"], D), dt, g)
+        s["k_tree"] = _randn((B, N, Hkv, D), dt, g)
+        s["v_tree"] = _randn((B, N, Hkv, D), dt, g)
+        s["parent"] = _parents(B, N, c["branch"], g)
+        s["n_nodes"] = _shuffled(_nodes(c), g) if c["ragged"] else None
+    else:
+        pages, table = _pages(c, lens, g, B * (2 + c["N"] // ps) + 3)
+        s["k"] = _pool((c["layers"], pages, ps, Hkv, D), dt, c["head_major"], g)
+        s["v"] = _pool((c["layers"], pages, ps, Hkv, D), dt, c["head_major"], g)
+        if c["op"] == "commit":
+            s["k_tree"] = _randn((c["layers"], B, N, Hkv, D), dt, g)
+            s["v_tree"] = _randn((c["layers"], B, N, Hkv, D), dt, g)
+            # accepted paths: the root, then n increasing node numbers
+            n = torch.randint(0, min(N, 6), (B,), generator=g, device="cuda")
+            order = torch.rand((B, N), generator=g, device="cuda")
+            order[:, 0] = -1.0
+            i = torch.arange(N, device="cuda").view(1, N)
+            path = torch.where(i <= n.view(B, 1), torch.argsort(order, -1), N).sort(-1).values
+            s["nodes"] = torch.where(path < N, path, -1).to(torch.int32).contiguous()
+            s["n_accepted"] = n.to(torch.int32)
+        else:
+            # systematic resampling of weights with a few dominant particles
+            w = torch.rand((B,), generator=g, device="cuda", dtype=torch.float64).pow(3)
+            cum = torch.cumsum(w, 0) / w.sum()
+            u = torch.rand((1,), generator=g, device="cuda", dtype=torch.float64)
+            at = (torch.arange(B, device="cuda") + u) / B
+            s["ancestor"] = torch.searchsorted(cum, at).clamp(max=B - 1).to(torch.int32)
+    s["table"], s["len"] = table, lens
+    return s
+
+
+# --------------------------------------------------------------- plain forms
+
+def _depths(parent):
+    """The nodes' depths and the ancestor-or-self relation [B, i, j]."""
+    B, N = parent.shape
+    eye = torch.eye(N, dtype=torch.bool, device=parent.device)
+    step = (parent.view(B, N, 1) == torch.arange(N, device=parent.device).view(1, 1, N)).float()
+    seen, reach = eye.float().expand(B, N, N), 1
+    hop = step + eye.float()
+    while reach < N:  # doubling: hop covers paths of `reach` steps
+        hop = (torch.matmul(hop, hop) > 0).float()
+        reach *= 2
+    seen = torch.matmul(seen, hop) > 0
+    return seen.sum(-1) - 1, seen
+
+
+def _plain_attention(s):
+    c = s["case"]
+    B, N, Hq, Hkv, D, ps = c["B"], c["N"], c["Hq"], c["Hkv"], c["D"], c["page"]
+    G, lens, dev = Hq // Hkv, s["len"].long(), s["q"].device
+    M = s["table"].shape[1] * ps
+    page = s["table"].long().clamp(min=0)
+    inside = (torch.arange(M, device=dev).view(1, M) < lens.view(B, 1))
+    k = torch.cat((s["k"][page].reshape(B, M, Hkv, D), s["k_tree"]), 1).float().permute(0, 2, 3, 1)
+    v = torch.cat((s["v"][page].reshape(B, M, Hkv, D), s["v_tree"]), 1).float().permute(0, 2, 1, 3)
+    q = s["q"].float().view(B, N, Hkv, G, D).permute(0, 2, 1, 3, 4).reshape(B, Hkv, N * G, D)
+    depth, seen = _depths(s["parent"])
+    n = torch.full((B,), N, device=dev) if s["n_nodes"] is None else s["n_nodes"].long()
+    node = torch.arange(N, device=dev)
+    here = node.view(1, N) < n.view(B, 1)
+    see_cache = inside.view(B, 1, M).expand(B, N, M)
+    if c["window"]:
+        pos = lens.view(B, 1, 1) + depth.view(B, N, 1)
+        j = torch.arange(M, device=dev).view(1, 1, M)
+        see_cache = see_cache & ((pos - j < c["window"]) | (j < c["sinks"]))
+        seen = seen & (depth.view(B, N, 1) - depth.view(B, 1, N) < c["window"])
+    see = torch.cat((see_cache, seen & here.view(B, 1, N)), 2)  # [B, N, M + N]
+    see = see.view(B, 1, N, 1, M + N).expand(B, Hkv, N, G, M + N).reshape(B, Hkv, N * G, M + N)
+    x = torch.matmul(q, k) * (1.0 / math.sqrt(D))
+    x = torch.where(see, x, -math.inf)
+    w = torch.exp(x - x.max(-1, keepdim=True).values)
+    o = torch.matmul(w, v) / w.sum(-1, keepdim=True)
+    o = o.view(B, Hkv, N, G, D).permute(0, 2, 1, 3, 4).reshape(B, N, Hq, D)
+    return torch.where(here.view(B, N, 1, 1), o, 0.0).to(s["q"].dtype)
+
+
+def _plain_verify(s):
+    p, q, tok, par = s["target"], s["draft"], s["tokens"].long(), s["parent"].long()
+    B, N, V = p.shape
+    dev, f8 = p.device, torch.float64
+    b = torch.arange(B, device=dev)
+    n_nodes = torch.full((B,), N, device=dev) if s["n_nodes"] is None else s["n_nodes"].long()
+    cur = torch.zeros(B, dtype=torch.int64, device=dev)
+    a, S = torch.zeros(B, dtype=f8, device=dev), torch.ones(B, dtype=f8, device=dev)
+    count = torch.zeros(B, dtype=torch.int64, device=dev)
+    tokens = torch.full((B, N), -1, dtype=torch.int64, device=dev)
+    nodes = torch.full((B, N), -1, dtype=torch.int64, device=dev)
+    nodes[:, 0] = 0
+    gone = torch.zeros((B, V), dtype=torch.bool, device=dev)  # without q: the refused children of cur
+
+    def residual():
+        w = p[b, cur].to(f8)
+        if q is None:
+            return torch.where(gone, 0.0, w)
+        row = q[b, cur.clamp(max=q.shape[1] - 1)].to(f8)
+        return torch.where(a.view(B, 1) > 0, (w - a.view(B, 1) * row).clamp(min=0.0), w)
+
+    for i in range(1, N):  # a node's children have larger numbers, in order
+        test = (par[:, i] == cur) & (i < n_nodes)
+        x = tok[:, i]
+        u, px = s["u_accept"][:, i].to(f8), p[b, cur, x].to(f8)
+        if q is None:
+            ok = (u * S < px) & ~gone[b, x]
+            S = torch.where(test & ~ok & ~gone[b, x], S - px, S)
+            gone[b, x] |= test & ~ok
+        else:
+            qx = q[b, cur.clamp(max=q.shape[1] - 1), x].to(f8)
+            ok = u * S * qx < px - a * qx
+            a = torch.where(test & ~ok, a + S, a)
+            S = torch.where(test & ~ok, residual().sum(-1), S)
+        take = test & ok
+        tokens[b, count] = torch.where(take, x, tokens[b, count])
+        count = count + take
+        nodes[b, count] = torch.where(take, i, nodes[b, count])
+        cur = torch.where(take, i, cur)
+        a, S = torch.where(take, 0.0, a), torch.where(take, 1.0, S)
+        gone &= ~take.view(B, 1)
+    cum = torch.cumsum(residual(), -1)
+    t = s["u_final"].to(f8) * cum[:, -1]
+    tokens[b, count] = (cum <= t.view(B, 1)).sum(-1)
+    return {"tokens": tokens.to(torch.int32), "nodes": nodes.to(torch.int32), "n_accepted": count.to(torch.int32)}
+
+
+def _free_pages(used_pages, pages, dev):
+    """Page numbers, the unused ones first, in rising order; and how many are unused."""
+    used = torch.zeros(pages + 1, dtype=torch.int32, device=dev)
+    used[used_pages] = 1  # place `pages` takes the entries that are not live
+    used = used[:pages]
+    return torch.argsort(used, stable=True), pages - used.sum()
+
+
+def _plain_commit(s):
+    c, k, v, table, lens = s["case"], s["k"], s["v"], s["table"].long(), s["len"].long()
+    B, N, ps, pages, dev = c["B"], c["N"], c["page"], s["k"].shape[1], s["k"].device
+    width = table.shape[1]
+    rows = s["n_accepted"].long() + 1
+    have = torch.div(lens + ps - 1, ps, rounding_mode="floor")
+    want = torch.div(lens + rows + ps - 1, ps, rounding_mode="floor")
+    col = torch.arange(width, device=dev).view(1, width)
+    live = col < have.view(B, 1)
+    order, n_free = _free_pages(torch.where(live, table, pages), pages, dev)
+    need = want - have
+    start = torch.cumsum(need, 0) - need
+    fits = need.sum() <= n_free
+    new = live.logical_not() & (col < want.view(B, 1)) & fits
+    pick = order[torch.where(new, start.view(B, 1) + col - have.view(B, 1), 0).clamp(max=pages - 1)]
+    out = torch.where(new, pick, torch.where(live, table, -1))
+    j = torch.arange(N, device=dev).view(1, N)
+    b, r = torch.nonzero((j < rows.view(B, 1)) & fits, as_tuple=True)
+    at = lens[b] + r
+    page, slot, node = out[b, torch.div(at, ps, rounding_mode="floor")], at % ps, s["nodes"].long()[b, r]
+    k[:, page, slot] = s["k_tree"][:, b, node]
+    v[:, page, slot] = s["v_tree"][:, b, node]
+    return {"table": out.to(torch.int32), "len": torch.where(fits, lens + rows, lens).to(torch.int32),
+            "status": (need.sum() - n_free).clamp(min=0).view(1).to(torch.int32), "k": k, "v": v}
+
+
+def _plain_fork(s):
+    c, k, v, table, lens = s["case"], s["k"], s["v"], s["table"].long(), s["len"].long()
+    B, ps, pages, dev = c["B"], c["page"], s["k"].shape[1], s["k"].device
+    width = table.shape[1]
+    anc = s["ancestor"].long()
+    b = torch.arange(B, device=dev)
+    keeper = ((anc.view(1, B) == anc.view(B, 1)) & (b.view(1, B) < b.view(B, 1))).any(-1).logical_not()
+    length = lens[anc]
+    full, part = torch.div(length, ps, rounding_mode="floor"), length % ps
+    col = torch.arange(width, device=dev).view(1, width)
+    new = (part > 0) & ~keeper
+    share = col < (full + ((part > 0) & keeper)).view(B, 1)
+    out = torch.where(share, table[anc], -1)
+    order, n_free = _free_pages(torch.where(share, out, pages), pages, dev)
+    rank = torch.cumsum(new.long(), 0) - 1
+    need = new.sum()
+    fits = need <= n_free
+    pick = order[rank.clamp(min=0, max=pages - 1)]
+    out = torch.where((col == full.view(B, 1)) & new.view(B, 1), pick.view(B, 1), out)
+    t = torch.nonzero(new & fits, as_tuple=True)[0]
+    src, dst = table[anc[t], full[t]], pick[t]
+    row = torch.arange(ps, device=dev).view(1, ps)
+    i, r = torch.nonzero(row < part[t].view(-1, 1), as_tuple=True)
+    k[:, dst[i], r] = k[:, src[i], r]
+    v[:, dst[i], r] = v[:, src[i], r]
+    old = torch.where(col < torch.div(lens + ps - 1, ps, rounding_mode="floor").view(B, 1), table, -1)
+    return {"table": torch.where(fits, out, old).to(torch.int32), "len": torch.where(fits, length, lens).to(torch.int32),
+            "status": (need - n_free).clamp(min=0).view(1).to(torch.int32), "k": k, "v": v}
+
+
+def run(state):
+    s = state
+    c = s["case"]
+    if own:
+        from rejection_sampling_verifier_amd import binding
+
+        if c["op"] == "attention":
+            return binding.tree_attention(s["q"], s["k"], s["v"], s["table"], s["len"], s["k_tree"], s["v_tree"],
+                                          s["parent"], s["n_nodes"], window=c["window"], sinks=c["sinks"])
+        if c["op"] == "verify":
+            tokens, nodes, n = binding.verify_tree(s["target"], s["draft"], s["tokens"], s["parent"], s["u_accept"],
+                                                   s["u_final"], s["n_nodes"])
+            return {"tokens": tokens, "nodes": nodes, "n_accepted": n}
+        if c["op"] == "commit":
+            table, length, status = binding.cache_commit(s["k"], s["v"], s["table"], s["len"], s["k_tree"], s["v_tree"],
+                                                         s["nodes"], s["n_accepted"])
+        else:
+            table, length, status = binding.cache_fork(s["k"], s["v"], s["table"], s["len"], s["ancestor"])
+        return {"table": table, "len": length, "status": status, "k": s["k"], "v": s["v"]}
+    return {"attention": _plain_attention, "verify": _plain_verify, "commit": _plain_commit,
+            "fork": _plain_fork}[c["op"]](s)
+
+
+# --------------------------------------------------------------- work
+
+def work(case):
+    c = case
+    size = {"bf16": 2, "fp16": 2, "fp32": 4}[c["dtype"]]
+    B, N = c["B"], c["N"]
+    if c["op"] == "attention":
+        bytes_, flops = 0, 0
+        for length, n in zip(_lengths(c), _nodes(c)):
+            keys = length
+            if c["window"]:
+                keys = min(length, max(0, c["window"] - 1) + min(c["sinks"], max(0, length - c["window"] + 1)))
+            row = c["D"] * size
+            bytes_ += 2 * (keys + n) * c["Hkv"] * row + 2 * n * c["Hq"] * row
+            flops += 4 * n * c["Hq"] * c["D"] * (keys + 1)
+        return {"bytes": bytes_, "flops": flops}
+    if c["op"] == "verify":
+        # the last node's rows of p and, where a child was refused there, of q
+        rows = 2 if c["draft"] else 1
+        return {"bytes": B * (rows * c["V"] * size + N * 16), "flops": B * c["V"] * 2 * rows}
+    row = c["layers"] * c["Hkv"] * c["D"] * size
+    blocks = sum((n + c["page"] - 1) // c["page"] for n in _lengths(c))
+    if c["op"] == "commit":
+        moved = B * (min(N, 6) + 1) / 2  # the accepted paths' rows on average
+    else:
+        moved = B * 0.5 * c["page"] / 2  # about half the slots copy half a page
+    return {"bytes": int(4 * moved * row + 8 * blocks), "flops": 0}
+
+
+# --------------------------------------------------------------- 64 bits
+
+def _exact_attention(s):
+    c = s["case"]
+    ps, D, G = c["page"], c["D"], c["Hq"] // c["Hkv"]
+    out = torch.zeros(s["q"].shape, dtype=torch.float64, device="cuda")
+    lens, parent = s["len"].tolist(), s["parent"].tolist()
+    counts = [c["N"]] * c["B"] if s["n_nodes"] is None else s["n_nodes"].tolist()
+    for b in range(c["B"]):
+        L, n = lens[b], counts[b]
+        paths = []
+        for i in range(n):
+            up, at = [], i
+            while at >= 0:
+                up.append(at)
+                at = parent[b][at] if at > 0 else -1
+            paths.append(up)
+        near = set(range(L)) if not c["window"] else set(range(min(L, c["sinks"]))) | set(
+            range(max(0, L - c["window"] + 1), L))
+        keys = torch.tensor(sorted(near), dtype=torch.int64, device="cuda")
+        page = s["table"][b].long()[torch.div(keys, ps, rounding_mode="floor")]
+        see = torch.zeros((n, len(near) + n), dtype=torch.bool)
+        at = keys.cpu()
+        for i, up in enumerate(paths):
+            d = len(up) - 1
+            see[i, :len(near)] = (at < c["sinks"]) | (L + d - at < c["window"]) if c["window"] else True
+            for back, j in enumerate(up):
+                see[i, len(near) + j] = not c["window"] or back < c["window"]
+        see = see.cuda()
+        for h in range(c["Hkv"]):
+            k = torch.cat((s["k"][page, keys % ps, h], s["k_tree"][b, :n, h])).double()
+            v = torch.cat((s["v"][page, keys % ps, h], s["v_tree"][b, :n, h])).double()
+            for e in range(h * G, h * G + G):
+                x = s["q"][b, :n, e].double().mm(k.t().contiguous()) / math.sqrt(D)
+                out[b, :n, e] = torch.softmax(x.masked_fill(~see, -math.inf), -1).mm(v)
+    return out
+
+
+def _exact_verify(s):
+    p, q = s["target"], s["draft"]
+    B, N, V = p.shape
+    tok, par, u = s["tokens"].tolist(), s["parent"].tolist(), s["u_accept"].double().tolist()
+    counts = [N] * B if s["n_nodes"] is None else s["n_nodes"].tolist()
+    last = s["u_final"].double().tolist()
+    tokens, nodes, n_acc = [], [], []
+    for b in range(B):
+        here, path, said = 0, [0], []
+        while True:
+            # the distribution that the next child is held against, renormalised at every refusal
+            dist, moved, left = p[b, here].double(), False, 1.0
+            for i in [i for i in range(1, counts[b]) if par[b][i] == here]:
+                x = tok[b][i]
+                if q is None:
+                    px = float(dist[x])
+                    if u[b][i] * left < px:
+                        moved = True
+                    else:
+                        left -= px
+                        dist = dist.clone()
+                        dist[x] = 0.0
+                else:
+                    qx, px = float(q[b, here, x].double()), float(dist[x])
+                    if u[b][i] * qx < px:
+                        moved = True
+                    else:
+                        dist = (dist - q[b, here].double()).clamp(min=0.0)
+                        dist = dist / dist.sum()
+                if moved:
+                    said.append(x)
+                    path.append(i)
+                    here = i
+                    break
+            if not moved:
+                break
+        cum = dist.cumsum(0)
+        said.append(int((cum <= last[b] * float(cum[-1])).sum()))
+        n_acc.append(len(path) - 1)
+        tokens.append(said + [-1] * (N - len(said)))
+        nodes.append(path + [-1] * (N - len(path)))
+    as_int = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    return {"tokens": as_int(tokens), "nodes": as_int(nodes), "n_accepted": as_int(n_acc)}
+
+
+def _exact_pages(s):
+    """The cache operators page by page on the host; the moved rows are copies, exact in any type."""
+    c = s["case"]
+    B, ps, pages = c["B"], c["page"], s["k"].shape[1]
+    table, lens, width = s["table"].tolist(), s["len"].tolist(), s["table"].shape[1]
+    k, v = s["k"].clone(), s["v"].clone()
+    need, moves = 0, []
+    if c["op"] == "commit":
+        rows = [n + 1 for n in s["n_accepted"].tolist()]
+        nodes = s["nodes"].tolist()
+        out = [table[b][:(lens[b] + ps - 1) // ps] for b in range(B)]
+        free = sorted(set(range(pages)) - {x for r in out for x in r})
+        for b in range(B):
+            for r in range(rows[b]):
+                if (lens[b] + r) // ps == len(out[b]):
+                    out[b].append(free[need])
+                    need += 1
+                moves.append((out[b][(lens[b] + r) // ps], (lens[b] + r) % ps, b, nodes[b][r]))
+        for page, slot, b, node in moves:
+            k[:, page, slot] = s["k_tree"][:, b, node]
+            v[:, page, slot] = s["v_tree"][:, b, node]
+        length = [lens[b] + rows[b] for b in range(B)]
+    else:
+        anc, kept, out, copies = s["ancestor"].tolist(), set(), [], []
+        for b, a in enumerate(anc):
+            own_pages = table[a][:(lens[a] + ps - 1) // ps]
+            if lens[a] % ps and a in kept:
+                copies.append((b, own_pages[-1], lens[a] % ps))
+                own_pages = own_pages[:-1]
+            kept.add(a)
+            out.append(list(own_pages))
+        free = sorted(set(range(pages)) - {x for r in out for x in r})
+        for i, (b, src, part) in enumerate(copies):
+            out[b].append(free[i])
+            k[:, free[i], :part] = k[:, src, :part]
+            v[:, free[i], :part] = v[:, src, :part]
+        length = [lens[a] for a in anc]
+    as_int = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    return {"table": as_int([r + [-1] * (width - len(r)) for r in out]), "len": as_int(length), "status": as_int([0]),
+            "k": k, "v": v}
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "attention":
+        return _exact_attention(s)
+    return _exact_verify(s) if case["op"] == "verify" else _exact_pages(s)
