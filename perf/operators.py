@@ -182,8 +182,9 @@ def prepare(case, seed):
     if c["op"] == "verify":
         V, dt = c["V"], DTYPES[c["dtype"]]
         parent = _parents(B, N, c["branch"], g)
-        # the target's logits, a draft model near them (about two in three of its samples pass), temperature 0.7
-        logits = _randn((B, N, V), torch.float32, g, 2.0)
+        # the target's logits, a draft model near them (about two in three of its samples pass), temperature 0.7;
+        # without one, more certain logits, of which the most probable ids are worth a try
+        logits = _randn((B, N, V), torch.float32, g, 2.0 if c["draft"] else 3.5)
         s["target"] = torch.softmax(logits / 0.7, -1).to(dt)
         at = parent.clamp(min=0).long()
         if c["draft"]:
