@@ -114,7 +114,8 @@ enum {
     SV_ENOMEM = -5,   /* scratch allocation failed */
     SV_EALIGN = -6,   /* a pointer is not aligned to its element size */
     SV_ECAPTURE = -7, /* the stream is being captured and the scratch would have to grow */
-    SV_ETOOBIG = -8   /* spec_verify_noalloc: the call needs more than its fixed scratch */
+    SV_ETOOBIG = -8   /* spec_verify_noalloc: the call needs more than its fixed scratch;
+                         tree and cache calls: the workspace is too small */
 };
 
 /* Probe record layout (float64), per row b and position j in [0, K]:
@@ -331,6 +332,214 @@ int spec_draft_produce(const sv_logits* target_logits, int32_t K, uint64_t seed,
                        void* draft_out, int64_t out_stride_b, int64_t out_stride_p,
                        int32_t* out_tokens, void* stream);
 
+/*
+ * ---- The tree round --------------------------------------------------------
+ *
+ * Drafts that form a tree (page "LogitSpec", gist.science 2507.01449, section
+ * 2: a draft tree with its attention mask; a chain is the tree whose parent of
+ * node i is node i - 1) over a paged key/value cache (page "HiSpec", section 2:
+ * block tables; page "Faster LLM Inference via Sequential Monte Carlo",
+ * section 2: particles that share and copy cache pages):
+ *
+ *   spec_tree_attention   every node attends to the cache and its ancestors;
+ *   spec_verify_tree      the target's probabilities accept a path of the tree;
+ *   spec_cache_commit     the accepted path's rows go into the cache;
+ *   spec_cache_fork       the slots of a batch continue their ancestors (the
+ *                         out_ancestor of spec_smc_step), or are freed.
+ *
+ * A tree has N <= SPECVERIFY_MAX_NODES nodes.  Node 0 is the last token of the
+ * sequence, whose keys and values are not in the cache yet; node i > 0 is a
+ * drafted token after node parent[i] < i.  Level order is not required.
+ *
+ * A sequence's cache is its row of the block table: row j of the sequence lies
+ * in slot j % page_size of page table[j / page_size].
+ *
+ * These calls take a workspace from the caller (its size from the functions
+ * below; contents need no preparation and mean nothing after the call), so
+ * they never allocate and any of them may be captured.  Two calls that may run
+ * at the same time, captured ones included, need workspaces of their own.
+ */
+#define SPECVERIFY_MAX_NODES 64
+#define SPECVERIFY_MAX_PAGES (1 << 20)
+enum { SV_F16 = 2 };  /* a dtype of the attention and the cache */
+
+/*
+ * spec_tree_attention -- for every sequence b, node i and query head e,
+ *
+ *   out[b, i, e] = sum_j softmax_j(scale * q[b, i, e] . k_j) v_j
+ *
+ * over the cache rows j < len[b] of key head e / (heads / kv_heads) and over
+ * the nodes j that are i or one of its ancestors.  Softmax statistics and sums
+ * are float32; the weights are rounded to the input type before they meet V.
+ *
+ * With window > 0, node i at depth d has position len + d and sees the cache
+ * rows with len + d - j < window, the first `sinks` cache rows, and the nearest
+ * `window` of itself and its ancestors.  window = 0: everything.
+ *
+ * dtype          SV_BF16 or SV_F16, of all tensors.
+ * B, N           1 <= B <= 65536 sequences, 1 <= N <= 64 nodes.
+ * heads, kv_heads  query and key heads; heads a multiple of kv_heads.
+ * dim            a multiple of 8, at most 128.
+ * q, out         [B, N, heads, dim]; k_tree, v_tree [B, N, kv_heads, dim];
+ *                strides in elements for (sequence, node, head).
+ * k_cache, v_cache  [pages, page_size, kv_heads, dim]; strides for (page,
+ *                slot, head); page_size a power of two, at most 1024.
+ *                The last axis of every tensor is contiguous; data and strides
+ *                are multiples of 16 bytes; strides are >= 0.
+ * table          device int32 [B, width], row stride table_stride.  An entry
+ *                outside [0, pages) hides its rows.  width * page_size <= 2^28.
+ * len            device int32 [B], rows in the cache (clamped to [0, width *
+ *                page_size]).
+ * parent         device int32 [B, N], contiguous; parent[b, 0] is not read.  A
+ *                parent outside [0, i) ends the line: node i has no ancestors.
+ * n_nodes        device int32 [B] or NULL (N for all), clamped to [0, N].  The
+ *                output of an absent node is zero.
+ * scale          finite.
+ * workspace      at least spec_tree_attention_workspace(args) bytes, aligned
+ *                to 16 bytes (may be NULL if that is 0).
+ *
+ * What a node does not see never reaches its output, whatever it holds (NaN
+ * and infinities included).  out must not overlap the inputs.
+ *
+ * Errors: SV_EINVAL (NULL, negative stride, scale, window or sinks < 0),
+ * SV_ESHAPE, SV_EDTYPE, SV_EALIGN, SV_ETOOBIG (workspace too small), SV_EHIP.
+ */
+typedef struct {
+    int32_t dtype;
+    int32_t B, N, heads, kv_heads, dim;
+    const void* q;
+    int64_t q_stride[3];
+    const void* k_tree;
+    const void* v_tree;
+    int64_t k_tree_stride[3], v_tree_stride[3];
+    const void* k_cache;
+    const void* v_cache;
+    int64_t k_cache_stride[3], v_cache_stride[3];
+    int32_t pages, page_size, width;
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* len;
+    const int32_t* parent;
+    const int32_t* n_nodes;
+    float scale;
+    int32_t window, sinks;
+    void* out;
+    int64_t out_stride[3];
+    void* workspace;
+    int64_t workspace_bytes;
+} sv_tree_attention;
+
+int spec_tree_attention(const sv_tree_attention* args, void* stream);
+
+/* Bytes of workspace the call needs, from its sizes (pointers are not looked
+ * at); a negative status for sizes the call refuses. */
+int64_t spec_tree_attention_workspace(const sv_tree_attention* args);
+
+/*
+ * spec_verify_tree -- verification of a tree of drafted tokens against the
+ * target's probabilities, from given random numbers: for callers with their
+ * own sampler (penalties, top-k, grammars), whose distributions are not the
+ * tempered softmax spec_verify computes.  With p and q the target's and the
+ * draft's row at the current node (node 0 at first), its children are tested
+ * in the order of their numbers:
+ *
+ *   with draft_probs (children drawn independently from q; the acceptance rule
+ *   and the corrected distribution of spec_verify, applied again after every
+ *   refusal to what is left of p):
+ *       accept x iff  u S q(x) < p(x) - a q(x);  a = 0, S = 1 at first, after
+ *       a refusal a += S and S = sum_v max(0, p(v) - a q(v));
+ *   without (children chosen, not drawn): accept x iff u S < p(x); a refusal
+ *       takes p(x) out of S and x out of p; x refused before is refused again.
+ *
+ * An accepted child becomes the current node.  Where all are refused, or there
+ * are none, one more token is drawn by inverse CDF in id order at u_final from
+ * what is left: max(0, p - a q), or p without the refused ids (p itself where
+ * nothing is left of it).  All in float64.
+ *
+ * target_probs   [B, N, V] (the descriptor's P = N <= 64): row i the target's
+ *                distribution after node i.  fp32 or bf16.  V <= SPECVERIFY_MAX_V.
+ * draft_probs    [B, P, V], same dtype, P <= N: row i the distribution the
+ *                children of node i were drawn from; or NULL.
+ * tokens         device int32 [B, N]: the nodes' ids (node 0's is not read).
+ * parent         device int32 [B, N] (node 0's is not read).
+ * n_nodes        device int32 [B] or NULL (N for all).
+ * u_accept       device float32 [B, N]: node i's uniform (node 0's is not read).
+ * u_final        device float32 [B].
+ * out_tokens     device int32 [B, N]: the n accepted ids, the last token, -1.
+ * out_nodes      device int32 [B, N]: the path: node 0, the n accepted nodes, -1.
+ * out_n_accepted device int32 [B]: n.
+ *
+ * A sequence is invalid (n = -1 and -1 throughout) when n_nodes lies outside
+ * [1, N], a node's parent outside [0, i) (with draft_probs, outside [0, P)),
+ * its id outside [0, V), its uniform or u_final outside [0, 1), or when a
+ * probability at a drafted id, or in a row that is read whole (the last node's
+ * row, and rows whose S is needed), is negative, infinite or NaN, or the last
+ * row has no positive entry.  Errors as spec_verify.
+ */
+int spec_verify_tree(const sv_logits* target_probs, const sv_logits* draft_probs, const int32_t* tokens,
+                     const int32_t* parent, const int32_t* n_nodes, const float* u_accept, const float* u_final,
+                     int32_t* out_tokens, int32_t* out_nodes, int32_t* out_n_accepted, void* stream);
+
+/*
+ * A paged cache of `layers` layers and the block tables of B sequences.  The
+ * tables are the whole state: a page is in use exactly if a live entry (one of
+ * the first ceil(len / page_size) of a row) names it, and free otherwise.
+ */
+typedef struct {
+    void* k;                /* [layers, pages, page_size, heads, dim] */
+    void* v;
+    int32_t dtype;          /* SV_F32, SV_BF16 or SV_F16; rows are moved, not computed with */
+    int32_t layers, pages, page_size, heads, dim;
+    int64_t k_stride[4], v_stride[4];  /* layer, page, slot, head */
+    const int32_t* table;   /* [B, width], row stride table_stride */
+    int64_t table_stride;
+    const int32_t* len;     /* [B] */
+    int32_t B, width;
+} sv_cache;
+
+/*
+ * spec_cache_commit -- append the accepted path of every sequence's tree:
+ * rows nodes[b, 0..n] of k_tree, v_tree ([layers, B, N, heads, dim], strides
+ * for layer, sequence, node, head) become the cache rows len..len+n, for n =
+ * n_accepted[b]; a negative n appends nothing.  nodes NULL: rows 0..n (a
+ * chain: the out_n_accepted of spec_verify).  A partly filled last page is
+ * filled up, and further pages are taken lowest free page first, in the order
+ * of the sequences.  A partly filled last page must belong to one sequence
+ * only (spec_cache_fork leaves it so).
+ *
+ * out_table [B, width] (row stride out_stride) and out_len [B] receive the new
+ * tables, -1 behind the live entries; they may be table and len themselves
+ * (same stride), and must not overlap them otherwise.
+ *
+ * out_status  device int32 [1]: 0; or the number of pages that were lacking;
+ *             or -1 when a length, count, node or live page number is out of
+ *             range or a table row too short.  Unless 0, nothing is appended
+ *             and tables and lengths go out as they came in.
+ *
+ * dim * element size, strides and data are multiples of 16 bytes; pages <=
+ * SPECVERIFY_MAX_PAGES; page_size a power of two, at most 1024; B, layers <=
+ * 65534; width * page_size <= 2^28.  workspace: spec_cache_workspace bytes.
+ */
+int spec_cache_commit(const sv_cache* cache, const void* k_tree, const void* v_tree, const int64_t k_tree_stride[4],
+                      const int64_t v_tree_stride[4], int32_t N, const int32_t* nodes, const int32_t* n_accepted,
+                      int32_t* out_table, int64_t out_stride, int32_t* out_len, int32_t* out_status, void* workspace,
+                      int64_t workspace_bytes, void* stream);
+
+/*
+ * spec_cache_fork -- slot k continues sequence ancestor[k] (its own: k; -1:
+ * the slot is freed).  Full pages are shared; a partly filled last page stays
+ * with the lowest slot that continues its sequence and is copied, in every
+ * layer, to the lowest free pages for the others.  Pages that no slot names
+ * any more are free.  Outputs, status and limits as spec_cache_commit, with
+ * out_table and out_len apart from table and len.
+ */
+int spec_cache_fork(const sv_cache* cache, const int32_t* ancestor, int32_t* out_table, int64_t out_stride,
+                    int32_t* out_len, int32_t* out_status, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace a commit of at most N rows per sequence, or a fork (N =
+ * 0), needs. */
+int64_t spec_cache_workspace(int32_t B, int32_t N, int32_t page_size);
+
 /* Human-readable text for a status code (for SV_EHIP, the last HIP error). */
 const char* spec_verify_strerror(int status);
 
@@ -346,7 +555,8 @@ int spec_verify_abi_version(void);
  * spec_verify_profile_read synchronises those events and writes, for each of
  * the n kernel kinds (0 statistics pass, 1 nucleus selection, 2 row pass:
  * decision and resample, or the SMC particle pass, 3 SMC resampling, 4 the
- * synthetic draft producer), the
+ * synthetic draft producer, 5 tree attention, 6 its join, 7 tree verification,
+ * 8 cache plan, 9 cache copies), the
  * summed duration in milliseconds and the number of launches since the last
  * read; it returns the number of kinds written.  Host arrays ms[n],
  * launches[n]. */

@@ -24,6 +24,8 @@ Modules:
   greedy  -- greedy verify (argmax acceptance) and the top-k of the last
              logits after the emitted token.
   produce -- the synthetic draft producer of the two-batch schedule.
+  tree    -- the tree round: attention of drafted trees over a paged cache,
+             tree verification, commit and fork of cache pages.
 """
 
 from .greedy import GreedyResult, argmax_lowest, greedy_verify, top_k_after_first  # noqa: F401

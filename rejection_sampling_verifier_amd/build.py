@@ -15,8 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libspecverify.so")
 ARCH = "gfx950"
 
-SOURCES = ["sv_kernels.hip", "sv_produce.hip", "sv_api.cpp"]
-DEPS = ["sv_internal.h", "sv_device.h"]
+SOURCES = ["sv_kernels.hip", "sv_produce.hip", "sv_tree_attn.hip", "sv_tree_verify.hip", "sv_cache.hip", "sv_api.cpp"]
+DEPS = ["sv_internal.h", "sv_device.h", "sv_tree.h"]
 
 
 def hipcc():

@@ -18,6 +18,7 @@
 
 #include "../../include/specverify.h"
 #include "sv_internal.h"
+#include "sv_tree.h"
 
 namespace {
 
@@ -568,6 +569,261 @@ int produce_impl(const sv_logits* tl, int32_t K, uint64_t seed, void* out, int64
                         [&](const sv::LaunchEvents& ev) { return sv::launch_produce_tokens(p, stream, ev); });
 }
 
+// ---- the tree round ----
+
+static_assert(SPECVERIFY_MAX_NODES == sv::kMaxNodes && SV_F16 == sv::kDTypeF16, "tree limits");
+
+bool pow2_page(int ps) { return ps >= 1 && ps <= 1024 && (ps & (ps - 1)) == 0; }
+
+// Strides of a tensor whose rows are read 16 bytes at a time; they come out
+// in units of `unit` elements.
+int check_rows(const void* data, const int64_t* stride, int n, int elem, int64_t* out, int64_t unit) {
+    if (!data) return SV_EINVAL;
+    for (int i = 0; i < n; ++i)
+        if (stride[i] < 0) return SV_EINVAL;
+    if (misaligned(data, 16)) return SV_EALIGN;
+    for (int i = 0; i < n; ++i) {
+        if (stride[i] * elem % 16) return SV_EALIGN;
+        out[i] = stride[i] / unit;
+    }
+    return SV_OK;
+}
+
+// How the attention's work is cut: rows and keys per workgroup tile by the
+// query rows that share a key head, parts by the device's size.
+struct TreePlan {
+    sv::TreeAttnShape s;
+    int MT = 1, clusters = 1, min_tiles = 1, merge = 0;
+    size_t start_bytes = 0, total = 0;
+};
+
+int plan_tree(const sv_tree_attention* a, TreePlan& t) {
+    if (!a) return SV_EINVAL;
+    if (a->dtype != SV_BF16 && a->dtype != SV_F16) return SV_EDTYPE;
+    if (a->B < 1 || a->B > 65536 || a->N < 1 || a->N > SPECVERIFY_MAX_NODES) return SV_ESHAPE;
+    if (a->heads < 1 || a->kv_heads < 1 || a->heads > 4096 || a->heads % a->kv_heads) return SV_ESHAPE;
+    if (a->dim < 8 || a->dim > 128 || a->dim % 8) return SV_ESHAPE;
+    if (a->pages < 1 || !pow2_page(a->page_size) || a->width < 0) return SV_ESHAPE;
+    if (static_cast<int64_t>(a->width) * a->page_size > (1ll << 28)) return SV_ESHAPE;
+    const int rows = a->N * (a->heads / a->kv_heads);
+    t.s.dp = a->dim <= 64 ? 64 : 128;
+    // one wave per 32 query rows; waves beyond that share the rows and split the keys
+    t.s.wr = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
+    t.s.rows = 32 * t.s.wr;
+    t.s.keys = t.s.dp == 128 && t.s.wr > 1 ? 64 : 128;
+    t.MT = (rows + t.s.rows - 1) / t.s.rows;
+    const int64_t tasks = static_cast<int64_t>(a->B) * a->kv_heads;
+    if (tasks > (1ll << 24)) return SV_ESHAPE;
+    const int64_t cap = static_cast<int64_t>(a->width) * a->page_size;
+    const int64_t most = (cap + t.s.keys - 1) / t.s.keys + 1;  // tiles of one (sequence, key head)
+    const int64_t blocks = 2ll * device_cus();                 // two workgroups per CU fit
+    if (most <= 4) {
+        // so short that a part is a whole (sequence, key head): nothing to join
+        t.merge = 0;
+        t.clusters = static_cast<int>(tasks);
+    } else {
+        t.merge = 1;
+        t.min_tiles = 2;
+        int64_t c = blocks / t.MT;
+        const int64_t need = (tasks * most + t.min_tiles - 1) / t.min_tiles;
+        if (c > need) c = need;
+        t.clusters = static_cast<int>(c < 1 ? 1 : c);
+        t.start_bytes = align256((static_cast<size_t>(a->B) + 1) * sizeof(int64_t));
+        t.total = t.start_bytes +
+                  static_cast<size_t>(t.clusters) * 2 * t.MT * t.s.rows * (t.s.dp + 2) * sizeof(float);
+    }
+    return SV_OK;
+}
+
+int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
+    TreePlan t;
+    int rc = plan_tree(a, t);
+    if (rc) return rc;
+    sv::TreeAttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (!a->out || !a->len || !a->parent || (a->width > 0 && !a->table)) return SV_EINVAL;
+    if (a->table_stride < 0 || a->window < 0 || a->sinks < 0 || !std::isfinite(a->scale)) return SV_EINVAL;
+    const struct {
+        const void* data;
+        const int64_t* stride;
+        int64_t* out;
+    } rows[] = {{a->q, a->q_stride, p.qs},
+                {a->k_tree, a->k_tree_stride, p.kts},
+                {a->v_tree, a->v_tree_stride, p.vts},
+                {a->k_cache, a->k_cache_stride, p.kcs},
+                {a->v_cache, a->v_cache_stride, p.vcs},
+                {a->out, a->out_stride, p.os}};
+    for (const auto& r : rows) {
+        rc = check_rows(r.data, r.stride, 3, 2, r.out, 1);
+        if (rc) return rc;
+    }
+    if (misaligned(a->table, 4) || misaligned(a->len, 4) || misaligned(a->parent, 4) ||
+        (a->n_nodes && misaligned(a->n_nodes, 4)))
+        return SV_EALIGN;
+    if (t.total > 0) {
+        if (!a->workspace) return SV_EINVAL;
+        if (misaligned(a->workspace, 16)) return SV_EALIGN;
+        if (a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < t.total) return SV_ETOOBIG;
+    }
+    p.q = static_cast<const uint8_t*>(a->q);
+    p.kt = static_cast<const uint8_t*>(a->k_tree);
+    p.vt = static_cast<const uint8_t*>(a->v_tree);
+    p.kc = static_cast<const uint8_t*>(a->k_cache);
+    p.vc = static_cast<const uint8_t*>(a->v_cache);
+    p.out = static_cast<uint8_t*>(a->out);
+    p.table = a->table;
+    p.table_stride = a->table_stride;
+    p.len = a->len;
+    p.parent = a->parent;
+    p.n_nodes = a->n_nodes;
+    p.B = a->B;
+    p.N = a->N;
+    p.Hkv = a->kv_heads;
+    p.G = a->heads / a->kv_heads;
+    p.D = a->dim;
+    p.pages = a->pages;
+    p.width = a->width;
+    p.ps_shift = __builtin_ctz(static_cast<unsigned>(a->page_size));
+    // beyond every length and depth both mean everything; the kernel subtracts row numbers from them
+    p.window = std::min(a->window, 1 << 29);
+    p.sinks = std::min(a->sinks, 1 << 29);
+    p.scale2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634074);
+    p.MT = t.MT;
+    p.clusters = t.clusters;
+    p.min_tiles = t.min_tiles;
+    p.merge = t.merge;
+    if (t.merge) {
+        p.start = static_cast<int64_t*>(a->workspace);
+        p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + t.start_bytes);
+    }
+    const int dtype = a->dtype == SV_BF16 ? static_cast<int>(sv::DT_BF16) : sv::kDTypeF16;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    rc = timed_launch(sv::KK_TREE_ATTN, stream,
+                      [&](const sv::LaunchEvents& ev) { return sv::launch_tree_attn(p, t.s, dtype, stream, ev); });
+    if (rc || !t.merge) return rc;
+    return timed_launch(sv::KK_TREE_MERGE, stream,
+                        [&](const sv::LaunchEvents& ev) { return sv::launch_tree_merge(p, t.s, dtype, stream, ev); });
+}
+
+int verify_tree_impl(const sv_logits* tp, const sv_logits* dp, const int32_t* tokens, const int32_t* parent,
+                     const int32_t* n_nodes, const float* u_accept, const float* u_final, int32_t* out_tokens,
+                     int32_t* out_nodes, int32_t* out_n, void* stream_v) {
+    int rc = check_logits(tp);
+    if (rc) return rc;
+    if (dp) {
+        rc = check_logits(dp);
+        if (rc) return rc;
+    }
+    if (!tokens || !parent || !u_accept || !u_final || !out_tokens || !out_nodes || !out_n) return SV_EINVAL;
+    if (misaligned(tokens, 4) || misaligned(parent, 4) || (n_nodes && misaligned(n_nodes, 4)) ||
+        misaligned(u_accept, 4) || misaligned(u_final, 4) || misaligned(out_tokens, 4) || misaligned(out_nodes, 4) ||
+        misaligned(out_n, 4))
+        return SV_EALIGN;
+    if (dp && dp->dtype != tp->dtype) return SV_EDTYPE;
+    const int B = tp->B, N = tp->P, V = tp->V;
+    if (B < 1 || B > (1 << 22) || N < 1 || N > SPECVERIFY_MAX_NODES || V < 1 || V > SPECVERIFY_MAX_V) return SV_ESHAPE;
+    if (dp && (dp->B != B || dp->V != V || dp->P < 1 || dp->P > N)) return SV_ESHAPE;
+    sv::TreeVerifyParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.tgt = static_cast<const uint8_t*>(tp->data);
+    p.tsb = tp->stride_b;
+    p.tsp = tp->stride_p;
+    if (dp) {
+        p.dft = static_cast<const uint8_t*>(dp->data);
+        p.dsb = dp->stride_b;
+        p.dsp = dp->stride_p;
+        p.P = dp->P;
+    }
+    p.tokens = tokens;
+    p.parent = parent;
+    p.n_nodes = n_nodes;
+    p.u_accept = u_accept;
+    p.u_final = u_final;
+    p.out_tokens = out_tokens;
+    p.out_nodes = out_nodes;
+    p.out_n = out_n;
+    p.B = B;
+    p.N = N;
+    p.V = V;
+    const int dtype = tp->dtype == SV_BF16 ? sv::DT_BF16 : sv::DT_F32;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    return timed_launch(sv::KK_TREE_VERIFY, stream,
+                        [&](const sv::LaunchEvents& ev) { return sv::launch_tree_verify(p, dtype, stream, ev); });
+}
+
+// Workspace of a commit or fork: the plan, one word per slot, the new pages.
+int64_t cache_workspace(int64_t B, int64_t N, int64_t page_size) {
+    const int64_t fresh = N > 0 ? (N + page_size - 1) / page_size + 1 : 1;
+    return 4 * B * (sv::kPlanWords + 1 + fresh);
+}
+
+int cache_impl(const sv_cache* c, const void* kt, const void* vt, const int64_t* kts, const int64_t* vts, int32_t N,
+               const int32_t* nodes, const int32_t* n_accepted, const int32_t* ancestor, bool fork,
+               int32_t* out_table, int64_t out_stride, int32_t* out_len, int32_t* out_status, void* ws,
+               int64_t ws_bytes, void* stream_v) {
+    if (!c) return SV_EINVAL;
+    if (c->dtype != SV_F32 && c->dtype != SV_BF16 && c->dtype != SV_F16) return SV_EDTYPE;
+    const int elem = c->dtype == SV_F32 ? 4 : 2;
+    if (c->B < 1 || c->B > 65534 || c->layers < 1 || c->layers > 65534 || c->heads < 1 || c->heads > 4096 ||
+        c->dim < 1 || c->dim > 65536 || c->pages < 1 || c->pages > SPECVERIFY_MAX_PAGES || !pow2_page(c->page_size) ||
+        c->width < 1 || static_cast<int64_t>(c->width) * c->page_size > (1ll << 28))
+        return SV_ESHAPE;
+    if (!fork && (N < 1 || N > SPECVERIFY_MAX_NODES)) return SV_ESHAPE;
+    if (!c->table || !c->len || !out_table || !out_len || !out_status || !ws) return SV_EINVAL;
+    if (fork ? !ancestor : !n_accepted) return SV_EINVAL;
+    if (c->table_stride < 0 || out_stride < c->width) return SV_EINVAL;
+    // a fork permutes rows; a commit may run in place, row on row
+    if (fork && (out_table == c->table || out_len == c->len)) return SV_EINVAL;
+    if (!fork && out_table == c->table && out_stride != c->table_stride) return SV_EINVAL;
+    if (misaligned(c->table, 4) || misaligned(c->len, 4) || misaligned(out_table, 4) || misaligned(out_len, 4) ||
+        misaligned(out_status, 4) || misaligned(ws, 4) || (nodes && misaligned(nodes, 4)) ||
+        (n_accepted && misaligned(n_accepted, 4)) || (ancestor && misaligned(ancestor, 4)))
+        return SV_EALIGN;
+    if (static_cast<int64_t>(c->dim) * elem % 16) return SV_EALIGN;
+    sv::CacheParams p;
+    std::memset(&p, 0, sizeof(p));
+    const int64_t unit = 16 / elem;
+    int rc = check_rows(c->k, c->k_stride, 4, elem, p.ks, unit);
+    if (!rc) rc = check_rows(c->v, c->v_stride, 4, elem, p.vs, unit);
+    if (!rc && !fork) {
+        if (!kts || !vts) return SV_EINVAL;
+        rc = check_rows(kt, kts, 4, elem, p.kts, unit);
+        if (!rc) rc = check_rows(vt, vts, 4, elem, p.vts, unit);
+    }
+    if (rc) return rc;
+    if (ws_bytes < cache_workspace(c->B, fork ? 0 : N, c->page_size)) return SV_ETOOBIG;
+    p.k = static_cast<uint8_t*>(c->k);
+    p.v = static_cast<uint8_t*>(c->v);
+    p.kt = static_cast<const uint8_t*>(kt);
+    p.vt = static_cast<const uint8_t*>(vt);
+    p.layers = c->layers;
+    p.pages = c->pages;
+    p.ps_shift = __builtin_ctz(static_cast<unsigned>(c->page_size));
+    p.heads = c->heads;
+    p.vec = static_cast<int>(c->dim / unit);
+    p.table = c->table;
+    p.len = c->len;
+    p.out_table = out_table;
+    p.out_len = out_len;
+    p.status = out_status;
+    p.table_stride = c->table_stride;
+    p.out_stride = out_stride;
+    p.B = c->B;
+    p.N = N;
+    p.width = c->width;
+    p.nodes = nodes;
+    p.n_accepted = n_accepted;
+    p.ancestor = ancestor;
+    p.fork = fork ? 1 : 0;
+    p.plan = static_cast<int32_t*>(ws);
+    const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    rc = timed_launch(sv::KK_CACHE_PLAN, stream,
+                      [&](const sv::LaunchEvents& ev) { return sv::launch_cache_plan(p, stream, ev); });
+    if (rc) return rc;
+    return timed_launch(sv::KK_CACHE_COPY, stream,
+                        [&](const sv::LaunchEvents& ev) { return sv::launch_cache_copy(p, stream, ev); });
+}
+
 }  // namespace
 
 extern "C" {
@@ -621,17 +877,52 @@ int spec_draft_produce(const sv_logits* target_logits, int32_t K, uint64_t seed,
     return produce_impl(target_logits, K, seed, draft_out, out_stride_b, out_stride_p, out_tokens, stream);
 }
 
+int spec_tree_attention(const sv_tree_attention* args, void* stream) { return tree_attention_impl(args, stream); }
+
+int64_t spec_tree_attention_workspace(const sv_tree_attention* args) {
+    TreePlan t;
+    const int rc = plan_tree(args, t);
+    return rc ? rc : static_cast<int64_t>(t.total);
+}
+
+int spec_verify_tree(const sv_logits* target_probs, const sv_logits* draft_probs, const int32_t* tokens,
+                     const int32_t* parent, const int32_t* n_nodes, const float* u_accept, const float* u_final,
+                     int32_t* out_tokens, int32_t* out_nodes, int32_t* out_n_accepted, void* stream) {
+    return verify_tree_impl(target_probs, draft_probs, tokens, parent, n_nodes, u_accept, u_final, out_tokens,
+                            out_nodes, out_n_accepted, stream);
+}
+
+int spec_cache_commit(const sv_cache* cache, const void* k_tree, const void* v_tree, const int64_t k_tree_stride[4],
+                      const int64_t v_tree_stride[4], int32_t N, const int32_t* nodes, const int32_t* n_accepted,
+                      int32_t* out_table, int64_t out_stride, int32_t* out_len, int32_t* out_status, void* workspace,
+                      int64_t workspace_bytes, void* stream) {
+    return cache_impl(cache, k_tree, v_tree, k_tree_stride, v_tree_stride, N, nodes, n_accepted, nullptr, false,
+                      out_table, out_stride, out_len, out_status, workspace, workspace_bytes, stream);
+}
+
+int spec_cache_fork(const sv_cache* cache, const int32_t* ancestor, int32_t* out_table, int64_t out_stride,
+                    int32_t* out_len, int32_t* out_status, void* workspace, int64_t workspace_bytes, void* stream) {
+    return cache_impl(cache, nullptr, nullptr, nullptr, nullptr, 0, nullptr, nullptr, ancestor, true, out_table,
+                      out_stride, out_len, out_status, workspace, workspace_bytes, stream);
+}
+
+int64_t spec_cache_workspace(int32_t B, int32_t N, int32_t page_size) {
+    if (B < 1 || N < 0 || !pow2_page(page_size)) return SV_ESHAPE;
+    return cache_workspace(B, N, page_size);
+}
+
 const char* spec_verify_strerror(int status) {
     switch (status) {
         case SV_OK: return "success";
-        case SV_EINVAL: return "invalid argument (NULL pointer, temperature, top_p or stride)";
+        case SV_EINVAL: return "invalid argument (NULL pointer, temperature, top_p, scale, window or stride)";
         case SV_ESHAPE: return "invalid shape (B, K, V out of range or target/draft mismatch)";
         case SV_EDTYPE: return "invalid or mismatched dtype";
         case SV_EHIP: return g_hip_msg.empty() ? "HIP runtime error" : g_hip_msg.c_str();
         case SV_ENOMEM: return "scratch allocation failed";
-        case SV_EALIGN: return "pointer not aligned to its element size";
+        case SV_EALIGN: return "pointer not aligned to its element size (tree and cache rows: to 16 bytes)";
         case SV_ECAPTURE: return "the stream is being captured and the call would have to grow its scratch";
-        case SV_ETOOBIG: return "the call needs more scratch than spec_verify_noalloc's fixed array holds";
+        case SV_ETOOBIG:
+            return "the call needs more scratch than spec_verify_noalloc's fixed array, or the given workspace, holds";
         default: return "unknown status";
     }
 }
@@ -669,7 +960,7 @@ int spec_verify_profile_read(double* ms, int64_t* launches, int n) {
         std::lock_guard<std::mutex> lk(g_mu);
         evs.swap(g_events);
     }
-    const int kinds = n < sv::KK_COUNT ? n : sv::KK_COUNT;
+    const int kinds = n < sv::KK_ALL ? n : static_cast<int>(sv::KK_ALL);
     for (int k = 0; k < kinds; ++k) {
         ms[k] = 0.0;
         launches[k] = 0;

@@ -1,0 +1,251 @@
+"""spec_tree_attention on the GPU against the float64 oracle: head layouts,
+tree shapes, lengths from none to many tiles, ragged batches, windows with and
+without sinks, strides, hidden rows that hold NaN, and HIP graphs."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import say
+from oracle import tree as ref
+from rejection_sampling_verifier_amd import binding
+from tree_helpers import attention_tolerance, dev, f64, parents, tables
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    binding.load()
+    yield
+    torch.cuda.synchronize()
+
+
+def make(B=2, N=5, H=4, Hkv=2, D=64, lens=(33, 7), ps=16, kind="random", dtype=torch.bfloat16, n_nodes=None,
+         head_major=False, seed=0, poison=True, extra=0):
+    """Inputs on the GPU; with `poison`, rows nothing may read hold NaN."""
+    rng = np.random.default_rng(seed)
+    lens = np.asarray(lens, np.int32)
+    pages, table = tables(lens, ps, rng, extra=extra)
+    g = lambda *s: rng.standard_normal(s)  # noqa: E731
+    k, v = g(pages, ps, Hkv, D), g(pages, ps, Hkv, D)
+    kt, vt, q = g(B, N, Hkv, D), g(B, N, Hkv, D), g(B, N, H, D) * 2
+    if poison:
+        used = np.zeros((pages, ps), bool)
+        for b in range(B):
+            for j in range(lens[b]):
+                used[table[b, j // ps], j % ps] = True
+        k[~used], v[~used] = np.nan, np.nan
+        if n_nodes is not None:
+            for b in range(B):
+                for t in (kt, vt, q):
+                    t[b, max(0, n_nodes[b]):] = np.nan
+    s = dict(q=dev(q, dtype), kt=dev(kt, dtype), vt=dev(vt, dtype), parent=dev(parents(kind, B, N, rng)),
+             table=dev(table), lens=dev(lens), n_nodes=None if n_nodes is None else dev(np.asarray(n_nodes, np.int32)))
+    for name, x in (("k", k), ("v", v)):
+        s[name] = dev(x.transpose(0, 2, 1, 3), dtype).transpose(1, 2) if head_major else dev(x, dtype)
+    return s
+
+
+def call(s, **kw):
+    return binding.tree_attention(s["q"], s["k"], s["v"], s["table"], s["lens"], s["kt"], s["vt"], s["parent"],
+                                  s["n_nodes"], **kw)
+
+
+def oracle_of(s, **kw):
+    n = None if s["n_nodes"] is None else s["n_nodes"].cpu().numpy()
+    return ref.tree_attention(f64(s["q"]), f64(s["k"]), f64(s["v"]), s["table"].cpu().numpy(), s["lens"].cpu().numpy(),
+                              f64(s["kt"]), f64(s["vt"]), s["parent"].cpu().numpy(), n, **kw)
+
+
+def check(s, label, **kw):
+    out = call(s, **kw)
+    torch.cuda.synchronize()
+    want, spread, reach = oracle_of(s, **kw)
+    got = f64(out)
+    vmax = max(float(np.nanmax(np.abs(f64(s["v"])), initial=0.0)), float(np.nanmax(np.abs(f64(s["vt"])))))
+    tol = attention_tolerance(spread, reach, want, s["q"].dtype, s["q"].shape[-1], vmax)
+    seen = np.isfinite(want)  # what a node sees may be NaN (a length that reaches into unwritten slots)
+    assert (np.isfinite(got) == seen).all(), label
+    worst = float(np.max(np.abs(got - want)[seen] / np.maximum(tol[seen], 1e-300), initial=0.0))
+    say(f"[tree attention] {label}: worst error {worst:.3f} of its bound")
+    assert (np.abs(got - want)[seen] <= tol[seen]).all(), (label, worst)
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,Hkv,N", [(4, 4, 1), (8, 2, 5), (8, 1, 9), (10, 2, 13), (16, 2, 16), (8, 2, 64), (3, 3, 33)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_heads_and_nodes(dtype, H, Hkv, N, D):
+    check(make(N=N, H=H, Hkv=Hkv, D=D, lens=(150, 61), dtype=dtype, seed=N), f"H={H} Hkv={Hkv} N={N} D={D} {dtype}")
+
+
+@pytest.mark.parametrize("D", [8, 40, 72, 80, 96, 112])
+def test_head_dimensions(D):
+    check(make(N=6, D=D, lens=(140, 3)), f"D={D}")
+
+
+@pytest.mark.parametrize("ps", [1, 2, 16, 64, 256, 1024])
+@pytest.mark.parametrize("length", [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300])
+def test_lengths_and_pages(length, ps):
+    check(make(B=1, N=4, lens=(length,), ps=ps, seed=length), f"len={length} page={ps}")
+
+
+@pytest.mark.parametrize("N", [3, 12, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_and_ragged(N, D):
+    """Lengths that differ by three orders of magnitude: parts cut across
+    sequences, and single sequences over many parts."""
+    lens = (2500, 0, 1, 700, 64, 1999)
+    check(make(B=6, N=N, H=8, Hkv=2, D=D, lens=lens, n_nodes=[N, 0, 1, N - 1, 2, N], seed=N),
+          f"ragged N={N} D={D}")
+
+
+def test_more_sequences_than_a_workgroup_has_threads():
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 90, 300)
+    lens[250] = 900
+    check(make(B=300, N=2, H=2, Hkv=1, D=64, lens=lens), "B=300")
+
+
+@pytest.mark.parametrize("kind", ["chain", "star", "level2", "level3", "random"])
+@pytest.mark.parametrize("N", [2, 31, 64])
+def test_tree_shapes(kind, N):
+    check(make(N=N, kind=kind, lens=(20, 0)), f"{kind} N={N}")
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (2, 3), (5, 0), (64, 4), (100, 130), (63, 1), (1000, 0), (128, 64)])
+@pytest.mark.parametrize("N,kind", [(1, "chain"), (7, "chain"), (20, "level2")])
+def test_windows(window, sinks, N, kind):
+    check(make(B=3, N=N, kind=kind, D=128, lens=(700, 130, 3)), f"window={window} sinks={sinks} N={N}", window=window,
+          sinks=sinks)
+
+
+def test_bad_parents_end_the_line():
+    s = make(B=1, N=6, lens=(9,))
+    s["parent"][0] = torch.tensor([7, 5, -3, 0, 3, 1], dtype=torch.int32)  # 1: forward, 2: negative
+    check(s, "bad parents")
+
+
+def test_pages_outside_the_pool_are_hidden():
+    s = make(B=2, N=4, lens=(100, 40), poison=True)
+    s["table"][0, 2] = -1
+    s["table"][0, 4] = 10 ** 6
+    s["table"][1, 0] = -7
+    check(s, "bad pages")
+    s["lens"][0] = 10 ** 8  # clamped to the table's width: the rows behind are pages of -1
+    check(s, "length beyond the table")
+    s["lens"][1] = -5
+    check(s, "negative length")
+
+
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -float("inf")])
+def test_hidden_nodes_do_not_reach_others(poison):
+    """A node's K and V reach its descendants only; cache rows outside a node's
+    window reach the nodes that see them only."""
+    s = make(B=1, N=6, kind="chain", lens=(200,), D=128, poison=False)
+    s["parent"][0] = torch.tensor([-1, 0, 0, 1, 2, 0], dtype=torch.int32)
+    clean = call(s)
+    for name in ("kt", "vt"):
+        t = make(B=1, N=6, kind="chain", lens=(200,), D=128, poison=False)
+        t["parent"] = s["parent"]
+        t[name][0, 2] = poison
+        got = call(t)
+        torch.cuda.synchronize()
+        hidden = [0, 1, 3, 5]
+        assert torch.equal(got[0, hidden], clean[0, hidden]), name
+        if name == "vt":
+            assert not torch.isfinite(got[0, [2, 4]]).any()
+    # chain under a window: row len - w + 1 + d leaves the window at depth d + 1
+    s = make(B=1, N=4, kind="chain", lens=(200,), D=128, poison=False)
+    clean = call(s, window=50, sinks=2)
+    s["v"][s["table"][0, 152 // 16].long(), 152 % 16] = poison
+    got = call(s, window=50, sinks=2)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0, 2:], clean[0, 2:])
+    assert not torch.isfinite(got[0, :2]).any()
+
+
+def test_visible_nan_is_not_swallowed():
+    s = make(B=1, N=2, kind="chain", lens=(40,), poison=False)
+    s["v"][s["table"][0, 0].long(), 3] = float("nan")
+    assert torch.isnan(call(s)).all()
+
+
+def test_large_scores():
+    """Scores in the thousands: the running maximum carries the softmax."""
+    s = make(B=2, N=8, D=128, lens=(500, 70))
+    s["q"] *= 40
+    check(s, "large scores")
+    s = make(B=2, N=8, D=128, lens=(500, 70))
+    s["q"].zero_()
+    check(s, "equal scores")
+    check(s, "negative scale", scale=-0.3)
+
+
+@pytest.mark.parametrize("head_major", [False, True])
+def test_strides(head_major):
+    s = make(B=2, N=5, H=6, Hkv=2, D=80, lens=(90, 31), head_major=head_major, poison=False)
+    plain = check(s, "strides")
+    B, N, H, D = s["q"].shape
+    packed = torch.zeros((B, N, H + 4, D), dtype=s["q"].dtype, device="cuda")
+    packed[:, :, :H], packed[:, :, H:H + 2], packed[:, :, H + 2:] = s["q"], s["kt"], s["vt"]
+    wide = torch.full((B, s["table"].shape[1] + 5), -9, dtype=torch.int32, device="cuda")
+    wide[:, :s["table"].shape[1]] = s["table"]
+    s.update(q=packed[:, :, :H], kt=packed[:, :, H:H + 2], vt=packed[:, :, H + 2:],
+             table=wide[:, :s["table"].shape[1]])
+    room = torch.full((N, B, H, D + 8), 7.0, dtype=plain.dtype, device="cuda")
+    out = room.transpose(0, 1)[..., :D]
+    assert call(s, out=out) is out
+    assert torch.equal(out, plain)
+    assert (room[..., D:] == 7.0).all()
+
+
+def test_shared_pages():
+    """Two sequences whose tables name the same pages."""
+    s = make(B=2, N=3, lens=(64, 50))
+    s["table"][1, :4] = s["table"][0, :4]
+    check(s, "shared pages")
+
+
+def test_parts_do_not_change_results_between_calls():
+    s = make(B=3, N=16, H=8, Hkv=2, D=128, lens=(3001, 5, 800))
+    first = call(s)
+    for _ in range(3):
+        assert torch.equal(call(s), first)
+
+
+def test_own_stream_and_two_streams_at_once():
+    a, b = make(B=3, N=6, lens=(900, 20, 300), seed=1), make(B=2, N=9, lens=(1500, 70), seed=2)
+    want_a, want_b = call(a), call(b)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        oa, ob = call(a, stream=s1), call(b, stream=s2)
+        s1.synchronize()
+        s2.synchronize()
+        assert torch.equal(oa, want_a) and torch.equal(ob, want_b)
+
+
+def test_graph_replays():
+    s = make(B=3, N=6, D=128, lens=(900, 20, 300))
+    other = make(B=3, N=6, D=128, lens=(900, 20, 300), seed=9)
+    call(s)
+    torch.cuda.synchronize()
+    graph, second = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(s)
+    with torch.cuda.graph(second):
+        out2 = call(other)
+    for rep in range(4):
+        n = make(B=3, N=6, D=128, lens=(900 - rep, 20 + rep, 300), seed=10 + rep)
+        s["lens"].copy_(n["lens"])
+        s["q"].copy_(n["q"])
+        want = call(s)
+        graph.replay()
+        second.replay()
+        torch.cuda.synchronize()
+        # bit for bit: the longer length reaches a slot that was never written (NaN)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)), rep
+        assert torch.equal(out2, call(other)), rep
