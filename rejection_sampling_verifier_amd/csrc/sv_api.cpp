@@ -607,16 +607,14 @@ int plan_tree(const sv_tree_attention* a, TreePlan& t) {
     if (static_cast<int64_t>(a->width) * a->page_size > (1ll << 28)) return SV_ESHAPE;
     const int rows = a->N * (a->heads / a->kv_heads);
     t.s.dp = a->dim <= 64 ? 64 : 128;
-    // one wave per 32 query rows; waves beyond that share the rows and split the keys
-    t.s.wr = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
-    t.s.rows = 32 * t.s.wr;
-    t.s.keys = t.s.dp == 128 && t.s.wr > 1 ? 64 : 128;
+    t.s.rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    t.s.keys = t.s.rows == 128 ? 64 : 128;
     t.MT = (rows + t.s.rows - 1) / t.s.rows;
     const int64_t tasks = static_cast<int64_t>(a->B) * a->kv_heads;
     if (tasks > (1ll << 24)) return SV_ESHAPE;
     const int64_t cap = static_cast<int64_t>(a->width) * a->page_size;
     const int64_t most = (cap + t.s.keys - 1) / t.s.keys + 1;  // tiles of one (sequence, key head)
-    const int64_t blocks = 2ll * device_cus();                 // two workgroups per CU fit
+    const int64_t blocks = (t.s.rows == 32 ? 2ll : 1ll) * device_cus();  // workgroups that are resident at once
     if (most <= 4) {
         // so short that a part is a whole (sequence, key head): nothing to join
         t.merge = 0;
@@ -687,7 +685,10 @@ int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
     // beyond every length and depth both mean everything; the kernel subtracts row numbers from them
     p.window = std::min(a->window, 1 << 29);
     p.sinks = std::min(a->sinks, 1 << 29);
-    p.scale2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634074);
+    // (-inf) * scale2 has to stay -inf: no zero, no denormal
+    p.scale2 = static_cast<float>(std::fabs(static_cast<double>(a->scale)) * 1.4426950408889634074);
+    if (p.scale2 < FLT_MIN) p.scale2 = FLT_MIN;
+    p.flip = a->scale < 0.f ? 1 : 0;
     p.MT = t.MT;
     p.clusters = t.clusters;
     p.min_tiles = t.min_tiles;

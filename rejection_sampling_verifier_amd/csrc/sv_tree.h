@@ -35,7 +35,8 @@ struct TreeAttnParams {
     int B, N, Hkv, G, D;                   // G = query heads per key head
     int pages, width, ps_shift;            // page size 1 << ps_shift
     int window, sinks;
-    float scale2;                          // scale * log2(e)
+    float scale2;                          // |scale| log2(e), a normal number
+    int flip;                              // scale < 0: the queries' signs are flipped
     int MT;                                // row tiles per (sequence, key head)
     int clusters;                          // parts the work is cut into
     int min_tiles;                         // no part is smaller
@@ -44,11 +45,13 @@ struct TreeAttnParams {
     float* part;                           // [clusters, 2, MT, rows, D32 + 2] workspace: partial results
 };
 
-// Rows per workgroup and keys per tile for `rows` = N * G query rows.
+// What a workgroup takes at a time, by the N * G query rows that share a key
+// head: up to 32 rows, 128 keys (32 rows per wave, the waves on different
+// keys); up to 64, 128 keys (64 rows per wave); else 128 rows, 64 keys (two
+// waves over rows, two over keys).
 struct TreeAttnShape {
-    int wr;    // waves over rows (32 rows each): 1, 2 or 4
-    int rows;  // 32 * wr
-    int keys;  // keys per tile
+    int rows;  // 32, 64 or 128
+    int keys;
     int dp;    // head dimension rounded up to 64 or 128
 };
 

@@ -117,6 +117,12 @@ __device__ __forceinline__ float shift_of(float a, float b) {
     return a == b ? 1.f : __builtin_amdgcn_exp2f(a - b);
 }
 
+// The 16-byte chunks of row r of a V tile are XORed with this.
+template <int DP>
+__device__ __forceinline__ uint32_t swizzle(int r) {
+    return DP == 128 ? ((r & 3) << 2) ^ ((r >> 2) & 3) : (((r >> 1) & 1) << 2) ^ ((r >> 2) & 3);
+}
+
 // The cache rows of one sequence in tiles: tiles [0, head) from the first row,
 // then from tile `head + gap` to the last (the gap is what the window hides
 // from every node), then one tile for the tree.
@@ -186,29 +192,25 @@ __device__ __forceinline__ uint64_t ancestors(const int32_t* parent, int n, int 
     return set;
 }
 
-template <int DT, int DP, int WR, int TK>
-__global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
-    constexpr int WK = kWaves / WR;           // waves over keys
-    constexpr int RB = 32 * WR;               // query rows
-    constexpr int KS = TK / (32 * WK);        // 32-key subtiles per wave
-    constexpr int NC = DP / 8;                // 16-byte chunks per row
-    constexpr int RPT = TK * NC / kThreads;   // rows of K (and of V) a thread stages
+template <int DT, int DP, int NT, int WR>
+__global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void k_tree_attn(TreeAttnParams p) {
+    constexpr int WK = kWaves / WR;      // waves over keys
+    constexpr int WROWS = 32 * NT;       // query rows of a wave
+    constexpr int RB = WROWS * WR;       // query rows of the workgroup
+    constexpr int TK = 32 * WK;          // keys per tile, 32 per wave
     constexpr int NQ = DP / 16, ND = DP / 32;
     constexpr int kRowB = DP * 2;
-    static_assert(TK * kRowB >= kWaves * 4096, "the slow path keeps a wave's weights in the K tile");
-    static_assert(2 * TK * kRowB >= (WK > 1 ? 2 * 64 * (DP / 2) * 4 : 0), "the waves' results are joined in the tiles");
+    constexpr int kTileB = 32 * kRowB;   // a wave's V tile
 
-    __shared__ __align__(16) uint8_t smem[2 * TK * kRowB];
-    __shared__ uint32_t s_bad[2][TK / 32];  // rows of the tile that nothing sees
-    __shared__ uint32_t s_nf[2];            // some row of a mixed tile holds an infinity or NaN
+    __shared__ __align__(16) uint8_t smem[kWaves * kTileB];
     __shared__ float s_ml[2][2][64];
     __shared__ int64_t s_sum[kWaves];
     __shared__ int32_t s_scan[kWaves];
     __shared__ int s_b;
     __shared__ int64_t s_before;
 
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int wr = w % WR, wk = w / WR, hh = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = w % WR, wk = w / WR, hh = lane >> 5, col = lane & 31;
     int c, m;
     if (p.MT == 1) {
         c = blockIdx.x;
@@ -271,35 +273,23 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
             if (!tell && carry * p.Hkv > f0) break;
         }
         if (tell && tid == 0) p.start[p.B] = seqs;
-        b = s_b;
+        b = __builtin_amdgcn_readfirstlane(s_b);
         before = s_before;
     }
-    if (tid < 2) s_nf[tid] = 0;
-    if (tid < 2 * (TK / 32)) s_bad[tid / (TK / 32)][tid % (TK / 32)] = 0;
-    __syncthreads();
 
-    uint8_t* const sk = smem;
-    uint8_t* const sv = smem + TK * kRowB;
-    // this thread's 16-byte chunk of the rows it stages
-    const int ch = tid % NC, row0 = tid / NC;
-    constexpr int kRowStep = kThreads / NC;
-    const bool ch_in = ch * 8 < p.D;
-    const int cin = ch_in ? ch : 0;
-    // the rows a thread stages are multiples of 16 (of 32 for 8 chunks) apart: one swizzle for all
-    const uint32_t k_at = row0 * kRowB + ((ch ^ (DP == 128 ? (row0 & 15) : ((row0 >> 1) & 7))) << 4);
-    const uint32_t v_at = row0 * kRowB + ((ch ^ (DP == 128 ? ((row0 & 3) << 2) : (((row0 >> 1) & 1) << 2))) << 4);
-    // lane parts of the LDS addresses; both tiles are XOR-swizzled by 16-byte
-    // chunk so that eight lanes of a read touch eight different bank groups
-    const int kx = DP == 128 ? (lane & 15) : ((lane >> 1) & 7);
-    const int vrow = (lane & 15) >> 2;
-    const int vx = DP == 128 ? vrow : (vrow >> 1);
-    const int vlow = (((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) * 16 + (lane & 1) * 8;
-    const int my_row = m * RB + wr * 32 + (lane & 31);
-    const int my_node = my_row / p.G;
-    const int my_head = my_row - my_node * p.G;
+    uint8_t* const sv = smem + w * kTileB;
+    // a lane stages the chunks 2 s + hh of row `col`; the tile is XOR-swizzled by
+    // 16-byte chunk: eight lanes of a write, and the sixteen of a transposing
+    // read (four rows, two chunks), touch different banks
+    const uint32_t v_at = col * kRowB;
+    const uint32_t v_x = swizzle<DP>(col);
+    const int vrow = (lane & 15) >> 2;                                // row of four in a transposing read
+    const int vchunk = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);     // its chunk of the four of 32 dimensions
+    const uint32_t vr_at = (4 * hh + vrow) * kRowB + (lane & 1) * 8;
     const bool win = p.window > 0;
+    const float scale2 = p.scale2;
+    const bool odd_end = p.D % 16 != 0;   // the last 32 bytes of a row are half a row's
 
-    int par = 0;
     int64_t f = f0;
     while (f < f1) {
         const Tiles tl = tiles_of<TK>(p, p.len[b]);
@@ -315,330 +305,340 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
             n = n < 0 ? 0 : n > p.N ? p.N : n;
         }
         const int rows = n * p.G;
-        const bool active = m * RB + wr * 32 < rows;  // wave-uniform
-        float mx = -INFINITY, l = 0.f;
-        v16f o[ND];
+        const int row0 = m * RB + wr * WROWS;  // the wave's first row
+        float mx[NT], l[NT];
+        v16f o[NT][ND];
 #pragma unroll
-        for (int dt = 0; dt < ND; ++dt)
+        for (int nt = 0; nt < NT; ++nt) {
+            mx[nt] = -INFINITY;
+            l[nt] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
+            for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[nt][dt][i] = 0.f;
+        }
 
-        if (m * RB < rows) {
-            // queries: the B operand, resident
-            v8s q[NQ];
-            {
-                const bool in = my_row < rows;
-                const int64_t off = b * p.qs[0] + my_node * p.qs[1] + static_cast<int64_t>(h * p.G + my_head) * p.qs[2];
-                const uint8_t* const src = p.q + 2 * (in ? off : 0);
+        if (row0 < rows) {  // the wave has rows; no barrier inside
+            // queries: the B operand, resident; a negative scale is moved into their sign
+            v8s q[NT][NQ];
+            uint64_t set[NT];
+            int low[NT];  // first cache row in the row's window
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int row = row0 + nt * 32 + col;
+                const bool in = row < rows;
+                const int node = in ? row / p.G : 0;
+                const int64_t off = b * p.qs[0] + node * p.qs[1] +
+                                    static_cast<int64_t>(h * p.G + (in ? row - node * p.G : 0)) * p.qs[2];
 #pragma unroll
                 for (int s = 0; s < NQ; ++s) {
                     const int d = s * 16 + hh * 8;
                     v8s z = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (in && d < p.D) z = *reinterpret_cast<const v8s*>(src + 2 * d);
-                    q[s] = z;
+                    if (in && d < p.D) z = *reinterpret_cast<const v8s*>(p.q + 2 * (off + d));
+                    q[nt][s] = p.flip ? z ^ static_cast<short>(0x8000) : z;
                 }
-            }
-            uint64_t set = 0;
-            int low = 0;  // first cache row in this row's window
-            if (t1 == T || win) {
-                const int32_t* const par_b = p.parent + static_cast<int64_t>(b) * p.N;
-                const uint64_t all = ancestors(par_b, n, lane, 0);
-                const int src = my_node < kMaxNodes ? my_node : 0;
-                set = __shfl(static_cast<unsigned long long>(all), src);
-                if (win) {
-                    low = tl.len + __popcll(set) - p.window;  // depth + 1 nodes on the line
-                    if (p.window < kMaxNodes)
-                        set = __shfl(static_cast<unsigned long long>(ancestors(par_b, n, lane, p.window)), src);
+                set[nt] = 0;
+                low[nt] = 0;
+                if (t1 == T || win) {
+                    const int32_t* const par_b = p.parent + static_cast<int64_t>(b) * p.N;
+                    const uint64_t all = ancestors(par_b, n, lane, 0);
+                    set[nt] = __shfl(static_cast<unsigned long long>(all), node);
+                    if (win) {
+                        low[nt] = tl.len + __popcll(set[nt]) - p.window;  // depth + 1 nodes on the line
+                        if (p.window < kMaxNodes)
+                            set[nt] = __shfl(static_cast<unsigned long long>(ancestors(par_b, n, lane, p.window)), node);
+                    }
                 }
             }
 
-            int pid[RPT];
-            uint4 rk[RPT], rv[RPT];
-            uint32_t okm = 0;
             const int32_t* const tab = p.table + b * p.table_stride;
-            // this (sequence, key head)'s first cache and tree rows, at this thread's chunk
-            const uint8_t* const kcb = p.kc + 2 * (h * p.kcs[2] + cin * 8);
-            const uint8_t* const vcb = p.vc + 2 * (h * p.vcs[2] + cin * 8);
-            const uint8_t* const ktb = p.kt + 2 * (b * p.kts[0] + h * p.kts[2] + cin * 8);
-            const uint8_t* const vtb = p.vt + 2 * (b * p.vts[0] + h * p.vts[2] + cin * 8);
-            auto pages = [&](int t) {
-#pragma unroll
-                for (int i = 0; i < RPT; ++i) {
-                    pid[i] = -1;
-                    if (t < tl.cache) {
-                        const int key = tl.key_tile(t) * TK + row0 + i * kRowStep;
-                        if (key < tl.len) pid[i] = tab[key >> p.ps_shift];
-                    }
-                }
+            // this (sequence, key head)'s rows, at this lane's first chunk
+            const uint8_t* const kcb = p.kc + 2 * (h * p.kcs[2] + hh * 8);
+            const uint8_t* const vcb = p.vc + 2 * (h * p.vcs[2] + hh * 8);
+            const uint8_t* const ktb = p.kt + 2 * (b * p.kts[0] + h * p.kts[2] + hh * 8);
+            const uint8_t* const vtb = p.vt + 2 * (b * p.vts[0] + h * p.vts[2] + hh * 8);
+            auto page = [&](int t) {  // the page of this lane's row of tile t
+                if (t >= tl.cache) return -1;
+                const int key = tl.key_tile(t) * TK + wk * 32 + col;
+                return key < tl.len ? tab[key >> p.ps_shift] : -1;
             };
-            auto load = [&](int t) {
-                // rows that nothing sees read a row that exists instead, and become zeros when staged
-                okm = 0;
+            // where this lane's row of tile t is; rows that nothing sees stand in for one that exists
+            auto place = [&](int t, int pid, const uint8_t*& ka, const uint8_t*& va) {
                 if (t >= tl.cache) {
+                    const int r = wk * 32 + col;
+                    const bool ok = r < n;
+                    const int64_t at = ok ? r : 0;
+                    ka = ktb + 2 * (at * p.kts[1]);
+                    va = vtb + 2 * (at * p.vts[1]);
+                    return ok;
+                }
+                const int slot = (tl.key_tile(t) * TK + wk * 32 + col) & ((1 << p.ps_shift) - 1);
+                const bool ok = static_cast<uint32_t>(pid) < static_cast<uint32_t>(p.pages);
+                const int64_t at = ok ? pid : 0;
+                ka = kcb + 2 * (at * p.kcs[0] + slot * p.kcs[1]);
+                va = vcb + 2 * (at * p.vcs[0] + slot * p.vcs[1]);
+                return ok;
+            };
+            auto fetch = [&](const uint8_t* a, v8s* r) {
+                if (p.D == DP) {
 #pragma unroll
-                    for (int i = 0; i < RPT; ++i) {
-                        const int r = row0 + i * kRowStep;
-                        const bool ok = r < n;
-                        okm |= ok ? 1u << i : 0u;
-                        const int64_t at = ok ? r : 0;
-                        rk[i] = *reinterpret_cast<const uint4*>(ktb + 2 * (at * p.kts[1]));
-                        rv[i] = *reinterpret_cast<const uint4*>(vtb + 2 * (at * p.vts[1]));
-                    }
+                    for (int s = 0; s < NQ; ++s) r[s] = *reinterpret_cast<const v8s*>(a + 32 * s);
                 } else {
-                    const int first = tl.key_tile(t) * TK + row0;
+                    const bool half = odd_end && hh;  // chunks past the row's end: read its start, then drop it
 #pragma unroll
-                    for (int i = 0; i < RPT; ++i) {
-                        const int slot = (first + i * kRowStep) & ((1 << p.ps_shift) - 1);
-                        const bool ok = static_cast<uint32_t>(pid[i]) < static_cast<uint32_t>(p.pages);
-                        okm |= ok ? 1u << i : 0u;
-                        const int64_t at = ok ? pid[i] : 0;
-                        rk[i] = *reinterpret_cast<const uint4*>(kcb + 2 * (at * p.kcs[0] + slot * p.kcs[1]));
-                        rv[i] = *reinterpret_cast<const uint4*>(vcb + 2 * (at * p.vcs[0] + slot * p.vcs[1]));
+                    for (int s = 0; s < NQ; ++s) {
+                        v8s z = {0, 0, 0, 0, 0, 0, 0, 0};
+                        if (16 * s + 16 <= p.D) {
+                            z = *reinterpret_cast<const v8s*>(a + 32 * s);
+                        } else if (16 * s < p.D) {
+                            const v8s y = *reinterpret_cast<const v8s*>(half ? a - 16 : a + 32 * s);
+                            z = half ? z : y;
+                        }
+                        r[s] = z;
                     }
                 }
             };
 
-            pages(t0);
-            load(t0);
-            if (t0 + 1 < t1) pages(t0 + 1);
-            for (int t = t0; t < t1; ++t, par ^= 1) {
+            v8s kr[NQ], vr[NQ];
+            const uint8_t *ka, *va;
+            bool ok = place(t0, page(t0), ka, va);
+            fetch(ka, kr);
+            fetch(va, vr);
+            int pid = t0 + 1 < t1 ? page(t0 + 1) : -1;
+            for (int t = t0; t < t1; ++t) {
                 const bool tree = t >= tl.cache;
-                const int kb = tree ? 0 : tl.key_tile(t) * TK;
+                const int kb = (tree ? 0 : tl.key_tile(t) * TK) + wk * 32;
                 const bool mixed = tree || (win && kb < tl.len + p.N - p.window);
-                const uint32_t keep = ch_in ? okm : 0u;
-                if (keep != (1u << RPT) - 1u) {
-#pragma unroll
-                    for (int i = 0; i < RPT; ++i)
-                        if (!(keep >> i & 1)) {
-                            rk[i] = make_uint4(0, 0, 0, 0);
-                            rv[i] = make_uint4(0, 0, 0, 0);
-                        }
-                }
-                __syncthreads();  // the previous tile has been read
-#pragma unroll
-                for (int i = 0; i < RPT; ++i) {
-                    if (mixed && (nonfinite2<DT>(rv[i].x) || nonfinite2<DT>(rv[i].y) || nonfinite2<DT>(rv[i].z) ||
-                                  nonfinite2<DT>(rv[i].w))) {
-                        s_nf[par] = 1;
-                        uint16_t e[8];
-                        __builtin_memcpy(e, &rv[i], 16);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (nonfinite2<DT>(e[j])) e[j] = 0;
-                        __builtin_memcpy(&rv[i], e, 16);
-                    }
-                    *reinterpret_cast<uint4*>(sk + k_at + i * kRowStep * kRowB) = rk[i];
-                    *reinterpret_cast<uint4*>(sv + v_at + i * kRowStep * kRowB) = rv[i];
-                }
-                if (ch == 0 && okm != (1u << RPT) - 1u) {
-#pragma unroll
-                    for (int i = 0; i < RPT; ++i) {
-                        const int r = row0 + i * kRowStep;
-                        if (!(okm >> i & 1)) atomicOr(&s_bad[par][r >> 5], 1u << (r & 31));
-                    }
-                }
-                __syncthreads();
-                // the other parity's marks have been read; its next writers wait at the next barrier
-                if (tid < TK / 32) s_bad[par ^ 1][tid] = 0;
-                if (tid == kThreads - 1) s_nf[par ^ 1] = 0;
-                if (t + 1 < t1) {
-                    load(t + 1);
-                    if (t + 2 < t1) pages(t + 2);
-                }
+                const uint32_t bad = ~static_cast<uint32_t>(__ballot(ok));  // rows nothing sees
+                const bool more = t + 1 < t1;
+                bool nf = false;
 
-                const bool nf = mixed && s_nf[par] != 0;
-                v16f x[KS];
-                if (active) {
-                    uint32_t bad[KS];
+                v16f x[NT];
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const int sub = wk * KS + ks;
-                        bad[ks] = __builtin_amdgcn_readfirstlane(s_bad[par][sub]);
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[ks][i] = 0.f;
-                        const uint8_t* const rowp = sk + (sub * 32 + (lane & 31)) * kRowB;
+                    for (int i = 0; i < 16; ++i) x[nt][i] = 0.f;
 #pragma unroll
-                        for (int s = 0; s < NQ; ++s) {
-                            const v8s a = *reinterpret_cast<const v8s*>(rowp + (((2 * s + hh) ^ kx) << 4));
-                            x[ks] = mfma<DT>(a, q[s], x[ks]);
+                for (int s = 0; s < NQ; ++s)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) x[nt] = mfma<DT>(kr[s], q[nt][s], x[nt]);
+                __builtin_amdgcn_sched_barrier(0);
+                bool ok_next = false;
+                const uint8_t* va_next = va;
+                if (more) {
+                    ok_next = place(t + 1, pid, ka, va_next);
+                    fetch(ka, kr);
+                }
+                // V rows into the wave's tile, hidden ones as zeros
+                if (bad != 0) {
+#pragma unroll
+                    for (int s = 0; s < NQ; ++s) vr[s] = ok ? vr[s] : static_cast<short>(0);
+                }
+                if (mixed) {
+#pragma unroll
+                    for (int s = 0; s < NQ; ++s) {
+                        const uint4 u = __builtin_bit_cast(uint4, vr[s]);
+                        if (nonfinite2<DT>(u.x) || nonfinite2<DT>(u.y) || nonfinite2<DT>(u.z) || nonfinite2<DT>(u.w)) {
+                            nf = true;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (nonfinite2<DT>(static_cast<uint16_t>(vr[s][j]))) vr[s][j] = 0;
                         }
                     }
-                    __builtin_amdgcn_sched_barrier(0);  // the phases stay apart: their operands would not fit together
-                    float top = -INFINITY;
+                    nf = __any(nf);
+                }
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const int sub = wk * KS + ks;
+                for (int s = 0; s < NQ; ++s)
+                    *reinterpret_cast<v8s*>(sv + v_at + (((2 * s + hh) ^ v_x) << 4)) = vr[s];
+                if (more) {
+                    fetch(va_next, vr);
+                    if (t + 2 < t1) pid = page(t + 2);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+
+                if (mixed || bad != 0) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[ks][i] *= p.scale2;
-                        if (mixed || bad[ks]) {
-                            // bit r: this lane's row sees row r of the subtile
-                            uint32_t see = ~bad[ks];
-                            if (tree)
-                                see &= sub < 2 ? static_cast<uint32_t>(set >> (32 * (sub & 1))) : 0u;
-                            else if (win)
-                                see &= bits_from(low - (kb + sub * 32)) | ~bits_from(p.sinks - (kb + sub * 32));
-                            see >>= 4 * hh;
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint32_t see = ~bad;  // bit r: this lane's row sees row r of the subtile
+                        if (tree)
+                            see &= wk < 2 ? static_cast<uint32_t>(set[nt] >> (32 * (wk & 1))) : 0u;
+                        else if (win)
+                            see &= bits_from(low[nt] - kb) | ~bits_from(p.sinks - kb);
+                        see >>= 4 * hh;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                x[ks][i] = see & (1u << (8 * (i >> 2) + (i & 3))) ? x[ks][i] : -INFINITY;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) top = fmaxf(top, x[ks][i]);
+                        for (int i = 0; i < 16; ++i)
+                            x[nt][i] = see & (1u << (8 * (i >> 2) + (i & 3))) ? x[nt][i] : -INFINITY;
                     }
-                    top = half_max(top);
-                    if (__any(top > mx + 8.f)) {
-                        const float mn = fmaxf(mx, top);
-                        const float a = shift_of(mx, mn);
-                        l *= a;
+                }
+                bool grows = false;
+                float top[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    top[nt] = x[nt][0];
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) top[nt] = fmaxf(top[nt], x[nt][i]);
+                    top[nt] = half_max(top[nt]) * scale2;
+                    grows = grows || top[nt] > mx[nt] + 8.f;
+                }
+                if (__any(grows)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float mn = fmaxf(mx[nt], top[nt]);
+                        const float a = shift_of(mx[nt], mn);
+                        l[nt] *= a;
 #pragma unroll
                         for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[dt][i] *= a;
-                        mx = mn;
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                    const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            x[ks][i] = __builtin_amdgcn_exp2f(x[ks][i] - ref);
-                            l += x[ks][i];
-                        }
-#pragma unroll
-                        for (int t2 = 0; t2 < 2; ++t2) {
-                            const v4s lo = pack4<DT>(x[ks][8 * t2], x[ks][8 * t2 + 1], x[ks][8 * t2 + 2],
-                                                     x[ks][8 * t2 + 3]);
-                            const v4s hi = pack4<DT>(x[ks][8 * t2 + 4], x[ks][8 * t2 + 5], x[ks][8 * t2 + 6],
-                                                     x[ks][8 * t2 + 7]);
-                            const v8s pf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                            const uint8_t* const rowp =
-                                sv + ((wk * KS + ks) * 32 + 16 * t2 + 4 * hh + vrow) * kRowB + vlow;
-#pragma unroll
-                            for (int dt = 0; dt < ND; ++dt) {
-                                const int cx = DP == 128 ? ((dt ^ vx) << 6) : ((dt ^ vx) << 6);
-                                const v4s a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(rowp + cx));
-                                const v4s a1 =
-                                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(rowp + 8 * kRowB + cx));
-                                o[dt] = mfma<DT>(__builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7), pf, o[dt]);
-                            }
-                        }
+                            for (int i = 0; i < 16; ++i) o[nt][dt][i] *= a;
+                        mx[nt] = mn;
                     }
                 }
+                v8s pf[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float ref = mx[nt] == -INFINITY ? 0.f : mx[nt];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        x[nt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[nt][i], scale2, -ref));
+                        l[nt] += x[nt][i];
+                    }
+#pragma unroll
+                    for (int t2 = 0; t2 < 2; ++t2) {
+                        const v4s lo = pack4<DT>(x[nt][8 * t2], x[nt][8 * t2 + 1], x[nt][8 * t2 + 2], x[nt][8 * t2 + 3]);
+                        const v4s hi =
+                            pack4<DT>(x[nt][8 * t2 + 4], x[nt][8 * t2 + 5], x[nt][8 * t2 + 6], x[nt][8 * t2 + 7]);
+                        pf[nt][t2] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                    }
+                }
+#pragma unroll
+                for (int t2 = 0; t2 < 2; ++t2)
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) {
+                        const uint32_t row = vr_at + 16 * t2 * kRowB;
+                        const v4s a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (lds_v4s*)(sv + row + (((4 * dt + vchunk) ^ swizzle<DP>(4 * hh + vrow)) << 4)));
+                        const v4s a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (lds_v4s*)(sv + row + 8 * kRowB + (((4 * dt + vchunk) ^ swizzle<DP>(8 + 4 * hh + vrow)) << 4)));
+                        const v8s a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) o[nt][dt] = mfma<DT>(a, pf[nt][t2], o[nt][dt]);
+                    }
                 if (nf) {  // rare: infinities or NaN among the values, for the rows that see them
-                    __syncthreads();
-                    float* const wp = reinterpret_cast<float*>(sk) + w * 1024;
+                    float* const wp = reinterpret_cast<float*>(sv);
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const int sub = wk * KS + ks;
-                        if (active) {
+                    for (int nt = 0; nt < NT; ++nt) {
+                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                wp[(8 * (i >> 2) + 4 * hh + (i & 3)) * 32 + (lane & 31)] = x[ks][i];
-                        }
-                        __syncthreads();
-                        if (active) {
-                            for (int r = 0; r < 32; ++r) {
-                                const int key = kb + sub * 32 + r;
-                                const uint8_t* src;
-                                if (tree) {
-                                    if (key >= n) break;
-                                    src = p.vt + 2 * (b * p.vts[0] + key * p.vts[1] + h * p.vts[2]);
-                                } else {
-                                    if (key >= tl.len) break;
-                                    const int pg = tab[key >> p.ps_shift];
-                                    if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) continue;
-                                    src = p.vc + 2 * (pg * p.vcs[0] + (key & ((1 << p.ps_shift) - 1)) * p.vcs[1] +
-                                                      h * p.vcs[2]);
-                                }
-                                const float wgt = wp[r * 32 + (lane & 31)];
-#pragma unroll
-                                for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-                                    for (int g = 0; g < 4; ++g) {
-                                        const int d = 32 * dt + 8 * g + 4 * hh;
-                                        if (32 * dt + 8 * g < p.D) {
-                                            const uint2 e = *reinterpret_cast<const uint2*>(src + 2 * d);
-                                            if (wgt != 0.f && (nonfinite2<DT>(e.x) || nonfinite2<DT>(e.y))) {
-                                                o[dt][4 * g] += nonfinite_term<DT>(wgt, e.x & 0xFFFFu);
-                                                o[dt][4 * g + 1] += nonfinite_term<DT>(wgt, e.x >> 16);
-                                                o[dt][4 * g + 2] += nonfinite_term<DT>(wgt, e.y & 0xFFFFu);
-                                                o[dt][4 * g + 3] += nonfinite_term<DT>(wgt, e.y >> 16);
-                                            }
-                                        }
-                                        asm volatile("" ::: "memory");  // one load at a time: registers stay with the main path
-                                    }
+                        for (int i = 0; i < 16; ++i) wp[(8 * (i >> 2) + 4 * hh + (i & 3)) * 32 + col] = x[nt][i];
+                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                        for (int r = 0; r < 32; ++r) {
+                            const int key = kb + r;
+                            const uint8_t* src;
+                            if (bad >> r & 1) continue;
+                            if (tree) {
+                                src = p.vt + 2 * (b * p.vts[0] + key * p.vts[1] + h * p.vts[2]);
+                            } else {
+                                const int pg = tab[key >> p.ps_shift];
+                                src = p.vc + 2 * (pg * p.vcs[0] + (key & ((1 << p.ps_shift) - 1)) * p.vcs[1] +
+                                                  h * p.vcs[2]);
                             }
-                        }
-                        __syncthreads();
-                    }
-                }
-            }
-            l = half_sum(l);
-
-            // waves that took other keys of the same rows hand their results over
-            if constexpr (WK > 1) {
-                float* const buf = reinterpret_cast<float*>(smem);
+                            const float wgt = wp[r * 32 + col];
 #pragma unroll
-                for (int half = WK / 2; half >= 1; half >>= 1) {
-                    const int slot = WR == 2 ? wr : wk % half;
+                            for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                                for (int g = 0; g < 4; ++g) {
+                                    if (32 * dt + 8 * g < p.D) {
+                                        const uint2 e = *reinterpret_cast<const uint2*>(src + 2 * (32 * dt + 8 * g + 4 * hh));
+                                        if (wgt != 0.f && (nonfinite2<DT>(e.x) || nonfinite2<DT>(e.y))) {
+                                            o[nt][dt][4 * g] += nonfinite_term<DT>(wgt, e.x & 0xFFFFu);
+                                            o[nt][dt][4 * g + 1] += nonfinite_term<DT>(wgt, e.x >> 16);
+                                            o[nt][dt][4 * g + 2] += nonfinite_term<DT>(wgt, e.y & 0xFFFFu);
+                                            o[nt][dt][4 * g + 3] += nonfinite_term<DT>(wgt, e.y >> 16);
+                                        }
+                                    }
+                                    asm volatile("" ::: "memory");  // one load at a time: registers stay with the main path
+                                }
+                        }
+                    }
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                }
+                ok = ok_next;
+                va = va_next;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) l[nt] = half_sum(l[nt]);
+        }
+
+        // waves that took other keys of the same rows hand their results over
+        if (m * RB < rows) {
+            float* const buf = reinterpret_cast<float*>(smem);
+#pragma unroll
+            for (int half = WK / 2; half >= 1; half >>= 1) {
+                const int slot = WR == 2 ? wr : wk % half;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
                     __syncthreads();
                     if (wk >= half && wk < 2 * half) {
 #pragma unroll
                         for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                buf[slot * 64 * (DP / 2) + (dt * 16 + i) * 64 + lane] = o[dt][i];
-                        s_ml[slot][0][lane] = mx;
-                        s_ml[slot][1][lane] = l;
+                                buf[slot * 64 * (DP / 2) + (dt * 16 + i) * 64 + lane] = o[nt][dt][i];
+                        s_ml[slot][0][lane] = mx[nt];
+                        s_ml[slot][1][lane] = l[nt];
                     }
                     __syncthreads();
                     if (wk < half) {
                         const float m2 = s_ml[slot][0][lane], l2 = s_ml[slot][1][lane];
-                        const float mn = fmaxf(mx, m2);
-                        const float a1 = shift_of(mx, mn), a2 = shift_of(m2, mn);
-                        l = l * a1 + l2 * a2;
-                        mx = mn;
+                        const float mn = fmaxf(mx[nt], m2);
+                        const float a1 = shift_of(mx[nt], mn), a2 = shift_of(m2, mn);
+                        l[nt] = l[nt] * a1 + l2 * a2;
+                        mx[nt] = mn;
 #pragma unroll
                         for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                o[dt][i] = o[dt][i] * a1 + buf[slot * 64 * (DP / 2) + (dt * 16 + i) * 64 + lane] * a2;
+                                o[nt][dt][i] =
+                                    o[nt][dt][i] * a1 + buf[slot * 64 * (DP / 2) + (dt * 16 + i) * 64 + lane] * a2;
                     }
                 }
             }
+            __syncthreads();  // the tiles are the waves' own again
         }
 
-        if (wk == 0 && my_row < p.N * p.G) {
-            if (whole) {
-                const bool in = my_row < rows;
-                const float inv = in ? 1.f / l : 0.f;
-                uint8_t* const dst = p.out + 2 * (b * p.os[0] + my_node * p.os[1] +
-                                                  static_cast<int64_t>(h * p.G + my_head) * p.os[2]);
+        if (wk == 0) {
 #pragma unroll
-                for (int dt = 0; dt < ND; ++dt)
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = wr * WROWS + nt * 32 + col, row = m * RB + r;
+                if (whole) {
+                    if (row < p.N * p.G) {
+                        const int node = row / p.G;
+                        const float inv = row < rows ? 1.f / l[nt] : 0.f;  // zeros for an absent node
+                        uint8_t* const dst = p.out + 2 * (b * p.os[0] + node * p.os[1] +
+                                                          static_cast<int64_t>(h * p.G + row - node * p.G) * p.os[2]);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int d = 32 * dt + 8 * g + 4 * hh;
-                        if (32 * dt + 8 * g < p.D) {
-                            const v4s r = pack4<DT>(o[dt][4 * g] * inv, o[dt][4 * g + 1] * inv, o[dt][4 * g + 2] * inv,
-                                              o[dt][4 * g + 3] * inv);  // zeros for an absent node
-                            *reinterpret_cast<v4s*>(dst + 2 * d) = r;
-                        }
+                        for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+                                if (32 * dt + 8 * g < p.D)
+                                    *reinterpret_cast<v4s*>(dst + 2 * (32 * dt + 8 * g + 4 * hh)) =
+                                        pack4<DT>(o[nt][dt][4 * g] * inv, o[nt][dt][4 * g + 1] * inv,
+                                                  o[nt][dt][4 * g + 2] * inv, o[nt][dt][4 * g + 3] * inv);
                     }
-            } else if (my_row < rows) {
-                float* const rec = p.part + ((static_cast<int64_t>(c) * 2 + (f == f0 ? 0 : 1)) * p.MT + m) *
-                                                (RB * (DP + 2));
-                const int r = wr * 32 + (lane & 31);
+                } else if (row < rows) {
+                    float* const rec =
+                        p.part + ((static_cast<int64_t>(c) * 2 + (f == f0 ? 0 : 1)) * p.MT + m) * (RB * (DP + 2));
 #pragma unroll
-                for (int dt = 0; dt < ND; ++dt)
+                    for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        *reinterpret_cast<float4*>(rec + r * DP + 32 * dt + 8 * g + 4 * hh) =
-                            make_float4(o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]);
-                if (hh == 0) {
-                    rec[RB * DP + r] = mx;
-                    rec[RB * DP + RB + r] = l;
+                        for (int g = 0; g < 4; ++g)
+                            *reinterpret_cast<float4*>(rec + r * DP + 32 * dt + 8 * g + 4 * hh) =
+                                make_float4(o[nt][dt][4 * g], o[nt][dt][4 * g + 1], o[nt][dt][4 * g + 2],
+                                            o[nt][dt][4 * g + 3]);
+                    if (hh == 0) {
+                        rec[RB * DP + r] = mx[nt];
+                        rec[RB * DP + RB + r] = l[nt];
+                    }
                 }
             }
         }
@@ -653,9 +653,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
 // Joins the partial results of the (sequence, key head)s that were divided:
 // o = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over the parts in order.
 // DP / 4 threads per row, four dimensions each.
-template <int DT, int DP, int WR>
+template <int DT, int DP, int RB>
 __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
-    constexpr int TPR = DP / 4, RPB = kThreads / TPR, RB = 32 * WR;
+    constexpr int TPR = DP / 4, RPB = kThreads / TPR;
     const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
     const int64_t s0 = p.start[b], T = p.start[b + 1] - s0;
     const int64_t total = p.start[p.B] * p.Hkv;
@@ -701,49 +701,48 @@ __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
     *reinterpret_cast<v4s*>(dst + 2 * d) = res;
 }
 
-template <int DT, int DP, int WR, int TK>
+template <int DT, int DP, int NT, int WR>
 hipError_t launch_one(const TreeAttnParams& p, hipStream_t st, const LaunchEvents& ev) {
-    const int64_t grid =
-        p.MT == 1 ? p.clusters : static_cast<int64_t>((p.clusters + 7) / 8) * 8 * p.MT;
-    hipExtLaunchKernelGGL((k_tree_attn<DT, DP, WR, TK>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st,
+    const int64_t grid = p.MT == 1 ? p.clusters : static_cast<int64_t>((p.clusters + 7) / 8) * 8 * p.MT;
+    hipExtLaunchKernelGGL((k_tree_attn<DT, DP, NT, WR>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st,
                           ev.start, ev.stop, 0, p);
     return hipGetLastError();
 }
 
-template <int DT, int DP, int WR>
+template <int DT, int DP, int RB>
 hipError_t merge_one(const TreeAttnParams& p, hipStream_t st, const LaunchEvents& ev) {
     constexpr int RPB = kThreads / (DP / 4);
-    hipExtLaunchKernelGGL((k_tree_merge<DT, DP, WR>), dim3(p.B * p.Hkv, (p.N * p.G + RPB - 1) / RPB), dim3(kThreads), 0,
+    hipExtLaunchKernelGGL((k_tree_merge<DT, DP, RB>), dim3(p.B * p.Hkv, (p.N * p.G + RPB - 1) / RPB), dim3(kThreads), 0,
                           st, ev.start, ev.stop, 0, p);
     return hipGetLastError();
+}
+
+template <int DT, int DP>
+hipError_t launch_rows_of(const TreeAttnParams& p, int rows, bool merge, hipStream_t st, const LaunchEvents& ev) {
+    if (rows == 32) return merge ? merge_one<DT, DP, 32>(p, st, ev) : launch_one<DT, DP, 1, 1>(p, st, ev);
+    if (rows == 64) return merge ? merge_one<DT, DP, 64>(p, st, ev) : launch_one<DT, DP, 2, 1>(p, st, ev);
+    return merge ? merge_one<DT, DP, 128>(p, st, ev) : launch_one<DT, DP, 2, 2>(p, st, ev);
+}
+
+hipError_t launch_any(const TreeAttnParams& p, const TreeAttnShape& s, int dtype, bool merge, hipStream_t st,
+                      const LaunchEvents& ev) {
+    if (dtype == DT_BF16)
+        return s.dp == 128 ? launch_rows_of<DT_BF16, 128>(p, s.rows, merge, st, ev)
+                           : launch_rows_of<DT_BF16, 64>(p, s.rows, merge, st, ev);
+    return s.dp == 128 ? launch_rows_of<kDTypeF16, 128>(p, s.rows, merge, st, ev)
+                       : launch_rows_of<kDTypeF16, 64>(p, s.rows, merge, st, ev);
 }
 
 }  // namespace
 
 hipError_t launch_tree_attn(const TreeAttnParams& p, const TreeAttnShape& s, int dtype, hipStream_t st,
                             const LaunchEvents& ev) {
-    const bool bf = dtype == DT_BF16;
-    if (s.dp == 128) {
-        if (s.wr == 1) return bf ? launch_one<DT_BF16, 128, 1, 128>(p, st, ev) : launch_one<kDTypeF16, 128, 1, 128>(p, st, ev);
-        if (s.wr == 2) return bf ? launch_one<DT_BF16, 128, 2, 64>(p, st, ev) : launch_one<kDTypeF16, 128, 2, 64>(p, st, ev);
-        return bf ? launch_one<DT_BF16, 128, 4, 64>(p, st, ev) : launch_one<kDTypeF16, 128, 4, 64>(p, st, ev);
-    }
-    if (s.wr == 1) return bf ? launch_one<DT_BF16, 64, 1, 128>(p, st, ev) : launch_one<kDTypeF16, 64, 1, 128>(p, st, ev);
-    if (s.wr == 2) return bf ? launch_one<DT_BF16, 64, 2, 128>(p, st, ev) : launch_one<kDTypeF16, 64, 2, 128>(p, st, ev);
-    return bf ? launch_one<DT_BF16, 64, 4, 128>(p, st, ev) : launch_one<kDTypeF16, 64, 4, 128>(p, st, ev);
+    return launch_any(p, s, dtype, false, st, ev);
 }
 
 hipError_t launch_tree_merge(const TreeAttnParams& p, const TreeAttnShape& s, int dtype, hipStream_t st,
                              const LaunchEvents& ev) {
-    const bool bf = dtype == DT_BF16;
-    if (s.dp == 128) {
-        if (s.wr == 1) return bf ? merge_one<DT_BF16, 128, 1>(p, st, ev) : merge_one<kDTypeF16, 128, 1>(p, st, ev);
-        if (s.wr == 2) return bf ? merge_one<DT_BF16, 128, 2>(p, st, ev) : merge_one<kDTypeF16, 128, 2>(p, st, ev);
-        return bf ? merge_one<DT_BF16, 128, 4>(p, st, ev) : merge_one<kDTypeF16, 128, 4>(p, st, ev);
-    }
-    if (s.wr == 1) return bf ? merge_one<DT_BF16, 64, 1>(p, st, ev) : merge_one<kDTypeF16, 64, 1>(p, st, ev);
-    if (s.wr == 2) return bf ? merge_one<DT_BF16, 64, 2>(p, st, ev) : merge_one<kDTypeF16, 64, 2>(p, st, ev);
-    return bf ? merge_one<DT_BF16, 64, 4>(p, st, ev) : merge_one<kDTypeF16, 64, 4>(p, st, ev);
+    return launch_any(p, s, dtype, true, st, ev);
 }
 
 }  // namespace sv
