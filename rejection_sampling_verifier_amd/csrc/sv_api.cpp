@@ -608,13 +608,13 @@ int plan_tree(const sv_tree_attention* a, TreePlan& t) {
     const int rows = a->N * (a->heads / a->kv_heads);
     t.s.dp = a->dim <= 64 ? 64 : 128;
     t.s.rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    t.s.keys = t.s.rows == 128 ? 64 : 128;
+    t.s.keys = t.s.rows == 32 ? 128 : 64;
     t.MT = (rows + t.s.rows - 1) / t.s.rows;
     const int64_t tasks = static_cast<int64_t>(a->B) * a->kv_heads;
     if (tasks > (1ll << 24)) return SV_ESHAPE;
     const int64_t cap = static_cast<int64_t>(a->width) * a->page_size;
     const int64_t most = (cap + t.s.keys - 1) / t.s.keys + 1;  // tiles of one (sequence, key head)
-    const int64_t blocks = (t.s.rows == 32 ? 2ll : 1ll) * device_cus();  // workgroups that are resident at once
+    const int64_t blocks = (t.s.rows == 32 && t.s.dp == 128 ? 1ll : 2ll) * device_cus();  // workgroups that are resident at once
     if (most <= 4) {
         // so short that a part is a whole (sequence, key head): nothing to join
         t.merge = 0;

@@ -117,10 +117,72 @@ __device__ __forceinline__ float shift_of(float a, float b) {
     return a == b ? 1.f : __builtin_amdgcn_exp2f(a - b);
 }
 
-// The 16-byte chunks of row r of a V tile are XORed with this.
+// What rows that do not exist, and dimensions past D, are staged from.
+__device__ const uint4 kZero = {0, 0, 0, 0};
+
+typedef __attribute__((address_space(1))) const uint32_t global_u32;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+
+// s_waitcnt vmcnt(0) with the other counters left alone (gfx9 encoding: vmcnt
+// in bits 0-3 and 14-15, expcnt 4-6, lgkmcnt 8-11).
+constexpr int kWaitVm0 = 0x0F70;
+
+// The K operand of one 32-key subtile, and the V operand of 16 keys, from a
+// stage.  The loads are assembly so that the compiler does not wait for the
+// next stage's loads before them (it cannot tell the stages apart); each block
+// waits for its own.
 template <int DP>
-__device__ __forceinline__ uint32_t swizzle(int r) {
-    return DP == 128 ? ((r & 3) << 2) ^ ((r >> 2) & 3) : (((r >> 1) & 1) << 2) ^ ((r >> 2) & 3);
+__device__ __forceinline__ void read_k(const uint32_t* rd, uint32_t stage, int ks, v8s* r) {
+    const uint32_t a0 = rd[0] + stage, a1 = rd[1] + stage, a2 = rd[2] + stage, a3 = rd[3] + stage;
+    const int off = ks * 64 * DP;
+    if constexpr (DP == 128)
+        asm volatile(
+            "ds_read_b128 %0, %8 offset:%12\n\tds_read_b128 %1, %9 offset:%12\n\t"
+            "ds_read_b128 %2, %10 offset:%12\n\tds_read_b128 %3, %11 offset:%12\n\t"
+            "ds_read_b128 %4, %8 offset:%13\n\tds_read_b128 %5, %9 offset:%13\n\t"
+            "ds_read_b128 %6, %10 offset:%13\n\tds_read_b128 %7, %11 offset:%13\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
+            : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "n"(off), "n"(off + 128)
+            : "memory");
+    else
+        asm volatile(
+            "ds_read_b128 %0, %4 offset:%8\n\tds_read_b128 %1, %5 offset:%8\n\t"
+            "ds_read_b128 %2, %6 offset:%8\n\tds_read_b128 %3, %7 offset:%8\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
+            : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "n"(off)
+            : "memory");
+}
+
+template <int DP>
+__device__ __forceinline__ void read_v(const uint32_t* rd, uint32_t stage, int step, v8s* r) {
+    const uint32_t a0 = rd[0] + stage, a1 = rd[1] + stage;
+    const int lo = step * 32 * DP, hi = lo + 16 * DP;  // rows 16 step and 8 more
+    v4s x[2 * (DP / 32)];
+    if constexpr (DP == 128) {
+        const uint32_t a2 = rd[2] + stage, a3 = rd[3] + stage;
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+            "ds_read_b64_tr_b16 %2, %9 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+            "ds_read_b64_tr_b16 %4, %10 offset:%12\n\tds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+            "ds_read_b64_tr_b16 %6, %11 offset:%12\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
+            : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "n"(lo), "n"(hi)
+            : "memory");
+    } else {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %4 offset:%6\n\tds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+            "ds_read_b64_tr_b16 %2, %5 offset:%6\n\tds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+            : "v"(a0), "v"(a1), "n"(lo), "n"(hi)
+            : "memory");
+    }
+#pragma unroll
+    for (int dt = 0; dt < DP / 32; ++dt)
+        r[dt] = __builtin_shufflevector(x[2 * dt], x[2 * dt + 1], 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // The cache rows of one sequence in tiles: tiles [0, head) from the first row,
@@ -192,17 +254,26 @@ __device__ __forceinline__ uint64_t ancestors(const int32_t* parent, int n, int 
     return set;
 }
 
-template <int DT, int DP, int NT, int WR>
-__global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void k_tree_attn(TreeAttnParams p) {
-    constexpr int WK = kWaves / WR;      // waves over keys
-    constexpr int WROWS = 32 * NT;       // query rows of a wave
-    constexpr int RB = WROWS * WR;       // query rows of the workgroup
-    constexpr int TK = 32 * WK;          // keys per tile, 32 per wave
+template <int DT, int DP, int WR>
+__global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
+    constexpr int WK = kWaves / WR;           // waves over keys
+    constexpr int RB = 32 * WR;               // query rows
+    constexpr bool kShared = WR > 1;          // the waves share their tiles
+    constexpr int TK = kShared ? 64 : 128;    // keys per tile
+    constexpr int GK = kShared ? 64 : 32;     // of them in one staged group: the tile, or a wave's quarter
+    constexpr int KS = TK / (32 * WK);        // 32-key subtiles per wave
+    constexpr int NC = DP / 8;                // 16-byte chunks per row
     constexpr int NQ = DP / 16, ND = DP / 32;
     constexpr int kRowB = DP * 2;
-    constexpr int kTileB = 32 * kRowB;   // a wave's V tile
+    constexpr int kRowsPerLoad = 64 / NC;     // rows one wide load of a wave stages
+    constexpr int kRowsPerWave = kShared ? GK / kWaves : GK;
+    constexpr int kLoads = kRowsPerWave / kRowsPerLoad;
+    constexpr int kVAt = GK * kRowB;          // V behind K in a stage
+    constexpr int kStageB = 2 * GK * kRowB;
+    constexpr int kGroups = kShared ? 1 : kWaves;
 
-    __shared__ __align__(16) uint8_t smem[kWaves * kTileB];
+    __shared__ __align__(16) uint8_t smem[kGroups * 2 * kStageB];
+    __shared__ int s_nf;
     __shared__ float s_ml[2][2][64];
     __shared__ int64_t s_sum[kWaves];
     __shared__ int32_t s_scan[kWaves];
@@ -277,18 +348,34 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void k_tree_attn(TreeAtt
         before = s_before;
     }
 
-    uint8_t* const sv = smem + w * kTileB;
-    // a lane stages the chunks 2 s + hh of row `col`; the tile is XOR-swizzled by
-    // 16-byte chunk: eight lanes of a write, and the sixteen of a transposing
-    // read (four rows, two chunks), touch different banks
-    const uint32_t v_at = col * kRowB;
-    const uint32_t v_x = swizzle<DP>(col);
-    const int vrow = (lane & 15) >> 2;                                // row of four in a transposing read
-    const int vchunk = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);     // its chunk of the four of 32 dimensions
-    const uint32_t vr_at = (4 * hh + vrow) * kRowB + (lane & 1) * 8;
+    uint8_t* const ring = smem + (kShared ? 0 : w * 2 * kStageB);  // two stages
+    // Staging: lane l of a load fills chunk position l % NC of row l / NC, with
+    // the chunk that the tile's XOR swizzle puts there.  K rows are read 16 bytes
+    // per lane, eight rows at a time; V rows by the transposing load, four rows of
+    // two chunks at a time; either way the banks differ.
+    const int ld_row = (kShared ? w * kRowsPerWave : 0) + lane / NC;  // row of the group in the first load
+    auto k_chunk = [&](int r) { return (lane % NC) ^ (r & 7); };
+    const int v_chunk = (lane % NC) ^ (DP == 128 ? ((lane / NC) & 3) << 2 : ((lane / NC >> 1) & 1) << 2);
+    // reading: byte addresses within a stage (K: four, the next four are 128 bytes on; V: one per 32 dimensions)
+    const uint32_t ring_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) uint8_t*)ring));
+    const int sub0 = kShared ? wk * KS : 0;  // the wave's first subtile of the group
+    uint32_t k_rd[4], v_rd[ND];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        k_rd[s] = ring_at + (sub0 * 32 + (lane & 31)) * kRowB + (((2 * s + hh) ^ (lane & 7)) << 4);
+    {
+        const int vrow = (lane & 15) >> 2;                             // row of four
+        const int low = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);     // chunk of the four of 32 dimensions
+        const int vx = DP == 128 ? vrow << 2 : (vrow >> 1) << 2;
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt)
+            v_rd[dt] = ring_at + kVAt + (sub0 * 32 + 4 * hh + vrow) * kRowB + (((4 * dt + low) ^ vx) << 4) +
+                       (lane & 1) * 8;
+    }
     const bool win = p.window > 0;
     const float scale2 = p.scale2;
-    const bool odd_end = p.D % 16 != 0;   // the last 32 bytes of a row are half a row's
+    const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero);
 
     int64_t f = f0;
     while (f < f1) {
@@ -305,340 +392,320 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 2 : 1) void k_tree_attn(TreeAtt
             n = n < 0 ? 0 : n > p.N ? p.N : n;
         }
         const int rows = n * p.G;
-        const int row0 = m * RB + wr * WROWS;  // the wave's first row
-        float mx[NT], l[NT];
-        v16f o[NT][ND];
+        const int my_row = m * RB + wr * 32 + col;
+        const bool active = m * RB + wr * 32 < rows;  // the wave has rows
+        float mx = -INFINITY, l = 0.f;
+        v16f o[ND];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            mx[nt] = -INFINITY;
-            l[nt] = 0.f;
+        for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
-            for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[nt][dt][i] = 0.f;
-        }
+            for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
 
-        if (row0 < rows) {  // the wave has rows; no barrier inside
-            // queries: the B operand, resident; a negative scale is moved into their sign
-            v8s q[NT][NQ];
-            uint64_t set[NT];
-            int low[NT];  // first cache row in the row's window
+        if (m * RB < rows) {
+            const int32_t* const tab = p.table + b * p.table_stride;
+            const uint8_t* const kcb = p.kc + 2 * (h * p.kcs[2]);
+            const uint8_t* const vcb = p.vc + 2 * (h * p.vcs[2]);
+            const uint8_t* const ktb = p.kt + 2 * (b * p.kts[0] + h * p.kts[2]);
+            const uint8_t* const vtb = p.vt + 2 * (b * p.vts[0] + h * p.vts[2]);
+            const int ps_mask = (1 << p.ps_shift) - 1;
+            // first row of the group of tile t: a cache row, or a node
+            auto first_row = [&](int t) {
+                return (t < tl.cache ? tl.key_tile(t) * TK : 0) + (kShared ? 0 : wk * 32);
+            };
+            // lane j: the page of row j of the group of tile t
+            auto page = [&](int t) {
+                int pg = -1;
+                if (t < tl.cache) {
+                    const int key = first_row(t) + (lane & (GK - 1));
+                    if (key < tl.len) pg = tab[key >> p.ps_shift];
+                }
+                return pg;
+            };
+            // starts staging tile t; returns the rows that exist (the others are staged as zeros)
+            auto stage = [&](int t, int pg, int at) {
+                const bool tree = t >= tl.cache;
+                const int first = first_row(t);
+                const bool have = tree ? first + (lane & (GK - 1)) < n
+                                       : static_cast<uint32_t>(pg) < static_cast<uint32_t>(p.pages);
+                const uint64_t okm = __ballot(have);
+                uint8_t* const dst = ring + at * kStageB + (kShared ? w * kRowsPerWave * kRowB : 0);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int row = row0 + nt * 32 + col;
-                const bool in = row < rows;
-                const int node = in ? row / p.G : 0;
+                for (int i = 0; i < kLoads; ++i) {
+                    const int r = ld_row + i * kRowsPerLoad;
+                    const bool ok = okm >> r & 1;
+                    const int kc = k_chunk(r);
+                    const uint8_t *ka, *va;
+                    if (tree) {
+                        ka = ktb + 2 * ((first + r) * p.kts[1]) + 16 * kc;
+                        va = vtb + 2 * ((first + r) * p.vts[1]) + 16 * v_chunk;
+                    } else {
+                        const int64_t page_of = __shfl(pg, r);
+                        const int slot = (first + r) & ps_mask;
+                        ka = kcb + 2 * (page_of * p.kcs[0] + slot * p.kcs[1]) + 16 * kc;
+                        va = vcb + 2 * (page_of * p.vcs[0] + slot * p.vcs[1]) + 16 * v_chunk;
+                    }
+                    ka = ok && kc * 8 < p.D ? ka : zero;
+                    va = ok && v_chunk * 8 < p.D ? va : zero;
+                    __builtin_amdgcn_global_load_lds((global_u32*)ka, (lds_u32*)(dst + i * kRowsPerLoad * kRowB), 16, 0, 0);
+                    __builtin_amdgcn_global_load_lds((global_u32*)va, (lds_u32*)(dst + kVAt + i * kRowsPerLoad * kRowB), 16,
+                                                     0, 0);
+                }
+                return okm;
+            };
+
+            int pg = page(t0);
+            int pg_next = t0 + 1 < t1 ? page(t0 + 1) : -1;
+            uint64_t okm = stage(t0, pg, 0);
+
+            // queries: the B operand, resident; a negative scale is moved into their sign
+            v8s q[NQ];
+            {
+                const bool in = my_row < rows;
+                const int node = in ? my_row / p.G : 0;
                 const int64_t off = b * p.qs[0] + node * p.qs[1] +
-                                    static_cast<int64_t>(h * p.G + (in ? row - node * p.G : 0)) * p.qs[2];
+                                    static_cast<int64_t>(h * p.G + (in ? my_row - node * p.G : 0)) * p.qs[2];
 #pragma unroll
                 for (int s = 0; s < NQ; ++s) {
                     const int d = s * 16 + hh * 8;
                     v8s z = {0, 0, 0, 0, 0, 0, 0, 0};
                     if (in && d < p.D) z = *reinterpret_cast<const v8s*>(p.q + 2 * (off + d));
-                    q[nt][s] = p.flip ? z ^ static_cast<short>(0x8000) : z;
+                    q[s] = p.flip ? z ^ static_cast<short>(0x8000) : z;
                 }
-                set[nt] = 0;
-                low[nt] = 0;
-                if (t1 == T || win) {
-                    const int32_t* const par_b = p.parent + static_cast<int64_t>(b) * p.N;
-                    const uint64_t all = ancestors(par_b, n, lane, 0);
-                    set[nt] = __shfl(static_cast<unsigned long long>(all), node);
-                    if (win) {
-                        low[nt] = tl.len + __popcll(set[nt]) - p.window;  // depth + 1 nodes on the line
-                        if (p.window < kMaxNodes)
-                            set[nt] = __shfl(static_cast<unsigned long long>(ancestors(par_b, n, lane, p.window)), node);
-                    }
+            }
+            uint64_t set = 0;  // the nodes the row sees
+            int low = 0;       // first cache row in the row's window
+            if (t1 == T || win) {
+                const int node = my_row < rows ? my_row / p.G : 0;
+                const int32_t* const par_b = p.parent + static_cast<int64_t>(b) * p.N;
+                const uint64_t all = ancestors(par_b, n, lane, 0);
+                set = __shfl(static_cast<unsigned long long>(all), node);
+                if (win) {
+                    low = tl.len + __popcll(set) - p.window;  // depth + 1 nodes on the line
+                    if (p.window < kMaxNodes)
+                        set = __shfl(static_cast<unsigned long long>(ancestors(par_b, n, lane, p.window)), node);
                 }
             }
 
-            const int32_t* const tab = p.table + b * p.table_stride;
-            // this (sequence, key head)'s rows, at this lane's first chunk
-            const uint8_t* const kcb = p.kc + 2 * (h * p.kcs[2] + hh * 8);
-            const uint8_t* const vcb = p.vc + 2 * (h * p.vcs[2] + hh * 8);
-            const uint8_t* const ktb = p.kt + 2 * (b * p.kts[0] + h * p.kts[2] + hh * 8);
-            const uint8_t* const vtb = p.vt + 2 * (b * p.vts[0] + h * p.vts[2] + hh * 8);
-            auto page = [&](int t) {  // the page of this lane's row of tile t
-                if (t >= tl.cache) return -1;
-                const int key = tl.key_tile(t) * TK + wk * 32 + col;
-                return key < tl.len ? tab[key >> p.ps_shift] : -1;
-            };
-            // where this lane's row of tile t is; rows that nothing sees stand in for one that exists
-            auto place = [&](int t, int pid, const uint8_t*& ka, const uint8_t*& va) {
-                if (t >= tl.cache) {
-                    const int r = wk * 32 + col;
-                    const bool ok = r < n;
-                    const int64_t at = ok ? r : 0;
-                    ka = ktb + 2 * (at * p.kts[1]);
-                    va = vtb + 2 * (at * p.vts[1]);
-                    return ok;
-                }
-                const int slot = (tl.key_tile(t) * TK + wk * 32 + col) & ((1 << p.ps_shift) - 1);
-                const bool ok = static_cast<uint32_t>(pid) < static_cast<uint32_t>(p.pages);
-                const int64_t at = ok ? pid : 0;
-                ka = kcb + 2 * (at * p.kcs[0] + slot * p.kcs[1]);
-                va = vcb + 2 * (at * p.vcs[0] + slot * p.vcs[1]);
-                return ok;
-            };
-            auto fetch = [&](const uint8_t* a, v8s* r) {
-                if (p.D == DP) {
-#pragma unroll
-                    for (int s = 0; s < NQ; ++s) r[s] = *reinterpret_cast<const v8s*>(a + 32 * s);
-                } else {
-                    const bool half = odd_end && hh;  // chunks past the row's end: read its start, then drop it
-#pragma unroll
-                    for (int s = 0; s < NQ; ++s) {
-                        v8s z = {0, 0, 0, 0, 0, 0, 0, 0};
-                        if (16 * s + 16 <= p.D) {
-                            z = *reinterpret_cast<const v8s*>(a + 32 * s);
-                        } else if (16 * s < p.D) {
-                            const v8s y = *reinterpret_cast<const v8s*>(half ? a - 16 : a + 32 * s);
-                            z = half ? z : y;
-                        }
-                        r[s] = z;
-                    }
-                }
-            };
-
-            v8s kr[NQ], vr[NQ];
-            const uint8_t *ka, *va;
-            bool ok = place(t0, page(t0), ka, va);
-            fetch(ka, kr);
-            fetch(va, vr);
-            int pid = t0 + 1 < t1 ? page(t0 + 1) : -1;
-            for (int t = t0; t < t1; ++t) {
+            int at = 0;
+            for (int t = t0; t < t1; ++t, at ^= 1) {
                 const bool tree = t >= tl.cache;
-                const int kb = (tree ? 0 : tl.key_tile(t) * TK) + wk * 32;
+                const int kb = first_row(t);
                 const bool mixed = tree || (win && kb < tl.len + p.N - p.window);
-                const uint32_t bad = ~static_cast<uint32_t>(__ballot(ok));  // rows nothing sees
-                const bool more = t + 1 < t1;
-                bool nf = false;
-
-                v16f x[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[nt][i] = 0.f;
-#pragma unroll
-                for (int s = 0; s < NQ; ++s)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) x[nt] = mfma<DT>(kr[s], q[nt][s], x[nt]);
+                // this wave's loads of tile t (all that is in flight) have landed; with the
+                // barrier everyone's, and everyone has read the other stage
+                __builtin_amdgcn_s_waitcnt(kWaitVm0);
+                if (kShared) __builtin_amdgcn_s_barrier();
                 __builtin_amdgcn_sched_barrier(0);
-                bool ok_next = false;
-                const uint8_t* va_next = va;
-                if (more) {
-                    ok_next = place(t + 1, pid, ka, va_next);
-                    fetch(ka, kr);
+                uint64_t okm_next = 0;
+                if (t + 1 < t1) {
+                    pg = pg_next;
+                    if (t + 2 < t1) pg_next = page(t + 2);
+                    okm_next = stage(t + 1, pg, at ^ 1);
                 }
-                // V rows into the wave's tile, hidden ones as zeros
-                if (bad != 0) {
-#pragma unroll
-                    for (int s = 0; s < NQ; ++s) vr[s] = ok ? vr[s] : static_cast<short>(0);
-                }
+                bool nf = false;
                 if (mixed) {
+                    // infinities and NaN among the values: out of the tile, added below
+                    bool mine = false;
+                    uint8_t* const part = ring + at * kStageB + kVAt + (kShared ? w * kRowsPerWave * kRowB : 0);
 #pragma unroll
-                    for (int s = 0; s < NQ; ++s) {
-                        const uint4 u = __builtin_bit_cast(uint4, vr[s]);
+                    for (int i = 0; i < kLoads; ++i) {
+                        v8s* const e = reinterpret_cast<v8s*>(part + i * 1024 + lane * 16);
+                        v8s y = *e;
+                        const uint4 u = __builtin_bit_cast(uint4, y);
                         if (nonfinite2<DT>(u.x) || nonfinite2<DT>(u.y) || nonfinite2<DT>(u.z) || nonfinite2<DT>(u.w)) {
-                            nf = true;
+                            mine = true;
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                if (nonfinite2<DT>(static_cast<uint16_t>(vr[s][j]))) vr[s][j] = 0;
+                                if (nonfinite2<DT>(static_cast<uint16_t>(y[j]))) y[j] = 0;
+                            *e = y;
                         }
                     }
-                    nf = __any(nf);
-                }
-#pragma unroll
-                for (int s = 0; s < NQ; ++s)
-                    *reinterpret_cast<v8s*>(sv + v_at + (((2 * s + hh) ^ v_x) << 4)) = vr[s];
-                if (more) {
-                    fetch(va_next, vr);
-                    if (t + 2 < t1) pid = page(t + 2);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-
-                if (mixed || bad != 0) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        uint32_t see = ~bad;  // bit r: this lane's row sees row r of the subtile
-                        if (tree)
-                            see &= wk < 2 ? static_cast<uint32_t>(set[nt] >> (32 * (wk & 1))) : 0u;
-                        else if (win)
-                            see &= bits_from(low[nt] - kb) | ~bits_from(p.sinks - kb);
-                        see >>= 4 * hh;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            x[nt][i] = see & (1u << (8 * (i >> 2) + (i & 3))) ? x[nt][i] : -INFINITY;
+                    if (kShared) {
+                        if (tid == 0) s_nf = 0;
+                        __syncthreads();
+                        if (mine) s_nf = 1;
+                        __syncthreads();
+                        nf = __builtin_amdgcn_readfirstlane(s_nf) != 0;
+                    } else {
+                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+                        nf = __any(mine);
                     }
                 }
-                bool grows = false;
-                float top[NT];
+                const uint32_t stage_at = at * kStageB;
+                v16f x[KS];
+                uint32_t bad[KS];  // rows that nothing sees
+                if (active) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    top[nt] = x[nt][0];
+                    for (int ks = 0; ks < KS; ++ks) {
+                        bad[ks] = ~static_cast<uint32_t>(okm >> (32 * (sub0 + ks)));
+                        v8s kf[NQ];
+                        read_k<DP>(k_rd, stage_at, ks, kf);
 #pragma unroll
-                    for (int i = 1; i < 16; ++i) top[nt] = fmaxf(top[nt], x[nt][i]);
-                    top[nt] = half_max(top[nt]) * scale2;
-                    grows = grows || top[nt] > mx[nt] + 8.f;
-                }
-                if (__any(grows)) {
+                        for (int i = 0; i < 16; ++i) x[ks][i] = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float mn = fmaxf(mx[nt], top[nt]);
-                        const float a = shift_of(mx[nt], mn);
-                        l[nt] *= a;
+                        for (int s = 0; s < NQ; ++s) x[ks] = mfma<DT>(kf[s], q[s], x[ks]);
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        if (mixed || bad[ks] != 0) {
+                            const int sub = sub0 + ks, key0 = kb + ks * 32 + sub0 * 32;
+                            uint32_t see = ~bad[ks];  // bit r: this lane's row sees row r of the subtile
+                            if (tree)
+                                see &= key0 < kMaxNodes ? static_cast<uint32_t>(set >> key0) : 0u;
+                            else if (win)
+                                see &= bits_from(low - key0) | ~bits_from(p.sinks - key0);
+                            (void)sub;
+                            see >>= 4 * hh;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                x[ks][i] = see & (1u << (8 * (i >> 2) + (i & 3))) ? x[ks][i] : -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) top = fmaxf(top, x[ks][i]);
+                    }
+                    top = half_max(top) * scale2;
+                    if (__any(top > mx + 8.f)) {
+                        const float mn = fmaxf(mx, top);
+                        const float a = shift_of(mx, mn);
+                        l *= a;
 #pragma unroll
                         for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[nt][dt][i] *= a;
-                        mx[nt] = mn;
+                            for (int i = 0; i < 16; ++i) o[dt][i] *= a;
+                        mx = mn;
                     }
-                }
-                v8s pf[NT][2];
+                    const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float ref = mx[nt] == -INFINITY ? 0.f : mx[nt];
+                    for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        x[nt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[nt][i], scale2, -ref));
-                        l[nt] += x[nt][i];
-                    }
+                        for (int i = 0; i < 16; ++i) {
+                            x[ks][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[ks][i], scale2, -ref));
+                            l += x[ks][i];
+                        }
 #pragma unroll
-                    for (int t2 = 0; t2 < 2; ++t2) {
-                        const v4s lo = pack4<DT>(x[nt][8 * t2], x[nt][8 * t2 + 1], x[nt][8 * t2 + 2], x[nt][8 * t2 + 3]);
-                        const v4s hi =
-                            pack4<DT>(x[nt][8 * t2 + 4], x[nt][8 * t2 + 5], x[nt][8 * t2 + 6], x[nt][8 * t2 + 7]);
-                        pf[nt][t2] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                    }
-                }
+                        for (int t2 = 0; t2 < 2; ++t2) {
+                            const v4s lo = pack4<DT>(x[ks][8 * t2], x[ks][8 * t2 + 1], x[ks][8 * t2 + 2],
+                                                     x[ks][8 * t2 + 3]);
+                            const v4s hi = pack4<DT>(x[ks][8 * t2 + 4], x[ks][8 * t2 + 5], x[ks][8 * t2 + 6],
+                                                     x[ks][8 * t2 + 7]);
+                            const v8s pf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                            v8s vf[ND];
+                            read_v<DP>(v_rd, stage_at, 2 * ks + t2, vf);
 #pragma unroll
-                for (int t2 = 0; t2 < 2; ++t2)
-#pragma unroll
-                    for (int dt = 0; dt < ND; ++dt) {
-                        const uint32_t row = vr_at + 16 * t2 * kRowB;
-                        const v4s a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (lds_v4s*)(sv + row + (((4 * dt + vchunk) ^ swizzle<DP>(4 * hh + vrow)) << 4)));
-                        const v4s a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (lds_v4s*)(sv + row + 8 * kRowB + (((4 * dt + vchunk) ^ swizzle<DP>(8 + 4 * hh + vrow)) << 4)));
-                        const v8s a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) o[nt][dt] = mfma<DT>(a, pf[nt][t2], o[nt][dt]);
-                    }
-                if (nf) {  // rare: infinities or NaN among the values, for the rows that see them
-                    float* const wp = reinterpret_cast<float*>(sv);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) wp[(8 * (i >> 2) + 4 * hh + (i & 3)) * 32 + col] = x[nt][i];
-                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                        for (int r = 0; r < 32; ++r) {
-                            const int key = kb + r;
-                            const uint8_t* src;
-                            if (bad >> r & 1) continue;
-                            if (tree) {
-                                src = p.vt + 2 * (b * p.vts[0] + key * p.vts[1] + h * p.vts[2]);
-                            } else {
-                                const int pg = tab[key >> p.ps_shift];
-                                src = p.vc + 2 * (pg * p.vcs[0] + (key & ((1 << p.ps_shift) - 1)) * p.vcs[1] +
-                                                  h * p.vcs[2]);
-                            }
-                            const float wgt = wp[r * 32 + col];
-#pragma unroll
-                            for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-                                for (int g = 0; g < 4; ++g) {
-                                    if (32 * dt + 8 * g < p.D) {
-                                        const uint2 e = *reinterpret_cast<const uint2*>(src + 2 * (32 * dt + 8 * g + 4 * hh));
-                                        if (wgt != 0.f && (nonfinite2<DT>(e.x) || nonfinite2<DT>(e.y))) {
-                                            o[nt][dt][4 * g] += nonfinite_term<DT>(wgt, e.x & 0xFFFFu);
-                                            o[nt][dt][4 * g + 1] += nonfinite_term<DT>(wgt, e.x >> 16);
-                                            o[nt][dt][4 * g + 2] += nonfinite_term<DT>(wgt, e.y & 0xFFFFu);
-                                            o[nt][dt][4 * g + 3] += nonfinite_term<DT>(wgt, e.y >> 16);
-                                        }
-                                    }
-                                    asm volatile("" ::: "memory");  // one load at a time: registers stay with the main path
-                                }
+                            for (int dt = 0; dt < ND; ++dt) o[dt] = mfma<DT>(vf[dt], pf, o[dt]);
                         }
                     }
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 }
-                ok = ok_next;
-                va = va_next;
+                if (nf) {  // rare: infinities or NaN among the values, for the rows that see them
+                    if (kShared) __syncthreads();  // the stage has been read
+                    float* const wp = reinterpret_cast<float*>(ring + at * kStageB + (kShared ? w * 4096 : 0));
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        if (active) {
+                            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) wp[(8 * (i >> 2) + 4 * hh + (i & 3)) * 32 + col] = x[ks][i];
+                            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+                            for (int r = 0; r < 32; ++r) {
+                                const int key = kb + (sub0 + ks) * 32 + r;
+                                const uint8_t* src;
+                                if (bad[ks] >> r & 1) continue;
+                                if (tree) {
+                                    src = vtb + 2 * (key * p.vts[1]);
+                                } else {
+                                    const int64_t page_of = tab[key >> p.ps_shift];
+                                    src = vcb + 2 * (page_of * p.vcs[0] + (key & ps_mask) * p.vcs[1]);
+                                }
+                                const float wgt = wp[r * 32 + col];
+#pragma unroll
+                                for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                                    for (int g = 0; g < 4; ++g) {
+                                        if (32 * dt + 8 * g < p.D) {
+                                            const uint2 e =
+                                                *reinterpret_cast<const uint2*>(src + 2 * (32 * dt + 8 * g + 4 * hh));
+                                            if (wgt != 0.f && (nonfinite2<DT>(e.x) || nonfinite2<DT>(e.y))) {
+                                                o[dt][4 * g] += nonfinite_term<DT>(wgt, e.x & 0xFFFFu);
+                                                o[dt][4 * g + 1] += nonfinite_term<DT>(wgt, e.x >> 16);
+                                                o[dt][4 * g + 2] += nonfinite_term<DT>(wgt, e.y & 0xFFFFu);
+                                                o[dt][4 * g + 3] += nonfinite_term<DT>(wgt, e.y >> 16);
+                                            }
+                                        }
+                                        asm volatile("" ::: "memory");  // one load at a time: registers stay with the main path
+                                    }
+                            }
+                        }
+                    }
+                    if (kShared) __syncthreads();
+                }
+                okm = okm_next;
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) l[nt] = half_sum(l[nt]);
-        }
+            l = half_sum(l);
 
-        // waves that took other keys of the same rows hand their results over
-        if (m * RB < rows) {
-            float* const buf = reinterpret_cast<float*>(smem);
+            // waves that took other keys of the same rows hand their results over
+            if constexpr (WK > 1) {
+                float* const buf = reinterpret_cast<float*>(smem);
 #pragma unroll
-            for (int half = WK / 2; half >= 1; half >>= 1) {
-                const int slot = WR == 2 ? wr : wk % half;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int half = WK / 2; half >= 1; half >>= 1) {
+                    const int slot = WR == 2 ? wr : wk % half;
                     __syncthreads();
                     if (wk >= half && wk < 2 * half) {
 #pragma unroll
                         for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                buf[slot * 64 * (DP / 2) + (dt * 16 + i) * 64 + lane] = o[nt][dt][i];
-                        s_ml[slot][0][lane] = mx[nt];
-                        s_ml[slot][1][lane] = l[nt];
+                                buf[slot * 64 * (DP / 2) + (dt * 16 + i) * 64 + lane] = o[dt][i];
+                        s_ml[slot][0][lane] = mx;
+                        s_ml[slot][1][lane] = l;
                     }
                     __syncthreads();
                     if (wk < half) {
                         const float m2 = s_ml[slot][0][lane], l2 = s_ml[slot][1][lane];
-                        const float mn = fmaxf(mx[nt], m2);
-                        const float a1 = shift_of(mx[nt], mn), a2 = shift_of(m2, mn);
-                        l[nt] = l[nt] * a1 + l2 * a2;
-                        mx[nt] = mn;
+                        const float mn = fmaxf(mx, m2);
+                        const float a1 = shift_of(mx, mn), a2 = shift_of(m2, mn);
+                        l = l * a1 + l2 * a2;
+                        mx = mn;
 #pragma unroll
                         for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                o[nt][dt][i] =
-                                    o[nt][dt][i] * a1 + buf[slot * 64 * (DP / 2) + (dt * 16 + i) * 64 + lane] * a2;
+                                o[dt][i] = o[dt][i] * a1 + buf[slot * 64 * (DP / 2) + (dt * 16 + i) * 64 + lane] * a2;
                     }
                 }
             }
-            __syncthreads();  // the tiles are the waves' own again
+            __syncthreads();  // the stages are free again
         }
 
         if (wk == 0) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int r = wr * WROWS + nt * 32 + col, row = m * RB + r;
-                if (whole) {
-                    if (row < p.N * p.G) {
-                        const int node = row / p.G;
-                        const float inv = row < rows ? 1.f / l[nt] : 0.f;  // zeros for an absent node
-                        uint8_t* const dst = p.out + 2 * (b * p.os[0] + node * p.os[1] +
-                                                          static_cast<int64_t>(h * p.G + row - node * p.G) * p.os[2]);
-#pragma unroll
-                        for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-                            for (int g = 0; g < 4; ++g)
-                                if (32 * dt + 8 * g < p.D)
-                                    *reinterpret_cast<v4s*>(dst + 2 * (32 * dt + 8 * g + 4 * hh)) =
-                                        pack4<DT>(o[nt][dt][4 * g] * inv, o[nt][dt][4 * g + 1] * inv,
-                                                  o[nt][dt][4 * g + 2] * inv, o[nt][dt][4 * g + 3] * inv);
-                    }
-                } else if (row < rows) {
-                    float* const rec =
-                        p.part + ((static_cast<int64_t>(c) * 2 + (f == f0 ? 0 : 1)) * p.MT + m) * (RB * (DP + 2));
+            if (whole) {
+                if (my_row < p.N * p.G) {
+                    const int node = my_row / p.G;
+                    const float inv = my_row < rows ? 1.f / l : 0.f;  // zeros for an absent node
+                    uint8_t* const dst = p.out + 2 * (b * p.os[0] + node * p.os[1] +
+                                                      static_cast<int64_t>(h * p.G + my_row - node * p.G) * p.os[2]);
 #pragma unroll
                     for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
                         for (int g = 0; g < 4; ++g)
-                            *reinterpret_cast<float4*>(rec + r * DP + 32 * dt + 8 * g + 4 * hh) =
-                                make_float4(o[nt][dt][4 * g], o[nt][dt][4 * g + 1], o[nt][dt][4 * g + 2],
-                                            o[nt][dt][4 * g + 3]);
-                    if (hh == 0) {
-                        rec[RB * DP + r] = mx[nt];
-                        rec[RB * DP + RB + r] = l[nt];
-                    }
+                            if (32 * dt + 8 * g < p.D)
+                                *reinterpret_cast<v4s*>(dst + 2 * (32 * dt + 8 * g + 4 * hh)) =
+                                    pack4<DT>(o[dt][4 * g] * inv, o[dt][4 * g + 1] * inv, o[dt][4 * g + 2] * inv,
+                                              o[dt][4 * g + 3] * inv);
+                }
+            } else if (my_row < rows) {
+                float* const rec =
+                    p.part + ((static_cast<int64_t>(c) * 2 + (f == f0 ? 0 : 1)) * p.MT + m) * (RB * (DP + 2));
+                const int r = wr * 32 + col;
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        *reinterpret_cast<float4*>(rec + r * DP + 32 * dt + 8 * g + 4 * hh) =
+                            make_float4(o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]);
+                if (hh == 0) {
+                    rec[RB * DP + r] = mx;
+                    rec[RB * DP + RB + r] = l;
                 }
             }
         }
@@ -701,10 +768,10 @@ __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
     *reinterpret_cast<v4s*>(dst + 2 * d) = res;
 }
 
-template <int DT, int DP, int NT, int WR>
+template <int DT, int DP, int WR>
 hipError_t launch_one(const TreeAttnParams& p, hipStream_t st, const LaunchEvents& ev) {
     const int64_t grid = p.MT == 1 ? p.clusters : static_cast<int64_t>((p.clusters + 7) / 8) * 8 * p.MT;
-    hipExtLaunchKernelGGL((k_tree_attn<DT, DP, NT, WR>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st,
+    hipExtLaunchKernelGGL((k_tree_attn<DT, DP, WR>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st,
                           ev.start, ev.stop, 0, p);
     return hipGetLastError();
 }
@@ -719,9 +786,9 @@ hipError_t merge_one(const TreeAttnParams& p, hipStream_t st, const LaunchEvents
 
 template <int DT, int DP>
 hipError_t launch_rows_of(const TreeAttnParams& p, int rows, bool merge, hipStream_t st, const LaunchEvents& ev) {
-    if (rows == 32) return merge ? merge_one<DT, DP, 32>(p, st, ev) : launch_one<DT, DP, 1, 1>(p, st, ev);
-    if (rows == 64) return merge ? merge_one<DT, DP, 64>(p, st, ev) : launch_one<DT, DP, 2, 1>(p, st, ev);
-    return merge ? merge_one<DT, DP, 128>(p, st, ev) : launch_one<DT, DP, 2, 2>(p, st, ev);
+    if (rows == 32) return merge ? merge_one<DT, DP, 32>(p, st, ev) : launch_one<DT, DP, 1>(p, st, ev);
+    if (rows == 64) return merge ? merge_one<DT, DP, 64>(p, st, ev) : launch_one<DT, DP, 2>(p, st, ev);
+    return merge ? merge_one<DT, DP, 128>(p, st, ev) : launch_one<DT, DP, 4>(p, st, ev);
 }
 
 hipError_t launch_any(const TreeAttnParams& p, const TreeAttnShape& s, int dtype, bool merge, hipStream_t st,
