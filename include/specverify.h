@@ -378,14 +378,14 @@ enum { SV_F16 = 2 };  /* a dtype of the attention and the cache */
  *
  * dtype          SV_BF16 or SV_F16, of all tensors.
  * B, N           1 <= B <= 65536 sequences, 1 <= N <= 64 nodes.
- * heads, kv_heads  query and key heads; heads a multiple of kv_heads.
+ * heads, kv_heads  query and key heads; heads <= 1024, a multiple of kv_heads.
  * dim            a multiple of 8, at most 128.
  * q, out         [B, N, heads, dim]; k_tree, v_tree [B, N, kv_heads, dim];
  *                strides in elements for (sequence, node, head).
  * k_cache, v_cache  [pages, page_size, kv_heads, dim]; strides for (page,
  *                slot, head); page_size a power of two, at most 1024.
  *                The last axis of every tensor is contiguous; data and strides
- *                are multiples of 16 bytes; strides are >= 0.
+ *                are multiples of 16 bytes; strides are >= 0, below 64 GB.
  * table          device int32 [B, width], row stride table_stride.  An entry
  *                outside [0, pages) hides its rows.  width * page_size <= 2^28.
  * len            device int32 [B], rows in the cache (clamped to [0, width *

@@ -9,6 +9,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <limits>
 #include <map>
 #include <mutex>
 #include <string>
@@ -576,15 +577,18 @@ static_assert(SPECVERIFY_MAX_NODES == sv::kMaxNodes && SV_F16 == sv::kDTypeF16, 
 bool pow2_page(int ps) { return ps >= 1 && ps <= 1024 && (ps & (ps - 1)) == 0; }
 
 // Strides of a tensor whose rows are read 16 bytes at a time; they come out
-// in units of `unit` elements.
-int check_rows(const void* data, const int64_t* stride, int n, int elem, int64_t* out, int64_t unit) {
+// in units of 16 bytes.
+template <typename I>
+int check_rows(const void* data, const int64_t* stride, int n, int elem, I* out) {
     if (!data) return SV_EINVAL;
     for (int i = 0; i < n; ++i)
         if (stride[i] < 0) return SV_EINVAL;
     if (misaligned(data, 16)) return SV_EALIGN;
     for (int i = 0; i < n; ++i) {
+        if (stride[i] > (1ll << 40) || stride[i] / (16 / elem) > static_cast<int64_t>(std::numeric_limits<I>::max()))
+            return SV_ESHAPE;
         if (stride[i] * elem % 16) return SV_EALIGN;
-        out[i] = stride[i] / unit;
+        out[i] = static_cast<I>(stride[i] / (16 / elem));
     }
     return SV_OK;
 }
@@ -601,7 +605,7 @@ int plan_tree(const sv_tree_attention* a, TreePlan& t) {
     if (!a) return SV_EINVAL;
     if (a->dtype != SV_BF16 && a->dtype != SV_F16) return SV_EDTYPE;
     if (a->B < 1 || a->B > 65536 || a->N < 1 || a->N > SPECVERIFY_MAX_NODES) return SV_ESHAPE;
-    if (a->heads < 1 || a->kv_heads < 1 || a->heads > 4096 || a->heads % a->kv_heads) return SV_ESHAPE;
+    if (a->heads < 1 || a->kv_heads < 1 || a->heads > 1024 || a->heads % a->kv_heads) return SV_ESHAPE;
     if (a->dim < 8 || a->dim > 128 || a->dim % 8) return SV_ESHAPE;
     if (a->pages < 1 || !pow2_page(a->page_size) || a->width < 0) return SV_ESHAPE;
     if (static_cast<int64_t>(a->width) * a->page_size > (1ll << 28)) return SV_ESHAPE;
@@ -644,7 +648,7 @@ int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
     const struct {
         const void* data;
         const int64_t* stride;
-        int64_t* out;
+        uint32_t* out;
     } rows[] = {{a->q, a->q_stride, p.qs},
                 {a->k_tree, a->k_tree_stride, p.kts},
                 {a->v_tree, a->v_tree_stride, p.vts},
@@ -652,7 +656,7 @@ int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
                 {a->v_cache, a->v_cache_stride, p.vcs},
                 {a->out, a->out_stride, p.os}};
     for (const auto& r : rows) {
-        rc = check_rows(r.data, r.stride, 3, 2, r.out, 1);
+        rc = check_rows(r.data, r.stride, 3, 2, r.out);
         if (rc) return rc;
     }
     if (misaligned(a->table, 4) || misaligned(a->len, 4) || misaligned(a->parent, 4) ||
@@ -784,12 +788,12 @@ int cache_impl(const sv_cache* c, const void* kt, const void* vt, const int64_t*
     sv::CacheParams p;
     std::memset(&p, 0, sizeof(p));
     const int64_t unit = 16 / elem;
-    int rc = check_rows(c->k, c->k_stride, 4, elem, p.ks, unit);
-    if (!rc) rc = check_rows(c->v, c->v_stride, 4, elem, p.vs, unit);
+    int rc = check_rows(c->k, c->k_stride, 4, elem, p.ks);
+    if (!rc) rc = check_rows(c->v, c->v_stride, 4, elem, p.vs);
     if (!rc && !fork) {
         if (!kts || !vts) return SV_EINVAL;
-        rc = check_rows(kt, kts, 4, elem, p.kts, unit);
-        if (!rc) rc = check_rows(vt, vts, 4, elem, p.vts, unit);
+        rc = check_rows(kt, kts, 4, elem, p.kts);
+        if (!rc) rc = check_rows(vt, vts, 4, elem, p.vts);
     }
     if (rc) return rc;
     if (ws_bytes < cache_workspace(c->B, fork ? 0 : N, c->page_size)) return SV_ETOOBIG;

@@ -27,9 +27,9 @@ enum TreeKernelKind : int {
 struct TreeAttnParams {
     const uint8_t *q, *kt, *vt, *kc, *vc;  // queries, tree K/V, cache K/V
     uint8_t* out;
-    int64_t qs[3], os[3];                  // strides in elements: sequence, node, head
-    int64_t kts[3], vts[3];
-    int64_t kcs[3], vcs[3];                // page, slot, head
+    uint32_t qs[3], os[3];                 // strides in 16-byte units: sequence, node, head
+    uint32_t kts[3], vts[3];
+    uint32_t kcs[3], vcs[3];               // page, slot, head
     const int32_t *table, *len, *parent, *n_nodes;  // n_nodes may be null
     int64_t table_stride;
     int B, N, Hkv, G, D;                   // G = query heads per key head

@@ -94,11 +94,6 @@ __device__ __forceinline__ float to_float(uint16_t u) {
         return static_cast<float>(__builtin_bit_cast(_Float16, u));
 }
 
-template <int DT>
-__device__ __forceinline__ float nonfinite_term(float wgt, uint32_t e) {
-    return nonfinite2<DT>(e) ? wgt * to_float<DT>(static_cast<uint16_t>(e)) : 0.f;
-}
-
 // The value in both half-waves: (of lane & 31, of (lane & 31) + 32).
 __device__ __forceinline__ float half_max(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -214,15 +209,35 @@ __device__ __forceinline__ Tiles tiles_of(const TreeAttnParams& p, int len) {
     return r;
 }
 
-// Parts the line of `total` tiles is cut into, and the part that tile f is in.
-__device__ __forceinline__ int parts_of(const TreeAttnParams& p, int64_t total) {
-    const int64_t most = (total + p.min_tiles - 1) / p.min_tiles;
-    return most < p.clusters ? static_cast<int>(most) : p.clusters;
+// Byte offsets of row numbers times strides in 16-byte units.
+__device__ __forceinline__ uint64_t units(uint32_t i, uint32_t s) { return (static_cast<uint64_t>(i) * s) << 4; }
+__device__ __forceinline__ uint64_t units(uint32_t i, uint32_t s, uint32_t j, uint32_t r) {
+    return (static_cast<uint64_t>(i) * s + static_cast<uint64_t>(j) * r) << 4;
 }
-__device__ __forceinline__ int64_t part_start(int64_t total, int parts, int c) { return total * c / parts; }
-__device__ __forceinline__ int part_of(int64_t total, int parts, int64_t f) {
-    return static_cast<int>(((f + 1) * parts - 1) / total);
-}
+
+// Parts the line of `total` tiles is cut into, and the part that tile f is in:
+// `extra` parts of `per` + 1 tiles, then parts of `per`.
+struct Cut {
+    int64_t per, extra;
+    int parts;
+    __device__ __forceinline__ Cut(const TreeAttnParams& p, int64_t total) {
+        const int64_t most = p.min_tiles == 1 ? total : (total + 1) >> 1;
+        parts = most < p.clusters ? static_cast<int>(most) : p.clusters;
+        if (total >> 32 == 0) {  // a 64-bit division costs about half a microsecond
+            per = static_cast<uint32_t>(total) / static_cast<uint32_t>(parts);
+        } else {
+            per = total / parts;
+        }
+        extra = total - per * parts;
+    }
+    __device__ __forceinline__ int64_t start(int c) const { return c * per + (c < extra ? c : extra); }
+    __device__ __forceinline__ int of(int64_t f) const {
+        const int64_t wide = extra * (per + 1);
+        const int64_t g = f < wide ? f : f - wide, by = f < wide ? per + 1 : per;
+        const int64_t q = (g | by) >> 32 == 0 ? static_cast<uint32_t>(g) / static_cast<uint32_t>(by) : g / by;
+        return static_cast<int>(f < wide ? q : extra + q);
+    }
+};
 
 // Ancestor-or-self sets of the nodes: lane i of a wave holds node i's.
 // `near` > 0 keeps the nearest `near` of them only.  A parent outside [0, i)
@@ -241,8 +256,7 @@ __device__ __forceinline__ uint64_t ancestors(const int32_t* parent, int n, int 
         }
         return set;
     }
-#pragma unroll
-    for (int s = 0; s < 6; ++s) {  // paths double in length: 64 nodes need 6 steps
+    for (int s = 1; s < n; s *= 2) {  // paths double in length
         const int at = up < 0 ? lane : up;
         const uint64_t theirs = __shfl(static_cast<unsigned long long>(set), at);
         const int next = __shfl(up, at);
@@ -273,8 +287,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
     constexpr int kGroups = kShared ? 1 : kWaves;
 
     __shared__ __align__(16) uint8_t smem[kGroups * 2 * kStageB];
+    constexpr int kSlowB = kShared && kStageB < 4 * 8192 ? 4 * 8192 : 0;  // where a stage is too small for the slow path
+    __shared__ __align__(16) uint8_t slow[kSlowB ? kSlowB : 16];
     __shared__ int s_nf;
-    __shared__ float s_ml[2][2][64];
+    constexpr int kOut = DP / 8 / WK;         // groups of four dimensions a wave's lane writes
+    static_assert(WK == 1 || kWaves * 32 * DP * 4 <= kGroups * 2 * kStageB, "the waves' results fit the stages");
+    __shared__ float s_ml[kWaves][2][64];
     __shared__ int64_t s_sum[kWaves];
     __shared__ int32_t s_scan[kWaves];
     __shared__ int s_b;
@@ -310,10 +328,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
         __syncthreads();
         const int64_t seqs = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
         const int64_t total = seqs * p.Hkv;
-        const int parts = parts_of(p, total);
-        if (c >= parts) return;
-        f0 = part_start(total, parts, c);
-        f1 = part_start(total, parts, c + 1);
+        const Cut cut(p, total);
+        if (c >= cut.parts) return;
+        f0 = cut.start(c);
+        f1 = cut.start(c + 1);
         const bool tell = c == 0 && m == 0;  // leaves the sequences' places for the merge
         int64_t carry = 0;
         for (int base = 0; base < p.B; base += kThreads) {
@@ -381,9 +399,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
     while (f < f1) {
         const Tiles tl = tiles_of<TK>(p, p.len[b]);
         const int T = tl.total();
-        const int64_t in_seq = f - before * p.Hkv;
-        const int h = static_cast<int>(in_seq / T);
-        const int t0 = static_cast<int>(in_seq - static_cast<int64_t>(h) * T);
+        const uint32_t in_seq = static_cast<uint32_t>(f - before * p.Hkv);  // below 1024 heads of 2^22 tiles
+        const int h = static_cast<int>(in_seq / static_cast<uint32_t>(T));
+        const int t0 = static_cast<int>(in_seq - static_cast<uint32_t>(h) * T);
         const int t1 = static_cast<int>(min(static_cast<int64_t>(T), t0 + (f1 - f)));
         const bool whole = t0 == 0 && t1 == T;
         int n = p.N;
@@ -401,12 +419,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
 
+        float4 fin[kOut];  // what the wave writes
+#pragma unroll
+        for (int j = 0; j < kOut; ++j) fin[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+
         if (m * RB < rows) {
             const int32_t* const tab = p.table + b * p.table_stride;
-            const uint8_t* const kcb = p.kc + 2 * (h * p.kcs[2]);
-            const uint8_t* const vcb = p.vc + 2 * (h * p.vcs[2]);
-            const uint8_t* const ktb = p.kt + 2 * (b * p.kts[0] + h * p.kts[2]);
-            const uint8_t* const vtb = p.vt + 2 * (b * p.vts[0] + h * p.vts[2]);
+            const uint8_t* const kcb = p.kc + units(h, p.kcs[2]);
+            const uint8_t* const vcb = p.vc + units(h, p.vcs[2]);
+            const uint8_t* const ktb = p.kt + units(b, p.kts[0], h, p.kts[2]);
+            const uint8_t* const vtb = p.vt + units(b, p.vts[0], h, p.vts[2]);
             const int ps_mask = (1 << p.ps_shift) - 1;
             // first row of the group of tile t: a cache row, or a node
             auto first_row = [&](int t) {
@@ -436,13 +458,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
                     const int kc = k_chunk(r);
                     const uint8_t *ka, *va;
                     if (tree) {
-                        ka = ktb + 2 * ((first + r) * p.kts[1]) + 16 * kc;
-                        va = vtb + 2 * ((first + r) * p.vts[1]) + 16 * v_chunk;
+                        ka = ktb + units(first + r, p.kts[1], kc, 1);
+                        va = vtb + units(first + r, p.vts[1], v_chunk, 1);
                     } else {
-                        const int64_t page_of = __shfl(pg, r);
+                        const uint32_t page_of = __shfl(pg, r);
                         const int slot = (first + r) & ps_mask;
-                        ka = kcb + 2 * (page_of * p.kcs[0] + slot * p.kcs[1]) + 16 * kc;
-                        va = vcb + 2 * (page_of * p.vcs[0] + slot * p.vcs[1]) + 16 * v_chunk;
+                        ka = kcb + units(page_of, p.kcs[0], slot, p.kcs[1]) + 16 * kc;
+                        va = vcb + units(page_of, p.vcs[0], slot, p.vcs[1]) + 16 * v_chunk;
                     }
                     ka = ok && kc * 8 < p.D ? ka : zero;
                     va = ok && v_chunk * 8 < p.D ? va : zero;
@@ -462,13 +484,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
             {
                 const bool in = my_row < rows;
                 const int node = in ? my_row / p.G : 0;
-                const int64_t off = b * p.qs[0] + node * p.qs[1] +
-                                    static_cast<int64_t>(h * p.G + (in ? my_row - node * p.G : 0)) * p.qs[2];
+                const uint8_t* const src = p.q + units(b, p.qs[0], node, p.qs[1]) +
+                                           units(h * p.G + (in ? my_row - node * p.G : 0), p.qs[2]);
 #pragma unroll
                 for (int s = 0; s < NQ; ++s) {
                     const int d = s * 16 + hh * 8;
                     v8s z = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (in && d < p.D) z = *reinterpret_cast<const v8s*>(p.q + 2 * (off + d));
+                    if (in && d < p.D) z = *reinterpret_cast<const v8s*>(src + 2 * d);
                     q[s] = p.flip ? z ^ static_cast<short>(0x8000) : z;
                 }
             }
@@ -507,7 +529,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
                     // infinities and NaN among the values: out of the tile, added below
                     bool mine = false;
                     uint8_t* const part = ring + at * kStageB + kVAt + (kShared ? w * kRowsPerWave * kRowB : 0);
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < kLoads; ++i) {
                         v8s* const e = reinterpret_cast<v8s*>(part + i * 1024 + lane * 16);
                         v8s y = *e;
@@ -599,41 +621,38 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
                 }
                 if (nf) {  // rare: infinities or NaN among the values, for the rows that see them
                     if (kShared) __syncthreads();  // the stage has been read
-                    float* const wp = reinterpret_cast<float*>(ring + at * kStageB + (kShared ? w * 4096 : 0));
+                    if (active) {
+                        // the wave's weights, and 32 dimensions of its sums at a time, in LDS
+                        float* const wp = reinterpret_cast<float*>(kSlowB ? slow + w * 8192 : ring + at * kStageB + (kShared ? w * 8192 : 0));
+                        float* const op = wp + 1024;
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        if (active) {
-                            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+                        for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) wp[(8 * (i >> 2) + 4 * hh + (i & 3)) * 32 + col] = x[ks][i];
-                            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-                            for (int r = 0; r < 32; ++r) {
-                                const int key = kb + (sub0 + ks) * 32 + r;
-                                const uint8_t* src;
-                                if (bad[ks] >> r & 1) continue;
-                                if (tree) {
-                                    src = vtb + 2 * (key * p.vts[1]);
-                                } else {
-                                    const int64_t page_of = tab[key >> p.ps_shift];
-                                    src = vcb + 2 * (page_of * p.vcs[0] + (key & ps_mask) * p.vcs[1]);
-                                }
-                                const float wgt = wp[r * 32 + col];
 #pragma unroll
-                                for (int dt = 0; dt < ND; ++dt)
+                            for (int dt = 0; dt < ND; ++dt) {
 #pragma unroll
-                                    for (int g = 0; g < 4; ++g) {
-                                        if (32 * dt + 8 * g < p.D) {
-                                            const uint2 e =
-                                                *reinterpret_cast<const uint2*>(src + 2 * (32 * dt + 8 * g + 4 * hh));
-                                            if (wgt != 0.f && (nonfinite2<DT>(e.x) || nonfinite2<DT>(e.y))) {
-                                                o[dt][4 * g] += nonfinite_term<DT>(wgt, e.x & 0xFFFFu);
-                                                o[dt][4 * g + 1] += nonfinite_term<DT>(wgt, e.x >> 16);
-                                                o[dt][4 * g + 2] += nonfinite_term<DT>(wgt, e.y & 0xFFFFu);
-                                                o[dt][4 * g + 3] += nonfinite_term<DT>(wgt, e.y >> 16);
-                                            }
-                                        }
-                                        asm volatile("" ::: "memory");  // one load at a time: registers stay with the main path
+                                for (int i = 0; i < 16; ++i) op[i * 64 + lane] = o[dt][i];
+                                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+#pragma unroll 1
+                                for (int r = 0; r < 32; ++r) {
+                                    if (bad[ks] >> r & 1) continue;
+                                    const int key = kb + (sub0 + ks) * 32 + r;
+                                    const uint8_t* const src =
+                                        tree ? vtb + units(key, p.vts[1])
+                                             : vcb + units(tab[key >> p.ps_shift], p.vcs[0], key & ps_mask, p.vcs[1]);
+                                    const float wgt = wp[r * 32 + col];
+#pragma unroll 1
+                                    for (int i = 0; i < 16; ++i) {
+                                        const int d = 32 * dt + 8 * (i >> 2) + 4 * hh + (i & 3);
+                                        if (d >= p.D || wgt == 0.f) continue;
+                                        const uint16_t e = *reinterpret_cast<const uint16_t*>(src + 2 * d);
+                                        if (nonfinite2<DT>(e)) op[i * 64 + lane] += wgt * to_float<DT>(e);
                                     }
+                                }
+                                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[dt][i] = op[i * 64 + lane];
                             }
                         }
                     }
@@ -643,70 +662,83 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
             }
             l = half_sum(l);
 
-            // waves that took other keys of the same rows hand their results over
+            // the waves that share rows join their results through LDS, each for a part of
+            // the dimensions: registers j0.. of every lane, four at a time
+            __syncthreads();
+            float* const buf = reinterpret_cast<float*>(smem);
             if constexpr (WK > 1) {
-                float* const buf = reinterpret_cast<float*>(smem);
-#pragma unroll
-                for (int half = WK / 2; half >= 1; half >>= 1) {
-                    const int slot = WR == 2 ? wr : wk % half;
-                    __syncthreads();
-                    if (wk >= half && wk < 2 * half) {
-#pragma unroll
-                        for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                buf[slot * 64 * (DP / 2) + (dt * 16 + i) * 64 + lane] = o[dt][i];
-                        s_ml[slot][0][lane] = mx;
-                        s_ml[slot][1][lane] = l;
-                    }
-                    __syncthreads();
-                    if (wk < half) {
-                        const float m2 = s_ml[slot][0][lane], l2 = s_ml[slot][1][lane];
-                        const float mn = fmaxf(mx, m2);
-                        const float a1 = shift_of(mx, mn), a2 = shift_of(m2, mn);
-                        l = l * a1 + l2 * a2;
-                        mx = mn;
-#pragma unroll
-                        for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[dt][i] = o[dt][i] * a1 + buf[slot * 64 * (DP / 2) + (dt * 16 + i) * 64 + lane] * a2;
-                    }
-                }
-            }
-            __syncthreads();  // the stages are free again
-        }
-
-        if (wk == 0) {
-            if (whole) {
-                if (my_row < p.N * p.G) {
-                    const int node = my_row / p.G;
-                    const float inv = my_row < rows ? 1.f / l : 0.f;  // zeros for an absent node
-                    uint8_t* const dst = p.out + 2 * (b * p.os[0] + node * p.os[1] +
-                                                      static_cast<int64_t>(h * p.G + my_row - node * p.G) * p.os[2]);
-#pragma unroll
-                    for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if (32 * dt + 8 * g < p.D)
-                                *reinterpret_cast<v4s*>(dst + 2 * (32 * dt + 8 * g + 4 * hh)) =
-                                    pack4<DT>(o[dt][4 * g] * inv, o[dt][4 * g + 1] * inv, o[dt][4 * g + 2] * inv,
-                                              o[dt][4 * g + 3] * inv);
-                }
-            } else if (my_row < rows) {
-                float* const rec =
-                    p.part + ((static_cast<int64_t>(c) * 2 + (f == f0 ? 0 : 1)) * p.MT + m) * (RB * (DP + 2));
-                const int r = wr * 32 + col;
 #pragma unroll
                 for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        *reinterpret_cast<float4*>(rec + r * DP + 32 * dt + 8 * g + 4 * hh) =
-                            make_float4(o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]);
-                if (hh == 0) {
-                    rec[RB * DP + r] = mx;
-                    rec[RB * DP + RB + r] = l;
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4*>(buf + (w * (DP / 8) + dt * 4 + i / 4) * 256 + lane * 4) =
+                            make_float4(o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]);
+                s_ml[w][0][lane] = mx;
+                s_ml[w][1][lane] = l;
+                __syncthreads();
+                float mw[WK], lw[WK];
+                float mn = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < WK; ++k) {
+                    mw[k] = s_ml[wr + k * WR][0][lane];
+                    lw[k] = s_ml[wr + k * WR][1][lane];
+                    mn = fmaxf(mn, mw[k]);
                 }
+                mx = mn;
+                l = 0.f;
+#pragma unroll
+                for (int k = 0; k < WK; ++k) {
+                    mw[k] = shift_of(mw[k], mn);
+                    l += mw[k] * lw[k];
+                }
+#pragma unroll
+                for (int j = 0; j < kOut; ++j) {
+                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < WK; ++k) {
+                        const float4 y = *reinterpret_cast<const float4*>(
+                            buf + ((wr + k * WR) * (DP / 8) + wk * kOut + j) * 256 + lane * 4);
+                        s.x += mw[k] * y.x;
+                        s.y += mw[k] * y.y;
+                        s.z += mw[k] * y.z;
+                        s.w += mw[k] * y.w;
+                    }
+                    fin[j] = s;
+                }
+                __syncthreads();  // the stages are free again
+            } else {
+#pragma unroll
+                for (int j = 0; j < kOut; ++j)
+                    fin[j] = make_float4(o[j / 4][4 * (j % 4)], o[j / 4][4 * (j % 4) + 1], o[j / 4][4 * (j % 4) + 2],
+                                         o[j / 4][4 * (j % 4) + 3]);
+            }
+        }
+
+        // group j of the wave's results: dimensions 8 (wk kOut + j) + 4 hh + 0..3
+        if (whole) {
+            if (my_row < p.N * p.G) {
+                const int node = my_row / p.G;
+                const float inv = my_row < rows ? 1.f / l : 0.f;  // zeros for an absent node
+                uint8_t* const dst = p.out + units(b, p.os[0], node, p.os[1]) +
+                                     units(h * p.G + my_row - node * p.G, p.os[2]);
+#pragma unroll
+                for (int j = 0; j < kOut; ++j) {
+                    const int d = 8 * (wk * kOut + j);
+                    if (d < p.D)
+                        *reinterpret_cast<v4s*>(dst + 2 * (d + 4 * hh)) =
+                            pack4<DT>(fin[j].x * inv, fin[j].y * inv, fin[j].z * inv, fin[j].w * inv);
+                }
+            }
+        } else if (my_row < rows) {
+            float* const rec =
+                p.part + ((static_cast<int64_t>(c) * 2 + (f == f0 ? 0 : 1)) * p.MT + m) * (RB * (DP + 2));
+            const int r = wr * 32 + col;
+#pragma unroll
+            for (int j = 0; j < kOut; ++j)
+                *reinterpret_cast<float4*>(rec + r * DP + 8 * (wk * kOut + j) + 4 * hh) = fin[j];
+            if (hh == 0 && wk == 0) {
+                rec[RB * DP + r] = mx;
+                rec[RB * DP + RB + r] = l;
             }
         }
         f += t1 - t0;
@@ -726,9 +758,9 @@ __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
     const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
     const int64_t s0 = p.start[b], T = p.start[b + 1] - s0;
     const int64_t total = p.start[p.B] * p.Hkv;
-    const int parts = parts_of(p, total);
+    const Cut cut(p, total);
     const int64_t first = s0 * p.Hkv + h * T;
-    const int c0 = part_of(total, parts, first), c1 = part_of(total, parts, first + T - 1);
+    const int c0 = cut.of(first), c1 = cut.of(first + T - 1);
     if (c0 == c1) return;
     const int row = blockIdx.y * RPB + threadIdx.x / TPR;
     const int d = (threadIdx.x % TPR) * 4;
@@ -744,7 +776,7 @@ __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
         const int m = row / RB, r = row - m * RB;
         const int64_t rec = RB * (DP + 2);
         // the first part's record is its second one unless the part begins here
-        const int slot0 = part_start(total, parts, c0) == first ? 0 : 1;
+        const int slot0 = cut.start(c0) == first ? 0 : 1;
         auto at = [&](int c) { return p.part + ((static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * p.MT + m) * rec; };
         float mx = -INFINITY;
         for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, at(c)[RB * DP + r]);
@@ -763,8 +795,7 @@ __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
         const float inv = 1.f / l;
         res = pack4<DT>(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     }
-    uint8_t* const dst =
-        p.out + 2 * (b * p.os[0] + node * p.os[1] + static_cast<int64_t>(h * p.G + head) * p.os[2]);
+    uint8_t* const dst = p.out + units(b, p.os[0], node, p.os[1]) + units(h * p.G + head, p.os[2]);
     *reinterpret_cast<v4s*>(dst + 2 * d) = res;
 }
 
