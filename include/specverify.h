@@ -385,7 +385,8 @@ enum { SV_F16 = 2 };  /* a dtype of the attention and the cache */
  * k_cache, v_cache  [pages, page_size, kv_heads, dim]; strides for (page,
  *                slot, head); page_size a power of two, at most 1024.
  *                The last axis of every tensor is contiguous; data and strides
- *                are multiples of 16 bytes; strides are >= 0, below 64 GB.
+ *                are multiples of 16 bytes; strides are >= 0, below 64 GB; those of
+ *                axes of one are not looked at.
  * table          device int32 [B, width], row stride table_stride.  An entry
  *                outside [0, pages) hides its rows.  width * page_size <= 2^28.
  * len            device int32 [B], rows in the cache (clamped to [0, width *
@@ -516,7 +517,7 @@ typedef struct {
  *             range or a table row too short.  Unless 0, nothing is appended
  *             and tables and lengths go out as they came in.
  *
- * dim * element size, strides and data are multiples of 16 bytes; pages <=
+ * dim * element size, strides (of axes longer than one) and data are multiples of 16 bytes; pages <=
  * SPECVERIFY_MAX_PAGES; page_size a power of two, at most 1024; B, layers <=
  * 65534; width * page_size <= 2^28.  workspace: spec_cache_workspace bytes.
  */

@@ -9,6 +9,7 @@ present, the calls raise.
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -355,59 +356,93 @@ def smc_step(target, draft, draft_tokens, logw_in, temperature=1.0, ess_fraction
 # verification from given random numbers, and the cache's commit and fork.
 
 _DTYPES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}
-_I64x3, _I64x4 = ctypes.c_int64 * 3, ctypes.c_int64 * 4
+_I32, _F32 = torch.int32, torch.float32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+# The argument blocks, packed in one go (an attribute of a ctypes structure
+# costs about 0.15 us, and a small call launches in a few): the fields of
+# SvLogits, SvTreeAttention and SvCache in order, padding where they have it.
+_PACK_LOGITS = struct.Struct("@Piiiiqq").pack
+_PACK_ATTENTION = struct.Struct("@iiiiiiP3qPP3q3qPP3q3qiii4xPqPPPfii4xP3qPq").pack
+_PACK_CACHE = struct.Struct("@PPiiiiii4q4qPqPii").pack
+_PACK_STRIDES = struct.Struct("@4q").pack
+_workspaces = {}  # bytes a call needs, by its sizes
+_calls = None
+
+
+def _tree_calls():
+    """The entry points, taking packed argument blocks."""
+    global _calls
+    if _calls is None:
+        lib = load()
+        vp, blob, i32, i64 = ctypes.c_void_p, ctypes.c_char_p, ctypes.c_int32, ctypes.c_int64
+
+        def entry(name, args, res=ctypes.c_int):
+            f = lib[name]
+            f.argtypes, f.restype = args, res
+            return f
+
+        _calls = (lib, entry("spec_tree_attention", [blob, vp]), entry("spec_tree_attention_workspace", [blob], i64),
+                  entry("spec_verify_tree", [blob, blob] + [vp] * 9),
+                  entry("spec_cache_commit", [blob, vp, vp, blob, blob, i32, vp, vp, vp, i64, vp, vp, vp, i64, vp]),
+                  entry("spec_cache_fork", [blob, vp, vp, i64, vp, vp, vp, i64, vp]))
+    return _calls
 
 
 @contextlib.contextmanager
-def _launch(dev, stream):
-    """The stream to launch on, its device current and the stream current, so
-    that what is allocated meanwhile belongs to it."""
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, not on {dev}")
-    if stream is None and (dev.index is None or dev.index == torch.cuda.current_device()):
-        yield torch.cuda.current_stream(dev).cuda_stream
-        return
-    with torch.cuda.device(dev):
+def _on(index, stream):
+    """The tensors' device current, and `stream` (None: the device's current
+    one), so that what is allocated meanwhile belongs to it."""
+    with torch.cuda.device(index):
         if stream is None:
-            yield torch.cuda.current_stream(dev).cuda_stream
+            yield
         else:
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+            if stream.device.index != index:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
             with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+                yield
 
 
-def _ints(t, name, shape, dev, dtype=torch.int32):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {str(dtype).split('.')[-1]} {list(shape)}, not {t.dtype} "
-                         f"{list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _elsewhere(index, stream):
+    """Whether the call has to change the current device or stream first."""
+    if index < 0:
+        raise ValueError("tensors must be on a GPU")
+    return stream is not None or index != torch.cuda.current_device()
+
+
+def _refuse(t, name, shape, dtype, index):
+    kind = str(dtype).split(".")[-1]
+    raise ValueError(f"{name} must be a contiguous {kind} {list(shape)} on device {index}, not {t.dtype} "
+                     f"{list(t.shape)} on device {t.get_device()} with strides {list(t.stride())}")
+
+
+def _array(t, name, shape, index, dtype=_I32):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, index)
     return t.data_ptr()
 
 
-def _table(t, name, B, dev, width=None):
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or (t.shape[1] > 1 and t.stride(1) != 1) or \
-            (width is not None and t.shape[1] != width):
-        raise ValueError(f"{name} must be int32 [{B}, {'width' if width is None else width}], contiguous along its rows")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
-    # a single row's stride may be anything
-    return t.data_ptr(), max(t.shape[1], 1) if B == 1 else t.stride(0)
-
-
-def _rows(t, name, shape, like):
-    """Pointer and strides of a tensor of rows; the stride of an axis of one is
-    of no meaning and may be anything."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if t.dtype != like.dtype:
-        raise ValueError(f"{name} is {t.dtype}, not {like.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if t.stride(-1) != 1 and shape[-1] > 1:
+def _rows(t, name, shape, dtype, index):
+    """Checks a tensor of rows: the last axis contiguous, the others strided.
+    (The library passes over the strides of axes of one.)"""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(t, name, shape, dtype, index)
+    st = t.stride()
+    if st[-1] != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    return t.data_ptr(), [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+    return st
+
+
+def _table(t, name, B, index, width=None):
+    if t.dtype is not _I32 or t.dim() != 2 or t.shape[0] != B or t.get_device() != index or \
+            (width is not None and t.shape[1] != width):
+        _refuse(t, name, (B, "width" if width is None else width), _I32, index)
+    st, n = t.stride(), t.shape[1]
+    if n > 1 and st[1] != 1:
+        raise ValueError(f"{name} must be contiguous along its rows")
+    # a single row's stride may be anything
+    return t.data_ptr(), (n or 1) if B == 1 else st[0]
 
 
 def _no_grad(*tensors):
@@ -429,47 +464,63 @@ def tree_attention(q, k_cache, v_cache, block_table, seq_len, k_tree, v_tree, pa
     0: none; sinks: the first cache rows that stay visible under a window.
     Returns out [B, N, heads, dim]; absent nodes' rows are zero.
     """
-    lib = load()
+    lib, call, size_of = _tree_calls()[:3]
     if q.dim() != 4 or k_cache.dim() != 4:
         raise ValueError("q must be [B, N, heads, dim] and k_cache [pages, page_size, kv_heads, dim]")
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"q: dtype {q.dtype} is not bfloat16 or float16")
+    dt, index = q.dtype, q.get_device()
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError(f"q: dtype {dt} is not bfloat16 or float16")
     _no_grad(q, k_cache, v_cache, k_tree, v_tree)
-    dev = q.device
-    B, N, heads, dim = q.shape
-    pages, page_size, kv_heads, _ = k_cache.shape
-    a = SvTreeAttention()
-    a.dtype, a.B, a.N, a.heads, a.kv_heads, a.dim = _DTYPES[q.dtype], B, N, heads, kv_heads, dim
-    a.pages, a.page_size = pages, page_size
-    a.q, st = _rows(q, "q", (B, N, heads, dim), q)
-    a.q_stride = _I64x3(*st)
-    a.k_tree, st = _rows(k_tree, "k_tree", (B, N, kv_heads, dim), q)
-    a.k_tree_stride = _I64x3(*st)
-    a.v_tree, st = _rows(v_tree, "v_tree", (B, N, kv_heads, dim), q)
-    a.v_tree_stride = _I64x3(*st)
-    a.k_cache, st = _rows(k_cache, "k_cache", (pages, page_size, kv_heads, dim), q)
-    a.k_cache_stride = _I64x3(*st)
-    a.v_cache, st = _rows(v_cache, "v_cache", (pages, page_size, kv_heads, dim), q)
-    a.v_cache_stride = _I64x3(*st)
-    a.table, a.table_stride = _table(block_table, "block_table", B, dev)
-    a.width = block_table.shape[1]
-    a.len = _ints(seq_len, "seq_len", (B,), dev)
-    a.parent = _ints(parent, "parent", (B, N), dev)
-    a.n_nodes = None if n_nodes is None else _ints(n_nodes, "n_nodes", (B,), dev)
-    a.scale = dim ** -0.5 if scale is None else scale
-    a.window, a.sinks = window, sinks
-    with _launch(dev, stream) as sh:
-        if out is None:
-            out = torch.empty((B, N, heads, dim), dtype=q.dtype, device=dev)
-        a.out, st = _rows(out, "out", (B, N, heads, dim), q)
-        a.out_stride = _I64x3(*st)
-        need = lib.spec_tree_attention_workspace(a)
+    shape, kc_shape = q.shape, k_cache.shape
+    B, N, heads, dim = shape
+    pages, page_size, kv_heads, _ = kc_shape
+    t_shape = (B, N, kv_heads, dim)
+    qs = _rows(q, "q", shape, dt, index)
+    kts = _rows(k_tree, "k_tree", t_shape, dt, index)
+    vts = _rows(v_tree, "v_tree", t_shape, dt, index)
+    kcs = _rows(k_cache, "k_cache", (pages, page_size, kv_heads, dim), dt, index)
+    vcs = _rows(v_cache, "v_cache", kc_shape, dt, index)
+    tab, tab_stride = _table(block_table, "block_table", B, index)
+    width = block_table.shape[1]
+    ln = _array(seq_len, "seq_len", (B,), index)
+    par = _array(parent, "parent", (B, N), index)
+    nn = 0 if n_nodes is None else _array(n_nodes, "n_nodes", (B,), index)
+    if out is not None:
+        _rows(out, "out", shape, dt, index)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return tree_attention(q, k_cache, v_cache, block_table, seq_len, k_tree, v_tree, parent, n_nodes,
+                                  scale=scale, window=window, sinks=sinks, out=out)
+    if out is None:
+        out = q.new_empty(shape)
+    os = out.stride()
+
+    def block(ws, need):
+        return _PACK_ATTENTION(_DTYPES[dt], B, N, heads, kv_heads, dim, q.data_ptr(), qs[0], qs[1], qs[2],
+                               k_tree.data_ptr(), v_tree.data_ptr(), kts[0], kts[1], kts[2], vts[0], vts[1], vts[2],
+                               k_cache.data_ptr(), v_cache.data_ptr(), kcs[0], kcs[1], kcs[2], vcs[0], vcs[1], vcs[2],
+                               pages, page_size, width, tab, tab_stride, ln, par, nn,
+                               dim ** -0.5 if scale is None else scale, window, sinks,
+                               out.data_ptr(), os[0], os[1], os[2], ws, need)
+
+    key = (index, B, N, heads, kv_heads, dim, page_size, width, pages)
+    need = _workspaces.get(key)
+    if need is None:
+        need = size_of(block(0, 0))
         _check(lib, need)
-        if need:
-            ws = torch.empty((need,), dtype=torch.uint8, device=dev)
-            a.workspace, a.workspace_bytes = ws.data_ptr(), need
-        _check(lib, lib.spec_tree_attention(a, sh))
+        _workspaces[key] = need
+    ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+    _check(lib, call(block(ws.data_ptr() if need else 0, need), _raw_stream(index)))
     return out
+
+
+def _probs(t, name):
+    if t.dim() != 3 or t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must be [B, P, V], contiguous along V")
+    if t.dtype is not _F32 and t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name}: dtype {t.dtype} is not float32 or bfloat16")
+    (B, P, V), st = t.shape, t.stride()
+    return _PACK_LOGITS(t.data_ptr(), _DTYPES[t.dtype], B, P, V, st[0], st[1])
 
 
 def verify_tree(target_probs, draft_probs, tokens, parent, u_accept, u_final, n_nodes=None, *, out_tokens=None,
@@ -483,62 +534,74 @@ def verify_tree(target_probs, draft_probs, tokens, parent, u_accept, u_final, n_
     float32 in [0, 1).  Returns (tokens [B, N], nodes [B, N], n_accepted [B]),
     int32.
     """
-    lib = load()
-    dev = target_probs.device
-    td = _desc(target_probs, "target_probs")
+    lib, _, _, call = _tree_calls()[:4]
+    td = _probs(target_probs, "target_probs")
+    index = target_probs.get_device()
     dd = None
     if draft_probs is not None:
-        dd = _desc(draft_probs, "draft_probs")
-        if draft_probs.device != dev:
-            raise ValueError(f"draft_probs is on {draft_probs.device}, not on {dev}")
+        dd = _probs(draft_probs, "draft_probs")
+        if draft_probs.get_device() != index:
+            raise ValueError(f"draft_probs is on {draft_probs.device}, not on {target_probs.device}")
     B, N, _ = target_probs.shape
-    ins = (_ints(tokens, "tokens", (B, N), dev), _ints(parent, "parent", (B, N), dev),
-           None if n_nodes is None else _ints(n_nodes, "n_nodes", (B,), dev),
-           _ints(u_accept, "u_accept", (B, N), dev, torch.float32), _ints(u_final, "u_final", (B,), dev, torch.float32))
-    with _launch(dev, stream) as sh:
-        if out_tokens is None:
-            out_tokens = torch.empty((B, N), dtype=torch.int32, device=dev)
-        if out_nodes is None:
-            out_nodes = torch.empty((B, N), dtype=torch.int32, device=dev)
-        if out_n_accepted is None:
-            out_n_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
-        _check(lib, lib.spec_verify_tree(td, dd, *ins, _ints(out_tokens, "out_tokens", (B, N), dev),
-                                         _ints(out_nodes, "out_nodes", (B, N), dev),
-                                         _ints(out_n_accepted, "out_n_accepted", (B,), dev), sh))
+    tok = _array(tokens, "tokens", (B, N), index)
+    par = _array(parent, "parent", (B, N), index)
+    nn = None if n_nodes is None else _array(n_nodes, "n_nodes", (B,), index)
+    ua = _array(u_accept, "u_accept", (B, N), index, _F32)
+    uf = _array(u_final, "u_final", (B,), index, _F32)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return verify_tree(target_probs, draft_probs, tokens, parent, u_accept, u_final, n_nodes,
+                               out_tokens=out_tokens, out_nodes=out_nodes, out_n_accepted=out_n_accepted)
+    if out_tokens is None:
+        out_tokens = tokens.new_empty((B, N))
+    if out_nodes is None:
+        out_nodes = tokens.new_empty((B, N))
+    if out_n_accepted is None:
+        out_n_accepted = tokens.new_empty((B,))
+    _check(lib, call(td, dd, tok, par, nn, ua, uf, _array(out_tokens, "out_tokens", (B, N), index),
+                     _array(out_nodes, "out_nodes", (B, N), index),
+                     _array(out_n_accepted, "out_n_accepted", (B,), index), _raw_stream(index)))
     return out_tokens, out_nodes, out_n_accepted
 
 
-def _cache(k_cache, v_cache, block_table, seq_len):
-    if k_cache.dim() != 5:
-        raise ValueError("k_cache must be [layers, pages, page_size, heads, dim]")
-    if k_cache.dtype not in _DTYPES:
-        raise ValueError(f"k_cache: dtype {k_cache.dtype} is not float32, bfloat16 or float16")
+def _cache(k_cache, v_cache, block_table, seq_len, index):
+    """The packed cache, its batch size and width, its shape."""
+    if k_cache.dim() != 5 or seq_len.dim() != 1:
+        raise ValueError("k_cache must be [layers, pages, page_size, heads, dim] and seq_len [B]")
+    dt, shape = k_cache.dtype, k_cache.shape
+    if dt not in _DTYPES:
+        raise ValueError(f"k_cache: dtype {dt} is not float32, bfloat16 or float16")
     _no_grad(k_cache, v_cache)
-    dev, shape = k_cache.device, tuple(k_cache.shape)
     B = seq_len.shape[0]
-    c = SvCache()
-    c.dtype = _DTYPES[k_cache.dtype]
-    c.layers, c.pages, c.page_size, c.heads, c.dim = shape
-    c.k, st = _rows(k_cache, "k_cache", shape, k_cache)
-    c.k_stride = _I64x4(*st)
-    c.v, st = _rows(v_cache, "v_cache", shape, k_cache)
-    c.v_stride = _I64x4(*st)
-    c.table, c.table_stride = _table(block_table, "block_table", B, dev)
-    c.len = _ints(seq_len, "seq_len", (B,), dev)
-    c.B, c.width = B, block_table.shape[1]
-    return c
+    ks = _rows(k_cache, "k_cache", shape, dt, index)
+    vs = _rows(v_cache, "v_cache", shape, dt, index)
+    tab, tab_stride = _table(block_table, "block_table", B, index)
+    width = block_table.shape[1]
+    blob = _PACK_CACHE(k_cache.data_ptr(), v_cache.data_ptr(), _DTYPES[dt], *shape, ks[0], ks[1], ks[2], ks[3], vs[0],
+                       vs[1], vs[2], vs[3], tab, tab_stride, _array(seq_len, "seq_len", (B,), index), B, width)
+    return blob, B, width, shape
 
 
-def _cache_outs(c, dev, out_table, out_len, out_status):
+def _cache_outs(seq_len, B, width, index, out_table, out_len, out_status):
     if out_table is None:
-        out_table = torch.empty((c.B, c.width), dtype=torch.int32, device=dev)
+        out_table = seq_len.new_empty((B, width))
     if out_len is None:
-        out_len = torch.empty((c.B,), dtype=torch.int32, device=dev)
+        out_len = seq_len.new_empty((B,))
     if out_status is None:
-        out_status = torch.empty((1,), dtype=torch.int32, device=dev)
-    tab, stride = _table(out_table, "out_table", c.B, dev, c.width)
-    return (out_table, out_len, out_status), (tab, stride, _ints(out_len, "out_len", (c.B,), dev),
-                                              _ints(out_status, "out_status", (1,), dev))
+        out_status = seq_len.new_empty((1,))
+    tab, stride = _table(out_table, "out_table", B, index, width)
+    return (out_table, out_len, out_status), (tab, stride, _array(out_len, "out_len", (B,), index),
+                                              _array(out_status, "out_status", (1,), index))
+
+
+def _cache_workspace(lib, like, B, N, page_size):
+    key = (B, N, page_size)
+    need = _workspaces.get(key)
+    if need is None:
+        need = lib.spec_cache_workspace(B, N, page_size)
+        _check(lib, need)
+        _workspaces[key] = need
+    return torch.empty((need,), dtype=torch.uint8, device=like.device), need
 
 
 def cache_commit(k_cache, v_cache, block_table, seq_len, k_tree, v_tree, nodes, n_accepted, *, out_table=None,
@@ -553,25 +616,26 @@ def cache_commit(k_cache, v_cache, block_table, seq_len, k_tree, v_tree, nodes, 
     themselves.  status [1]: 0, the number of pages lacking, or -1 for bad
     indices; unless 0, nothing was appended.
     """
-    lib = load()
-    c = _cache(k_cache, v_cache, block_table, seq_len)
+    lib, _, _, _, call, _ = _tree_calls()
+    index = k_cache.get_device()
+    blob, B, width, shape = _cache(k_cache, v_cache, block_table, seq_len, index)
     _no_grad(k_tree, v_tree)
-    dev = k_cache.device
     if k_tree.dim() != 5:
         raise ValueError("k_tree must be [layers, B, N, heads, dim]")
     N = k_tree.shape[2]
-    want = (c.layers, c.B, N, c.heads, c.dim)
-    kt, kst = _rows(k_tree, "k_tree", want, k_cache)
-    vt, vst = _rows(v_tree, "v_tree", want, k_cache)
-    nd = None if nodes is None else _ints(nodes, "nodes", (c.B, N), dev)
-    na = _ints(n_accepted, "n_accepted", (c.B,), dev)
-    with _launch(dev, stream) as sh:
-        outs, ptrs = _cache_outs(c, dev, out_table, out_len, out_status)
-        need = lib.spec_cache_workspace(c.B, N, c.page_size)
-        _check(lib, need)
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
-        _check(lib, lib.spec_cache_commit(c, kt, vt, _I64x4(*kst), _I64x4(*vst), N, nd, na, *ptrs, ws.data_ptr(), need,
-                                          sh))
+    want = (shape[0], B, N, shape[3], shape[4])
+    kts = _rows(k_tree, "k_tree", want, k_cache.dtype, index)
+    vts = _rows(v_tree, "v_tree", want, k_cache.dtype, index)
+    nd = None if nodes is None else _array(nodes, "nodes", (B, N), index)
+    na = _array(n_accepted, "n_accepted", (B,), index)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return cache_commit(k_cache, v_cache, block_table, seq_len, k_tree, v_tree, nodes, n_accepted,
+                                out_table=out_table, out_len=out_len, out_status=out_status)
+    outs, ptrs = _cache_outs(seq_len, B, width, index, out_table, out_len, out_status)
+    ws, need = _cache_workspace(lib, k_cache, B, N, shape[2])
+    _check(lib, call(blob, k_tree.data_ptr(), v_tree.data_ptr(), _PACK_STRIDES(*kts[:4]), _PACK_STRIDES(*vts[:4]), N,
+                     nd, na, *ptrs, ws.data_ptr(), need, _raw_stream(index)))
     return outs
 
 
@@ -582,16 +646,17 @@ def cache_fork(k_cache, v_cache, block_table, seq_len, ancestor, *, out_table=No
     copied.  ancestor [B] int32, as smc_step returns it; the rest as
     cache_commit, with outputs apart from block_table and seq_len.
     """
-    lib = load()
-    c = _cache(k_cache, v_cache, block_table, seq_len)
-    dev = k_cache.device
-    anc = _ints(ancestor, "ancestor", (c.B,), dev)
-    with _launch(dev, stream) as sh:
-        outs, ptrs = _cache_outs(c, dev, out_table, out_len, out_status)
-        need = lib.spec_cache_workspace(c.B, 0, c.page_size)
-        _check(lib, need)
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
-        _check(lib, lib.spec_cache_fork(c, anc, *ptrs, ws.data_ptr(), need, sh))
+    lib, _, _, _, _, call = _tree_calls()
+    index = k_cache.get_device()
+    blob, B, width, shape = _cache(k_cache, v_cache, block_table, seq_len, index)
+    anc = _array(ancestor, "ancestor", (B,), index)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return cache_fork(k_cache, v_cache, block_table, seq_len, ancestor, out_table=out_table, out_len=out_len,
+                              out_status=out_status)
+    outs, ptrs = _cache_outs(seq_len, B, width, index, out_table, out_len, out_status)
+    ws, need = _cache_workspace(lib, k_cache, B, 0, shape[2])
+    _check(lib, call(blob, anc, *ptrs, ws.data_ptr(), need, _raw_stream(index)))
     return outs
 
 

@@ -576,15 +576,17 @@ static_assert(SPECVERIFY_MAX_NODES == sv::kMaxNodes && SV_F16 == sv::kDTypeF16, 
 
 bool pow2_page(int ps) { return ps >= 1 && ps <= 1024 && (ps & (ps - 1)) == 0; }
 
-// Strides of a tensor whose rows are read 16 bytes at a time; they come out
-// in units of 16 bytes.
+// Strides of a tensor whose rows are read 16 bytes at a time, `size` along its
+// axes; they come out in units of 16 bytes, 0 for an axis of one.
 template <typename I>
-int check_rows(const void* data, const int64_t* stride, int n, int elem, I* out) {
+int check_rows(const void* data, const int64_t* stride, const int32_t* size, int n, int elem, I* out) {
     if (!data) return SV_EINVAL;
     for (int i = 0; i < n; ++i)
-        if (stride[i] < 0) return SV_EINVAL;
+        if (size[i] > 1 && stride[i] < 0) return SV_EINVAL;
     if (misaligned(data, 16)) return SV_EALIGN;
     for (int i = 0; i < n; ++i) {
+        out[i] = 0;
+        if (size[i] == 1) continue;
         if (stride[i] > (1ll << 40) || stride[i] / (16 / elem) > static_cast<int64_t>(std::numeric_limits<I>::max()))
             return SV_ESHAPE;
         if (stride[i] * elem % 16) return SV_EALIGN;
@@ -645,18 +647,21 @@ int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
     std::memset(&p, 0, sizeof(p));
     if (!a->out || !a->len || !a->parent || (a->width > 0 && !a->table)) return SV_EINVAL;
     if (a->table_stride < 0 || a->window < 0 || a->sinks < 0 || !std::isfinite(a->scale)) return SV_EINVAL;
+    const int32_t nodes[3] = {a->B, a->N, a->heads}, tree[3] = {a->B, a->N, a->kv_heads},
+                  cache[3] = {a->pages, a->page_size, a->kv_heads};
     const struct {
         const void* data;
         const int64_t* stride;
+        const int32_t* size;
         uint32_t* out;
-    } rows[] = {{a->q, a->q_stride, p.qs},
-                {a->k_tree, a->k_tree_stride, p.kts},
-                {a->v_tree, a->v_tree_stride, p.vts},
-                {a->k_cache, a->k_cache_stride, p.kcs},
-                {a->v_cache, a->v_cache_stride, p.vcs},
-                {a->out, a->out_stride, p.os}};
+    } rows[] = {{a->q, a->q_stride, nodes, p.qs},
+                {a->k_tree, a->k_tree_stride, tree, p.kts},
+                {a->v_tree, a->v_tree_stride, tree, p.vts},
+                {a->k_cache, a->k_cache_stride, cache, p.kcs},
+                {a->v_cache, a->v_cache_stride, cache, p.vcs},
+                {a->out, a->out_stride, nodes, p.os}};
     for (const auto& r : rows) {
-        rc = check_rows(r.data, r.stride, 3, 2, r.out);
+        rc = check_rows(r.data, r.stride, r.size, 3, 2, r.out);
         if (rc) return rc;
     }
     if (misaligned(a->table, 4) || misaligned(a->len, 4) || misaligned(a->parent, 4) ||
@@ -788,12 +793,13 @@ int cache_impl(const sv_cache* c, const void* kt, const void* vt, const int64_t*
     sv::CacheParams p;
     std::memset(&p, 0, sizeof(p));
     const int64_t unit = 16 / elem;
-    int rc = check_rows(c->k, c->k_stride, 4, elem, p.ks);
-    if (!rc) rc = check_rows(c->v, c->v_stride, 4, elem, p.vs);
+    const int32_t size[4] = {c->layers, c->pages, c->page_size, c->heads}, tree[4] = {c->layers, c->B, N, c->heads};
+    int rc = check_rows(c->k, c->k_stride, size, 4, elem, p.ks);
+    if (!rc) rc = check_rows(c->v, c->v_stride, size, 4, elem, p.vs);
     if (!rc && !fork) {
         if (!kts || !vts) return SV_EINVAL;
-        rc = check_rows(kt, kts, 4, elem, p.kts);
-        if (!rc) rc = check_rows(vt, vts, 4, elem, p.vts);
+        rc = check_rows(kt, kts, tree, 4, elem, p.kts);
+        if (!rc) rc = check_rows(vt, vts, tree, 4, elem, p.vts);
     }
     if (rc) return rc;
     if (ws_bytes < cache_workspace(c->B, fork ? 0 : N, c->page_size)) return SV_ETOOBIG;

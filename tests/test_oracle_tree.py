@@ -179,6 +179,7 @@ def _attn(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=0), -3), (dict(dtype=3), -3),
+    (dict(q_stride=(1 << 41, 512, 64)), -2), (dict(heads=1026), -2),
     (dict(B=0), -2), (dict(B=65537), -2), (dict(N=0), -2), (dict(N=65), -2), (dict(heads=0), -2),
     (dict(kv_heads=0), -2), (dict(heads=7), -2), (dict(dim=0), -2), (dict(dim=12), -2), (dict(dim=136), -2),
     (dict(pages=0), -2), (dict(page_size=0), -2), (dict(page_size=24), -2), (dict(page_size=2048), -2),
@@ -294,6 +295,23 @@ def test_forced_launch_failure(lib, monkeypatch):
     assert _verify(lib) == -4 and _verify(lib, draft=False) == -4
     assert _cache_call(lib) == -4 and _cache_call(lib, fork=True) == -4
     assert lib.spec_tree_attention(_attn(dim=12), None) == -2
+
+
+def test_packed_argument_blocks():
+    """The binding packs what the C structures hold, field by field."""
+    def flat(s):
+        out = []
+        for name, _ in s._fields_:
+            x = getattr(s, name)
+            out += list(x) if hasattr(x, "__len__") else [x or 0]
+        return out
+
+    for pack, cls, n in ((binding._PACK_LOGITS, binding.SvLogits, 7), (binding._PACK_CACHE, binding.SvCache, 21),
+                         (binding._PACK_ATTENTION, binding.SvTreeAttention, 43)):
+        values = list(range(1, n + 1))
+        blob = pack(*values)
+        assert len(blob) == ctypes.sizeof(cls)
+        assert flat(cls.from_buffer_copy(blob)) == values
 
 
 def test_binding_refuses_before_the_library():
