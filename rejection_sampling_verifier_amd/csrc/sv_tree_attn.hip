@@ -751,10 +751,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
 
 // Joins the partial results of the (sequence, key head)s that were divided:
 // o = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over the parts in order.
-// DP / 4 threads per row, four dimensions each.
-template <int DT, int DP, int RB>
+// DP / 4 threads are a team that takes four dimensions each.  With many parts
+// per (sequence, key head), a few rows on many CUs, all teams of a workgroup
+// share one row's parts; else each team has a row of its own.
+template <int DT, int DP, int RB, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
-    constexpr int TPR = DP / 4, RPB = kThreads / TPR;
+    constexpr int TEAM = DP / 4, TEAMS = kThreads / TEAM;
+    constexpr int kFlight = 8;  // parts a thread loads at a time
+    __shared__ float s_m[kWaves], s_l[TEAMS];
+    __shared__ float4 s_o[SPLIT ? kThreads : 1];
+    const int tid = threadIdx.x;
     const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
     const int64_t s0 = p.start[b], T = p.start[b + 1] - s0;
     const int64_t total = p.start[p.B] * p.Hkv;
@@ -762,9 +768,10 @@ __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
     const int64_t first = s0 * p.Hkv + h * T;
     const int c0 = cut.of(first), c1 = cut.of(first + T - 1);
     if (c0 == c1) return;
-    const int row = blockIdx.y * RPB + threadIdx.x / TPR;
-    const int d = (threadIdx.x % TPR) * 4;
-    if (row >= p.N * p.G || d >= p.D) return;
+    const int team = tid / TEAM;
+    const int row = SPLIT ? blockIdx.y : blockIdx.y * TEAMS + team;
+    const int d = (tid % TEAM) * 4;
+    if (row >= p.N * p.G) return;
     int n = p.N;
     if (p.n_nodes) {
         n = p.n_nodes[b];
@@ -778,23 +785,57 @@ __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
         // the first part's record is its second one unless the part begins here
         const int slot0 = cut.start(c0) == first ? 0 : 1;
         auto at = [&](int c) { return p.part + ((static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * p.MT + m) * rec; };
+        constexpr int kStep = SPLIT ? kThreads : TEAM;
         float mx = -INFINITY;
-        for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, at(c)[RB * DP + r]);
+        for (int c = c0 + tid % kStep; c <= c1; c += kStep) mx = fmaxf(mx, at(c)[RB * DP + r]);
+        for (int o = 1; o < (SPLIT ? 64 : TEAM); o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+        if (SPLIT) {
+            if ((tid & 63) == 0) s_m[tid >> 6] = mx;
+            __syncthreads();
+            mx = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+        }
         float l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; ++c) {
-            const float* const q = at(c);
-            const float a = shift_of(q[RB * DP + r], mx);
-            const float4 v = *reinterpret_cast<const float4*>(q + r * DP + d);
-            l += a * q[RB * DP + RB + r];
-            o.x += a * v.x;
-            o.y += a * v.y;
-            o.z += a * v.z;
-            o.w += a * v.w;
+        constexpr int kStride = SPLIT ? TEAMS : 1;
+        for (int c = c0 + (SPLIT ? team : 0); c <= c1; c += kFlight * kStride) {
+            float mc[kFlight], lc[kFlight];
+            float4 v[kFlight];
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+                const float* const q = at(min(c + k * kStride, c1));
+                mc[k] = q[RB * DP + r];
+                lc[k] = q[RB * DP + RB + r];
+                v[k] = *reinterpret_cast<const float4*>(q + r * DP + d);
+            }
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k)
+                if (c + k * kStride <= c1) {
+                    const float a = shift_of(mc[k], mx);
+                    l += a * lc[k];
+                    o.x += a * v[k].x;
+                    o.y += a * v[k].y;
+                    o.z += a * v[k].z;
+                    o.w += a * v[k].w;
+                }
+        }
+        if (SPLIT) {
+            s_o[tid] = o;
+            if (tid % TEAM == 0) s_l[team] = l;
+            __syncthreads();
+            if (team > 0) return;
+            for (int k = 1; k < TEAMS; ++k) {
+                const float4 y = s_o[k * TEAM + tid];
+                l += s_l[k];
+                o.x += y.x;
+                o.y += y.y;
+                o.z += y.z;
+                o.w += y.w;
+            }
         }
         const float inv = 1.f / l;
         res = pack4<DT>(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     }
+    if (d >= p.D || (SPLIT && team > 0)) return;
     uint8_t* const dst = p.out + units(b, p.os[0], node, p.os[1]) + units(h * p.G + head, p.os[2]);
     *reinterpret_cast<v4s*>(dst + 2 * d) = res;
 }
@@ -809,9 +850,14 @@ hipError_t launch_one(const TreeAttnParams& p, hipStream_t st, const LaunchEvent
 
 template <int DT, int DP, int RB>
 hipError_t merge_one(const TreeAttnParams& p, hipStream_t st, const LaunchEvents& ev) {
-    constexpr int RPB = kThreads / (DP / 4);
-    hipExtLaunchKernelGGL((k_tree_merge<DT, DP, RB>), dim3(p.B * p.Hkv, (p.N * p.G + RPB - 1) / RPB), dim3(kThreads), 0,
-                          st, ev.start, ev.stop, 0, p);
+    constexpr int TEAMS = kThreads / (DP / 4);
+    const int tasks = p.B * p.Hkv, rows = p.N * p.G;
+    if (p.clusters > 4 * tasks)
+        hipExtLaunchKernelGGL((k_tree_merge<DT, DP, RB, true>), dim3(tasks, rows), dim3(kThreads), 0, st, ev.start,
+                              ev.stop, 0, p);
+    else
+        hipExtLaunchKernelGGL((k_tree_merge<DT, DP, RB, false>), dim3(tasks, (rows + TEAMS - 1) / TEAMS), dim3(kThreads),
+                              0, st, ev.start, ev.stop, 0, p);
     return hipGetLastError();
 }
 

@@ -35,7 +35,9 @@ namespace {
 
 constexpr int kVThreads = 1024;
 constexpr int kVWaves = kVThreads / 64;
-constexpr int kVUnroll = 4;
+constexpr int kVUnroll = 4;  // blocks of ids a wave has in flight
+
+typedef uint16_t v2u16 __attribute__((ext_vector_type(2)));
 
 template <int DT>
 struct Prob;
@@ -48,6 +50,10 @@ struct Prob<DT_F32> {
     static __device__ __forceinline__ float get(const uint4& v, int j) {
         return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
     }
+    // the largest bit pattern: above `kLargest` something is negative (or -0), infinite or NaN
+    static constexpr uint32_t kLargest = 0x7F7FFFFFu;
+    static __device__ __forceinline__ uint32_t top(uint32_t m, uint32_t x) { return m > x ? m : x; }
+    static __device__ __forceinline__ bool over(uint32_t m) { return m > kLargest; }
 };
 template <>
 struct Prob<DT_BF16> {
@@ -59,6 +65,11 @@ struct Prob<DT_BF16> {
         const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
         return __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
     }
+    static __device__ __forceinline__ uint32_t top(uint32_t m, uint32_t x) {
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(v2u16, m),
+                                                                      __builtin_bit_cast(v2u16, x)));
+    }
+    static __device__ __forceinline__ bool over(uint32_t m) { return (m & 0xFFFFu) > 0x7F7Fu || (m >> 16) > 0x7F7Fu; }
 };
 
 __device__ __forceinline__ bool is_prob(float p) { return p >= 0.f && p <= 3.402823466e38f; }
@@ -82,21 +93,15 @@ struct Residual {
     int gone;  // per lane
     bool any_gone;
 
-    // the weights of this lane's ids [id, id + E), zero past V; ok: all are probabilities
-    __device__ __forceinline__ void weights(int id, int base, const uint4& pv, const uint4& qv, double* w,
-                                            bool& ok) const {
+    // the weights of this lane's ids [id, id + E) of the block at `base`
+    template <bool Q>
+    __device__ __forceinline__ void weights(int id, int base, const uint4& pv, const uint4& qv, double* w) const {
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            const float x = Prob<DT>::get(pv, j);
-            ok = ok && is_prob(x);
-            w[j] = static_cast<double>(x);
-            if (use_q) {
-                const float y = Prob<DT>::get(qv, j);
-                ok = ok && is_prob(y);
-                w[j] = fmax(w[j] - a * static_cast<double>(y), 0.0);
-            }
+            w[j] = static_cast<double>(Prob<DT>::get(pv, j));
+            if (Q) w[j] = fmax(__builtin_fma(-a, static_cast<double>(Prob<DT>::get(qv, j)), w[j]), 0.0);
         }
-        if (any_gone) {
+        if (!Q && any_gone) {
             uint64_t hit = __ballot(gone >= base && gone < base + kBlock);
             while (hit) {
                 const int at = __shfl(gone, __ffsll(static_cast<unsigned long long>(hit)) - 1) - id;
@@ -106,52 +111,75 @@ struct Residual {
             }
         }
     }
-    // rows need not start on 16-byte boundaries
+    // a whole vector; rows need not start on 16-byte boundaries
     __device__ __forceinline__ uint4 vec(const uint8_t* r, int id) const {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (id + E <= V) {
-            __builtin_memcpy(&v, r + static_cast<int64_t>(id) * (16 / E), 16);
-        } else if (id < V) {
-            uint32_t wv[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (id + j < V) {
-                    const uint32_t f = __float_as_uint(Prob<DT>::at(r, id + j));
-                    if (E == 4)
-                        wv[j & 3] = f;
-                    else
-                        wv[j >> 1] |= j & 1 ? f : f >> 16;
-                }
-            v = make_uint4(wv[0], wv[1], wv[2], wv[3]);
-        }
+        uint4 v;
+        __builtin_memcpy(&v, r + static_cast<int64_t>(id) * (16 / E), 16);
         return v;
     }
-    // the sum over ids [lo, hi), lo and hi - lo multiples of kBlock: per wave, the same in every lane
-    __device__ __forceinline__ double sum(int lo, int hi, int lane, bool& ok) const {
-        double acc = 0.0;
+    // the same near the row's end, zeros behind it
+    __device__ __forceinline__ uint4 vec_end(const uint8_t* r, int id) const {
+        if (id + E <= V) return vec(r, id);
+        uint32_t wv[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            if (id + j < V) {
+                const uint32_t f = __float_as_uint(Prob<DT>::at(r, id + j));
+                if (E == 4)
+                    wv[j & 3] = f;
+                else
+                    wv[j >> 1] |= j & 1 ? f : f >> 16;
+            }
+        return make_uint4(wv[0], wv[1], wv[2], wv[3]);
+    }
+    __device__ __forceinline__ uint32_t top_of(uint32_t m, const uint4& v) const {
+        return Prob<DT>::top(Prob<DT>::top(Prob<DT>::top(Prob<DT>::top(m, v.x), v.y), v.z), v.w);
+    }
+    // The sum over ids [lo, hi), lo and hi - lo multiples of kBlock: per wave, the
+    // same in every lane.  ok: all entries are probabilities.
+    template <bool Q>
+    __device__ __forceinline__ double sum_of(int lo, int hi, int lane, bool& ok) const {
+        double acc[2] = {0.0, 0.0};
+        uint32_t m = 0;
         if (hi > V) hi = V;
-        for (int base = lo; base < hi; base += kBlock * kVUnroll) {
+        int base = lo;
+        for (; base + kBlock * kVUnroll <= hi; base += kBlock * kVUnroll) {
             uint4 pv[kVUnroll], qv[kVUnroll];
 #pragma unroll
             for (int k = 0; k < kVUnroll; ++k) {
-                const int id = base + k * kBlock + lane * E;
-                pv[k] = make_uint4(0, 0, 0, 0);
-                qv[k] = make_uint4(0, 0, 0, 0);
-                if (base + k * kBlock < hi) {
-                    pv[k] = vec(p, id);
-                    if (use_q) qv[k] = vec(q, id);
-                }
+                pv[k] = vec(p, base + k * kBlock + lane * E);
+                if (Q) qv[k] = vec(q, base + k * kBlock + lane * E);
             }
 #pragma unroll
             for (int k = 0; k < kVUnroll; ++k) {
-                const int at = base + k * kBlock;
                 double w[E];
-                weights(at + lane * E, at, pv[k], qv[k], w, ok);
+                m = top_of(m, pv[k]);
+                if (Q) m = top_of(m, qv[k]);
+                weights<Q>(base + k * kBlock + lane * E, base + k * kBlock, pv[k], qv[k], w);
 #pragma unroll
-                for (int j = 0; j < E; ++j) acc += w[j];
+                for (int j = 0; j < E; ++j) acc[j & 1] += w[j];
             }
         }
-        return wave_sum(acc);
+        for (; base < hi; base += kBlock) {
+            const int id = base + lane * E;
+            const uint4 pv = vec_end(p, id), qv = Q ? vec_end(q, id) : make_uint4(0, 0, 0, 0);
+            double w[E];
+            m = top_of(m, pv);
+            if (Q) m = top_of(m, qv);
+            weights<Q>(id, base, pv, qv, w);
+#pragma unroll
+            for (int j = 0; j < E; ++j) acc[j & 1] += w[j];
+        }
+        if (__any(Prob<DT>::over(m))) {  // a bad entry, or -0
+            for (int id = lo + lane; id < hi; id += 64) {
+                if (!is_prob(Prob<DT>::at(p, id))) ok = false;
+                if (Q && !is_prob(Prob<DT>::at(q, id))) ok = false;
+            }
+        }
+        return wave_sum(acc[0] + acc[1]);
+    }
+    __device__ __forceinline__ double sum(int lo, int hi, int lane, bool& ok) const {
+        return use_q ? sum_of<true>(lo, hi, lane, ok) : sum_of<false>(lo, hi, lane, ok);
     }
 };
 
@@ -319,10 +347,12 @@ __global__ __launch_bounds__(kVThreads) void k_tree_verify(TreeVerifyParams p) {
                 double cum = 0.0;
                 for (int base = lo; base < hi && found < 0; base += R::kBlock) {
                     const int id = base + lane * E;
-                    const uint4 pv = left.vec(left.p, id);
-                    const uint4 qv = left.use_q ? left.vec(left.q, id) : make_uint4(0, 0, 0, 0);
+                    const uint4 pv = left.vec_end(left.p, id);
                     double wt[E];
-                    left.weights(id, base, pv, qv, wt, ok);
+                    if (left.use_q)
+                        left.template weights<true>(id, base, pv, left.vec_end(left.q, id), wt);
+                    else
+                        left.template weights<false>(id, base, pv, pv, wt);
                     double mass = 0.0;
                     int pos = -1;
 #pragma unroll
