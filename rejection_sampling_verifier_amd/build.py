@@ -31,8 +31,6 @@ def compile_flags():
         "-fPIC",
         "-Wall",
         "-Wno-unused-function",
-        # the tree attention asks for 256 registers where its LDS leaves one workgroup per CU
-        "-Wno-pass-failed",
         # packed fp32 instructions stay off: hipcc forms them by itself otherwise
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         f"-I{os.path.join(ROOT, 'include')}",

@@ -599,7 +599,7 @@ int check_rows(const void* data, const int64_t* stride, const int32_t* size, int
 // query rows that share a key head, parts by the device's size.
 struct TreePlan {
     sv::TreeAttnShape s;
-    int MT = 1, clusters = 1, min_tiles = 1, merge = 0;
+    int MT = 1, clusters = 1, merge = 0;
     size_t start_bytes = 0, total = 0;
 };
 
@@ -627,10 +627,8 @@ int plan_tree(const sv_tree_attention* a, TreePlan& t) {
         t.clusters = static_cast<int>(tasks);
     } else {
         t.merge = 1;
-        t.min_tiles = 2;
         int64_t c = blocks / t.MT;
-        const int64_t need = (tasks * most + t.min_tiles - 1) / t.min_tiles;
-        if (c > need) c = need;
+        if (c > tasks * most) c = tasks * most;
         t.clusters = static_cast<int>(c < 1 ? 1 : c);
         t.start_bytes = align256((static_cast<size_t>(a->B) + 1) * sizeof(int64_t));
         t.total = t.start_bytes +
@@ -700,7 +698,6 @@ int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
     p.flip = a->scale < 0.f ? 1 : 0;
     p.MT = t.MT;
     p.clusters = t.clusters;
-    p.min_tiles = t.min_tiles;
     p.merge = t.merge;
     if (t.merge) {
         p.start = static_cast<int64_t*>(a->workspace);

@@ -39,7 +39,6 @@ struct TreeAttnParams {
     int flip;                              // scale < 0: the queries' signs are flipped
     int MT;                                // row tiles per (sequence, key head)
     int clusters;                          // parts the work is cut into
-    int min_tiles;                         // no part is smaller
     int merge;                             // 0: every (sequence, key head) is one part
     int64_t* start;                        // [B + 1] workspace: first tile of each sequence, over the key heads
     float* part;                           // [clusters, 2, MT, rows, D32 + 2] workspace: partial results

@@ -43,6 +43,10 @@
 
 #include <hip/hip_ext.h>
 
+#include <mutex>
+#include <set>
+#include <utility>
+
 #include "sv_tree.h"
 
 namespace sv {
@@ -117,6 +121,11 @@ __device__ const uint4 kZero = {0, 0, 0, 0};
 
 typedef __attribute__((address_space(1))) const uint32_t global_u32;
 typedef __attribute__((address_space(3))) uint32_t lds_u32;
+
+// 16 bytes per lane from `src` to the 1024 at `dst`, without registers.
+__device__ __forceinline__ void to_lds(const uint8_t* src, uint8_t* dst) {
+    __builtin_amdgcn_global_load_lds((global_u32*)src, (lds_u32*)dst, 16, 0, 0);
+}
 
 // s_waitcnt vmcnt(0) with the other counters left alone (gfx9 encoding: vmcnt
 // in bits 0-3 and 14-15, expcnt 4-6, lgkmcnt 8-11).
@@ -221,8 +230,7 @@ struct Cut {
     int64_t per, extra;
     int parts;
     __device__ __forceinline__ Cut(const TreeAttnParams& p, int64_t total) {
-        const int64_t most = p.min_tiles == 1 ? total : (total + 1) >> 1;
-        parts = most < p.clusters ? static_cast<int>(most) : p.clusters;
+        parts = total < p.clusters ? static_cast<int>(total) : p.clusters;
         if (total >> 32 == 0) {  // a 64-bit division costs about half a microsecond
             per = static_cast<uint32_t>(total) / static_cast<uint32_t>(parts);
         } else {
@@ -286,9 +294,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
     constexpr int kStageB = 2 * GK * kRowB;
     constexpr int kGroups = kShared ? 1 : kWaves;
 
-    __shared__ __align__(16) uint8_t smem[kGroups * 2 * kStageB];
+    // dynamic: with a size it knew, the compiler would give a kernel of one
+    // workgroup per CU accumulation registers, and move the sums in and out of
+    // them in every tile
+    extern __shared__ __align__(16) uint8_t smem[];
     constexpr int kSlowB = kShared && kStageB < 4 * 8192 ? 4 * 8192 : 0;  // where a stage is too small for the slow path
-    __shared__ __align__(16) uint8_t slow[kSlowB ? kSlowB : 16];
+    uint8_t* const slow = smem + kGroups * 2 * kStageB;
     __shared__ int s_nf;
     constexpr int kOut = DP / 8 / WK;         // groups of four dimensions a wave's lane writes
     static_assert(WK == 1 || kWaves * 32 * DP * 4 <= kGroups * 2 * kStageB, "the waves' results fit the stages");
@@ -391,6 +402,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
             v_rd[dt] = ring_at + kVAt + (sub0 * 32 + 4 * hh + vrow) * kRowB + (((4 * dt + low) ^ vx) << 4) +
                        (lane & 1) * 8;
     }
+    // byte offsets of the lane's chunk from the first row of a load, where a wave's rows lie
+    // on one page and are stored in full (strides of a page's rows below 2^32 / 8 bytes)
+    const uint32_t k_lane[2] = {static_cast<uint32_t>(units(lane / NC, p.kcs[1], k_chunk(ld_row), 1)),
+                                static_cast<uint32_t>(units(lane / NC, p.kcs[1], k_chunk(ld_row + kRowsPerLoad), 1))};
+    const uint32_t v_lane = static_cast<uint32_t>(units(lane / NC, p.vcs[1], v_chunk, 1));
+    const bool wave_page = p.D == DP && (1 << p.ps_shift) >= kRowsPerWave && p.kcs[1] < (1u << 25) && p.vcs[1] < (1u << 25);
     const bool win = p.window > 0;
     const float scale2 = p.scale2;
     const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero);
@@ -447,30 +464,46 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
             auto stage = [&](int t, int pg, int at) {
                 const bool tree = t >= tl.cache;
                 const int first = first_row(t);
-                const bool have = tree ? first + (lane & (GK - 1)) < n
-                                       : static_cast<uint32_t>(pg) < static_cast<uint32_t>(p.pages);
-                const uint64_t okm = __ballot(have);
                 uint8_t* const dst = ring + at * kStageB + (kShared ? w * kRowsPerWave * kRowB : 0);
+                if (tree) {
+                    const uint64_t okm = __ballot(first + (lane & (GK - 1)) < n);
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int r = ld_row + i * kRowsPerLoad;
-                    const bool ok = okm >> r & 1;
-                    const int kc = k_chunk(r);
-                    const uint8_t *ka, *va;
-                    if (tree) {
-                        ka = ktb + units(first + r, p.kts[1], kc, 1);
-                        va = vtb + units(first + r, p.vts[1], v_chunk, 1);
-                    } else {
+                    for (int i = 0; i < kLoads; ++i) {
+                        const int r = ld_row + i * kRowsPerLoad, kc = k_chunk(r);
+                        const bool ok = okm >> r & 1;
+                        const uint8_t* const ka = ktb + units(first + r, p.kts[1], kc, 1);
+                        const uint8_t* const va = vtb + units(first + r, p.vts[1], v_chunk, 1);
+                        to_lds(ok && kc * 8 < p.D ? ka : zero, dst + i * 1024);
+                        to_lds(ok && v_chunk * 8 < p.D ? va : zero, dst + kVAt + i * 1024);
+                    }
+                    return okm;
+                }
+                const uint64_t okm = __ballot(static_cast<uint32_t>(pg) < static_cast<uint32_t>(p.pages));
+                if (okm == ~0ull && wave_page) {
+                    // whole rows that all exist, the wave's on one page: scalar addresses
+                    const uint32_t page_of = __builtin_amdgcn_readlane(pg, kShared ? w * kRowsPerWave : 0);
+                    const uint32_t slot = (first + (kShared ? w * kRowsPerWave : 0)) & ps_mask;
+                    const uint8_t* ka = kcb + units(page_of, p.kcs[0], slot, p.kcs[1]);
+                    const uint8_t* va = vcb + units(page_of, p.vcs[0], slot, p.vcs[1]);
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        to_lds(ka + k_lane[i & 1], dst + i * 1024);
+                        to_lds(va + v_lane, dst + kVAt + i * 1024);
+                        ka += units(kRowsPerLoad, p.kcs[1]);
+                        va += units(kRowsPerLoad, p.vcs[1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        const int r = ld_row + i * kRowsPerLoad, kc = k_chunk(r);
+                        const bool ok = okm >> r & 1;
                         const uint32_t page_of = __shfl(pg, r);
                         const int slot = (first + r) & ps_mask;
-                        ka = kcb + units(page_of, p.kcs[0], slot, p.kcs[1]) + 16 * kc;
-                        va = vcb + units(page_of, p.vcs[0], slot, p.vcs[1]) + 16 * v_chunk;
+                        const uint8_t* const ka = kcb + units(page_of, p.kcs[0], slot, p.kcs[1]) + 16 * kc;
+                        const uint8_t* const va = vcb + units(page_of, p.vcs[0], slot, p.vcs[1]) + 16 * v_chunk;
+                        to_lds(ok && kc * 8 < p.D ? ka : zero, dst + i * 1024);
+                        to_lds(ok && v_chunk * 8 < p.D ? va : zero, dst + kVAt + i * 1024);
                     }
-                    ka = ok && kc * 8 < p.D ? ka : zero;
-                    va = ok && v_chunk * 8 < p.D ? va : zero;
-                    __builtin_amdgcn_global_load_lds((global_u32*)ka, (lds_u32*)(dst + i * kRowsPerLoad * kRowB), 16, 0, 0);
-                    __builtin_amdgcn_global_load_lds((global_u32*)va, (lds_u32*)(dst + kVAt + i * kRowsPerLoad * kRowB), 16,
-                                                     0, 0);
                 }
                 return okm;
             };
@@ -802,7 +835,8 @@ __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
             float4 v[kFlight];
 #pragma unroll
             for (int k = 0; k < kFlight; ++k) {
-                const float* const q = at(min(c + k * kStride, c1));
+                if (c + k * kStride > c1) break;
+                const float* const q = at(c + k * kStride);
                 mc[k] = q[RB * DP + r];
                 lc[k] = q[RB * DP + RB + r];
                 v[k] = *reinterpret_cast<const float4*>(q + r * DP + d);
@@ -840,10 +874,35 @@ __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
     *reinterpret_cast<v4s*>(dst + 2 * d) = res;
 }
 
+// Lets a kernel use more than 64 KB of LDS, once per kernel and device.
+hipError_t allow_lds(const void* kernel, int bytes) {
+    static std::mutex mu;
+    static std::set<std::pair<const void*, int>> done;
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    std::lock_guard<std::mutex> lk(mu);
+    if (done.count({kernel, dev})) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done.insert({kernel, dev});
+    return e;
+}
+
+// LDS of k_tree_attn: two stages of 64 rows of K and V, or of 32 for each wave,
+// and the slow path's 32 KB where they are too small for it.
+constexpr int attn_lds(int dp, int wr) {
+    return wr == 1 ? 4 * 2 * 2 * 32 * dp * 2 : 2 * 2 * 64 * dp * 2 + (2 * 64 * dp * 2 < 32768 ? 32768 : 0);
+}
+
 template <int DT, int DP, int WR>
 hipError_t launch_one(const TreeAttnParams& p, hipStream_t st, const LaunchEvents& ev) {
+    constexpr int lds = attn_lds(DP, WR);
+    if (lds > 65536) {
+        const hipError_t e = allow_lds(reinterpret_cast<const void*>(k_tree_attn<DT, DP, WR>), lds);
+        if (e != hipSuccess) return e;
+    }
     const int64_t grid = p.MT == 1 ? p.clusters : static_cast<int64_t>((p.clusters + 7) / 8) * 8 * p.MT;
-    hipExtLaunchKernelGGL((k_tree_attn<DT, DP, WR>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st,
+    hipExtLaunchKernelGGL((k_tree_attn<DT, DP, WR>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, st,
                           ev.start, ev.stop, 0, p);
     return hipGetLastError();
 }
