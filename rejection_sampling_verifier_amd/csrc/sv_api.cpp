@@ -758,10 +758,10 @@ int verify_tree_impl(const sv_logits* tp, const sv_logits* dp, const int32_t* to
                         [&](const sv::LaunchEvents& ev) { return sv::launch_tree_verify(p, dtype, stream, ev); });
 }
 
-// Workspace of a commit or fork: the plan, one word per slot, the new pages.
+// Workspace of a commit or fork: the plan, its own words, the new pages.
 int64_t cache_workspace(int64_t B, int64_t N, int64_t page_size) {
     const int64_t fresh = N > 0 ? (N + page_size - 1) / page_size + 1 : 1;
-    return 4 * B * (sv::kPlanWords + 1 + fresh);
+    return 4 * B * (sv::kPlanWords + sv::kPlanSpare + fresh);
 }
 
 int cache_impl(const sv_cache* c, const void* kt, const void* vt, const int64_t* kts, const int64_t* vts, int32_t N,

@@ -55,43 +55,74 @@ __device__ __forceinline__ int blocks_of(int rows, int ps_shift) {
 
 // The lowest slot that continues `a` (written by atomics, so read past the L1).
 __device__ __forceinline__ int first_of(const int32_t* first, int a) {
-    return __hip_atomic_load(first + a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return a < 0 ? -1 : __hip_atomic_load(first + a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// Per-sequence values of the plan: in LDS for up to as many sequences as the
+// workgroup has threads, else in the workspace (one word each per sequence).
+struct PlanArrays {
+    int32_t *len, *have, *row, *first;
+};
+
+// SMALL: one thread per sequence.  Loads are issued for many sequences or
+// entries at a time; what the kernel costs is a chain of three memory
+// latencies (lengths, tables, writes), about 2 us, and the launch.
+template <bool SMALL>
 __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
     extern __shared__ uint32_t used[];  // W words
     __shared__ int s_wave[kPlanWaves];
     __shared__ int s_bad;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    __shared__ int32_t s_arr[SMALL ? 4 * kPlanThreads : 1];
+    const int tid = threadIdx.x;
     const int W = (p.pages + 31) / 32;
     const int64_t cap = static_cast<int64_t>(p.width) << p.ps_shift;
     int32_t* const plan = p.plan;
-    int32_t* const first = plan + static_cast<int64_t>(p.B) * kPlanWords;  // fork: lowest slot of each ancestor
-    int32_t* const fresh = first + p.B;                                    // the new pages, in order
+    int32_t* const spare = plan + static_cast<int64_t>(p.B) * kPlanWords;
+    int32_t* const fresh = spare + static_cast<int64_t>(p.B) * kPlanSpare;  // the new pages, in order
+    // rows of the tables that count (have entries of row `row`), old lengths, and for a fork the
+    // lowest slot of each ancestor
+    const PlanArrays s = SMALL ? PlanArrays{s_arr, s_arr + kPlanThreads, s_arr + 2 * kPlanThreads,
+                                            s_arr + 3 * kPlanThreads}
+                               : PlanArrays{spare, spare + p.B, spare + 2 * static_cast<int64_t>(p.B),
+                                            spare + 3 * static_cast<int64_t>(p.B)};
+    bool bad = false;
+    // the tables' first entries are on their way while the lengths are looked at
+    constexpr int kAhead = 4;
+    const int64_t entries = static_cast<int64_t>(p.B) * p.width;
+    int32_t ahead[kAhead];
+    uint32_t seq[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int64_t i = tid + static_cast<int64_t>(k) * kPlanThreads;
+        ahead[k] = 0;
+        seq[k] = i < entries ? static_cast<uint32_t>(i) / static_cast<uint32_t>(p.width) : 0;
+        if (i < entries) ahead[k] = p.table[seq[k] * p.table_stride + (i - static_cast<int64_t>(seq[k]) * p.width)];
+    }
+    for (int b = tid; b < p.B; b += kPlanThreads) {
+        s.len[b] = p.len[b];
+        if (p.fork) s.first[b] = 0x7FFFFFFF;
+    }
     for (int i = tid; i < W; i += kPlanThreads) used[i] = 0;
     if (tid == 0) s_bad = 0;
-    if (p.fork)
-        for (int b = tid; b < p.B; b += kPlanThreads) first[b] = 0x7FFFFFFF;
     __syncthreads();
-    bool bad = false;
     if (p.fork) {
         for (int b = tid; b < p.B; b += kPlanThreads) {
             const int a = p.ancestor[b];
             if (a >= p.B || a < -1)
                 bad = true;
             else if (a >= 0)
-                atomicMin(first + a, b);
+                atomicMin(s.first + a, b);
+            s.row[b] = a >= 0 && a < p.B ? a : -1;
         }
         __syncthreads();
     }
-    // lengths, live pages kept, new pages
+    // lengths, pages kept, new pages; of row b of the tables `have[b]` entries are in use
     for (int b = tid; b < p.B; b += kPlanThreads) {
-        const int old = p.len[b];
+        const int old = s.len[b];
         int len = old, want = 0, have = 0;
         if (p.fork) {
-            const int a = p.ancestor[b];
-            const bool in = a >= 0 && a < p.B;
-            len = in ? p.len[a] : 0;
+            const int a = s.row[b];
+            len = a >= 0 ? s.len[a] : 0;
             if (old < 0 || old > cap || len < 0 || len > cap) {
                 bad = true;
                 len = 0;
@@ -99,7 +130,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
             want = blocks_of(len, p.ps_shift);
             have = len >> p.ps_shift;
             // a partly filled last page stays with the lowest slot
-            if (have < want && first_of(first, in ? a : 0) == b) have = want;
+            if (have < want && first_of(s.first, a) == b) have = want;
+            // the whole ancestor counts, if someone continues it
+            const bool go_on = first_of(s.first, b) != 0x7FFFFFFF && old >= 0 && old <= cap;
+            s.have[b] = go_on ? blocks_of(old, p.ps_shift) : 0;
         } else {
             int rows = p.n_accepted[b] + 1;
             if (rows < 0) rows = 0;
@@ -107,11 +141,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
                 bad = true;
                 len = rows = 0;
             }
-            for (int j = 0; j < rows; ++j) {
-                const int node = p.nodes ? p.nodes[static_cast<int64_t>(b) * p.N + j] : j;
-                if (node < 0 || node >= p.N) bad = true;
-            }
             have = blocks_of(len, p.ps_shift);
+            s.have[b] = have;
+            s.row[b] = rows;
             len += rows;
             want = blocks_of(len, p.ps_shift);
         }
@@ -122,21 +154,42 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
         e[3] = want - have;
     }
     __syncthreads();
-    // the pages in use: one wave per sequence, of each ancestor once
-    for (int b = w; b < p.B; b += kPlanWaves) {
-        int have = plan[static_cast<int64_t>(b) * kPlanWords + 2], row = b;
-        if (p.fork) {
-            row = p.ancestor[b];
-            if (row < 0 || row >= p.B) continue;
-            if (first_of(first, row) != b) continue;
+    // the pages in use
+    auto mark = [&](uint32_t b, int64_t j, int pg) {
+        if (j >= s.have[b]) return;
+        if (pg < 0 || pg >= p.pages)
+            bad = true;
+        else
+            atomicOr(&used[pg % W], 1u << (pg / W));
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int64_t i = tid + static_cast<int64_t>(k) * kPlanThreads;
+        if (i < entries) mark(seq[k], i - static_cast<int64_t>(seq[k]) * p.width, ahead[k]);
+    }
+    for (int64_t at = tid + static_cast<int64_t>(kAhead) * kPlanThreads; at < entries;
+         at += static_cast<int64_t>(kAhead) * kPlanThreads) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t i = at + static_cast<int64_t>(k) * kPlanThreads;
+            seq[k] = i >> 32 ? static_cast<uint32_t>(i / p.width)
+                             : static_cast<uint32_t>(i) / static_cast<uint32_t>(p.width);
+            const int64_t j = i - static_cast<int64_t>(seq[k]) * p.width;
+            ahead[k] = i < entries && j < s.have[seq[k]] ? p.table[seq[k] * p.table_stride + j] : 0;
         }
-        const int32_t* const tab = p.table + row * p.table_stride;
-        for (int j = lane; j < have; j += 64) {
-            const int pg = tab[j];
-            if (pg < 0 || pg >= p.pages)
-                bad = true;
-            else
-                atomicOr(&used[pg % W], 1u << (pg / W));
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t i = at + static_cast<int64_t>(k) * kPlanThreads;
+            if (i < entries) mark(seq[k], i - static_cast<int64_t>(seq[k]) * p.width, ahead[k]);
+        }
+    }
+    if (!p.fork && p.nodes) {
+        for (int i = tid; i < p.B * p.N; i += kPlanThreads) {
+            const int b = i / p.N, j = i - b * p.N;
+            if (j < s.row[b]) {
+                const int node = p.nodes[i];
+                if (node < 0 || node >= p.N) bad = true;
+            }
         }
     }
     if (bad) s_bad = 1;
@@ -169,7 +222,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
 __global__ __launch_bounds__(kThreads) void k_cache_copy(CacheParams p) {
     const int b = blockIdx.x, tid = threadIdx.x;
     const int32_t* const e = p.plan + static_cast<int64_t>(b) * kPlanWords;
-    const int32_t* const fresh = p.plan + static_cast<int64_t>(p.B) * (kPlanWords + 1);
+    const int32_t* const fresh = p.plan + static_cast<int64_t>(p.B) * (kPlanWords + kPlanSpare);
     const int old = e[0], len = e[1], have = e[2];
     const bool done = *p.status == 0;
     const int a = p.fork ? p.ancestor[b] : b;
@@ -199,51 +252,90 @@ __global__ __launch_bounds__(kThreads) void k_cache_copy(CacheParams p) {
     const int psm = (1 << p.ps_shift) - 1;
     uint8_t* const kl = p.k + 16 * (layer * p.ks[0]);
     uint8_t* const vl = p.v + 16 * (layer * p.vs[0]);
+    const int per_row = p.heads * p.vec;
+    const int64_t ksr = p.fork ? p.ks[2] : p.kts[2], ksh = p.fork ? p.ks[3] : p.kts[3];
+    const int64_t vsr = p.fork ? p.vs[2] : p.vts[2], vsh = p.fork ? p.vs[3] : p.vts[3];
+    const uint8_t *ksrc, *vsrc;
+    int64_t page_new = 0;
+    int total;
     if (p.fork) {
         const int want = blocks_of(len, p.ps_shift);
         if (have == want) return;  // nothing to copy: empty, full pages only, or the page's keeper
-        const int64_t from = p.table[a * p.table_stride + have], to = fresh[e[3]];
-        const int rows = len & psm;
-        const int total = rows * p.heads * p.vec;
-        for (int i = tid; i < total; i += kThreads) {
-            const int v = i % p.vec, rh = i / p.vec;
-            const int h = rh % p.heads, r = rh / p.heads;
-            const uint4 x = *reinterpret_cast<const uint4*>(kl + 16 * (from * p.ks[1] + r * p.ks[2] + h * p.ks[3] + v));
-            const uint4 y = *reinterpret_cast<const uint4*>(vl + 16 * (from * p.vs[1] + r * p.vs[2] + h * p.vs[3] + v));
-            *reinterpret_cast<uint4*>(kl + 16 * (to * p.ks[1] + r * p.ks[2] + h * p.ks[3] + v)) = x;
-            *reinterpret_cast<uint4*>(vl + 16 * (to * p.vs[1] + r * p.vs[2] + h * p.vs[3] + v)) = y;
-        }
-        return;
+        const int64_t page_old = p.table[a * p.table_stride + have];
+        page_new = fresh[e[3]];
+        total = (len & psm) * per_row;
+        ksrc = kl + 16 * (page_old * p.ks[1]);
+        vsrc = vl + 16 * (page_old * p.vs[1]);
+    } else {
+        total = (len - old) * per_row;
+        ksrc = p.kt + 16 * (layer * p.kts[0] + b * p.kts[1]);
+        vsrc = p.vt + 16 * (layer * p.vts[0] + b * p.vts[1]);
     }
-    const int rows = len - old;
-    const int total = rows * p.heads * p.vec;
-    const uint8_t* const kt = p.kt + 16 * (layer * p.kts[0] + b * p.kts[1]);
-    const uint8_t* const vt = p.vt + 16 * (layer * p.vts[0] + b * p.vts[1]);
     const int32_t* const tab = p.table + b * p.table_stride;
-    for (int i = tid; i < total; i += kThreads) {
-        const int v = i % p.vec, rh = i / p.vec;
-        const int h = rh % p.heads, r = rh / p.heads;
-        const int node = p.nodes ? p.nodes[static_cast<int64_t>(b) * p.N + r] : r;
-        const int at = old + r, blk = at >> p.ps_shift, slot = at & psm;
-        const int64_t page = blk < have ? tab[blk] : fresh[e[3] + blk - have];
-        const uint4 x = *reinterpret_cast<const uint4*>(kt + 16 * (node * p.kts[2] + h * p.kts[3] + v));
-        const uint4 y = *reinterpret_cast<const uint4*>(vt + 16 * (node * p.vts[2] + h * p.vts[3] + v));
-        *reinterpret_cast<uint4*>(kl + 16 * (page * p.ks[1] + slot * p.ks[2] + h * p.ks[3] + v)) = x;
-        *reinterpret_cast<uint4*>(vl + 16 * (page * p.vs[1] + slot * p.vs[2] + h * p.vs[3] + v)) = y;
+    // element i of the rows to move: source row, destination page and slot, head, vector
+    struct Place {
+        int node, slot, h, v;
+        int64_t page;
+    };
+    auto place = [&](int i) __attribute__((always_inline)) {
+        Place q;
+        const int r = i / per_row, hv = i - r * per_row;
+        q.h = hv / p.vec;
+        q.v = hv - q.h * p.vec;
+        if (p.fork) {
+            q.node = q.slot = r;
+            q.page = page_new;
+        } else {
+            q.node = p.nodes ? p.nodes[static_cast<int64_t>(b) * p.N + r] : r;
+            const int at = old + r, blk = at >> p.ps_shift;
+            q.page = blk < have ? tab[blk] : fresh[e[3] + blk - have];
+            q.slot = at & psm;
+        }
+        return q;
+    };
+    auto from = [&](const uint8_t* s, int64_t sr, int64_t sh, const Place& q) __attribute__((always_inline)) {
+        return *reinterpret_cast<const uint4*>(s + 16 * (q.node * sr + q.h * sh + q.v));
+    };
+    auto put = [&](uint8_t* d, const int64_t* s, const Place& q, const uint4& x) __attribute__((always_inline)) {
+        *reinterpret_cast<uint4*>(d + 16 * (q.page * s[1] + q.slot * s[2] + q.h * s[3] + q.v)) = x;
+    };
+    // four loads under way per thread before the first store
+    int i = tid;
+    for (; i + kThreads < total; i += 2 * kThreads) {
+        const Place q0 = place(i), q1 = place(i + kThreads);
+        const uint4 k0 = from(ksrc, ksr, ksh, q0), v0 = from(vsrc, vsr, vsh, q0);
+        const uint4 k1 = from(ksrc, ksr, ksh, q1), v1 = from(vsrc, vsr, vsh, q1);
+        put(kl, p.ks, q0, k0);
+        put(vl, p.vs, q0, v0);
+        put(kl, p.ks, q1, k1);
+        put(vl, p.vs, q1, v1);
+    }
+    if (i < total) {
+        const Place q = place(i);
+        const uint4 k0 = from(ksrc, ksr, ksh, q), v0 = from(vsrc, vsr, vsh, q);
+        put(kl, p.ks, q, k0);
+        put(vl, p.vs, q, v0);
     }
 }
 
 }  // namespace
 
-hipError_t launch_cache_plan(const CacheParams& p, hipStream_t st, const LaunchEvents& ev) {
+namespace {
+template <bool SMALL>
+hipError_t plan_launch(const CacheParams& p, hipStream_t st, const LaunchEvents& ev) {
     const unsigned lds = static_cast<unsigned>((p.pages + 31) / 32) * 4;
     if (lds > (32u << 10)) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_cache_plan),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_cache_plan<SMALL>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
         if (e != hipSuccess) return e;
     }
-    hipExtLaunchKernelGGL(k_cache_plan, dim3(1), dim3(kPlanThreads), lds, st, ev.start, ev.stop, 0, p);
+    hipExtLaunchKernelGGL((k_cache_plan<SMALL>), dim3(1), dim3(kPlanThreads), lds, st, ev.start, ev.stop, 0, p);
     return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_cache_plan(const CacheParams& p, hipStream_t st, const LaunchEvents& ev) {
+    return p.B <= kPlanThreads ? plan_launch<true>(p, st, ev) : plan_launch<false>(p, st, ev);
 }
 
 hipError_t launch_cache_copy(const CacheParams& p, hipStream_t st, const LaunchEvents& ev) {

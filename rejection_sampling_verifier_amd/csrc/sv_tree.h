@@ -85,9 +85,10 @@ struct CacheParams {
     const int32_t* ancestor;            // fork
     int fork;
     // workspace: what the plan decides and the copies carry out
-    int32_t* plan;                // [B, kPlanWords], [B] lowest slots, the new pages
+    int32_t* plan;                // [B, kPlanWords], [kPlanSpare, B], the new pages
 };
 constexpr int kPlanWords = 4;     // old length, new length, pages kept, place of the new pages
+constexpr int kPlanSpare = 4;     // words per sequence the plan itself uses for large batches
 hipError_t launch_cache_plan(const CacheParams& p, hipStream_t st, const LaunchEvents& ev);
 hipError_t launch_cache_copy(const CacheParams& p, hipStream_t st, const LaunchEvents& ev);
 
