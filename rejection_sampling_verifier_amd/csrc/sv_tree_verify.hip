@@ -74,6 +74,14 @@ struct Prob<DT_BF16> {
 
 __device__ __forceinline__ bool is_prob(float p) { return p >= 0.f && p <= 3.402823466e38f; }
 
+// A lane's value, the lane the same for the whole wave.
+__device__ __forceinline__ double of_lane(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(u), lane));
+    const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(u >> 32), lane));
+    return __builtin_bit_cast(double, hi << 32 | lo);
+}
+
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
     for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
@@ -104,7 +112,7 @@ struct Residual {
         if (!Q && any_gone) {
             uint64_t hit = __ballot(gone >= base && gone < base + kBlock);
             while (hit) {
-                const int at = __shfl(gone, __ffsll(static_cast<unsigned long long>(hit)) - 1) - id;
+                const int at = __builtin_amdgcn_readlane(gone, __ffsll(static_cast<unsigned long long>(hit)) - 1) - id;
                 hit &= hit - 1;
 #pragma unroll
                 for (int j = 0; j < E; ++j) w[j] = at == j ? 0.0 : w[j];
@@ -266,8 +274,8 @@ __global__ __launch_bounds__(kVThreads) void k_tree_verify(TreeVerifyParams p) {
             const uint64_t kids = __ballot(lane > tested && par == cur);
             if (!kids) break;
             const int i = __ffsll(static_cast<unsigned long long>(kids)) - 1;
-            const int x = __shfl(tok, i);
-            const double ui = __shfl(u, i), pi = __shfl(px, i), qi = __shfl(qx, i);
+            const int x = __builtin_amdgcn_readlane(tok, i);
+            const double ui = of_lane(u, i), pi = of_lane(px, i), qi = of_lane(qx, i);
             const bool again = !dft && __any((gone >> lane & 1) && tok == x);
             const bool take = dft ? ui * S * qi < pi - a * qi : !again && ui * S < pi;
             tested = i;
