@@ -71,7 +71,9 @@
  * assumes for the float32 kept-mass ratio when it classifies ids before the
  * exact ratio is known: 0 sends every row through the exact second round, a
  * wide band fills the ambiguous groups.  The result is the same either way;
- * only the path (and its time) changes.
+ * only the path (and its time) changes.  SPECVERIFY_VERIFY_LOOKS (0 to 64) is
+ * how often a workgroup of spec_verify_tree looks for another's partial sum
+ * before it computes it itself; the result is the same again.
  */
 #ifndef SPECVERIFY_H
 #define SPECVERIFY_H
@@ -475,11 +477,20 @@ int64_t spec_tree_attention_workspace(const sv_tree_attention* args);
  * its id outside [0, V), its uniform or u_final outside [0, 1), or when a
  * probability at a drafted id, or in a row that is read whole (the last node's
  * row, and rows whose S is needed), is negative, infinite or NaN, or the last
- * row has no positive entry.  Errors as spec_verify.
+ * row has no positive entry.
+ *
+ * workspace      at least spec_verify_tree_workspace bytes, aligned to 8.
+ *
+ * Errors as spec_verify, SV_ETOOBIG for too small a workspace.
  */
 int spec_verify_tree(const sv_logits* target_probs, const sv_logits* draft_probs, const int32_t* tokens,
                      const int32_t* parent, const int32_t* n_nodes, const float* u_accept, const float* u_final,
-                     int32_t* out_tokens, int32_t* out_nodes, int32_t* out_n_accepted, void* stream);
+                     int32_t* out_tokens, int32_t* out_nodes, int32_t* out_n_accepted, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace the call needs, by its sizes and whether it has
+ * draft_probs; 0 for large batches and without them (then NULL will do). */
+int64_t spec_verify_tree_workspace(int32_t B, int32_t N, int32_t V, int32_t dtype, int32_t draft);
 
 /*
  * A paged cache of `layers` layers and the block tables of B sequences.  The
@@ -556,8 +567,8 @@ int spec_verify_abi_version(void);
  * spec_verify_profile_read synchronises those events and writes, for each of
  * the n kernel kinds (0 statistics pass, 1 nucleus selection, 2 row pass:
  * decision and resample, or the SMC particle pass, 3 SMC resampling, 4 the
- * synthetic draft producer, 5 tree attention, 6 its join, 7 tree verification,
- * 8 cache plan, 9 cache copies), the
+ * synthetic draft producer, 5 tree attention, 6 its join, 7 the clearing of tree
+ * verification's workspace, 8 tree verification, 9 cache plan, 10 cache copies), the
  * summed duration in milliseconds and the number of launches since the last
  * read; it returns the number of kinds written.  Host arrays ms[n],
  * launches[n]. */

@@ -21,12 +21,12 @@ MAX_NODES = 64
 PROBE_POS, PROBE_ROW = 8, 4
 STATUS = {0: "SV_OK", -1: "SV_EINVAL", -2: "SV_ESHAPE", -3: "SV_EDTYPE", -4: "SV_EHIP", -5: "SV_ENOMEM",
           -6: "SV_EALIGN", -7: "SV_ECAPTURE", -8: "SV_ETOOBIG"}
-KERNEL_KINDS = ("stats", "topp", "rows", "smc", "produce", "tree_attention", "tree_join", "tree_verify", "cache_plan",
-                "cache_copy")
+KERNEL_KINDS = ("stats", "topp", "rows", "smc", "produce", "tree_attention", "tree_join", "verify_clear",
+                "tree_verify", "cache_plan", "cache_copy")
 
 EXPORTS = ("spec_verify", "spec_verify_noalloc", "spec_verify_probe", "spec_greedy_verify", "spec_hispec_verify", "spec_smc_step",
            "spec_draft_produce",
-           "spec_tree_attention", "spec_tree_attention_workspace", "spec_verify_tree",
+           "spec_tree_attention", "spec_tree_attention_workspace", "spec_verify_tree", "spec_verify_tree_workspace",
            "spec_cache_commit", "spec_cache_fork", "spec_cache_workspace",
            "spec_verify_strerror",
            "spec_verify_release",
@@ -144,8 +144,10 @@ def load(path=LIB_PATH):
     lib.spec_tree_attention.restype = ctypes.c_int
     lib.spec_tree_attention_workspace.argtypes = [P(SvTreeAttention)]
     lib.spec_tree_attention_workspace.restype = ctypes.c_int64
-    lib.spec_verify_tree.argtypes = [P(SvLogits), P(SvLogits)] + [vp] * 9
+    lib.spec_verify_tree.argtypes = [P(SvLogits), P(SvLogits)] + [vp] * 9 + [ctypes.c_int64, vp]
     lib.spec_verify_tree.restype = ctypes.c_int
+    lib.spec_verify_tree_workspace.argtypes = [ctypes.c_int32] * 5
+    lib.spec_verify_tree_workspace.restype = ctypes.c_int64
     i64x4 = ctypes.c_int64 * 4
     lib.spec_cache_commit.argtypes = [P(SvCache), vp, vp, i64x4, i64x4, ctypes.c_int32, vp, vp, vp, ctypes.c_int64, vp,
                                       vp, vp, ctypes.c_int64, vp]
@@ -384,7 +386,7 @@ def _tree_calls():
             return f
 
         _calls = (lib, entry("spec_tree_attention", [blob, vp]), entry("spec_tree_attention_workspace", [blob], i64),
-                  entry("spec_verify_tree", [blob, blob] + [vp] * 9),
+                  entry("spec_verify_tree", [blob, blob] + [vp] * 9 + [i64, vp]),
                   entry("spec_cache_commit", [blob, vp, vp, blob, blob, i32, vp, vp, vp, i64, vp, vp, vp, i64, vp]),
                   entry("spec_cache_fork", [blob, vp, vp, i64, vp, vp, vp, i64, vp]))
     return _calls
@@ -542,7 +544,7 @@ def verify_tree(target_probs, draft_probs, tokens, parent, u_accept, u_final, n_
         dd = _probs(draft_probs, "draft_probs")
         if draft_probs.get_device() != index:
             raise ValueError(f"draft_probs is on {draft_probs.device}, not on {target_probs.device}")
-    B, N, _ = target_probs.shape
+    B, N, V = target_probs.shape
     tok = _array(tokens, "tokens", (B, N), index)
     par = _array(parent, "parent", (B, N), index)
     nn = None if n_nodes is None else _array(n_nodes, "n_nodes", (B,), index)
@@ -558,9 +560,17 @@ def verify_tree(target_probs, draft_probs, tokens, parent, u_accept, u_final, n_
         out_nodes = tokens.new_empty((B, N))
     if out_n_accepted is None:
         out_n_accepted = tokens.new_empty((B,))
+    key = ("verify", index, B, N, V, target_probs.dtype, dd is None)
+    need = _workspaces.get(key)
+    if need is None:
+        need = lib.spec_verify_tree_workspace(B, N, V, _DTYPES[target_probs.dtype], dd is not None)
+        _check(lib, need)
+        _workspaces[key] = need
+    ws = torch.empty((need,), dtype=torch.uint8, device=target_probs.device) if need else None
     _check(lib, call(td, dd, tok, par, nn, ua, uf, _array(out_tokens, "out_tokens", (B, N), index),
                      _array(out_nodes, "out_nodes", (B, N), index),
-                     _array(out_n_accepted, "out_n_accepted", (B,), index), _raw_stream(index)))
+                     _array(out_n_accepted, "out_n_accepted", (B,), index), ws.data_ptr() if need else None, need,
+                     _raw_stream(index)))
     return out_tokens, out_nodes, out_n_accepted
 
 

@@ -712,9 +712,27 @@ int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
                         [&](const sv::LaunchEvents& ev) { return sv::launch_tree_merge(p, t.s, dtype, stream, ev); });
 }
 
+// Workgroups per sequence: as many as give every CU one (each fills it), while
+// a range keeps at least one block of ids (256 float32, 512 bfloat16).  A team
+// pays for the launch that clears its workspace where a sequence makes several
+// passes: one sequence of V = 128256 (float32, trees of two drawn children) 19
+// us with sixteen and 30 with one, 64 of them 37 with four and 63 with one.
+// Without draft probabilities there is one pass (one sequence: 16 and 13 us).
+int verify_team(int B, int V, int dtype, bool draft) {
+    if (!draft) return 1;
+    int team = device_cus() / B;
+    const int most = V / (sv::kVerifyWaves * (dtype == SV_BF16 ? 512 : 256));
+    team = std::min(std::min(team, most), sv::kMaxTeam);
+    return team < 4 ? 1 : team;
+}
+
+int64_t verify_workspace(int64_t B, int64_t N, int team) {
+    return team > 1 ? B * (N + 2) * team * sv::kVerifyWaves * static_cast<int64_t>(sizeof(uint64_t)) : 0;
+}
+
 int verify_tree_impl(const sv_logits* tp, const sv_logits* dp, const int32_t* tokens, const int32_t* parent,
                      const int32_t* n_nodes, const float* u_accept, const float* u_final, int32_t* out_tokens,
-                     int32_t* out_nodes, int32_t* out_n, void* stream_v) {
+                     int32_t* out_nodes, int32_t* out_n, void* ws, int64_t ws_bytes, void* stream_v) {
     int rc = check_logits(tp);
     if (rc) return rc;
     if (dp) {
@@ -730,6 +748,12 @@ int verify_tree_impl(const sv_logits* tp, const sv_logits* dp, const int32_t* to
     const int B = tp->B, N = tp->P, V = tp->V;
     if (B < 1 || B > (1 << 22) || N < 1 || N > SPECVERIFY_MAX_NODES || V < 1 || V > SPECVERIFY_MAX_V) return SV_ESHAPE;
     if (dp && (dp->B != B || dp->V != V || dp->P < 1 || dp->P > N)) return SV_ESHAPE;
+    const int team = verify_team(B, V, tp->dtype, dp != nullptr);
+    if (team > 1) {
+        if (!ws) return SV_EINVAL;
+        if (misaligned(ws, 8)) return SV_EALIGN;
+        if (ws_bytes < verify_workspace(B, N, team)) return SV_ETOOBIG;
+    }
     sv::TreeVerifyParams p;
     std::memset(&p, 0, sizeof(p));
     p.tgt = static_cast<const uint8_t*>(tp->data);
@@ -752,8 +776,18 @@ int verify_tree_impl(const sv_logits* tp, const sv_logits* dp, const int32_t* to
     p.B = B;
     p.N = N;
     p.V = V;
+    p.team = team;
+    p.passes = N + 2;
+    // SPECVERIFY_VERIFY_LOOKS replaces it (tests: with 0 every workgroup sums the rows by itself)
+    p.looks = std::min(std::max(env_int("SPECVERIFY_VERIFY_LOOKS", 16), 0), 64);
+    p.rec = static_cast<uint64_t*>(ws);
     const int dtype = tp->dtype == SV_BF16 ? sv::DT_BF16 : sv::DT_F32;
     const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    if (team > 1) {
+        rc = timed_launch(sv::KK_VERIFY_CLEAR, stream,
+                          [&](const sv::LaunchEvents& ev) { return sv::launch_verify_clear(p, stream, ev); });
+        if (rc) return rc;
+    }
     return timed_launch(sv::KK_TREE_VERIFY, stream,
                         [&](const sv::LaunchEvents& ev) { return sv::launch_tree_verify(p, dtype, stream, ev); });
 }
@@ -895,9 +929,16 @@ int64_t spec_tree_attention_workspace(const sv_tree_attention* args) {
 
 int spec_verify_tree(const sv_logits* target_probs, const sv_logits* draft_probs, const int32_t* tokens,
                      const int32_t* parent, const int32_t* n_nodes, const float* u_accept, const float* u_final,
-                     int32_t* out_tokens, int32_t* out_nodes, int32_t* out_n_accepted, void* stream) {
+                     int32_t* out_tokens, int32_t* out_nodes, int32_t* out_n_accepted, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
     return verify_tree_impl(target_probs, draft_probs, tokens, parent, n_nodes, u_accept, u_final, out_tokens,
-                            out_nodes, out_n_accepted, stream);
+                            out_nodes, out_n_accepted, workspace, workspace_bytes, stream);
+}
+
+int64_t spec_verify_tree_workspace(int32_t B, int32_t N, int32_t V, int32_t dtype, int32_t draft) {
+    if (dtype != SV_F32 && dtype != SV_BF16) return SV_EDTYPE;
+    if (B < 1 || B > (1 << 22) || N < 1 || N > SPECVERIFY_MAX_NODES || V < 1 || V > SPECVERIFY_MAX_V) return SV_ESHAPE;
+    return verify_workspace(B, N, verify_team(B, V, dtype, draft != 0));
 }
 
 int spec_cache_commit(const sv_cache* cache, const void* k_tree, const void* v_tree, const int64_t k_tree_stride[4],

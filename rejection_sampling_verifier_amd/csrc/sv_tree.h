@@ -17,6 +17,7 @@ constexpr int kDTypeF16 = 2;         // after DT_F32 and DT_BF16
 enum TreeKernelKind : int {
     KK_TREE_ATTN = KK_COUNT,
     KK_TREE_MERGE,
+    KK_VERIFY_CLEAR,
     KK_TREE_VERIFY,
     KK_CACHE_PLAN,
     KK_CACHE_COPY,
@@ -67,7 +68,14 @@ struct TreeVerifyParams {
     const float *u_accept, *u_final;           // [B, N], [B]
     int32_t *out_tokens, *out_nodes, *out_n;   // [B, N], [B, N], [B]
     int B, N, P, V;
+    int team;                     // workgroups per sequence
+    int passes;                   // passes over rows a sequence may need: N + 2
+    int looks;                    // times a workgroup looks for another's sum (about a microsecond each)
+    uint64_t* rec;                // [B, passes, team * 16] workspace: the ranges' sums (team > 1)
 };
+constexpr int kMaxTeam = 16;
+constexpr int kVerifyWaves = 16;  // waves of a workgroup, ranges of a row per workgroup
+hipError_t launch_verify_clear(const TreeVerifyParams& p, hipStream_t st, const LaunchEvents& ev);
 hipError_t launch_tree_verify(const TreeVerifyParams& p, int dtype, hipStream_t st, const LaunchEvents& ev);
 
 // ---- cache pages ----

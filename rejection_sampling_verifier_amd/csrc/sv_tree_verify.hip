@@ -18,11 +18,16 @@
 // unless u Z lies within the rounding of the sums (about 1e-15 Z) of a
 // boundary.
 //
-// One workgroup of 16 waves per sequence.  A sequence's passes depend on each
-// other, so a row is not split over workgroups; 64 sequences read about as
-// fast as the whole device can (each CU up to 64 bytes per clock).  Each wave
-// sums a contiguous range of ids, so the pick re-reads 1/16 of the row, then
-// 1/256 of it, then one block of ids.
+// A sequence's passes depend on each other, and one CU reads a row of 128256
+// float32 p and q in about 8 us (64 bytes per clock), so small batches give a
+// sequence a team of workgroups.  All of a team walk alike.  A pass over a row
+// is cut into 16 ranges per workgroup, one per wave; each workgroup sums its
+// ranges, leaves the sums in the workspace, one 64-bit word each, and looks for
+// the others'.  It looks a fixed number of times; what it has not found by then
+// it computes itself, so no workgroup depends on another one running.  Sums of
+// a range are the same whoever computes them, so every workgroup decides alike.
+// The first one draws: it re-reads the range that holds the token, then a
+// sixteenth of it, then blocks of ids.
 
 #include <hip/hip_ext.h>
 
@@ -35,7 +40,7 @@ namespace {
 
 constexpr int kVThreads = 1024;
 constexpr int kVWaves = kVThreads / 64;
-constexpr int kVUnroll = 4;  // blocks of ids a wave has in flight
+static_assert(kVWaves == kVerifyWaves, "ranges per workgroup");
 
 typedef uint16_t v2u16 __attribute__((ext_vector_type(2)));
 
@@ -128,17 +133,18 @@ struct Residual {
     // the same near the row's end, zeros behind it
     __device__ __forceinline__ uint4 vec_end(const uint8_t* r, int id) const {
         if (id + E <= V) return vec(r, id);
-        uint32_t wv[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (id + j < V) {
-                const uint32_t f = __float_as_uint(Prob<DT>::at(r, id + j));
-                if (E == 4)
-                    wv[j & 3] = f;
-                else
-                    wv[j >> 1] |= j & 1 ? f : f >> 16;
-            }
-        return make_uint4(wv[0], wv[1], wv[2], wv[3]);
+        uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+        for (int j = 0; j < E && id + j < V; ++j) {
+            const uint32_t f = __float_as_uint(Prob<DT>::at(r, id + j)) >> (E == 8 ? 16 : 0);
+            const int at = j * (128 / E);
+            if (at < 64)
+                lo |= static_cast<uint64_t>(f) << at;
+            else
+                hi |= static_cast<uint64_t>(f) << (at - 64);
+        }
+        return make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                          static_cast<uint32_t>(hi >> 32));
     }
     __device__ __forceinline__ uint32_t top_of(uint32_t m, const uint4& v) const {
         return Prob<DT>::top(Prob<DT>::top(Prob<DT>::top(Prob<DT>::top(m, v.x), v.y), v.z), v.w);
@@ -147,6 +153,8 @@ struct Residual {
     // same in every lane.  ok: all entries are probabilities.
     template <bool Q>
     __device__ __forceinline__ double sum_of(int lo, int hi, int lane, bool& ok) const {
+        // blocks in flight per wave; the float64 values of more would not fit the registers
+        constexpr int kVUnroll = E == 8 ? 2 : 4;
         double acc[2] = {0.0, 0.0};
         uint32_t m = 0;
         if (hi > V) hi = V;
@@ -166,6 +174,7 @@ struct Residual {
                 weights<Q>(base + k * kBlock + lane * E, base + k * kBlock, pv[k], qv[k], w);
 #pragma unroll
                 for (int j = 0; j < E; ++j) acc[j & 1] += w[j];
+                __builtin_amdgcn_sched_barrier(0);  // one block's float64 values in registers at a time
             }
         }
         for (; base < hi; base += kBlock) {
@@ -191,14 +200,27 @@ struct Residual {
     }
 };
 
-template <int DT>
+// What a wave leaves of a range's sum: the sum, or -1 where an entry of the range
+// is no probability.  All bits set: not there yet.
+constexpr uint64_t kNone = ~0ull;
+__global__ __launch_bounds__(kThreads) void k_verify_clear(uint64_t* p, int64_t n) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (i < n) p[i] = kNone;
+}
+
+// TEAM: several workgroups per sequence.
+template <int DT, bool TEAM>
 __global__ __launch_bounds__(kVThreads) void k_tree_verify(TreeVerifyParams p) {
     using R = Residual<DT>;
     constexpr int E = R::E;
-    __shared__ double s_sum[2][kVWaves];
-    __shared__ int s_ok[2][kVWaves];
-    __shared__ int s_token;
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    __shared__ double s_sum[(TEAM ? kMaxTeam : 1) * kVWaves];
+    __shared__ int s_token, s_missing;
+    // the team of a sequence on one XCD (workgroups go to the eight in turn)
+    const int team = TEAM ? p.team : 1;
+    const int b = TEAM ? (blockIdx.x / (8 * team)) * 8 + (blockIdx.x & 7) : blockIdx.x;
+    const int me = TEAM ? (blockIdx.x % (8 * team)) / 8 : 0;
+    if (b >= p.B) return;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int64_t bn = static_cast<int64_t>(b) * p.N;
     const int n = p.n_nodes ? p.n_nodes[b] : p.N;
     const uint8_t* const tgt = p.tgt + b * p.tsb * (16 / E);
@@ -230,32 +252,68 @@ __global__ __launch_bounds__(kVThreads) void k_tree_verify(TreeVerifyParams p) {
     const float ul = p.u_final[b];
     good = !__any(!good) && ul >= 0.f && ul < 1.f;  // the same in every wave
 
-    int flip = 0;
     R left;
     left.V = p.V;
     left.any_gone = false;
     left.gone = -1;
-    const int range = (((p.V + kVWaves - 1) / kVWaves + R::kBlock - 1) / R::kBlock) * R::kBlock;
-    // the row's sum; per-wave sums stay in s_sum[flip ^ 1]
-    auto total = [&]() {
-        bool ok = true;
-        const double mine = left.sum(w * range, (w + 1) * range, lane, ok);
-        ok = !__any(!ok);
-        if (lane == 0) {
-            s_sum[flip][w] = mine;
-            s_ok[flip][w] = ok;
+    // the row in kVWaves ranges per workgroup of the team, one per wave
+    const int ranges = team * kVWaves;
+    const int range = (((p.V + ranges - 1) / ranges + R::kBlock - 1) / R::kBlock) * R::kBlock;
+    const int per_lane = TEAM ? (ranges + 63) / 64 : 1;
+    int pass = 0;
+    // the sum of what the row has left; the ranges' sums stay in s_sum
+    auto total = [&]() __attribute__((always_inline)) {
+        uint64_t* const rec = p.rec + (static_cast<int64_t>(b) * p.passes + pass) * ranges;
+        ++pass;
+        __syncthreads();  // s_sum's last readers are done
+        if (TEAM && tid == 0) s_missing = 0;
+        int todo = 1 << me;  // whose ranges this workgroup sums: its own, then those it does not find
+        for (bool looked = !TEAM;; looked = true) {
+            while (todo) {
+                const int r = (__ffs(todo) - 1) * kVWaves + w;
+                todo &= todo - 1;
+                bool ok = true;
+                const double x = left.sum(r * range, (r + 1) * range, lane, ok);
+                const double mine = __any(!ok) ? -1.0 : x;
+                if (lane == 0) {
+                    s_sum[r] = mine;
+                    if (!looked)
+                        __hip_atomic_store(rec + r, __builtin_bit_cast(uint64_t, mine), __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+                }
+            }
+            __syncthreads();
+            if (looked) break;
+            // the others' sums, each a whole word that is there or not
+            if (tid < ranges && tid / kVWaves != me) {
+                uint64_t x = kNone;
+                for (int k = 0; k < p.looks && x == kNone; ++k)
+                    x = __hip_atomic_load(rec + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                s_sum[tid] = __builtin_bit_cast(double, x);
+                if (x == kNone) atomicOr(&s_missing, 1 << (tid / kVWaves));
+            }
+            __syncthreads();
+            todo = s_missing;
         }
-        __syncthreads();
         double z = 0.0;
         bool all = true;
+        if (!TEAM) {
 #pragma unroll
-        for (int i = 0; i < kVWaves; ++i) {
-            z += s_sum[flip][i];
-            all = all && s_ok[flip][i];
+            for (int i = 0; i < kVWaves; ++i) {
+                z += s_sum[i];
+                all = all && s_sum[i] >= 0.0;
+            }
+            good = good && all;
+            return z;
         }
-        good = good && all;
-        flip ^= 1;
-        return z;
+        for (int j = 0; j < per_lane; ++j) {
+            const int i = lane * per_lane + j;
+            const double x = i < ranges ? s_sum[i] : 0.0;
+            all = all && x >= 0.0;
+            z += x;
+        }
+        good = good && !__any(!all);
+        return wave_sum(z);
     };
 
     int out_tok = -1, out_node = lane == 0 ? 0 : -1;
@@ -263,95 +321,121 @@ __global__ __launch_bounds__(kVThreads) void k_tree_verify(TreeVerifyParams p) {
     if (good) {
         int cur = 0, tested = 0;
         double a = 0.0, S = 1.0;
-        auto rows = [&]() {
+        uint64_t gone = 0;  // without q: the current node's refused children
+        bool last = false;
+        double z = 0.0;
+        while (good) {
+            const uint64_t kids = last ? 0 : __ballot(lane > tested && par == cur);
+            bool sum = !kids;
+            if (kids) {
+                const int i = __ffsll(static_cast<unsigned long long>(kids)) - 1;
+                const int x = __builtin_amdgcn_readlane(tok, i);
+                const double ui = of_lane(u, i), pi = of_lane(px, i), qi = of_lane(qx, i);
+                const bool again = !dft && __any((gone >> lane & 1) && tok == x);
+                const bool take = dft ? ui * S * qi < pi - a * qi : !again && ui * S < pi;
+                tested = i;
+                if (take) {
+                    if (lane == count) out_tok = x;
+                    ++count;
+                    if (lane == count) out_node = i;
+                    cur = i;
+                    a = 0.0;
+                    S = 1.0;
+                    gone = 0;
+                } else if (dft) {
+                    a = a + S;
+                    sum = (kids & (kids - 1)) != 0;  // a sibling follows
+                } else {
+                    gone |= 1ull << i;
+                    if (!again) S = S - pi;
+                }
+            }
+            if (!sum) continue;
+            // what is left at cur: for the next sibling, or for the last token; where nothing is
+            // left for that (rounding of the rows), the target's row itself
             left.p = tgt + cur * p.tsp * (16 / E);
             left.q = dft ? dft + cur * p.dsp * (16 / E) : nullptr;
             left.a = a;
-            left.use_q = dft && a > 0.0;
-        };
-        uint64_t gone = 0;  // without q: the current node's refused children
-        while (good) {
-            const uint64_t kids = __ballot(lane > tested && par == cur);
-            if (!kids) break;
-            const int i = __ffsll(static_cast<unsigned long long>(kids)) - 1;
-            const int x = __builtin_amdgcn_readlane(tok, i);
-            const double ui = of_lane(u, i), pi = of_lane(px, i), qi = of_lane(qx, i);
-            const bool again = !dft && __any((gone >> lane & 1) && tok == x);
-            const bool take = dft ? ui * S * qi < pi - a * qi : !again && ui * S < pi;
-            tested = i;
-            if (take) {
-                if (lane == count) out_tok = x;
-                ++count;
-                if (lane == count) out_node = i;
-                cur = i;
-                a = 0.0;
-                S = 1.0;
-                gone = 0;
-            } else if (dft) {
-                a = a + S;
-                if (kids & (kids - 1)) {  // a sibling follows
-                    rows();
-                    S = total();
-                }
+            left.use_q = dft && a > 0.0 && !last;
+            left.any_gone = !dft && !last && gone != 0;
+            left.gone = left.any_gone && (gone >> lane & 1) ? tok : -1;
+            const double s = total();
+            if (kids) {
+                S = s;
             } else {
-                gone |= 1ull << i;
-                if (!again) S = S - pi;
+                z = s;
+                if (z > 0.0 || last) break;
+                last = true;
             }
         }
-        // the last token, from what is left at cur
-        double z = 0.0;
-        if (good) {
-            rows();
-            if (!dft) {
-                left.gone = gone >> lane & 1 ? tok : -1;
-                left.any_gone = gone != 0;
-            }
-            z = total();
-            if (good && !(z > 0.0)) {  // nothing left (rounding of the rows): the target's row itself
-                left.use_q = false;
-                left.any_gone = false;
-                left.gone = -1;
-                z = total();
-            }
-            good = good && z > 0.0;
-        }
+        if (me != 0) return;  // one of the team draws
+        good = good && z > 0.0;
         if (good) {
             double t = static_cast<double>(ul) * z;
-            // the wave's range that holds t, then the sixteenth of it; where rounding leaves
-            // none, the last one with weight
-            auto find = [&](const double* sums) {
-                int at = -1, last = 0;
+            // the range that holds t, of sixteen sums; where rounding leaves none, the last one
+            // with weight.  t becomes what is left of it there.
+            auto find16 = [&](const double* sums) {
+                int at = -1, last_one = 0;
                 double cum = 0.0, before = 0.0, before_last = 0.0;
+#pragma unroll
                 for (int i = 0; i < kVWaves; ++i) {
-                    if (at < 0 && sums[i] > 0.0) {
-                        last = i;
+                    const double x = sums[i];
+                    if (at < 0 && x > 0.0) {
+                        last_one = i;
                         before_last = cum;
+                        if (cum + x > t) {
+                            at = i;
+                            before = cum;
+                        }
                     }
-                    if (at < 0 && cum + sums[i] > t) {
-                        at = i;
+                    cum += x;
+                }
+                t -= at < 0 ? before_last : before;
+                return at < 0 ? last_one : at;
+            };
+            // the same of `number` sums, per lane `each` of them
+            auto find = [&](const double* sums, int number, int each) {
+                double mine = 0.0;
+                for (int j = 0; j < each; ++j) {
+                    const int i = lane * each + j;
+                    mine += i < number ? sums[i] : 0.0;
+                }
+                double incl = mine;
+                for (int o = 1; o < 64; o <<= 1) {
+                    const double up = __shfl_up(incl, o);
+                    if (lane >= o) incl += up;
+                }
+                const uint64_t over = __ballot(incl > t && mine > 0.0), some = __ballot(mine > 0.0);
+                const int at = over ? __ffsll(static_cast<unsigned long long>(over)) - 1
+                                    : 63 - __clzll(static_cast<long long>(some));
+                double cum = of_lane(incl - mine, at), before = cum;
+                int found = -1, last_one = -1;
+                for (int j = 0; j < each; ++j) {
+                    const int i = at * each + j;
+                    const double x = i < number ? sums[i] : 0.0;
+                    if (found < 0 && x > 0.0) {
+                        last_one = i;
                         before = cum;
                     }
-                    cum += sums[i];
-                }
-                if (at < 0) {
-                    at = last;
-                    before = before_last;
+                    if (found < 0 && x > 0.0 && cum + x > t) found = i;
+                    cum += x;
                 }
                 t -= before;
-                return at;
+                return found >= 0 ? found : last_one;
             };
-            const int w1 = find(s_sum[flip ^ 1]);
+            const int r1 = TEAM ? find(s_sum, ranges, per_lane) : find16(s_sum);
+            __syncthreads();
             const int part = (((range + kVWaves - 1) / kVWaves + R::kBlock - 1) / R::kBlock) * R::kBlock;
-            const int lo1 = w1 * range;
+            const int lo1 = r1 * range;
             bool ok = true;
             const double mine = left.sum(min(lo1 + w * part, lo1 + range), min(lo1 + (w + 1) * part, lo1 + range), lane,
                                          ok);
-            if (lane == 0) s_sum[flip][w] = mine;
+            if (lane == 0) s_sum[w] = mine;
             __syncthreads();
-            const int w2 = find(s_sum[flip]);
+            const int r2 = find16(s_sum);
             if (w == 0) {
-                const int lo = lo1 + w2 * part, hi = min(min(lo + part, lo1 + range), p.V);
-                int found = -1, last = -1;
+                const int lo = lo1 + r2 * part, hi = min(min(lo + part, lo1 + range), p.V);
+                int found = -1, last_id = -1;
                 double cum = 0.0;
                 for (int base = lo; base < hi && found < 0; base += R::kBlock) {
                     const int id = base + lane * E;
@@ -384,16 +468,16 @@ __global__ __launch_bounds__(kVThreads) void k_tree_verify(TreeVerifyParams p) {
                     const uint64_t have = __ballot(mine_at >= 0);
                     if (have) found = __shfl(mine_at, __ffsll(static_cast<unsigned long long>(have)) - 1);
                     const uint64_t some = __ballot(pos >= 0);
-                    if (some) last = __shfl(pos, 63 - __clzll(static_cast<long long>(some)));
+                    if (some) last_id = __shfl(pos, 63 - __clzll(static_cast<long long>(some)));
                     cum += __shfl(incl, 63);
                 }
-                if (lane == 0) s_token = found >= 0 ? found : last;
+                if (lane == 0) s_token = found >= 0 ? found : last_id;
             }
             __syncthreads();
             if (lane == count) out_tok = s_token;
         }
     }
-    if (w == 0 && lane < p.N) {
+    if (me == 0 && w == 0 && lane < p.N) {
         p.out_tokens[bn + lane] = good ? out_tok : -1;
         p.out_nodes[bn + lane] = good ? out_node : -1;
         if (lane == 0) p.out_n[b] = good ? count : -1;
@@ -402,12 +486,29 @@ __global__ __launch_bounds__(kVThreads) void k_tree_verify(TreeVerifyParams p) {
 
 }  // namespace
 
-hipError_t launch_tree_verify(const TreeVerifyParams& p, int dtype, hipStream_t st, const LaunchEvents& ev) {
-    if (dtype == DT_BF16)
-        hipExtLaunchKernelGGL(k_tree_verify<DT_BF16>, dim3(p.B), dim3(kVThreads), 0, st, ev.start, ev.stop, 0, p);
-    else
-        hipExtLaunchKernelGGL(k_tree_verify<DT_F32>, dim3(p.B), dim3(kVThreads), 0, st, ev.start, ev.stop, 0, p);
+hipError_t launch_verify_clear(const TreeVerifyParams& p, hipStream_t st, const LaunchEvents& ev) {
+    const int64_t n = static_cast<int64_t>(p.B) * p.passes * p.team * kVWaves;
+    hipExtLaunchKernelGGL(k_verify_clear, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                          st, ev.start, ev.stop, 0, p.rec, n);
     return hipGetLastError();
+}
+
+namespace {
+template <bool TEAM>
+hipError_t verify_launch(const TreeVerifyParams& p, int dtype, hipStream_t st, const LaunchEvents& ev) {
+    const unsigned grid = static_cast<unsigned>(TEAM ? (p.B + 7) / 8 * 8 * p.team : p.B);
+    if (dtype == DT_BF16)
+        hipExtLaunchKernelGGL((k_tree_verify<DT_BF16, TEAM>), dim3(grid), dim3(kVThreads), 0, st, ev.start, ev.stop, 0,
+                              p);
+    else
+        hipExtLaunchKernelGGL((k_tree_verify<DT_F32, TEAM>), dim3(grid), dim3(kVThreads), 0, st, ev.start, ev.stop, 0,
+                              p);
+    return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_tree_verify(const TreeVerifyParams& p, int dtype, hipStream_t st, const LaunchEvents& ev) {
+    return p.team > 1 ? verify_launch<true>(p, dtype, st, ev) : verify_launch<false>(p, dtype, st, ev);
 }
 
 }  // namespace sv

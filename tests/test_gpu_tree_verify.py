@@ -181,8 +181,35 @@ def test_largest_vocabulary():
         check(s, f"V=2^21 u={uf}") if uf else call(s)
 
 
+@pytest.mark.parametrize("looks", ["0", "1", "64"])
+def test_teams_do_not_depend_on_each_other(monkeypatch, looks):
+    """However often a workgroup looks for the others' sums (0: it computes
+    every one itself), the result is the same."""
+    for B, V, dtype in ((1, 70001, torch.float32), (9, 50000, torch.bfloat16), (40, 30000, torch.float32)):
+        s = make(B, 10, V, kind="level3", noise=3.0, dtype=dtype, seed=B)
+        assert binding.load().spec_verify_tree_workspace(B, 10, V, 1 if dtype == torch.bfloat16 else 0, 1) > 0
+        want = check(s, f"team B={B} V={V}")
+        monkeypatch.setenv("SPECVERIFY_VERIFY_LOOKS", looks)
+        got = [t.cpu().numpy() for t in call(s)]
+        monkeypatch.delenv("SPECVERIFY_VERIFY_LOOKS")
+        for a, b in zip(got, want):
+            np.testing.assert_array_equal(a, b)
+
+
+def test_two_teams_at_once():
+    a, b = make(1, 8, 60000, seed=1), make(3, 8, 60000, kind="star", noise=4.0, seed=2)
+    want_a, want_b = [[t.clone() for t in call(x)] for x in (a, b)]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        oa, ob = call(a, stream=s1), call(b, stream=s2)
+        s1.synchronize()
+        s2.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(oa, want_a))
+        assert all(torch.equal(x, y) for x, y in zip(ob, want_b))
+
+
 def test_graph_replays_and_streams():
-    s = make(8, 7, 2000, seed=1)
+    s = make(8, 7, 20000, seed=1)
     call(s)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -190,7 +217,7 @@ def test_graph_replays_and_streams():
         outs = call(s)
     stream = torch.cuda.Stream()
     for rep in range(4):
-        n = make(8, 7, 2000, seed=20 + rep)
+        n = make(8, 7, 20000, seed=20 + rep)
         for k in ("p", "q", "tok", "ua", "uf"):
             s[k].copy_(n[k])
         want = call(s)

@@ -208,13 +208,14 @@ def test_attention_workspace(lib):
                                                        page_size=1024)) < 1 << 34
 
 
-def _verify(lib, B=2, N=4, P=3, V=100, dtype=0, ddtype=0, tdata=0x1000, ddata=0x2000, draft=True, ptrs=None, dV=None):
+def _verify(lib, B=2, N=4, P=3, V=100, dtype=0, ddtype=0, tdata=0x1000, ddata=0x2000, draft=True, ptrs=None, dV=None,
+            ws_bytes=1 << 30):
     t = binding.SvLogits(tdata, dtype, B, N, V, N * V, V)
     d = binding.SvLogits(ddata, ddtype, B, P, V if dV is None else dV, P * V, V)
-    names = ("tokens", "parent", "n_nodes", "u_accept", "u_final", "out_tokens", "out_nodes", "out_n")
+    names = ("tokens", "parent", "n_nodes", "u_accept", "u_final", "out_tokens", "out_nodes", "out_n", "ws")
     at = {n: 0x3000 + 0x1000 * i for i, n in enumerate(names)}
     at.update(ptrs or {})
-    return lib.spec_verify_tree(t, d if draft else None, *[at[n] for n in names], None)
+    return lib.spec_verify_tree(t, d if draft else None, *[at[n] for n in names], ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -223,10 +224,19 @@ def _verify(lib, B=2, N=4, P=3, V=100, dtype=0, ddtype=0, tdata=0x1000, ddata=0x
     (dict(ddata=0), -1), (dict(tdata=0x1002), -6), (dict(ptrs=dict(tokens=None)), -1),
     (dict(ptrs=dict(parent=None)), -1), (dict(ptrs=dict(u_accept=None)), -1), (dict(ptrs=dict(u_final=None)), -1),
     (dict(ptrs=dict(out_tokens=None)), -1), (dict(ptrs=dict(out_nodes=None)), -1), (dict(ptrs=dict(out_n=None)), -1),
+    (dict(V=50000, ptrs=dict(ws=None)), -1), (dict(V=50000, ptrs=dict(ws=0xB004)), -6), (dict(V=50000, ws_bytes=64), -8),
     (dict(ptrs=dict(tokens=0x3002)), -6), (dict(ptrs=dict(n_nodes=0x5001)), -6), (dict(ptrs=dict(out_n=0xA002)), -6),
 ])
 def test_verify_host_validation(lib, kw, code):
     assert _verify(lib, **kw) == code
+
+
+def test_verify_workspace(lib):
+    assert lib.spec_verify_tree_workspace(1, 8, 128256, 0, 1) > 0
+    for none in ((300, 8, 128256, 0, 1), (1, 8, 100, 0, 1), (1, 8, 128256, 0, 0)):
+        assert lib.spec_verify_tree_workspace(*none) == 0
+    for bad, code in (((0, 8, 100, 0), -2), ((1, 65, 100, 0), -2), ((1, 8, 0, 0), -2), ((1, 8, 100, 2), -3)):
+        assert lib.spec_verify_tree_workspace(*bad, 1) == code
 
 
 def _cache_call(lib, fork=False, N=4, kts=(4096, 2048, 512, 64), ws_bytes=1 << 20, out_stride=9, **kw):
