@@ -379,7 +379,8 @@ enum { SV_F16 = 2 };  /* a dtype of the attention and the cache */
  * `window` of itself and its ancestors.  window = 0: everything.
  *
  * dtype          SV_BF16 or SV_F16, of all tensors.
- * B, N           1 <= B <= 65536 sequences, 1 <= N <= 64 nodes.
+ * B, N           1 <= B <= 65536 sequences, 1 <= N <= 64 nodes; B * kv_heads *
+ *                (N * heads / kv_heads / 128, rounded up) below 2^24.
  * heads, kv_heads  query and key heads; heads <= 1024, a multiple of kv_heads.
  * dim            a multiple of 8, at most 128.
  * q, out         [B, N, heads, dim]; k_tree, v_tree [B, N, kv_heads, dim];
@@ -402,9 +403,11 @@ enum { SV_F16 = 2 };  /* a dtype of the attention and the cache */
  *                to 16 bytes (may be NULL if that is 0).
  *
  * What a node does not see never reaches its output, whatever it holds (NaN
- * and infinities included).  out must not overlap the inputs.
+ * and infinities included).  out must not overlap the inputs, nor its rows each
+ * other.
  *
- * Errors: SV_EINVAL (NULL, negative stride, scale, window or sinks < 0),
+ * Errors: SV_EINVAL (NULL, negative stride, out with a stride of 0 along an
+ * axis longer than one, scale not finite, window or sinks < 0),
  * SV_ESHAPE, SV_EDTYPE, SV_EALIGN, SV_ETOOBIG (workspace too small), SV_EHIP.
  */
 typedef struct {
@@ -471,6 +474,7 @@ int64_t spec_tree_attention_workspace(const sv_tree_attention* args);
  * out_tokens     device int32 [B, N]: the n accepted ids, the last token, -1.
  * out_nodes      device int32 [B, N]: the path: node 0, the n accepted nodes, -1.
  * out_n_accepted device int32 [B]: n.
+ *                Outputs must not overlap the inputs or each other.  B < 2^22.
  *
  * A sequence is invalid (n = -1 and -1 throughout) when n_nodes lies outside
  * [1, N], a node's parent outside [0, i) (with draft_probs, outside [0, P)),
@@ -530,7 +534,10 @@ typedef struct {
  *
  * dim * element size, strides (of axes longer than one) and data are multiples of 16 bytes; pages <=
  * SPECVERIFY_MAX_PAGES; page_size a power of two, at most 1024; B, layers <=
- * 65534; width * page_size <= 2^28.  workspace: spec_cache_workspace bytes.
+ * 65534; width * page_size <= 2^28; a page, and a sequence's N rows, of one layer
+ * at most 16 GB.  The cache's rows must not overlap each other or the tree's (a stride of
+ * 0 along an axis of the cache longer than one is refused).  workspace:
+ * spec_cache_workspace bytes.
  */
 int spec_cache_commit(const sv_cache* cache, const void* k_tree, const void* v_tree, const int64_t k_tree_stride[4],
                       const int64_t v_tree_stride[4], int32_t N, const int32_t* nodes, const int32_t* n_accepted,

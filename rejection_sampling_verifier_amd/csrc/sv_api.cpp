@@ -572,7 +572,8 @@ int produce_impl(const sv_logits* tl, int32_t K, uint64_t seed, void* out, int64
 
 // ---- the tree round ----
 
-static_assert(SPECVERIFY_MAX_NODES == sv::kMaxNodes && SV_F16 == sv::kDTypeF16, "tree limits");
+static_assert(SPECVERIFY_MAX_NODES == sv::kMaxNodes && SPECVERIFY_MAX_PAGES == sv::kMaxPages &&
+                  SV_F16 == sv::kDTypeF16, "tree limits");
 
 bool pow2_page(int ps) { return ps >= 1 && ps <= 1024 && (ps & (ps - 1)) == 0; }
 
@@ -593,6 +594,15 @@ int check_rows(const void* data, const int64_t* stride, const int32_t* size, int
         out[i] = static_cast<I>(stride[i] / (16 / elem));
     }
     return SV_OK;
+}
+
+// Rows that are written must not fall together (from check_rows' strides): an
+// axis longer than one with stride 0 is an expanded tensor.
+template <typename I>
+bool expanded(const I* stride, const int32_t* size, int n) {
+    for (int i = 0; i < n; ++i)
+        if (size[i] > 1 && stride[i] == 0) return true;
+    return false;
 }
 
 // How the attention's work is cut: rows and keys per workgroup tile by the
@@ -617,7 +627,7 @@ int plan_tree(const sv_tree_attention* a, TreePlan& t) {
     t.s.keys = t.s.rows == 32 ? 128 : 64;
     t.MT = (rows + t.s.rows - 1) / t.s.rows;
     const int64_t tasks = static_cast<int64_t>(a->B) * a->kv_heads;
-    if (tasks > (1ll << 24)) return SV_ESHAPE;
+    if (tasks * t.MT >= 1ll << 24) return SV_ESHAPE;  // a launch has fewer than 2^32 threads
     const int64_t cap = static_cast<int64_t>(a->width) * a->page_size;
     const int64_t most = (cap + t.s.keys - 1) / t.s.keys + 1;  // tiles of one (sequence, key head)
     const int64_t blocks = (t.s.rows == 32 && t.s.dp == 128 ? 1ll : 2ll) * device_cus();  // workgroups that are resident at once
@@ -662,6 +672,7 @@ int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
         rc = check_rows(r.data, r.stride, r.size, 3, 2, r.out);
         if (rc) return rc;
     }
+    if (expanded(p.os, nodes, 3)) return SV_EINVAL;
     if (misaligned(a->table, 4) || misaligned(a->len, 4) || misaligned(a->parent, 4) ||
         (a->n_nodes && misaligned(a->n_nodes, 4)))
         return SV_EALIGN;
@@ -746,7 +757,11 @@ int verify_tree_impl(const sv_logits* tp, const sv_logits* dp, const int32_t* to
         return SV_EALIGN;
     if (dp && dp->dtype != tp->dtype) return SV_EDTYPE;
     const int B = tp->B, N = tp->P, V = tp->V;
-    if (B < 1 || B > (1 << 22) || N < 1 || N > SPECVERIFY_MAX_NODES || V < 1 || V > SPECVERIFY_MAX_V) return SV_ESHAPE;
+    if (B < 1 || B >= 1 << 22 || N < 1 || N > SPECVERIFY_MAX_NODES || V < 1 || V > SPECVERIFY_MAX_V) return SV_ESHAPE;
+    // another workgroup of the team may still read the inputs when the first one writes
+    for (const int32_t* in : {tokens, parent, n_nodes})
+        if (in && (in == out_tokens || in == out_nodes || in == out_n)) return SV_EINVAL;
+    if (out_tokens == out_nodes) return SV_EINVAL;
     if (dp && (dp->B != B || dp->V != V || dp->P < 1 || dp->P > N)) return SV_ESHAPE;
     const int team = verify_team(B, V, tp->dtype, dp != nullptr);
     if (team > 1) {
@@ -810,6 +825,8 @@ int cache_impl(const sv_cache* c, const void* kt, const void* vt, const int64_t*
         c->width < 1 || static_cast<int64_t>(c->width) * c->page_size > (1ll << 28))
         return SV_ESHAPE;
     if (!fork && (N < 1 || N > SPECVERIFY_MAX_NODES)) return SV_ESHAPE;
+    // 16-byte vectors a sequence moves per layer: the copies count them in 32 bits
+    if (static_cast<int64_t>(c->heads) * c->dim * elem / 16 * (fork ? c->page_size : N) > (1ll << 30)) return SV_ESHAPE;
     if (!c->table || !c->len || !out_table || !out_len || !out_status || !ws) return SV_EINVAL;
     if (fork ? !ancestor : !n_accepted) return SV_EINVAL;
     if (c->table_stride < 0 || out_stride < c->width) return SV_EINVAL;
@@ -827,6 +844,7 @@ int cache_impl(const sv_cache* c, const void* kt, const void* vt, const int64_t*
     const int32_t size[4] = {c->layers, c->pages, c->page_size, c->heads}, tree[4] = {c->layers, c->B, N, c->heads};
     int rc = check_rows(c->k, c->k_stride, size, 4, elem, p.ks);
     if (!rc) rc = check_rows(c->v, c->v_stride, size, 4, elem, p.vs);
+    if (!rc && (expanded(p.ks, size, 4) || expanded(p.vs, size, 4))) rc = SV_EINVAL;
     if (!rc && !fork) {
         if (!kts || !vts) return SV_EINVAL;
         rc = check_rows(kt, kts, tree, 4, elem, p.kts);
@@ -937,7 +955,7 @@ int spec_verify_tree(const sv_logits* target_probs, const sv_logits* draft_probs
 
 int64_t spec_verify_tree_workspace(int32_t B, int32_t N, int32_t V, int32_t dtype, int32_t draft) {
     if (dtype != SV_F32 && dtype != SV_BF16) return SV_EDTYPE;
-    if (B < 1 || B > (1 << 22) || N < 1 || N > SPECVERIFY_MAX_NODES || V < 1 || V > SPECVERIFY_MAX_V) return SV_ESHAPE;
+    if (B < 1 || B >= 1 << 22 || N < 1 || N > SPECVERIFY_MAX_NODES || V < 1 || V > SPECVERIFY_MAX_V) return SV_ESHAPE;
     return verify_workspace(B, N, verify_team(B, V, dtype, draft != 0));
 }
 

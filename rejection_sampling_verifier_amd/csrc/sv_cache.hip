@@ -135,8 +135,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
             const bool go_on = first_of(s.first, b) != 0x7FFFFFFF && old >= 0 && old <= cap;
             s.have[b] = go_on ? blocks_of(old, p.ps_shift) : 0;
         } else {
-            int rows = p.n_accepted[b] + 1;
-            if (rows < 0) rows = 0;
+            const int n = p.n_accepted[b];
+            int rows = n < 0 ? 0 : n >= p.N ? p.N + 1 : n + 1;
             if (len < 0 || len > cap || rows > p.N || len + static_cast<int64_t>(rows) > cap) {
                 bad = true;
                 len = rows = 0;
@@ -325,8 +325,9 @@ template <bool SMALL>
 hipError_t plan_launch(const CacheParams& p, hipStream_t st, const LaunchEvents& ev) {
     const unsigned lds = static_cast<unsigned>((p.pages + 31) / 32) * 4;
     if (lds > (32u << 10)) {
+        // always the largest amount: calls of other sizes may run at the same time
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_cache_plan<SMALL>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, kMaxPages / 8);
         if (e != hipSuccess) return e;
     }
     hipExtLaunchKernelGGL((k_cache_plan<SMALL>), dim3(1), dim3(kPlanThreads), lds, st, ev.start, ev.stop, 0, p);

@@ -11,6 +11,7 @@
 namespace sv {
 
 constexpr int kMaxNodes = 64;        // nodes of a tree: one bit each of a 64-bit ancestor set
+constexpr int kMaxPages = 1 << 20;   // of a cache whose tables are changed: one bit each in LDS
 constexpr int kDTypeF16 = 2;         // after DT_F32 and DT_BF16
 
 // Kernel kinds of the timing interface, after the verify step's.
@@ -45,10 +46,10 @@ struct TreeAttnParams {
     float* part;                           // [clusters, 2, MT, rows, D32 + 2] workspace: partial results
 };
 
-// What a workgroup takes at a time, by the N * G query rows that share a key
-// head: up to 32 rows, 128 keys (32 rows per wave, the waves on different
-// keys); up to 64, 128 keys (64 rows per wave); else 128 rows, 64 keys (two
-// waves over rows, two over keys).
+// What a workgroup of four waves takes at a time, by the N * G query rows that
+// share a key head.  A wave always has 32 rows: up to 32 rows, the waves take a
+// quarter of 128 keys each; up to 64, two waves over rows and two over 64 keys;
+// else four waves over 128 rows, all on the same 64 keys.
 struct TreeAttnShape {
     int rows;  // 32, 64 or 128
     int keys;

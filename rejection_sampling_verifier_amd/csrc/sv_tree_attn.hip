@@ -610,7 +610,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
                                 see &= key0 < kMaxNodes ? static_cast<uint32_t>(set >> key0) : 0u;
                             else if (win)
                                 see &= bits_from(low - key0) | ~bits_from(p.sinks - key0);
-                            (void)sub;
                             see >>= 4 * hh;
 #pragma unroll
                             for (int i = 0; i < 16; ++i)

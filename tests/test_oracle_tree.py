@@ -198,6 +198,34 @@ def test_attention_host_validation(lib, kw, code):
     assert lib.spec_tree_attention(_attn(**kw), None) == code
 
 
+@pytest.mark.parametrize("stride", [(0, 512, 64), (4096, 0, 64), (4096, 512, 0)])
+def test_expanded_output_is_refused(lib, stride):
+    """Rows written on top of each other; inputs may be expanded."""
+    assert lib.spec_tree_attention(_attn(out_stride=stride), None) == -1
+    size = dict(zip((0, 1, 2), ("B", "N", "heads")))[stride.index(0)]
+    one = {"B": dict(B=1), "N": dict(N=1), "heads": dict(heads=1, kv_heads=1)}[size]
+    assert lib.spec_tree_attention(_attn(out_stride=stride, workspace_bytes=-1, **one), None) == -8
+    assert lib.spec_tree_attention(_attn(q_stride=stride, workspace_bytes=-1), None) == -8
+
+
+def test_launches_stay_below_the_largest_grid(lib):
+    big = dict(B=65536, N=1, width=4, kv_heads=256, dim=8)
+    assert lib.spec_tree_attention_workspace(_attn(heads=256, **big)) == -2
+    assert lib.spec_tree_attention_workspace(_attn(heads=255, **{**big, "kv_heads": 255})) == 0
+    assert lib.spec_tree_attention_workspace(_attn(**{**big, "N": 64, "heads": 512, "kv_heads": 128})) == -2
+    assert _verify(lib, B=1 << 22) == -2
+    assert lib.spec_verify_tree_workspace(1 << 22, 4, 100, 0, 1) == -2
+    assert lib.spec_verify_tree_workspace((1 << 22) - 1, 4, 100, 0, 1) == 0
+
+
+@pytest.mark.parametrize("out", ["out_tokens", "out_nodes", "out_n"])
+def test_verify_outputs_on_inputs_are_refused(lib, out):
+    """Another workgroup of a team may still read them."""
+    for at in (0x3000, 0x4000, 0x5000):
+        assert _verify(lib, ptrs={out: at}) == -1
+    assert _verify(lib, ptrs=dict(out_tokens=0x9000, out_nodes=0x9000)) == -1
+
+
 def test_attention_workspace(lib):
     assert lib.spec_tree_attention_workspace(_attn()) > 0
     assert lib.spec_tree_attention_workspace(_attn(dim=12)) == -2
@@ -291,6 +319,15 @@ def test_commit_host_validation(lib, kw, code):
 ])
 def test_fork_host_validation(lib, kw, code):
     assert _cache_call(lib, fork=True, **kw) == code
+
+
+@pytest.mark.parametrize("fork", [False, True])
+def test_cache_rows_written_twice_or_uncountable_are_refused(lib, fork):
+    """An expanded cache; more 16-byte vectors per sequence than 32 bits count."""
+    for stride in ((0, 2048, 128, 64), (65536, 0, 128, 64), (65536, 2048, 0, 64), (65536, 2048, 128, 0)):
+        assert _cache_call(lib, fork=fork, k_stride=stride) == -1
+    assert _cache_call(lib, fork=fork, heads=4096, dim=65536, page_size=1024, N=64, ws_bytes=20) == -2
+    assert _cache_call(lib, fork=fork, heads=4096, dim=65536, page_size=32, N=32, ws_bytes=20) == -8
 
 
 def test_cache_workspace(lib):
