@@ -738,6 +738,151 @@ def hispec_bench(args, binding, torch, dev):
 
 
 # ---------------------------------------------------------------------------
+# --tree: a round of a drafted tree over a paged cache
+# ---------------------------------------------------------------------------
+TREE = dict(B=64, N=16, branch=3, layers=2, heads=32, kv_heads=8, dim=128, page=64, length=4096)
+
+
+def _oracle_tree(args):
+    """One sequence: the attention of one key head's queries (times key heads
+    and layers that is the sequence's attention) and the verification."""
+    import numpy as np
+
+    from oracle import tree
+
+    q, k, v, kt, vt, par, p, qd, tok, ua, uf = _SAMPLE[args]
+    # the sequence's rows as one page
+    tree.tree_attention(q[None], k[None, :, None], v[None, :, None], np.zeros((1, 1), np.int32), np.array([len(k)]),
+                        kt[None], vt[None], par[None])
+    tree.verify_tree(p[None], qd[None], tok[None], par[None], ua[None], uf[None])
+    return 1
+
+
+def tree_bench(args, binding, torch, dev):
+    """A step: the attention of every layer, the verification and the commit of
+    the accepted rows (written behind the same lengths each time), and beside
+    it the fork of a set of particles."""
+    import numpy as np
+
+    from rejection_sampling_verifier_amd import workloads
+
+    c = TREE
+    B, N, L, H, Hkv, D, ps, V = (c["B"], c["N"], c["layers"], c["heads"], c["kv_heads"], c["dim"], c["page"],
+                                 workloads.V_LLAMA3)
+    rng = np.random.default_rng(11)
+    gen = torch.Generator(device=dev).manual_seed(11)
+    print(f"[bench] generating the tree round: {B} sequences, {N} nodes, {L} layers", file=sys.stderr, flush=True)
+    lens_h = rng.integers(c["length"] // 2, c["length"] + 1, B).astype(np.int32)
+    blocks = -(-lens_h // ps)
+    width = int(blocks.max()) + 2
+    pages = int(blocks.sum()) + 2 * B
+    perm, at = rng.permutation(pages), 0
+    table_h = np.full((B, width), -1, np.int32)
+    for b in range(B):
+        table_h[b, :blocks[b]] = perm[at:at + blocks[b]]
+        at += blocks[b]
+    par_h = np.full((B, N), -1, np.int32)
+    par_h[:, 1:] = (np.arange(1, N) - 1) // c["branch"]
+    P = int(par_h.max()) + 1
+
+    def rows(*s):
+        return torch.randn(s, generator=gen, device=dev, dtype=torch.float32).to(torch.bfloat16)
+
+    k, v = rows(L, pages, ps, Hkv, D), rows(L, pages, ps, Hkv, D)
+    kt, vt, q = rows(L, B, N, Hkv, D), rows(L, B, N, Hkv, D), rows(L, B, N, H, D)
+    table, lens, par = (torch.from_numpy(a).to(dev) for a in (table_h, lens_h, par_h))
+    logits = torch.randn((B, N, V), generator=gen, device=dev) * 2
+    qd = torch.softmax(logits[:, :P] + 0.7 * torch.randn((B, P, V), generator=gen, device=dev), -1)
+    p = torch.softmax(logits, -1)
+    del logits
+    tok = torch.zeros((B, N), dtype=torch.int32, device=dev)
+    for i in range(1, N):
+        tok[:, i] = torch.multinomial(qd[:, int(par_h[0, i])], 1, generator=gen)[:, 0].int()
+    ua = torch.from_numpy(rng.random((B, N), np.float32)).to(dev)
+    uf = torch.from_numpy(rng.random(B, np.float32)).to(dev)
+    anc = torch.from_numpy((np.arange(B) // 2 * 2).astype(np.int32)).to(dev)
+    outs = [torch.empty_like(q[i]) for i in range(L)]
+    stream = torch.cuda.current_stream(dev)
+    last = {}
+
+    def step(i):
+        for j in range(L):
+            binding.tree_attention(q[j], k[j], v[j], table, lens, kt[j], vt[j], par, out=outs[j])
+        _, nodes, last["n"] = binding.verify_tree(p, qd, tok, par, ua, uf)
+        last["status"] = binding.cache_commit(k, v, table, lens, kt, vt, nodes, last["n"])[2]
+
+    def fork(i):
+        last["status"] = binding.cache_fork(k, v, table, lens, anc)[2]
+
+    def timed(fn):
+        for i in range(args.warmup):
+            fn(i)
+        torch.cuda.synchronize()
+        assert int(last["status"]) == 0
+        e0, e1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        e0.record(stream)
+        for i in range(args.steps):
+            fn(i)
+        e1.record(stream)
+        torch.cuda.synchronize()
+        ms = e0.elapsed_time(e1) / args.steps
+        binding.profile_read()
+        binding.profile_enable(True)
+        for i in range(args.steps):
+            fn(i)
+        torch.cuda.synchronize()
+        binding.profile_enable(False)
+        return ms, {kind: round(x[0] / x[1] * 1e3, 3) for kind, x in binding.profile_read().items() if x[1]}
+
+    ms_step, us = timed(step)
+    fork_ms, fork_us = timed(fork)
+    n = last["n"].cpu().numpy()
+    kv_bytes = 2 * int(lens_h.sum()) * Hkv * D * 2
+    print(f"[bench] tree round {args.steps} steps: {ms_step * 1e3:.2f} us/step, fork {fork_ms * 1e3:.2f} us; kernels {us}",
+          file=sys.stderr, flush=True)
+    dist = per_call_distribution(torch, stream, step, args.steps)
+    cpu = None
+    if not args.no_cpu_baseline:
+        global _SAMPLE
+        h = lambda t: t.double().cpu().numpy()  # noqa: E731
+        _SAMPLE = []
+        for b in range(8):
+            pg = torch.from_numpy(table_h[b, :blocks[b]].astype(np.int64)).to(dev)
+            kk, vv = (h(x[0, pg, :, 0].reshape(-1, D)[:lens_h[b]]) for x in (k, v))
+            _SAMPLE.append((h(q[0, b, :, :H // Hkv]), kk, vv, h(kt[0, b, :, :1]), h(vt[0, b, :, :1]), par_h[b], h(p[b]),
+                            h(qd[b]), tok[b].cpu().numpy(), ua[b].cpu().numpy(), uf[b:b + 1].cpu().numpy()[0]))
+        cores = max(1, min(8, os.cpu_count() or 1))
+        done, dt, passes = _timed_passes(_oracle_tree, list(range(8)), cores)
+        cpu = {"value": done * N / dt, "unit": "nodes/s", "cores": cores, "kind": "oracle",
+               "sample": f"8 sequences of the tree round, one key head of one layer and the verification each, {passes} "
+                         f"passes, float64 NumPy oracle over {cores} processes, {dt:.1f} s wall"}
+    line = {
+        "metric": "tree round: nodes attended and verified/sec + cache HBM GB/s (% of peak) at B=64,N=16,V=128256",
+        "value": round(B * N / (ms_step / 1e3), 1),
+        "unit": "nodes/s",
+        "n_gpus": 1,
+        "steps": args.steps,
+        "warmup": args.warmup,
+        "ms_per_step": round(ms_step, 6),
+        "higher_is_better": True,
+        "scaling": "weak",
+        "vs_baseline": None,
+        "dtype": "bf16 attention, f64 verification",
+        "data": "synthetic",
+        "config": {"workload": f"tree round B={B} N={N} (branches of {c['branch']}) {L} layers {H}/{Hkv} heads of {D}, "
+                               f"{int(lens_h.min())}..{int(lens_h.max())} cached rows, V={V} fp32 probabilities",
+                   "accepted_per_sequence": round(float(n.mean()), 3), "cache_bytes_per_layer": kv_bytes,
+                   "attention_GBps": round(kv_bytes / (us["tree_attention"] / 1e6) / 1e9, 1),
+                   "attention_frac_of_peak": round(kv_bytes / (us["tree_attention"] / 1e6) / 1e9 / HBM_PEAK_GBS, 4)},
+        "kernels_us": us,
+        "fork": {"us_per_call": round(fork_ms * 1e3, 3), "kernels_us": fork_us},
+        "per_call": dist,
+        "cpu_baseline": cpu,
+    }
+    print(json.dumps(line), flush=True)
+
+
+# ---------------------------------------------------------------------------
 # GPU timing
 # ---------------------------------------------------------------------------
 def main():
@@ -757,6 +902,9 @@ def main():
                     help="time the two-batch schedule: verify on one stream, the synthetic draft producer on another")
     ap.add_argument("--hispec", action="store_true",
                     help="time the two-stage verify (spec_hispec_verify) on three synthetic exit layers")
+    ap.add_argument("--tree", action="store_true",
+                    help="time a round of drafted trees over a paged cache: spec_tree_attention per layer, "
+                         "spec_verify_tree, spec_cache_commit; and spec_cache_fork")
     ap.add_argument("--smc", action="store_true",
                     help="time the SMC-SD step (spec_smc_step) on the same inputs instead of the verify step")
     ap.add_argument("--calibrate", action="store_true",
@@ -781,6 +929,9 @@ def main():
 
     if args.hispec:
         hispec_bench(args, binding, torch, dev)
+        return
+    if args.tree:
+        tree_bench(args, binding, torch, dev)
         return
 
     print(f"[bench] generating {N_SETS} input sets of workload {args.workload}", file=sys.stderr, flush=True)
