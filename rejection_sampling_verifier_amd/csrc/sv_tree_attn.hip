@@ -24,7 +24,7 @@
 //   then 16 t + 8 + 4 h + 0..3).  V^T is the A operand in that order, read
 //   from the row-major tile by the 4 x 16 transposing LDS load.
 //
-// The rounding of the weights (bf16: 2^-9 relative each, fp16: 2^-12) is the
+// The rounding of the weights (bf16: 2^-8 relative at most, fp16: 2^-11) is the
 // only one below float32 before the output's own.  The maximum is raised only
 // when a row's new scores exceed it by more than 2^8, so weights reach 256 at
 // most; the sum uses the unrounded weights.
@@ -35,6 +35,17 @@
 // sequence fills the device.  A (sequence, key head) that a cut divides leaves
 // partial (O, m, l) records that k_tree_merge joins in part order, so results
 // do not depend on timing.
+//
+// What bounds it: up to 64 rows per key head the cache's bytes (64 sequences of
+// 8192 rows, 8 key heads of 128: 2.1 GB at 5.9 TB/s with 4 to 24 rows, 5.5 with
+// 64, of the 7.1 a plain read reaches; 13 TB/s where the rows come from the L2),
+// then the matrix instructions and the softmax between them (128 rows 650
+// TFLOP/s, 256 rows 740).  A workgroup's two stages keep 32 KB (64 KB with 32
+// rows) of K and V under way while the tile before is computed.  Separate slots
+// for K and V, refilled one by one, made more instructions and ran 4 to 12 %
+// slower; one stage and two workgroups per CU (32 rows) ran 10 % slower from
+// memory.  Short calls are a chain of latencies (lengths, table, first tile,
+// join): one sequence of a thousand rows takes 11 us and 4 for the join.
 //
 // Rows of the tile that no query sees (past the length, past the tree, on a
 // page outside the pool) are staged as zeros.  Where some rows see a key and
@@ -604,7 +615,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
                         if (mixed || bad[ks] != 0) {
-                            const int sub = sub0 + ks, key0 = kb + ks * 32 + sub0 * 32;
+                            const int key0 = kb + (sub0 + ks) * 32;
                             uint32_t see = ~bad[ks];  // bit r: this lane's row sees row r of the subtile
                             if (tree)
                                 see &= key0 < kMaxNodes ? static_cast<uint32_t>(set >> key0) : 0u;
@@ -767,7 +778,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
             const int r = wr * 32 + col;
 #pragma unroll
             for (int j = 0; j < kOut; ++j)
-                *reinterpret_cast<float4*>(rec + r * DP + 8 * (wk * kOut + j) + 4 * hh) = fin[j];
+                if (8 * (wk * kOut + j) < p.D)
+                    *reinterpret_cast<float4*>(rec + r * DP + 8 * (wk * kOut + j) + 4 * hh) = fin[j];
             if (hh == 0 && wk == 0) {
                 rec[RB * DP + r] = mx;
                 rec[RB * DP + RB + r] = l;
@@ -838,7 +850,7 @@ __global__ __launch_bounds__(kThreads) void k_tree_merge(TreeAttnParams p) {
                 const float* const q = at(c + k * kStride);
                 mc[k] = q[RB * DP + r];
                 lc[k] = q[RB * DP + RB + r];
-                v[k] = *reinterpret_cast<const float4*>(q + r * DP + d);
+                v[k] = d < p.D ? *reinterpret_cast<const float4*>(q + r * DP + d) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int k = 0; k < kFlight; ++k)
@@ -910,7 +922,9 @@ template <int DT, int DP, int RB>
 hipError_t merge_one(const TreeAttnParams& p, hipStream_t st, const LaunchEvents& ev) {
     constexpr int TEAMS = kThreads / (DP / 4);
     const int tasks = p.B * p.Hkv, rows = p.N * p.G;
-    if (p.clusters > 4 * tasks)
+    // many parts per (sequence, key head): a context of 20001 rows over the whole device 4 us
+    // shared and 23 alone; with 12 parts of 115 rows each 12 us shared and 7 alone
+    if (p.clusters > 16 * tasks)
         hipExtLaunchKernelGGL((k_tree_merge<DT, DP, RB, true>), dim3(tasks, rows), dim3(kThreads), 0, st, ev.start,
                               ev.stop, 0, p);
     else

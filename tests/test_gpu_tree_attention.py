@@ -102,6 +102,13 @@ def test_long_and_ragged(N, D):
           f"ragged N={N} D={D}")
 
 
+@pytest.mark.parametrize("D", [40, 80, 128])
+@pytest.mark.parametrize("N,H", [(1, 1), (1, 8), (23, 5)])
+def test_many_parts_of_few_sequences(N, H, D):
+    """One long sequence over the whole device: its parts are joined by whole workgroups."""
+    check(make(B=1, N=N, H=H, Hkv=1, D=D, lens=(9001,), ps=16, seed=N + D), f"one sequence N={N} H={H} D={D}")
+
+
 def test_more_sequences_than_a_workgroup_has_threads():
     rng = np.random.default_rng(5)
     lens = rng.integers(0, 90, 300)
