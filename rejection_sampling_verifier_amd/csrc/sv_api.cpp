@@ -606,7 +606,10 @@ bool expanded(const I* stride, const int32_t* size, int n) {
 }
 
 // How the attention's work is cut: rows and keys per workgroup tile by the
-// query rows that share a key head, parts by the device's size.
+// query rows that share a key head, parts by the device's size.  64 sequences
+// of 4096 rows, 8 key heads of 128, us with tiles of 32 / 64 / 128 rows: 24
+// rows 201 / 210 / 221, 36 rows 237 / 211, 64 rows 241 / 212 / 230, 128 rows
+// - / 266 / 237.
 struct TreePlan {
     sv::TreeAttnShape s;
     int MT = 1, clusters = 1, merge = 0;
@@ -630,9 +633,14 @@ int plan_tree(const sv_tree_attention* a, TreePlan& t) {
     if (tasks * t.MT >= 1ll << 24) return SV_ESHAPE;  // a launch has fewer than 2^32 threads
     const int64_t cap = static_cast<int64_t>(a->width) * a->page_size;
     const int64_t most = (cap + t.s.keys - 1) / t.s.keys + 1;  // tiles of one (sequence, key head)
-    const int64_t blocks = (t.s.rows == 32 && t.s.dp == 128 ? 1ll : 2ll) * device_cus();  // workgroups that are resident at once
+    // As many parts as workgroups are resident at once: 32 rows of 128 dimensions take
+    // 128 KB of LDS, one workgroup per CU; else two.  As above with one and two parts per
+    // CU: 24 rows 197 and 208 us, 64 rows 223 and 213, 128 rows 258 and 238.
+    const int64_t blocks = (t.s.rows == 32 && t.s.dp == 128 ? 1ll : 2ll) * device_cus();
     if (most <= 4) {
-        // so short that a part is a whole (sequence, key head): nothing to join
+        // So short that a part is a whole (sequence, key head) and nothing is joined: 64
+        // sequences of 384 rows 35 us, divided and joined 34 + 4; one sequence of 384 rows 14
+        // and 11 + 4, of 768 (more than four tiles) 17 and 11 + 4.
         t.merge = 0;
         t.clusters = static_cast<int>(tasks);
     } else {
