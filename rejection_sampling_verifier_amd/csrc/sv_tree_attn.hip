@@ -761,7 +761,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
         if (whole) {
             if (my_row < p.N * p.G) {
                 const int node = my_row / p.G;
-                const float inv = my_row < rows ? 1.f / l : 0.f;  // zeros for an absent node
+                const bool present = my_row < rows;  // an absent node's row is zero, not 0 * fin: fin may be NaN
+                const float inv = 1.f / l;
                 uint8_t* const dst = p.out + units(b, p.os[0], node, p.os[1]) +
                                      units(h * p.G + my_row - node * p.G, p.os[2]);
 #pragma unroll
@@ -769,7 +770,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
                     const int d = 8 * (wk * kOut + j);
                     if (d < p.D)
                         *reinterpret_cast<v4s*>(dst + 2 * (d + 4 * hh)) =
-                            pack4<DT>(fin[j].x * inv, fin[j].y * inv, fin[j].z * inv, fin[j].w * inv);
+                            present ? pack4<DT>(fin[j].x * inv, fin[j].y * inv, fin[j].z * inv, fin[j].w * inv)
+                                    : v4s{0, 0, 0, 0};
                 }
             }
         } else if (my_row < rows) {

@@ -256,3 +256,22 @@ def test_graph_replays():
         # bit for bit: the longer length reaches a slot that was never written (NaN)
         assert torch.equal(out.view(torch.int16), want.view(torch.int16)), rep
         assert torch.equal(out2, call(other)), rep
+
+
+@pytest.mark.parametrize("name", ["k", "v", "kt", "vt"])
+@pytest.mark.parametrize("lens", [(100, 40), (9000, 40)])  # one part each; the first divided
+@pytest.mark.parametrize("N,H", [(6, 4), (20, 4), (40, 6)])  # rows that fill 32, 64 and more than 64
+def test_absent_nodes_stay_zero_beside_visible_nan(N, H, lens, name):
+    """An absent node's row is zero whatever the rows hold that others see."""
+    for bad in (float("nan"), float("inf")):
+        s = make(B=2, N=N, H=H, kind="chain", lens=lens, n_nodes=[2, 3], poison=False, seed=N)
+        for b in range(2):
+            if name in ("k", "v"):
+                s[name][s["table"][b, 0].long(), 3] = bad
+            else:
+                s[name][b, 0] = bad
+        out = call(s)
+        torch.cuda.synchronize()
+        for b, n in enumerate((2, 3)):
+            assert (out[b, n:] == 0).all(), (b, bad)
+            assert not torch.isfinite(out[b, 0]).any(), (b, bad)
