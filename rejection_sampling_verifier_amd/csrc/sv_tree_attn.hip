@@ -24,10 +24,12 @@
 //   then 16 t + 8 + 4 h + 0..3).  V^T is the A operand in that order, read
 //   from the row-major tile by the 4 x 16 transposing LDS load.
 //
-// The rounding of the weights (bf16: 2^-8 relative at most, fp16: 2^-11) is the
-// only one below float32 before the output's own.  The maximum is raised only
-// when a row's new scores exceed it by more than 2^8, so weights reach 256 at
-// most; the sum uses the unrounded weights.
+// The rounding of the weights is the only one below float32 before the output's
+// own: bf16 2^-8 relative at most; fp16 2^-11 relative, or 2^-32 of the row's
+// reference weight where that is more (below 2^-21 of it).  The maximum is
+// raised only when a row's new scores exceed it by more than 8 (a factor of
+// 2^8), so a key may weigh 256 times the reference; the sum uses the unrounded
+// weights.
 //
 // The tiles of all sequences and key heads form one line that is cut into
 // equal parts (one per workgroup, or per group of workgroups when the rows
@@ -126,6 +128,13 @@ __device__ __forceinline__ uint32_t bits_from(int n) { return n <= 0 ? ~0u : n >
 __device__ __forceinline__ float shift_of(float a, float b) {
     return a == b ? 1.f : __builtin_amdgcn_exp2f(a - b);
 }
+
+// Weights are 2^(x - m + kUp), m the running maximum.  float16's normal numbers
+// end at 2^-14: times 2^7 (8 of slack in m: 2^15 at most, of 65504) a long tail
+// behind a dominant key keeps its share of the output, with 2^-25 * 2^-7 lost
+// per key at most.  The sum takes the same factor, so nothing else changes.
+template <int DT>
+constexpr float kUp = DT == DT_BF16 ? 0.f : 7.f;
 
 // What rows that do not exist, and dimensions past D, are staged from.
 __device__ const uint4 kZero = {0, 0, 0, 0};
@@ -640,7 +649,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
                             for (int i = 0; i < 16; ++i) o[dt][i] *= a;
                         mx = mn;
                     }
-                    const float ref = mx == -INFINITY ? 0.f : mx;
+                    const float ref = (mx == -INFINITY ? 0.f : mx) - kUp<DT>;
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll

@@ -275,3 +275,39 @@ def test_absent_nodes_stay_zero_beside_visible_nan(N, H, lens, name):
         for b, n in enumerate((2, 3)):
             assert (out[b, n:] == 0).all(), (b, bad)
             assert not torch.isfinite(out[b, 0]).any(), (b, bad)
+
+
+@pytest.mark.parametrize("bits", [21.6, 25.5])
+@pytest.mark.parametrize("N,H", [(2, 8), (8, 8), (16, 8)])  # 16, 64 and 128 rows per key head
+def test_float16_tail_behind_a_dominant_key(N, H, bits):
+    """One key (an attention sink) `bits` powers of two above 32767 equal ones:
+    their weights are far below float16's normal numbers next to its own.  As
+    many (sequence, key head)s as the device has parts, so that none is divided
+    and the tail meets the sink's maximum; all sequences share their pages.
+
+    Bound: attention_tolerance's with its absolute term at 2^-32 a key.  Weights
+    are held times 2^7, so half the spacing of float16's subnormals, 2^-25, is
+    2^-32 of the row's reference (parts' and waves' own references are below the
+    row's, and their errors shrink with them)."""
+    B, Hkv, D, ps, n = 512, 1, 64, 1024, 32768
+    rng = np.random.default_rng(1)
+    k, v = np.zeros((n // ps, ps, Hkv, D)), 1 + 0.25 * rng.random((n // ps, ps, Hkv, D))
+    k[0, 0, 0, 0], v[0, 0] = bits * np.log(2), 0.0
+    q, kt, vt = np.zeros((1, N, H, D)), np.zeros((1, N, Hkv, D)), 1 + 0.25 * rng.random((1, N, Hkv, D))
+    q[..., 0] = 1.0
+    table = np.arange(n // ps, dtype=np.int32)[None]
+    par = parents("chain", 1, N, rng)
+    all_of = lambda a, dtype=None: dev(np.repeat(a, B, 0), dtype)  # noqa: E731
+    f16 = torch.float16
+    s = dict(q=all_of(q, f16), kt=all_of(kt, f16), vt=all_of(vt, f16), parent=all_of(par), table=all_of(table),
+             lens=dev(np.full(B, n, np.int32)), n_nodes=None, k=dev(k, f16), v=dev(v, f16))
+    out = call(s, scale=1.0)
+    torch.cuda.synchronize()
+    assert (out == out[:1]).all()
+    want, spread, reach = ref.tree_attention(f64(s["q"][:1]), f64(s["k"]), f64(s["v"]), table, np.array([n]),
+                                             f64(s["kt"][:1]), f64(s["vt"][:1]), par, scale=1.0)
+    vmax = 1.25
+    tol = attention_tolerance(spread, reach, want, f16, D, 0.0) + reach[..., 1:2] * 2.0 ** -32 * vmax
+    worst = float((np.abs(f64(out[:1]) - want) / tol).max())
+    say(f"[tree attention] {bits} bits, {N * H} rows: output {want.max():.2e}, worst error {worst:.3f} of its bound")
+    assert worst <= 1
