@@ -561,6 +561,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
                 }
             }
 
+            // bit r: this lane's row sees row r of the subtile that begins at key0
+            auto seen_of = [&](int key0, uint32_t bad, bool tree) {
+                uint32_t see = ~bad;
+                if (tree)
+                    see &= key0 < kMaxNodes ? static_cast<uint32_t>(set >> key0) : 0u;
+                else if (win)
+                    see &= bits_from(low - key0) | ~bits_from(p.sinks - key0);
+                return see;
+            };
+
             int at = 0;
             for (int t = t0; t < t1; ++t, at ^= 1) {
                 const bool tree = t >= tl.cache;
@@ -624,13 +634,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
                         if (mixed || bad[ks] != 0) {
-                            const int key0 = kb + (sub0 + ks) * 32;
-                            uint32_t see = ~bad[ks];  // bit r: this lane's row sees row r of the subtile
-                            if (tree)
-                                see &= key0 < kMaxNodes ? static_cast<uint32_t>(set >> key0) : 0u;
-                            else if (win)
-                                see &= bits_from(low - key0) | ~bits_from(p.sinks - key0);
-                            see >>= 4 * hh;
+                            const uint32_t see = seen_of(kb + (sub0 + ks) * 32, bad[ks], tree) >> 4 * hh;
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 x[ks][i] = see & (1u << (8 * (i >> 2) + (i & 3))) ? x[ks][i] : -INFINITY;
@@ -679,8 +683,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
                         float* const op = wp + 1024;
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks) {
+                            // -1: hidden from the row (a weight of 0 may be a visible key's)
+                            const uint32_t see = seen_of(kb + (sub0 + ks) * 32, bad[ks], tree) >> 4 * hh;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) wp[(8 * (i >> 2) + 4 * hh + (i & 3)) * 32 + col] = x[ks][i];
+                            for (int i = 0; i < 16; ++i)
+                                wp[(8 * (i >> 2) + 4 * hh + (i & 3)) * 32 + col] =
+                                    see & (1u << (8 * (i >> 2) + (i & 3))) ? x[ks][i] : -1.f;
 #pragma unroll
                             for (int dt = 0; dt < ND; ++dt) {
 #pragma unroll
@@ -697,7 +705,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
 #pragma unroll 1
                                     for (int i = 0; i < 16; ++i) {
                                         const int d = 32 * dt + 8 * (i >> 2) + 4 * hh + (i & 3);
-                                        if (d >= p.D || wgt == 0.f) continue;
+                                        if (d >= p.D || wgt < 0.f) continue;
                                         const uint16_t e = *reinterpret_cast<const uint16_t*>(src + 2 * d);
                                         if (nonfinite2<DT>(e)) op[i * 64 + lane] += wgt * to_float<DT>(e);
                                     }

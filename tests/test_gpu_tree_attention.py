@@ -311,3 +311,23 @@ def test_float16_tail_behind_a_dominant_key(N, H, bits):
     worst = float((np.abs(f64(out[:1]) - want) / tol).max())
     say(f"[tree attention] {bits} bits, {N * H} rows: output {want.max():.2e}, worst error {worst:.3f} of its bound")
     assert worst <= 1
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("N,H", [(4, 4), (20, 4), (40, 6)])
+def test_visible_nan_of_vanishing_weight_is_not_swallowed(N, H, bad):
+    """A node that sees a NaN or infinite value gives no finite number, also
+    where the key's weight is below float32's smallest: in the tree, and in a
+    tile of which the window hides rows from some nodes."""
+    s = make(B=1, N=N, H=H, kind="chain", lens=(200,), poison=False)
+    D = s["q"].shape[-1]
+    s["q"][0, 2], s["kt"][0, 0], s["vt"][0, 0] = 8.0, -8.0, bad  # a score of -512 beside ones of size 10
+    out = call(s)
+    torch.cuda.synchronize()
+    assert not torch.isfinite(out).any()
+    s = make(B=1, N=N, H=H, kind="chain", lens=(200,), poison=False)
+    pg, slot = s["table"][0, 152 // 16].long(), 152 % 16  # the root and its child see row 152, the others do not
+    s["q"][0, 1], s["k"][pg, slot], s["v"][pg, slot] = 8.0, -8.0, bad
+    out = call(s, window=50)
+    torch.cuda.synchronize()
+    assert D == 64 and not torch.isfinite(out[0, :2]).any() and torch.isfinite(out[0, 2:]).all()
