@@ -393,7 +393,8 @@ enum { SV_F16 = 2 };  /* a dtype of the attention and the cache */
  *                are multiples of 16 bytes; strides are >= 0, below 64 GB; those of
  *                axes of one are not looked at.
  * table          device int32 [B, width], row stride table_stride.  An entry
- *                outside [0, pages) hides its rows.  width * page_size <= 2^28.
+ *                outside [0, pages) hides its rows.  width * page_size <= 2^28
+ *                (with 1024 key heads of more than 32 rows each, 2^28 - 64).
  * len            device int32 [B], rows in the cache (clamped to [0, width *
  *                page_size]).
  * parent         device int32 [B, N], contiguous; parent[b, 0] is not read.  A

@@ -633,6 +633,7 @@ int plan_tree(const sv_tree_attention* a, TreePlan& t) {
     if (tasks * t.MT >= 1ll << 24) return SV_ESHAPE;  // a launch has fewer than 2^32 threads
     const int64_t cap = static_cast<int64_t>(a->width) * a->page_size;
     const int64_t most = (cap + t.s.keys - 1) / t.s.keys + 1;  // tiles of one (sequence, key head)
+    if (a->kv_heads * most > 1ll << 32) return SV_ESHAPE;  // the kernel counts a sequence's tiles in 32 bits
     // As many parts as workgroups are resident at once: 32 rows of 128 dimensions take
     // 128 KB of LDS, one workgroup per CU; else two.  As above with one and two parts per
     // CU: 24 rows 197 and 208 us, 64 rows 223 and 213, 128 rows 258 and 238.

@@ -436,7 +436,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
     while (f < f1) {
         const Tiles tl = tiles_of<TK>(p, p.len[b]);
         const int T = tl.total();
-        const uint32_t in_seq = static_cast<uint32_t>(f - before * p.Hkv);  // below 1024 heads of 2^22 tiles
+        const uint32_t in_seq = static_cast<uint32_t>(f - before * p.Hkv);  // the host refuses more than 2^32 tiles
         const int h = static_cast<int>(in_seq / static_cast<uint32_t>(T));
         const int t0 = static_cast<int>(in_seq - static_cast<uint32_t>(h) * T);
         const int t1 = static_cast<int>(min(static_cast<int64_t>(T), t0 + (f1 - f)));

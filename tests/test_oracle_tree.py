@@ -399,3 +399,15 @@ def test_binding_refuses_before_the_library():
         binding.cache_fork(c, c, i(2, 5), i(2), i(3))
     with pytest.raises(ValueError, match="GPU"):
         binding.cache_fork(c, c, i(2, 5), i(2), i(2))
+
+
+def test_a_line_of_tiles_stays_below_32_bits(lib):
+    """1024 key heads of 2^28 cache rows and the tree's tile are 2^32 + 1024
+    tiles of 64 keys: refused, where the kernel's count would wrap to head 0."""
+    big = dict(B=1, heads=1024, kv_heads=1024, dim=64, page_size=1024, table_stride=1 << 18)
+    assert lib.spec_tree_attention_workspace(_attn(N=33, width=1 << 18, **big)) == -2
+    assert lib.spec_tree_attention(_attn(N=33, width=1 << 18, **big), None) == -2
+    assert lib.spec_tree_attention_workspace(_attn(N=33, width=(1 << 18) - 1, **big)) > 0
+    assert lib.spec_tree_attention_workspace(_attn(N=32, width=1 << 18, **big)) > 0  # tiles of 128 keys
+    fewer = dict(big, heads=1023, kv_heads=1023)
+    assert lib.spec_tree_attention_workspace(_attn(N=33, width=1 << 18, **fewer)) > 0
