@@ -381,8 +381,9 @@ enum { SV_F16 = 2 };  /* a dtype of the attention and the cache */
  * `window` of itself and its ancestors.  window = 0: everything.
  *
  * dtype          SV_BF16 or SV_F16, of all tensors.
- * B, N           1 <= B <= 65536 sequences, 1 <= N <= 64 nodes; B * kv_heads *
- *                (N * heads / kv_heads / 128, rounded up) below 2^24.
+ * B, N           1 <= B <= 65536 sequences, 1 <= N <= 64 nodes; B * kv_heads
+ *                below 2^24, and with t = N * heads / kv_heads / 128, rounded
+ *                up, above 1: B * kv_heads, rounded up to eights, times t too.
  * heads, kv_heads  query and key heads; heads <= 1024, a multiple of kv_heads.
  * dim            a multiple of 8, at most 128.
  * q, out         [B, N, heads, dim]; k_tree, v_tree [B, N, kv_heads, dim];

@@ -630,7 +630,8 @@ int plan_tree(const sv_tree_attention* a, TreePlan& t) {
     t.s.keys = t.s.rows == 32 ? 128 : 64;
     t.MT = (rows + t.s.rows - 1) / t.s.rows;
     const int64_t tasks = static_cast<int64_t>(a->B) * a->kv_heads;
-    if (tasks * t.MT >= 1ll << 24) return SV_ESHAPE;  // a launch has fewer than 2^32 threads
+    // a launch has fewer than 2^32 threads; several row tiles go in groups of eight parts
+    if ((t.MT > 1 ? (tasks + 7) / 8 * 8 : tasks) * t.MT >= 1ll << 24) return SV_ESHAPE;
     const int64_t cap = static_cast<int64_t>(a->width) * a->page_size;
     const int64_t most = (cap + t.s.keys - 1) / t.s.keys + 1;  // tiles of one (sequence, key head)
     if (a->kv_heads * most > 1ll << 32) return SV_ESHAPE;  // the kernel counts a sequence's tiles in 32 bits

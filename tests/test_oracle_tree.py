@@ -411,3 +411,12 @@ def test_a_line_of_tiles_stays_below_32_bits(lib):
     assert lib.spec_tree_attention_workspace(_attn(N=32, width=1 << 18, **big)) > 0  # tiles of 128 keys
     fewer = dict(big, heads=1023, kv_heads=1023)
     assert lib.spec_tree_attention_workspace(_attn(N=33, width=1 << 18, **fewer)) > 0
+
+
+def test_rounded_launches_stay_below_the_largest_grid(lib):
+    """Several row tiles are launched in groups of eight parts: 5592405 parts of
+    three tiles are fewer than 2^24 workgroups, rounded up they are not."""
+    big = dict(width=4, dim=8, N=48, table_stride=4)  # 384 rows per key head
+    assert lib.spec_tree_attention_workspace(_attn(B=46995, heads=952, kv_heads=119, **big)) == -2
+    assert lib.spec_tree_attention(_attn(B=46995, heads=952, kv_heads=119, **big), None) == -2
+    assert lib.spec_tree_attention_workspace(_attn(B=46994, heads=952, kv_heads=119, **big)) == 0
