@@ -524,8 +524,8 @@ typedef struct {
  * n_accepted[b]; a negative n appends nothing.  nodes NULL: rows 0..n (a
  * chain: the out_n_accepted of spec_verify).  A partly filled last page is
  * filled up, and further pages are taken lowest free page first, in the order
- * of the sequences.  A partly filled last page must belong to one sequence
- * only (spec_cache_fork leaves it so).
+ * of the sequences.  A partly filled last page that is appended to must be
+ * named by no other live entry (spec_cache_fork leaves it so).
  *
  * out_table [B, width] (row stride out_stride) and out_len [B] receive the new
  * tables, -1 behind the live entries; they may be table and len themselves
@@ -533,8 +533,9 @@ typedef struct {
  *
  * out_status  device int32 [1]: 0; or the number of pages that were lacking;
  *             or -1 when a length, count, node or live page number is out of
- *             range or a table row too short.  Unless 0, nothing is appended
- *             and tables and lengths go out as they came in.
+ *             range, a table row too short, or a partly filled page that is to
+ *             be appended to is shared.  Unless 0, nothing is appended and
+ *             tables and lengths go out as they came in.
  *
  * dim * element size, strides (of axes longer than one) and data are multiples of 16 bytes; pages <=
  * SPECVERIFY_MAX_PAGES; page_size a power of two, at most 1024; B, layers <=

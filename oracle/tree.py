@@ -200,6 +200,10 @@ def cache_commit(k, v, table, lens, k_tree, v_tree, nodes, n_accepted):
             return _unchanged(table, lens, ps, -1)
         rows.append(live)
         move.append(at)
+    # a page that is appended to belongs to one sequence only
+    named = [x for r in rows for x in r]
+    if any(at and lens[b] % ps and named.count(rows[b][-1]) > 1 for b, at in enumerate(move)):
+        return _unchanged(table, lens, ps, -1)
     free = _lowest_free(rows, pages)
     need = [_blocks(int(lens[b]) + len(move[b]), ps) - len(rows[b]) for b in range(B)]
     if sum(need) > len(free):

@@ -624,7 +624,8 @@ def cache_commit(k_cache, v_cache, block_table, seq_len, k_tree, v_tree, nodes, 
     chain) and n_accepted [B]: int32.  Returns (table, length, status): new
     tensors, or out_table and out_len, which may be block_table and seq_len
     themselves.  status [1]: 0, the number of pages lacking, or -1 for bad
-    indices; unless 0, nothing was appended.
+    indices or a shared page that would be appended to; unless 0, nothing was
+    appended.
     """
     lib, _, _, _, call, _ = _tree_calls()
     index = k_cache.get_device()

@@ -65,6 +65,8 @@ struct PlanArrays {
     int32_t *len, *have, *row, *first;
 };
 
+constexpr int kOwn = -2;  // such a page is there, not read yet (-1: there is none)
+
 // SMALL: one thread per sequence.  Loads are issued for many sequences or
 // entries at a time; what the kernel costs is a chain of three memory
 // latencies (lengths, tables, writes), about 2 us, and the launch.
@@ -80,8 +82,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
     int32_t* const plan = p.plan;
     int32_t* const spare = plan + static_cast<int64_t>(p.B) * kPlanWords;
     int32_t* const fresh = spare + static_cast<int64_t>(p.B) * kPlanSpare;  // the new pages, in order
-    // rows of the tables that count (have entries of row `row`), old lengths, and for a fork the
-    // lowest slot of each ancestor
+    // rows of the tables that count (have entries of row `row`), old lengths, and `first`: for a fork
+    // the lowest slot of each ancestor, for a commit the partly filled page that is appended to
     const PlanArrays s = SMALL ? PlanArrays{s_arr, s_arr + kPlanThreads, s_arr + 2 * kPlanThreads,
                                             s_arr + 3 * kPlanThreads}
                                : PlanArrays{spare, spare + p.B, spare + 2 * static_cast<int64_t>(p.B),
@@ -145,6 +147,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
             have = blocks_of(len, p.ps_shift);
             s.have[b] = have;
             s.row[b] = rows;
+            s.first[b] = rows > 0 && (len & ((1 << p.ps_shift) - 1)) ? kOwn : -1;
             len += rows;
             want = blocks_of(len, p.ps_shift);
         }
@@ -160,6 +163,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
         if (j >= s.have[b]) return;
         if (pg < 0 || pg >= p.pages)
             bad = true;
+        else if (!p.fork && j == s.have[b] - 1 && s.first[b] == kOwn)
+            s.first[b] = pg;  // marked after all others
         else
             atomicOr(&used[pg % W], 1u << (pg / W));
     };
@@ -191,6 +196,16 @@ __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
                 const int node = p.nodes[i];
                 if (node < 0 || node >= p.N) bad = true;
             }
+        }
+    }
+    if (!p.fork) {
+        // the pages that are appended to: nobody else may name them
+        __syncthreads();
+        for (int b = tid; b < p.B; b += kPlanThreads) {
+            const int pg = s.first[b];
+            if (pg < 0) continue;
+            const uint32_t bit = 1u << (pg / W);
+            if (atomicOr(&used[pg % W], bit) & bit) bad = true;
         }
     }
     if (bad) s_bad = 1;

@@ -246,3 +246,38 @@ def test_graph_replays():
         torch.cuda.synchronize()
         for a, b in zip((t1, n1, st1, t2, n2, st2, s["k"], s["v"]), (*e, *e2, *want)):
             assert torch.equal(a, b), rep
+
+
+@pytest.mark.parametrize("B", [3, 1500])  # one thread per sequence, and more sequences than threads
+@pytest.mark.parametrize("how", ["both", "one", "neither", "full", "itself", "behind"])
+def test_commit_into_a_shared_page_is_refused(how, B):
+    """Two live entries name a partly filled page that is appended to: nothing
+    is.  Its neighbours in the batch lie anywhere in it."""
+    s = make([14] * B, ps=8, N=3, Hkv=1, layers=1, spare=2 * B + 4, seed=5)
+    s["nodes"] = None
+    s["n"].fill_(1)
+    a, b = B // 3, B - 1
+    s["table"][b, 0] = s["table"][a, 0]  # a shared full page
+    if how in ("both", "one", "neither"):
+        s["table"][b, 1] = s["table"][a, 1]
+        s["n"][a] = 1 if how == "both" else -1
+        s["n"][b] = -1 if how == "neither" else 1
+    elif how == "full":
+        s["lens"][b], s["n"][b] = 16, -1
+        s["table"][b, 1] = s["table"][a, 1]
+    elif how == "itself":
+        s["table"][a, 0] = s["table"][a, 1]
+    else:
+        s["table"][b, 2:] = s["table"][a, 1]  # not live
+    got = check_commit(s)
+    assert int(got[2]) == (0 if how in ("neither", "behind") else -1)
+
+
+def test_commit_after_a_fork_owns_its_pages():
+    """spec_cache_fork leaves every partly filled page to one slot."""
+    s = make([13, 16, 21, 3], ps=8, spare=20, N=4)
+    got = check_fork(s, [2, 2, 0, 2])
+    s["table"], s["lens"] = got[0], got[1]
+    s["nodes"] = None
+    s["n"].fill_(2)
+    assert int(check_commit(s)[2]) == 0

@@ -420,3 +420,26 @@ def test_rounded_launches_stay_below_the_largest_grid(lib):
     assert lib.spec_tree_attention_workspace(_attn(B=46995, heads=952, kv_heads=119, **big)) == -2
     assert lib.spec_tree_attention(_attn(B=46995, heads=952, kv_heads=119, **big), None) == -2
     assert lib.spec_tree_attention_workspace(_attn(B=46994, heads=952, kv_heads=119, **big)) == 0
+
+
+def test_commit_into_a_shared_page_is_refused():
+    """A partly filled page that two live entries name is not appended to;
+    shared full pages, and a shared page nobody appends to, are fine."""
+    k = np.zeros((1, 12, 4, 1, 1))
+    kt = np.arange(1.0, 7).reshape(1, 3, 2, 1, 1)
+    lens = np.array([6, 6, 4], np.int32)
+    apart = np.array([[3, 5, -1], [3, 6, -1], [3, -1, -1]], np.int32)
+    for table, n, want in ((apart, [0, 1, 0], 0),
+                           ([[3, 5, -1], [3, 5, -1], [3, -1, -1]], [0, 1, 0], -1),   # both append
+                           ([[3, 5, -1], [3, 5, -1], [3, -1, -1]], [0, -1, 0], -1),  # one does
+                           ([[3, 5, -1], [3, 5, -1], [3, -1, -1]], [-1, -1, 0], 0),  # neither
+                           ([[3, 5, -1], [3, 6, -1], [5, -1, -1]], [0, 0, -1], -1),  # another's full page
+                           ([[5, 5, -1], [3, 6, -1], [3, -1, -1]], [0, -1, -1], -1),  # its own
+                           ([[3, 5, 5], [3, 6, 6], [3, 6, 5]], [0, 0, 0], 0)):  # entries behind the live ones
+        kk, vv = k.copy(), k.copy()
+        t, m, status = ref.cache_commit(kk, vv, np.array(table, np.int32), lens, kt, -kt, None, np.array(n, np.int32))
+        assert status == want, (table, n)
+        if want:
+            assert not kk.any() and (m == lens).all() and (t[:, :2] == np.array(table)[:, :2])[:2].all()
+        else:
+            assert (m == lens + np.array(n) + 1).all()
