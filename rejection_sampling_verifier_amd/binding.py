@@ -369,7 +369,8 @@ _PACK_LOGITS = struct.Struct("@Piiiiqq").pack
 _PACK_ATTENTION = struct.Struct("@iiiiiiP3qPP3q3qPP3q3qiii4xPqPPPfii4xP3qPq").pack
 _PACK_CACHE = struct.Struct("@PPiiiiii4q4qPqPii").pack
 _PACK_STRIDES = struct.Struct("@4q").pack
-_workspaces = {}  # bytes a call needs, by its sizes
+_workspaces = {}  # bytes a call needs, by its sizes; at most _KEPT of them
+_KEPT = 1024
 _calls = None
 
 
@@ -447,6 +448,18 @@ def _table(t, name, B, index, width=None):
     return t.data_ptr(), (n or 1) if B == 1 else st[0]
 
 
+def _workspace_bytes(lib, key, ask):
+    """What `ask()` says a call with the sizes `key` needs, asked once."""
+    need = _workspaces.get(key)
+    if need is None:
+        need = ask()
+        _check(lib, need)
+        if len(_workspaces) >= _KEPT:
+            _workspaces.clear()
+        _workspaces[key] = need
+    return need
+
+
 def _no_grad(*tensors):
     if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
         raise ValueError("no backward pass: call it under torch.no_grad()")
@@ -505,12 +518,7 @@ def tree_attention(q, k_cache, v_cache, block_table, seq_len, k_tree, v_tree, pa
                                dim ** -0.5 if scale is None else scale, window, sinks,
                                out.data_ptr(), os[0], os[1], os[2], ws, need)
 
-    key = (index, B, N, heads, kv_heads, dim, page_size, width, pages)
-    need = _workspaces.get(key)
-    if need is None:
-        need = size_of(block(0, 0))
-        _check(lib, need)
-        _workspaces[key] = need
+    need = _workspace_bytes(lib, (index, B, N, heads, kv_heads, dim, page_size, width), lambda: size_of(block(0, 0)))
     ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
     _check(lib, call(block(ws.data_ptr() if need else 0, need), _raw_stream(index)))
     return out
@@ -560,12 +568,8 @@ def verify_tree(target_probs, draft_probs, tokens, parent, u_accept, u_final, n_
         out_nodes = tokens.new_empty((B, N))
     if out_n_accepted is None:
         out_n_accepted = tokens.new_empty((B,))
-    key = ("verify", index, B, N, V, target_probs.dtype, dd is None)
-    need = _workspaces.get(key)
-    if need is None:
-        need = lib.spec_verify_tree_workspace(B, N, V, _DTYPES[target_probs.dtype], dd is not None)
-        _check(lib, need)
-        _workspaces[key] = need
+    need = _workspace_bytes(lib, ("verify", index, B, N, V, target_probs.dtype, dd is None),
+                            lambda: lib.spec_verify_tree_workspace(B, N, V, _DTYPES[target_probs.dtype], dd is not None))
     ws = torch.empty((need,), dtype=torch.uint8, device=target_probs.device) if need else None
     _check(lib, call(td, dd, tok, par, nn, ua, uf, _array(out_tokens, "out_tokens", (B, N), index),
                      _array(out_nodes, "out_nodes", (B, N), index),
@@ -605,12 +609,7 @@ def _cache_outs(seq_len, B, width, index, out_table, out_len, out_status):
 
 
 def _cache_workspace(lib, like, B, N, page_size):
-    key = (B, N, page_size)
-    need = _workspaces.get(key)
-    if need is None:
-        need = lib.spec_cache_workspace(B, N, page_size)
-        _check(lib, need)
-        _workspaces[key] = need
+    need = _workspace_bytes(lib, (B, N, page_size), lambda: lib.spec_cache_workspace(B, N, page_size))
     return torch.empty((need,), dtype=torch.uint8, device=like.device), need
 
 

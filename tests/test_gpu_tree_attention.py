@@ -331,3 +331,17 @@ def test_visible_nan_of_vanishing_weight_is_not_swallowed(N, H, bad):
     out = call(s, window=50)
     torch.cuda.synchronize()
     assert D == 64 and not torch.isfinite(out[0, :2]).any() and torch.isfinite(out[0, 2:]).all()
+
+
+def test_tables_of_ever_new_widths_keep_a_bounded_record():
+    """A decoder that sizes its tables to the batch: the kept workspace sizes
+    do not grow with it."""
+    s = make(B=1, N=1, lens=(5,))
+    wide = torch.full((1, 1200), -1, dtype=torch.int32, device="cuda")
+    wide[:, :s["table"].shape[1]] = s["table"]
+    for w in range(1, 1201):
+        s["table"] = wide[:, :w]
+        call(s)
+    torch.cuda.synchronize()
+    assert len(binding._workspaces) <= 1024
+    check(s, "1200 pages wide")

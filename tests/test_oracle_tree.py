@@ -443,3 +443,24 @@ def test_commit_into_a_shared_page_is_refused():
             assert not kk.any() and (m == lens).all() and (t[:, :2] == np.array(table)[:, :2])[:2].all()
         else:
             assert (m == lens + np.array(n) + 1).all()
+
+
+def test_kept_workspace_sizes_are_bounded(monkeypatch):
+    """A decoder whose tables grow with its batch asks for ever new sizes."""
+    monkeypatch.setattr(binding, "_workspaces", {})
+    asked = []
+    for i in range(5000):
+        for _ in range(2):
+            assert binding._workspace_bytes(None, ("sizes", i), lambda: asked.append(i) or i) == i
+    assert asked == list(range(5000))
+    assert len(binding._workspaces) <= 1024
+    a = dict(index=0, B=1, N=2, heads=4, kv_heads=2, dim=64, page_size=16, width=5)
+    assert binding._workspace_bytes(None, tuple(a.values()), lambda: 7) == 7
+
+
+def test_refused_sizes_are_not_kept(lib, monkeypatch):
+    monkeypatch.setattr(binding, "_workspaces", {})
+    for _ in range(2):
+        with pytest.raises(binding.SpecVerifyError):
+            binding._workspace_bytes(lib, ("bad",), lambda: -2)
+    assert not binding._workspaces
