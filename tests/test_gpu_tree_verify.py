@@ -227,3 +227,30 @@ def test_graph_replays_and_streams():
         stream.synchronize()
         for a, b, c in zip(outs, want, other):
             assert torch.equal(a, b) and torch.equal(c, b), rep
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,V,first", [(1, 1 << 21, 1234567), (3, 128256, 100000), (300, 20001, 19999), (2, 700, 0)])
+def test_draw_at_zero_is_the_first_id_with_weight(B, V, first, dtype):
+    """u_final = 0 draws the first id of which something is left, whatever the
+    order of the sums: exact, there is no border below it."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    p = torch.softmax(torch.randn((B, 2, V), device="cuda", generator=g), -1).to(dtype)
+    q = p[:, :1].clone()
+    q[:, :, first:] = torch.softmax(torch.randn((B, 1, V), device="cuda", generator=g), -1).to(dtype)[:, :, first:]
+    q[:, 0, -1] = p[:, 0, -1] * 4  # the child: refused at u next to 1
+    q[:, 0, first] = p[:, 0, first] / 2
+    s = dict(p=p, q=q, tok=dev(np.tile(np.array([[0, V - 1]], np.int32), (B, 1))),
+             par=dev(np.tile(np.array([[-1, 0]], np.int32), (B, 1))),
+             ua=dev(np.tile(np.array([[0, 1 - 2.0 ** -24]], np.float32), (B, 1))), uf=dev(np.zeros(B, np.float32)), n=None)
+    want = (f64(p[:, 0]) - f64(q[:, 0]) > 0).argmax(-1)
+    assert (want == first).all()
+    t, nd, n = [x.cpu().numpy() for x in call(s)]
+    assert (n == 0).all() and (nd == np.array([0, -1])).all()
+    np.testing.assert_array_equal(t[:, 0], want)
+    # chosen children: the first id but the refused one
+    p[:, 0, :first] = 0.0
+    s.update(q=None, tok=dev(np.tile(np.array([[0, first]], np.int32), (B, 1))))
+    t, nd, n = [x.cpu().numpy() for x in call(s)]
+    assert (n == 0).all()
+    np.testing.assert_array_equal(t[:, 0], np.full(B, first + 1))
