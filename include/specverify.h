@@ -373,8 +373,8 @@ enum { SV_F16 = 2 };  /* a dtype of the attention and the cache */
  * over the cache rows j < len[b] of key head e / (heads / kv_heads) and over
  * the nodes j that are i or one of its ancestors.  Softmax statistics and sums
  * are float32; the weights are rounded to the input type before they meet V
- * (fp16: absolutely, by 2^-32 of the row's reference weight, where they are
- * below 2^-21 of it).
+ * (fp16: absolutely, by at most 2^-32 of the row's largest weight, where they
+ * are below 2^-21 of it).
  *
  * With window > 0, node i at depth d has position len + d and sees the cache
  * rows with len + d - j < window, the first `sinks` cache rows, and the nearest

@@ -26,10 +26,10 @@
 //
 // The rounding of the weights is the only one below float32 before the output's
 // own: bf16 2^-8 relative at most; fp16 2^-11 relative, or 2^-32 of the row's
-// reference weight where that is more (below 2^-21 of it).  The maximum is
-// raised only when a row's new scores exceed it by more than 8 (a factor of
-// 2^8), so a key may weigh 256 times the reference; the sum uses the unrounded
-// weights.
+// largest weight where that is more (weights below 2^-21 of it).  The reference
+// m is raised to the largest score (fp16: 7 less) only when a row's new scores
+// exceed it by more than 8 (15), so weights reach 2^8 (2^15) at most; the sum
+// uses the unrounded weights.
 //
 // The tiles of all sequences and key heads form one line that is cut into
 // equal parts (one per workgroup, or per group of workgroups when the rows
@@ -129,12 +129,25 @@ __device__ __forceinline__ float shift_of(float a, float b) {
     return a == b ? 1.f : __builtin_amdgcn_exp2f(a - b);
 }
 
-// Weights are 2^(x - m + kUp), m the running maximum.  float16's normal numbers
-// end at 2^-14: times 2^7 (8 of slack in m: 2^15 at most, of 65504) a long tail
-// behind a dominant key keeps its share of the output, with 2^-25 * 2^-7 lost
-// per key at most.  The sum takes the same factor, so nothing else changes.
+// The reference m is the running maximum less kUp.  float16's normal numbers end
+// at 2^-14: with weights around 2^7 (8 of slack in m: 2^15 at most, of 65504) a
+// long tail behind a dominant key keeps its share of the output, with 2^-25 of
+// 2^m, 2^-32 of the largest weight, lost per key at most.
 template <int DT>
 constexpr float kUp = DT == DT_BF16 ? 0.f : 7.f;
+
+// A score and what is left of it above the reference, rounded each: fused, the
+// row's largest score would come out as its rounding (not small beside 1 from
+// 2^24 on, 2^128 and an infinite weight from 2^31 on) instead of 0.  Time with
+// the two: wide trees 557 us, 554 fused; the other shapes alike.
+__device__ __forceinline__ float scaled(float x, float scale2) {
+#pragma clang fp contract(off)
+    return x * scale2;
+}
+__device__ __forceinline__ float less(float x, float ref) {
+#pragma clang fp contract(off)
+    return x - ref;
+}
 
 // What rows that do not exist, and dimensions past D, are staged from.
 __device__ const uint4 kZero = {0, 0, 0, 0};
@@ -642,9 +655,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) top = fmaxf(top, x[ks][i]);
                     }
-                    top = half_max(top) * scale2;
-                    if (__any(top > mx + 8.f)) {
-                        const float mn = fmaxf(mx, top);
+                    top = scaled(half_max(top), scale2);
+                    if (__any(top - mx > kUp<DT> + 8.f)) {
+                        const float mn = fmaxf(mx, top - kUp<DT>);
                         const float a = shift_of(mx, mn);
                         l *= a;
 #pragma unroll
@@ -653,12 +666,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attn(TreeAttnParams p) {
                             for (int i = 0; i < 16; ++i) o[dt][i] *= a;
                         mx = mn;
                     }
-                    const float ref = (mx == -INFINITY ? 0.f : mx) - kUp<DT>;
+                    const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            x[ks][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[ks][i], scale2, -ref));
+                            x[ks][i] = __builtin_amdgcn_exp2f(less(scaled(x[ks][i], scale2), ref));
                             l += x[ks][i];
                         }
 #pragma unroll

@@ -345,3 +345,31 @@ def test_tables_of_ever_new_widths_keep_a_bounded_record():
     torch.cuda.synchronize()
     assert len(binding._workspaces) <= 1024
     check(s, "1200 pages wide")
+
+
+@pytest.mark.parametrize("dtype,size,far", [(torch.bfloat16, 60, 4), (torch.bfloat16, 30, 10), (torch.bfloat16, 8, 8),
+                                            (torch.float16, 15, 14), (torch.float16, 12, 11), (torch.float16, 8, 4)])
+@pytest.mark.parametrize("N,H", [(2, 8), (8, 8), (16, 8)])  # 16, 64 and 128 rows per key head
+@pytest.mark.parametrize("lens", [(190,), (3001,)])
+def test_scores_beyond_the_float32_spacing(lens, N, H, dtype, size, far):
+    """Scores so large that float32 keeps no fraction of them: the key of the
+    largest one (its neighbours in the input type are far below it) has all the
+    weight, and its value is the output, exactly."""
+    s = make(B=1, N=N, H=H, Hkv=1, kind="chain", lens=lens, dtype=dtype, poison=False)
+    rng = np.random.default_rng(3)
+    n, D = lens[0], s["q"].shape[-1]
+    for name in ("q", "k", "kt"):
+        s[name].zero_()
+    s["q"][..., 0] = 2.0 ** size
+    x = rng.permutation(n)  # one key of 3.5 * 2^far, the others from 1 to 2 times that power
+    pages, slots = s["table"][0, np.arange(n) // 16].long(), torch.from_numpy(np.arange(n) % 16).cuda()
+    s["k"][pages, slots, 0, 0] = dev(np.where(x == 0, 3.5, 1 + x / n) * 2.0 ** far, dtype)
+    top = int((x == 0).argmax())
+    s["q"][0, 1:, :, 0] *= -1  # for the other nodes the root's, the only one below zero
+    s["kt"][0, :, 0, 0] = 8.0
+    s["kt"][0, 0, 0, 0] = -8.0
+    out = call(s, scale=0.3)
+    torch.cuda.synchronize()
+    root = s["v"][pages[top], slots[top], 0]
+    assert torch.equal(out[0, 0], root.expand(H, D))
+    assert torch.equal(out[0, 1:], s["vt"][0, 0, 0].expand(N - 1, H, D))
