@@ -19,6 +19,8 @@ Readings taken where the pages are silent:
   * free pages are taken lowest number first, in the order of the sequences.
 """
 
+from collections import Counter
+
 import numpy as np
 
 
@@ -201,8 +203,8 @@ def cache_commit(k, v, table, lens, k_tree, v_tree, nodes, n_accepted):
         rows.append(live)
         move.append(at)
     # a page that is appended to belongs to one sequence only
-    named = [x for r in rows for x in r]
-    if any(at and lens[b] % ps and named.count(rows[b][-1]) > 1 for b, at in enumerate(move)):
+    named = Counter(x for r in rows for x in r)
+    if any(at and lens[b] % ps and named[rows[b][-1]] > 1 for b, at in enumerate(move)):
         return _unchanged(table, lens, ps, -1)
     free = _lowest_free(rows, pages)
     need = [_blocks(int(lens[b]) + len(move[b]), ps) - len(rows[b]) for b in range(B)]

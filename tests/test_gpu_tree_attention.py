@@ -373,3 +373,54 @@ def test_scores_beyond_the_float32_spacing(lens, N, H, dtype, size, far):
     root = s["v"][pages[top], slots[top], 0]
     assert torch.equal(out[0, 0], root.expand(H, D))
     assert torch.equal(out[0, 1:], s["vt"][0, 0, 0].expand(N - 1, H, D))
+
+
+def test_largest_batches_and_row_counts():
+    """The limits the header states: 65536 sequences, 65536 query rows per key
+    head, an empty table, windows and sinks up to 2^31 - 1."""
+    B = 65536
+    for width in (1, 300):  # whole parts, and parts over several sequences
+        s = make(B=2, N=1, H=2, Hkv=1, D=8, lens=(9, 16), ps=16, poison=False)
+        lens = torch.arange(B, dtype=torch.int32, device="cuda") % 17
+        q = torch.randn((B, 1, 2, 8), device="cuda").bfloat16()
+        kt, vt = torch.randn((B, 1, 1, 8), device="cuda").bfloat16(), torch.randn((B, 1, 1, 8), device="cuda").bfloat16()
+        table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+        table[:, 0] = torch.arange(B, device="cuda") % s["k"].shape[0]
+        out = binding.tree_attention(q, s["k"], s["v"], table, lens, kt, vt,
+                                     torch.full((B, 1), -1, dtype=torch.int32, device="cuda"))
+        kk = torch.cat((s["k"][table[:, 0].long(), :, 0], kt[:, :, 0]), 1).double()
+        vv = torch.cat((s["v"][table[:, 0].long(), :, 0], vt[:, :, 0]), 1).double()
+        x = (kk.unsqueeze(1) * q[:, 0].double().unsqueeze(2)).sum(-1) * 8 ** -0.5  # [B, heads, 17]
+        j = torch.arange(17, device="cuda")
+        x = torch.where((j < lens.view(B, 1, 1)) | (j == 16), x, -torch.inf)
+        w = torch.softmax(x, -1)
+        want = (w.unsqueeze(-1) * vv.unsqueeze(1)).sum(2)
+        spread = (w.unsqueeze(-1) * vv.abs().unsqueeze(1)).sum(2)
+        tol = 2.0 ** -8 * (spread + want.abs()) * 1.01 + 1e-30  # two roundings; float32's are 2^-14 of them
+        assert ((out[:, 0].double() - want).abs() <= tol).all(), width
+    s = make(B=1, N=64, H=1024, Hkv=1, D=8, lens=(70,), ps=16)
+    check(s, "65536 rows")
+    s = make(B=3, N=5, lens=(0, 0, 0))
+    s["table"] = torch.empty((3, 0), dtype=torch.int32, device="cuda")
+    check(s, "an empty table")
+    s = make(B=2, N=5, lens=(200, 40))
+    plain = call(s)
+    big = 2 ** 31 - 1
+    for kw in (dict(window=big), dict(window=big, sinks=big), dict(window=1, sinks=big)):
+        out = call(s, **kw)
+        torch.cuda.synchronize()
+        if kw["window"] == big:
+            assert torch.equal(out, plain)
+        else:
+            check(s, "all sinks", **kw)
+
+
+def test_expanded_inputs():
+    """One set of rows for all sequences and one key head for all."""
+    s = make(B=3, N=4, H=4, Hkv=2, D=64, lens=(50, 9, 31), poison=False)
+    e = dict(s, q=s["q"][:1].expand(3, -1, -1, -1), kt=s["kt"][:, :, :1].expand(-1, -1, 2, -1),
+             vt=s["vt"][:, :1].expand(-1, 4, -1, -1), k=s["k"][:, :, :1].expand(-1, -1, 2, -1),
+             table=s["table"][:1].expand(3, -1))
+    got = check(e, "expanded")
+    whole = {n: (t.contiguous() if t is not None else None) for n, t in e.items()}
+    assert torch.equal(call(whole), got)

@@ -281,3 +281,24 @@ def test_commit_after_a_fork_owns_its_pages():
     s["nodes"] = None
     s["n"].fill_(2)
     assert int(check_commit(s)[2]) == 0
+
+
+def test_most_sequences_and_most_layers():
+    """The limits the header states: 65534 sequences, 65534 layers."""
+    rng = np.random.default_rng(2)
+    B = 65534
+    s = make(rng.integers(0, 8, B), N=2, ps=2, layers=1, Hkv=1, D=8, spare=2 * B, extra=2)
+    assert int(check_commit(s)[2]) == 0
+    s["n"].fill_(-1)
+    anc = rng.integers(-1, B, B)
+    assert int(check_fork(s, anc)[2]) == 0
+    s = make([3, 0, 2], N=3, ps=2, layers=65534, Hkv=1, D=8, spare=8)
+    assert int(check_commit(s)[2]) == 0
+    assert int(check_fork(s, [0, 0, 2])[2]) == 0
+
+
+def test_expanded_tree_rows():
+    """The same tree rows for every sequence and head."""
+    s = make([5, 100, 0, 31], Hkv=4)
+    s["kt"], s["vt"] = s["kt"][:, :1, :, :1].expand(-1, 4, -1, 4, -1), s["vt"][:, :, :, 1:2].expand(-1, -1, -1, 4, -1)
+    assert int(check_commit(s)[2]) == 0

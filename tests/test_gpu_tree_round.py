@@ -4,6 +4,9 @@ paged cache, verifies and commits for several rounds.  Every call is compared
 with the oracle on the inputs it had, and at the end the cache must hold, page
 by page, the rows of the tokens that were accepted and nothing of the others."""
 
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -285,3 +288,37 @@ def test_a_count_past_the_tree_appends_nothing():
         table, lens, status = binding.cache_commit(s["k"], s["v"], s["table"], s["lens"], kt, kt, None, counts)
         assert int(status) == -1 and int(lens.abs().sum()) == 0 and bool((table == -1).all())
         assert bool(torch.isnan(s["k"]).all())
+
+
+def test_first_call_of_a_process_captured():
+    """Nothing has to run before the first capture."""
+    code = '''
+import torch
+from rejection_sampling_verifier_amd import binding as b
+z = lambda *s: torch.randn(s, device="cuda").bfloat16()
+i = lambda v, *s: torch.full(s, v, dtype=torch.int32, device="cuda")
+q, kc, vc, kt, vt = z(2, 3, 8, 128), z(1, 40, 64, 2, 128), z(1, 40, 64, 2, 128), z(1, 2, 3, 2, 128), z(1, 2, 3, 2, 128)
+table = torch.arange(40, dtype=torch.int32, device="cuda").view(2, 20)
+lens, par = i(700, 2), i(0, 2, 3)
+p, u = torch.softmax(torch.randn((2, 3, 30000), device="cuda"), -1), torch.rand((2, 3), device="cuda")
+tok, uf = i(7, 2, 3), u[:, 0].contiguous()
+torch.cuda.synchronize()
+def step():
+    o = b.tree_attention(q, kc[0], vc[0], table, lens, kt[0], vt[0], par)
+    t = b.verify_tree(p, p[:, :1], tok, par, u, uf)
+    c = b.cache_commit(kc, vc, table, lens, kt, vt, t[1], t[2])
+    f = b.cache_fork(kc, vc, c[0], c[1], par[:, 0].contiguous())
+    return (o, *t, *c, *f)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    outs = step()
+for _ in range(3):
+    g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(outs, step()):
+        assert torch.equal(x, y)
+torch.cuda.synchronize()
+print("captured")
+'''
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "captured" in r.stdout, (r.returncode, r.stderr[-2000:])

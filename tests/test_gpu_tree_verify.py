@@ -254,3 +254,30 @@ def test_draw_at_zero_is_the_first_id_with_weight(B, V, first, dtype):
     t, nd, n = [x.cpu().numpy() for x in call(s)]
     assert (n == 0).all()
     np.testing.assert_array_equal(t[:, 0], np.full(B, first + 1))
+
+
+def test_largest_batch():
+    """2^22 - 1 sequences of one node: the token is the inverse CDF's."""
+    B, V = (1 << 22) - 1, 3
+    g = torch.Generator(device="cuda").manual_seed(0)
+    p = torch.rand((B, 1, V), device="cuda", generator=g)
+    uf = torch.rand((B,), device="cuda", generator=g)
+    z = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    t, nd, n = binding.verify_tree(p, None, z, z, torch.zeros((B, 1), device="cuda"), uf)
+    cum = p[:, 0].double().cumsum(-1)
+    at = uf.double() * cum[:, -1]
+    clear = ((cum[:, :2] - at.view(B, 1)).abs() > 1e-12).all(-1)
+    assert clear.float().mean() > 0.999
+    want = (cum[:, :2] <= at.view(B, 1)).sum(-1).int()
+    assert torch.equal(t[clear, 0], want[clear])
+    assert not nd.any() and not n.any()
+
+
+@pytest.mark.parametrize("draft", [True, False])
+def test_expanded_inputs(draft):
+    """One set of rows for all sequences; one row for all nodes."""
+    s = make(5, 9, 2003, draft=draft, seed=6)
+    e = dict(s, p=s["p"][:1].expand(5, -1, -1), q=s["q"][:1, :1].expand(5, 8, -1) if draft else None)
+    check(e, "expanded over the batch")
+    e = dict(s, p=s["p"][:, :1].expand(-1, 9, -1))
+    check(e, "expanded over the nodes")
