@@ -113,7 +113,7 @@ enum {
     SV_ESHAPE = -2,   /* B, K or V out of range, or the two tensors disagree */
     SV_EDTYPE = -3,   /* unknown dtype, or target and draft dtypes differ */
     SV_EHIP = -4,     /* a HIP runtime call failed; see spec_verify_strerror */
-    SV_ENOMEM = -5,   /* scratch allocation failed */
+    SV_ENOMEM = -5,   /* an allocation failed (scratch, or host memory) */
     SV_EALIGN = -6,   /* a pointer is not aligned to its element size */
     SV_ECAPTURE = -7, /* the stream is being captured and the scratch would have to grow */
     SV_ETOOBIG = -8   /* spec_verify_noalloc: the call needs more than its fixed scratch;

@@ -203,6 +203,17 @@ int get_scratch(hipStream_t stream, size_t bytes, void** data) {
     return SV_OK;
 }
 
+// What a C entry point returns: no exception passes it (a host allocation that
+// fails, for a message or a map's entry).
+template <typename F>
+auto entry(F&& call) noexcept -> decltype(call()) {
+    try {
+        return call();
+    } catch (...) {
+        return SV_ENOMEM;
+    }
+}
+
 template <typename F>
 int timed_launch(int kind, hipStream_t stream, F&& launch) {
     EvPair ev{nullptr, nullptr, kind};
@@ -901,15 +912,19 @@ extern "C" {
 int spec_verify(const sv_logits* target_logits, const sv_logits* draft_logits, const int32_t* draft_tokens,
                 const int32_t* draft_len, float temperature, float top_p, uint64_t seed, int32_t* out_tokens,
                 int32_t* out_n_accepted, void* stream) {
-    return verify_impl(target_logits, draft_logits, draft_tokens, draft_len, temperature, top_p, seed, out_tokens,
-                       out_n_accepted, nullptr, nullptr, stream);
+    return entry([&] {
+        return verify_impl(target_logits, draft_logits, draft_tokens, draft_len, temperature, top_p, seed, out_tokens,
+                           out_n_accepted, nullptr, nullptr, stream);
+    });
 }
 
 int spec_verify_noalloc(const sv_logits* target_logits, const sv_logits* draft_logits, const int32_t* draft_tokens,
                         const int32_t* draft_len, float temperature, float top_p, uint64_t seed, int32_t* out_tokens,
                         int32_t* out_n_accepted, void* stream) {
-    return verify_noalloc_impl(target_logits, draft_logits, draft_tokens, draft_len, temperature, top_p, seed,
-                               out_tokens, out_n_accepted, stream);
+    return entry([&] {
+        return verify_noalloc_impl(target_logits, draft_logits, draft_tokens, draft_len, temperature, top_p, seed,
+                                   out_tokens, out_n_accepted, stream);
+    });
 }
 
 int spec_verify_probe(const sv_logits* target_logits, const sv_logits* draft_logits, const int32_t* draft_tokens,
@@ -918,69 +933,91 @@ int spec_verify_probe(const sv_logits* target_logits, const sv_logits* draft_log
                       void* stream) {
     if (!probe_pos || !probe_row) return SV_EINVAL;
     if (misaligned(probe_pos, 8) || misaligned(probe_row, 8)) return SV_EALIGN;
-    return verify_impl(target_logits, draft_logits, draft_tokens, draft_len, temperature, top_p, seed, out_tokens,
-                       out_n_accepted, probe_pos, probe_row, stream);
+    return entry([&] {
+        return verify_impl(target_logits, draft_logits, draft_tokens, draft_len, temperature, top_p, seed, out_tokens,
+                           out_n_accepted, probe_pos, probe_row, stream);
+    });
 }
 
 int spec_greedy_verify(const sv_logits* target_logits, const int32_t* draft_tokens, const int32_t* draft_len,
                        int32_t k, int32_t* out_tokens, int32_t* out_n_accepted, int32_t* out_topk, void* stream) {
-    return greedy_impl(target_logits, draft_tokens, draft_len, k, out_tokens, out_n_accepted, out_topk, stream);
+    return entry([&] {
+        return greedy_impl(target_logits, draft_tokens, draft_len, k, out_tokens, out_n_accepted, out_topk, stream);
+    });
 }
 
 int spec_hispec_verify(const sv_logits* final_logits, const sv_logits* inter_logits, const sv_logits* draft_logits,
                        const int32_t* draft_tokens, const int32_t* draft_len, float temperature, float top_p,
                        uint64_t seed, int32_t* out_tokens, int32_t* out_n_accepted, int32_t* out_n_stage1,
                        void* stream) {
-    return hispec_impl(final_logits, inter_logits, draft_logits, draft_tokens, draft_len, temperature, top_p, seed,
-                       out_tokens, out_n_accepted, out_n_stage1, stream);
+    return entry([&] {
+        return hispec_impl(final_logits, inter_logits, draft_logits, draft_tokens, draft_len, temperature, top_p, seed,
+                           out_tokens, out_n_accepted, out_n_stage1, stream);
+    });
 }
 
 int spec_smc_step(const sv_logits* target_logits, const sv_logits* draft_logits, const int32_t* draft_tokens,
                   const double* logw_in, float temperature, double ess_fraction, uint64_t seed, int32_t* out_bonus,
                   double* out_logw, int32_t* out_ancestor, double* out_ess, int32_t* out_resampled, void* stream) {
-    return smc_impl(target_logits, draft_logits, draft_tokens, logw_in, temperature, ess_fraction, seed, out_bonus,
-                    out_logw, out_ancestor, out_ess, out_resampled, stream);
+    return entry([&] {
+        return smc_impl(target_logits, draft_logits, draft_tokens, logw_in, temperature, ess_fraction, seed, out_bonus,
+                        out_logw, out_ancestor, out_ess, out_resampled, stream);
+    });
 }
 
 int spec_draft_produce(const sv_logits* target_logits, int32_t K, uint64_t seed, void* draft_out,
                        int64_t out_stride_b, int64_t out_stride_p, int32_t* out_tokens, void* stream) {
-    return produce_impl(target_logits, K, seed, draft_out, out_stride_b, out_stride_p, out_tokens, stream);
+    return entry([&] {
+        return produce_impl(target_logits, K, seed, draft_out, out_stride_b, out_stride_p, out_tokens, stream);
+    });
 }
 
-int spec_tree_attention(const sv_tree_attention* args, void* stream) { return tree_attention_impl(args, stream); }
+int spec_tree_attention(const sv_tree_attention* args, void* stream) {
+    return entry([&] {
+        return tree_attention_impl(args, stream);
+    });
+}
 
 int64_t spec_tree_attention_workspace(const sv_tree_attention* args) {
-    TreePlan t;
-    const int rc = plan_tree(args, t);
-    return rc ? rc : static_cast<int64_t>(t.total);
+    return entry([&] {
+        TreePlan t;
+        const int rc = plan_tree(args, t);
+        return rc ? rc : static_cast<int64_t>(t.total);
+    });
 }
 
 int spec_verify_tree(const sv_logits* target_probs, const sv_logits* draft_probs, const int32_t* tokens,
                      const int32_t* parent, const int32_t* n_nodes, const float* u_accept, const float* u_final,
                      int32_t* out_tokens, int32_t* out_nodes, int32_t* out_n_accepted, void* workspace,
                      int64_t workspace_bytes, void* stream) {
-    return verify_tree_impl(target_probs, draft_probs, tokens, parent, n_nodes, u_accept, u_final, out_tokens,
-                            out_nodes, out_n_accepted, workspace, workspace_bytes, stream);
+    return entry([&] {
+        return verify_tree_impl(target_probs, draft_probs, tokens, parent, n_nodes, u_accept, u_final, out_tokens,
+                                out_nodes, out_n_accepted, workspace, workspace_bytes, stream);
+    });
 }
 
 int64_t spec_verify_tree_workspace(int32_t B, int32_t N, int32_t V, int32_t dtype, int32_t draft) {
     if (dtype != SV_F32 && dtype != SV_BF16) return SV_EDTYPE;
     if (B < 1 || B >= 1 << 22 || N < 1 || N > SPECVERIFY_MAX_NODES || V < 1 || V > SPECVERIFY_MAX_V) return SV_ESHAPE;
-    return verify_workspace(B, N, verify_team(B, V, dtype, draft != 0));
+    return entry([&] { return verify_workspace(B, N, verify_team(B, V, dtype, draft != 0)); });
 }
 
 int spec_cache_commit(const sv_cache* cache, const void* k_tree, const void* v_tree, const int64_t k_tree_stride[4],
                       const int64_t v_tree_stride[4], int32_t N, const int32_t* nodes, const int32_t* n_accepted,
                       int32_t* out_table, int64_t out_stride, int32_t* out_len, int32_t* out_status, void* workspace,
                       int64_t workspace_bytes, void* stream) {
-    return cache_impl(cache, k_tree, v_tree, k_tree_stride, v_tree_stride, N, nodes, n_accepted, nullptr, false,
-                      out_table, out_stride, out_len, out_status, workspace, workspace_bytes, stream);
+    return entry([&] {
+        return cache_impl(cache, k_tree, v_tree, k_tree_stride, v_tree_stride, N, nodes, n_accepted, nullptr, false,
+                          out_table, out_stride, out_len, out_status, workspace, workspace_bytes, stream);
+    });
 }
 
 int spec_cache_fork(const sv_cache* cache, const int32_t* ancestor, int32_t* out_table, int64_t out_stride,
                     int32_t* out_len, int32_t* out_status, void* workspace, int64_t workspace_bytes, void* stream) {
-    return cache_impl(cache, nullptr, nullptr, nullptr, nullptr, 0, nullptr, nullptr, ancestor, true, out_table,
-                      out_stride, out_len, out_status, workspace, workspace_bytes, stream);
+    return entry([&] {
+        return cache_impl(cache, nullptr, nullptr, nullptr, nullptr, 0, nullptr, nullptr, ancestor, true, out_table,
+                          out_stride, out_len, out_status, workspace, workspace_bytes, stream);
+    });
 }
 
 int64_t spec_cache_workspace(int32_t B, int32_t N, int32_t page_size) {
@@ -995,7 +1032,7 @@ const char* spec_verify_strerror(int status) {
         case SV_ESHAPE: return "invalid shape (B, K, V out of range or target/draft mismatch)";
         case SV_EDTYPE: return "invalid or mismatched dtype";
         case SV_EHIP: return g_hip_msg.empty() ? "HIP runtime error" : g_hip_msg.c_str();
-        case SV_ENOMEM: return "scratch allocation failed";
+        case SV_ENOMEM: return "an allocation failed";
         case SV_EALIGN: return "pointer not aligned to its element size (tree and cache rows: to 16 bytes)";
         case SV_ECAPTURE: return "the stream is being captured and the call would have to grow its scratch";
         case SV_ETOOBIG:
@@ -1020,8 +1057,10 @@ int spec_verify_stream_read(const void* buf, int64_t bytes, uint32_t* sink, int 
     if (!buf || !sink || bytes < 16) return SV_EINVAL;
     if (misaligned(buf, 16) || misaligned(sink, 4)) return SV_EALIGN;
     if (unroll != 2 && unroll != 4 && unroll != 8) return SV_EINVAL;
-    const hipError_t e = sv::launch_stream_read(buf, bytes, sink, unroll, static_cast<hipStream_t>(stream));
-    return e == hipSuccess ? SV_OK : hip_fail(e, "stream read launch");
+    return entry([&] {
+        const hipError_t e = sv::launch_stream_read(buf, bytes, sink, unroll, static_cast<hipStream_t>(stream));
+        return e == hipSuccess ? SV_OK : hip_fail(e, "stream read launch");
+    });
 }
 
 int spec_verify_profile_enable(int enable) {
@@ -1032,30 +1071,32 @@ int spec_verify_profile_enable(int enable) {
 
 int spec_verify_profile_read(double* ms, int64_t* launches, int n) {
     if (n < 0 || (n > 0 && (!ms || !launches))) return SV_EINVAL;
-    std::vector<EvPair> evs;
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        evs.swap(g_events);
-    }
-    const int kinds = n < sv::KK_ALL ? n : static_cast<int>(sv::KK_ALL);
-    for (int k = 0; k < kinds; ++k) {
-        ms[k] = 0.0;
-        launches[k] = 0;
-    }
-    int rc = SV_OK;
-    for (const EvPair& e : evs) {
-        float t = 0.f;
-        hipError_t err = hipEventSynchronize(e.b);
-        if (err == hipSuccess) err = hipEventElapsedTime(&t, e.a, e.b);
-        if (err != hipSuccess) rc = hip_fail(err, "hipEventElapsedTime");
-        if (e.kind < kinds) {
-            ms[e.kind] += t;
-            launches[e.kind] += 1;
+    return entry([&] {
+        std::vector<EvPair> evs;
+        {
+            std::lock_guard<std::mutex> lk(g_mu);
+            evs.swap(g_events);
         }
-        (void)hipEventDestroy(e.a);
-        (void)hipEventDestroy(e.b);
-    }
-    return rc == SV_OK ? kinds : rc;
+        const int kinds = n < sv::KK_ALL ? n : static_cast<int>(sv::KK_ALL);
+        for (int k = 0; k < kinds; ++k) {
+            ms[k] = 0.0;
+            launches[k] = 0;
+        }
+        int rc = SV_OK;
+        for (const EvPair& e : evs) {
+            float t = 0.f;
+            hipError_t err = hipEventSynchronize(e.b);
+            if (err == hipSuccess) err = hipEventElapsedTime(&t, e.a, e.b);
+            if (err != hipSuccess) rc = hip_fail(err, "hipEventElapsedTime");
+            if (e.kind < kinds) {
+                ms[e.kind] += t;
+                launches[e.kind] += 1;
+            }
+            (void)hipEventDestroy(e.a);
+            (void)hipEventDestroy(e.b);
+        }
+        return rc == SV_OK ? kinds : rc;
+    });
 }
 
 }  // extern "C"

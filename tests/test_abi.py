@@ -6,6 +6,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 
@@ -184,3 +185,60 @@ def test_release_without_scratch_is_harmless(lib):
     lib.spec_verify_release()
     lib.spec_verify_release()
     assert lib.spec_verify_abi_version() == 1
+
+
+_THROWING_NEW = r"""
+#include <cstdlib>
+#include <new>
+static bool failing = false;
+extern "C" void fail_new(int on) { failing = on != 0; }
+void* operator new(std::size_t n) {
+    void* p = failing ? nullptr : std::malloc(n);
+    if (!p) throw std::bad_alloc();
+    return p;
+}
+void operator delete(void* p) noexcept { std::free(p); }
+void operator delete(void* p, std::size_t) noexcept { std::free(p); }
+"""
+
+_CALLS_WITHOUT_MEMORY = r"""
+import ctypes, sys
+new, lib = ctypes.CDLL(sys.argv[1]), ctypes.CDLL(sys.argv[2])
+i32, i64, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+def logits(at, dtype, B, P, V):
+    return ctypes.create_string_buffer(__import__("struct").pack("@Piiiiqq", at, dtype, B, P, V, P * V, V))
+t, d = logits(0x1000, 0, 2, 4, 100), logits(0x2000, 0, 2, 3, 100)
+cache = ctypes.create_string_buffer(__import__("struct").pack(
+    "@PPiiiiii4q4qPqPii", 0x10000, 0x20000, 1, 2, 50, 16, 2, 64, 65536, 2048, 128, 64, 65536, 2048, 128, 64, 0x30000, 9,
+    0x40000, 3, 9))
+strides = (i64 * 4)(4096, 2048, 512, 64)
+calls = {
+    "verify": lambda: lib.spec_verify(t, d, vp(0x3000), None, ctypes.c_float(1), ctypes.c_float(1), ctypes.c_uint64(0),
+                                      vp(0x4000), vp(0x5000), None),
+    "tree": lambda: lib.spec_verify_tree(t, d, *[vp(0x3000 + 0x1000 * i) for i in range(9)], i64(1 << 30), None),
+    "commit": lambda: lib.spec_cache_commit(cache, vp(0x50000), vp(0x60000), strides, strides, i32(4), vp(0x70000),
+                                            vp(0x80000), vp(0x90000), i64(9), vp(0xA0000), vp(0xB0000), vp(0xC0000),
+                                            i64(1 << 20), None),
+    "fork": lambda: lib.spec_cache_fork(cache, vp(0xD0000), vp(0x90000), i64(9), vp(0xA0000), vp(0xB0000), vp(0xC0000),
+                                        i64(1 << 20), None),
+}
+call = calls[sys.argv[3]]
+first = call()
+new.fail_new(1)
+second = call()
+new.fail_new(0)
+print("statuses", first, second, call())
+"""
+
+
+@pytest.mark.parametrize("name", ["verify", "tree", "commit", "fork"])
+def test_no_exception_leaves_an_entry_point(lib, tmp_path, name):
+    """A host allocation that fails inside a call (here for the message of a
+    forced launch failure) is a status, not the end of the process."""
+    so = str(tmp_path / "new.so")
+    (tmp_path / "new.cpp").write_text(_THROWING_NEW)
+    subprocess.run(["g++", "-O1", "-fPIC", "-shared", "-o", so, str(tmp_path / "new.cpp")], check=True)
+    r = subprocess.run([sys.executable, "-c", _CALLS_WITHOUT_MEMORY, so, binding.LIB_PATH, name], capture_output=True,
+                       text=True, env=dict(os.environ, LD_PRELOAD=so, SPECVERIFY_FAIL_LAUNCH="1"))
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+    assert r.stdout.split() == ["statuses", "-4", "-5", "-4"]
