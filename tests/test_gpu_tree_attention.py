@@ -424,3 +424,44 @@ def test_expanded_inputs():
     got = check(e, "expanded")
     whole = {n: (t.contiguous() if t is not None else None) for n, t in e.items()}
     assert torch.equal(call(whole), got)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,H", [(1, 1), (8, 8), (16, 8)])
+def test_the_longest_cache(N, H, dtype):
+    """2^28 cache rows: a table of 2^18 pages that are all one of two, so that
+    the softmax is that of two pages, each key 2^17 times.
+
+    The sums are float32: a wave adds its weights key by key (32 lanes' worth at
+    a time), up to 2^28 / 512 parts / 4 keys of one row, each rounding at most
+    2^-24 of the running sum, and the matrix unit's sums 2^-23; relative to
+    sums of positive terms 2^17 * 2^-23 at worst, where roundings do not cancel.
+    They do: 2^-9 (their square root times 2^-1) is allowed beside the roundings
+    to the input type."""
+    D, ps, width = 64, 1024, 1 << 18
+    s = make(B=1, N=N, H=H, Hkv=1, D=D, kind="chain", lens=(2 * ps,), ps=ps, dtype=dtype, poison=False)
+    two = s["table"][0, :2].clone()
+    s["table"] = two.repeat(width // 2).view(1, width).contiguous()
+    s["lens"].fill_(1 << 28)
+    out = call(s)
+    torch.cuda.synchronize()
+    k = torch.cat((s["k"][two.long()].reshape(-1, D), s["kt"][0, :, 0])).double()
+    v = torch.cat((s["v"][two.long()].reshape(-1, D), s["vt"][0, :, 0])).double()
+    x = (s["q"][0].double().reshape(-1, D).mm(k.t().contiguous()) * D ** -0.5).view(N, H, -1)
+    w = torch.exp(x - x.amax(-1, keepdim=True))
+    w[..., :2 * ps] *= width // 2
+    w[..., 2 * ps:] *= (torch.arange(N, device="cuda").view(1, N) <= torch.arange(N, device="cuda").view(N, 1)).unsqueeze(1)
+    w /= w.sum(-1, keepdim=True)
+    want, spread = (w.view(N * H, -1).mm(t) for t in (v, v.abs()))
+    err = (out[0].double().view(N * H, D) - want).abs()
+    h = torch.finfo(dtype).eps / 2
+    assert (err <= (h + 2.0 ** -9) * spread + h * want.abs() + 1e-6).all(), float((err / spread).max())
+    # a window of all but the first rows, and of a few rows at the end
+    for window in ((1 << 28) - 100, 3000):
+        part = call(s, window=window, sinks=5)
+        torch.cuda.synchronize()
+        assert torch.isfinite(part).all()
+    near = dict(s, table=s["table"][:, :4].contiguous(), lens=torch.full((1,), 4 * ps, dtype=torch.int32, device="cuda"))
+    a, b = call(s, window=3000), call(near, window=3000)
+    torch.cuda.synchronize()
+    assert ((a.double() - b.double()).abs() <= 4 * h * spread.amax().item()).all()
