@@ -750,6 +750,10 @@ int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
 // passes: one sequence of V = 128256 (float32, trees of two drawn children) 19
 // us with sixteen and 30 with one, 64 of them 37 with four and 63 with one.
 // Without draft probabilities there is one pass (one sequence: 16 and 13 us).
+// From 65 sequences on there is no team: with one / two / three workgroups each,
+// trees of 16 drawn nodes take 44 / 38 / 37 us (65 sequences), 56 / 46 / 47 (96),
+// 66 / 55 / 64 (128), 73 / 73 / 82 (192), in bfloat16 41 / 35 / 32, 47 / 39 / 39,
+// 47 / 42 / 51, 50 / 56 / 62: teams of two up to 128 would gain an eighth.
 int verify_team(int B, int V, int dtype, bool draft) {
     if (!draft) return 1;
     int team = device_cus() / B;

@@ -68,8 +68,11 @@ struct PlanArrays {
 constexpr int kOwn = -2;  // such a page is there, not read yet (-1: there is none)
 
 // SMALL: one thread per sequence.  Loads are issued for many sequences or
-// entries at a time; what the kernel costs is a chain of three memory
-// latencies (lengths, tables, writes), about 2 us, and the launch.
+// entries at a time; what the kernel costs for a pool of a few thousand pages is
+// a chain of three memory latencies (lengths, tables, writes), the barriers and
+// the launch: 4 to 7 us.  Looking for free pages, each thread at its run of the
+// bitmap page by page, outgrows that in larger pools: commit 41 us at 65536
+// pages and 0.56 ms at 2^20 (fork 32 us and 0.44 ms).
 template <bool SMALL>
 __global__ __launch_bounds__(kPlanThreads) void k_cache_plan(CacheParams p) {
     extern __shared__ uint32_t used[];  // W words

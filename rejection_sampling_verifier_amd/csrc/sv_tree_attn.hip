@@ -41,7 +41,7 @@
 // What bounds it: up to 64 rows per key head the cache's bytes (64 sequences of
 // 8192 rows, 8 key heads of 128: 2.1 GB at 5.9 TB/s with 4 to 24 rows, 5.5 with
 // 64, of the 7.1 a plain read reaches; 13 TB/s where the rows come from the L2),
-// then the matrix instructions and the softmax between them (128 rows 650
+// then the matrix instructions and the softmax between them (128 rows 620
 // TFLOP/s, 256 rows 740).  A workgroup's two stages keep 32 KB (64 KB with 32
 // rows) of K and V under way while the tile before is computed.  Separate slots
 // for K and V, refilled one by one, made more instructions and ran 4 to 12 %
