@@ -724,8 +724,9 @@ int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
     // beyond every length and depth both mean everything; the kernel subtracts row numbers from them
     p.window = std::min(a->window, 1 << 29);
     p.sinks = std::min(a->sinks, 1 << 29);
-    // (-inf) * scale2 has to stay -inf: no zero, no denormal
-    p.scale2 = static_cast<float>(std::fabs(static_cast<double>(a->scale)) * 1.4426950408889634074);
+    // (-inf) * scale2 has to stay -inf, and 0 * scale2 0: no zero, no denormal, not infinite
+    p.scale2 = static_cast<float>(
+        std::min(std::fabs(static_cast<double>(a->scale)) * 1.4426950408889634074, static_cast<double>(FLT_MAX)));
     if (p.scale2 < FLT_MIN) p.scale2 = FLT_MIN;
     p.flip = a->scale < 0.f ? 1 : 0;
     p.MT = t.MT;

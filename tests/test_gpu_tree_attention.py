@@ -465,3 +465,20 @@ def test_the_longest_cache(N, H, dtype):
     a, b = call(s, window=3000), call(near, window=3000)
     torch.cuda.synchronize()
     assert ((a.double() - b.double()).abs() <= 4 * h * spread.amax().item()).all()
+
+
+@pytest.mark.parametrize("scale", [3.4e38, -3.4e38, 2.4e38])
+def test_scales_near_the_largest_float(scale):
+    """scale log2(e) lies beyond float32 there: equal scores stay equal, and the
+    key of the largest score has all the weight."""
+    s = make(B=1, N=3, kind="chain", lens=(40,), poison=False)
+    for name in ("q", "k", "kt"):
+        s[name].zero_()
+    check(s, f"scale {scale}", scale=scale)
+    s["q"][..., 0] = 1.0 if scale > 0 else -1.0
+    page = s["table"][0, 1].long()
+    s["k"][page, 3, :, 0] = 2.0 ** -30
+    out = call(s, scale=scale)
+    torch.cuda.synchronize()
+    want = s["v"][page, 3].repeat_interleave(2, 0)
+    assert torch.equal(out[0], want.expand(3, -1, -1))
