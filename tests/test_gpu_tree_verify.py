@@ -281,3 +281,16 @@ def test_expanded_inputs(draft):
     check(e, "expanded over the batch")
     e = dict(s, p=s["p"][:, :1].expand(-1, 9, -1))
     check(e, "expanded over the nodes")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("V", [300, 70001])
+def test_smallest_and_largest_probabilities(V, draft, dtype):
+    """Rows of denormal numbers, and rows (not distributions) near the largest."""
+    for factor in (2.0 ** -130, 2.0 ** 125):
+        s = make(3, 6, V, draft=draft, dtype=dtype, seed=V)
+        s["p"] = (s["p"].double() / s["p"].double().amax() * factor).to(dtype)
+        if draft:
+            s["q"] = (s["q"].double() / s["q"].double().amax() * factor).to(dtype)
+        check(s, f"times {factor:.0e}")
