@@ -564,6 +564,77 @@ int spec_cache_fork(const sv_cache* cache, const int32_t* ancestor, int32_t* out
  * 0), needs. */
 int64_t spec_cache_workspace(int32_t B, int32_t N, int32_t page_size);
 
+/*
+ * ---- Latent rows -----------------------------------------------------------
+ *
+ * Models whose heads share one row per token: its first elements are the latent
+ * vector that keys and values are made of, the rest a part that carries
+ * positions.  A paged cache holds that row only, [pages, page_size, dim].  It is
+ * committed and forked like any cache (spec_cache_commit, spec_cache_fork), its
+ * row's two halves given as k and v.
+ */
+#define SPECVERIFY_MAX_LATENT 576
+
+/*
+ * spec_latent_attention -- attention on the rows themselves (the absorbed form:
+ * queries multiplied into the latent space, results to be multiplied out of
+ * it; spec_head_product does both).  For every sequence b, node i and head e,
+ *
+ *   out[b, i, e] = sum_j softmax_j(scale * q[b, i, e] . c_j) c_j[0 .. dim_v)
+ *
+ * over the cache rows j < len[b] and the nodes j that are i or one of its
+ * ancestors, c_j their rows.  Trees, tables and lengths are spec_tree_attention's,
+ * and so are statistics and roundings.
+ *
+ * dtype          SV_BF16 or SV_F16, of all tensors.
+ * B, N           1 <= B <= 65536 sequences, 1 <= N <= 64 nodes.
+ * heads          at most 1024; B, rounded up to eights, times N * heads / 128, rounded up, below 2^23.
+ * dim, dim_v     multiples of 8; dim <= SPECVERIFY_MAX_LATENT, dim_v <= dim and 512.
+ * q              [B, N, heads, dim]; out [B, N, heads, dim_v]; strides in
+ *                elements for (sequence, node, head).
+ * rows           [B, N, dim], the nodes' own rows (not in the cache yet);
+ *                strides for (sequence, node).
+ * cache          [pages, page_size, dim]; strides for (page, slot).
+ *                The last axis of every tensor is contiguous; data and strides
+ *                are multiples of 16 bytes; strides as spec_tree_attention's.
+ * table, table_stride, len, n_nodes, width, scale, workspace  as spec_tree_attention.
+ * parent         device int32 [B, N], or NULL: node i's parent is node i - 1.
+ *
+ * What a node does not see never reaches its output.  A node that sees a node
+ * (itself included) with an infinity or NaN among its row's first dim_v elements
+ * gets NaN.  The output of an absent node is zero.  out must not overlap the
+ * inputs, nor its rows each other.
+ *
+ * Errors as spec_tree_attention.
+ */
+typedef struct {
+    int32_t dtype;
+    int32_t B, N, heads, dim, dim_v;
+    const void* q;
+    int64_t q_stride[3];
+    const void* rows;
+    int64_t rows_stride[2];
+    const void* cache;
+    int64_t cache_stride[2];
+    int32_t pages, page_size, width;
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* len;
+    const int32_t* parent;
+    const int32_t* n_nodes;
+    float scale;
+    void* out;
+    int64_t out_stride[3];
+    void* workspace;
+    int64_t workspace_bytes;
+} sv_latent_attention;
+
+int spec_latent_attention(const sv_latent_attention* args, void* stream);
+
+/* Bytes of workspace the call needs, from its sizes (pointers are not looked
+ * at); a negative status for sizes the call refuses. */
+int64_t spec_latent_attention_workspace(const sv_latent_attention* args);
+
 /* Human-readable text for a status code (for SV_EHIP, the last HIP error). */
 const char* spec_verify_strerror(int status);
 

@@ -22,12 +22,13 @@ PROBE_POS, PROBE_ROW = 8, 4
 STATUS = {0: "SV_OK", -1: "SV_EINVAL", -2: "SV_ESHAPE", -3: "SV_EDTYPE", -4: "SV_EHIP", -5: "SV_ENOMEM",
           -6: "SV_EALIGN", -7: "SV_ECAPTURE", -8: "SV_ETOOBIG"}
 KERNEL_KINDS = ("stats", "topp", "rows", "smc", "produce", "tree_attention", "tree_join", "verify_clear",
-                "tree_verify", "cache_plan", "cache_copy")
+                "tree_verify", "cache_plan", "cache_copy", "latent_attention", "latent_join")
 
 EXPORTS = ("spec_verify", "spec_verify_noalloc", "spec_verify_probe", "spec_greedy_verify", "spec_hispec_verify", "spec_smc_step",
            "spec_draft_produce",
            "spec_tree_attention", "spec_tree_attention_workspace", "spec_verify_tree", "spec_verify_tree_workspace",
            "spec_cache_commit", "spec_cache_fork", "spec_cache_workspace",
+           "spec_latent_attention", "spec_latent_attention_workspace",
            "spec_verify_strerror",
            "spec_verify_release",
            "spec_verify_abi_version", "spec_verify_profile_enable", "spec_verify_profile_read",
@@ -668,6 +669,87 @@ def cache_fork(k_cache, v_cache, block_table, seq_len, ancestor, *, out_table=No
     ws, need = _cache_workspace(lib, k_cache, B, 0, shape[2])
     _check(lib, call(blob, anc, *ptrs, ws.data_ptr(), need, _raw_stream(index)))
     return outs
+
+
+# ---- latent rows: one row per token, shared by the heads
+
+# sv_latent_attention's fields in order
+_PACK_LATENT = struct.Struct("@iiiiiiP3qP2qP2qiii4xPqPPPf4xP3qPq").pack
+_latent = None
+
+
+def _latent_calls():
+    """The entry points, taking packed argument blocks."""
+    global _latent
+    if _latent is None:
+        lib = load()
+        vp, blob, i64 = ctypes.c_void_p, ctypes.c_char_p, ctypes.c_int64
+
+        def entry(name, args, res=ctypes.c_int):
+            f = lib[name]
+            f.argtypes, f.restype = args, res
+            return f
+
+        _latent = (lib, entry("spec_latent_attention", [blob, vp]),
+                   entry("spec_latent_attention_workspace", [blob], i64))
+    return _latent
+
+
+def _half(t, name):
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
+        raise ValueError(f"{name}: dtype {t.dtype} is not bfloat16 or float16")
+    return t.dtype
+
+
+def latent_attention(q, cache, block_table, seq_len, rows, parent=None, n_nodes=None, *, dim_v, scale, out=None,
+                     stream=None):
+    """Attention of new tokens or a drafted tree's nodes on a paged cache of
+    latent rows and their ancestors' rows (spec_latent_attention).
+
+    q [B, N, heads, dim], cache [pages, page_size, dim] and the nodes' own rows
+    [B, N, dim]: bfloat16 or float16, last axis contiguous, other strides any
+    multiples of 8 elements.  block_table [B, width], seq_len [B], parent
+    [B, N] (None: chains) and n_nodes [B] (None: N nodes each): int32.  Values
+    are the rows' first dim_v elements.  Returns out [B, N, heads, dim_v];
+    absent nodes' rows are zero.
+    """
+    lib, call, size_of = _latent_calls()[:3]
+    if q.dim() != 4 or cache.dim() != 3:
+        raise ValueError("q must be [B, N, heads, dim] and cache [pages, page_size, dim]")
+    dt, index = _half(q, "q"), q.get_device()
+    _no_grad(q, cache, rows)
+    shape = q.shape
+    B, N, heads, dim = shape
+    pages, page_size, _ = cache.shape
+    qs = _rows(q, "q", shape, dt, index)
+    cs = _rows(cache, "cache", (pages, page_size, dim), dt, index)
+    rs = _rows(rows, "rows", (B, N, dim), dt, index)
+    tab, tab_stride = _table(block_table, "block_table", B, index)
+    width = block_table.shape[1]
+    ln = _array(seq_len, "seq_len", (B,), index)
+    par = 0 if parent is None else _array(parent, "parent", (B, N), index)
+    nn = 0 if n_nodes is None else _array(n_nodes, "n_nodes", (B,), index)
+    out_shape = (B, N, heads, dim_v)
+    if out is not None:
+        _rows(out, "out", out_shape, dt, index)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return latent_attention(q, cache, block_table, seq_len, rows, parent, n_nodes, dim_v=dim_v, scale=scale,
+                                    out=out)
+    if out is None:
+        out = q.new_empty(out_shape)
+    os = out.stride()
+
+    def block(ws, need):
+        return _PACK_LATENT(_DTYPES[dt], B, N, heads, dim, dim_v, q.data_ptr(), qs[0], qs[1], qs[2], rows.data_ptr(),
+                            rs[0], rs[1], cache.data_ptr(), cs[0], cs[1], pages, page_size, width, tab, tab_stride, ln,
+                            par, nn, scale, out.data_ptr(), os[0], os[1], os[2], ws, need)
+
+    need = _workspace_bytes(lib, ("latent", index, B, N, heads, dim, dim_v, page_size, width),
+                            lambda: size_of(block(0, 0)))
+    ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+    _check(lib, call(block(ws.data_ptr() if need else 0, need), _raw_stream(index)))
+    return out
 
 
 def profile_enable(on=True):

@@ -19,6 +19,7 @@
 
 #include "../../include/specverify.h"
 #include "sv_internal.h"
+#include "sv_latent.h"
 #include "sv_tree.h"
 
 namespace {
@@ -616,6 +617,13 @@ bool expanded(const I* stride, const int32_t* size, int n) {
     return false;
 }
 
+// |scale| log2(e).  (-inf) times it has to stay -inf, and 0 times it 0: no zero, no denormal, not infinite.
+float score_scale(float scale) {
+    const float s = static_cast<float>(
+        std::min(std::fabs(static_cast<double>(scale)) * 1.4426950408889634074, static_cast<double>(FLT_MAX)));
+    return s < FLT_MIN ? FLT_MIN : s;
+}
+
 // How the attention's work is cut: rows and keys per workgroup tile by the
 // query rows that share a key head, parts by the device's size.  64 sequences
 // of 4096 rows, 8 key heads of 128, us with tiles of 32 / 64 / 128 rows: 24
@@ -724,10 +732,7 @@ int tree_attention_impl(const sv_tree_attention* a, void* stream_v) {
     // beyond every length and depth both mean everything; the kernel subtracts row numbers from them
     p.window = std::min(a->window, 1 << 29);
     p.sinks = std::min(a->sinks, 1 << 29);
-    // (-inf) * scale2 has to stay -inf, and 0 * scale2 0: no zero, no denormal, not infinite
-    p.scale2 = static_cast<float>(
-        std::min(std::fabs(static_cast<double>(a->scale)) * 1.4426950408889634074, static_cast<double>(FLT_MAX)));
-    if (p.scale2 < FLT_MIN) p.scale2 = FLT_MIN;
+    p.scale2 = score_scale(a->scale);
     p.flip = a->scale < 0.f ? 1 : 0;
     p.MT = t.MT;
     p.clusters = t.clusters;
@@ -910,6 +915,104 @@ int cache_impl(const sv_cache* c, const void* kt, const void* vt, const int64_t*
                         [&](const sv::LaunchEvents& ev) { return sv::launch_cache_copy(p, stream, ev); });
 }
 
+// How the latent attention's work is cut: rows per workgroup tile by the query
+// rows that share a sequence's cache rows, parts by the device's size.
+struct LatentPlan {
+    sv::LatentShape s;
+    int MT = 1, clusters = 1, merge = 0;
+    size_t start_bytes = 0, total = 0;
+};
+
+int plan_latent(const sv_latent_attention* a, LatentPlan& t) {
+    if (!a) return SV_EINVAL;
+    if (a->dtype != SV_BF16 && a->dtype != SV_F16) return SV_EDTYPE;
+    if (a->B < 1 || a->B > 65536 || a->N < 1 || a->N > SPECVERIFY_MAX_NODES) return SV_ESHAPE;
+    if (a->heads < 1 || a->heads > 1024) return SV_ESHAPE;
+    if (a->dim < 8 || a->dim > SPECVERIFY_MAX_LATENT || a->dim % 8) return SV_ESHAPE;
+    if (a->dim_v < 8 || a->dim_v > a->dim || a->dim_v > 512 || a->dim_v % 8) return SV_ESHAPE;
+    if (a->pages < 1 || !pow2_page(a->page_size) || a->width < 0) return SV_ESHAPE;
+    if (static_cast<int64_t>(a->width) * a->page_size > (1ll << 28)) return SV_ESHAPE;
+    const int rows = a->N * a->heads;
+    t.s.wide = a->dim > 320 || a->dim_v > 256;
+    t.s.rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    t.MT = (rows + t.s.rows - 1) / t.s.rows;
+    // a launch has fewer than 2^32 threads
+    if ((static_cast<int64_t>(a->B) + 7) / 8 * 8 * t.MT >= 1ll << 23) return SV_ESHAPE;
+    const int64_t cap = static_cast<int64_t>(a->width) * a->page_size;
+    const int64_t most = (cap + 31) / 32 + (a->N + 31) / 32;  // tiles of one sequence
+    if (most <= 4) {
+        t.merge = 0;
+        t.clusters = a->B;
+    } else {
+        t.merge = 1;
+        int64_t c = device_cus() / t.MT;
+        if (c > a->B * most) c = a->B * most;
+        t.clusters = static_cast<int>(c < 1 ? 1 : c);
+        t.start_bytes = align256((static_cast<size_t>(a->B) + 1) * sizeof(int64_t));
+        t.total = t.start_bytes + static_cast<size_t>(t.clusters) * 2 * t.MT * t.s.rows *
+                                      (sv::latent_dv(t.s.wide) + 2) * sizeof(float);
+    }
+    return SV_OK;
+}
+
+int latent_attention_impl(const sv_latent_attention* a, void* stream_v) {
+    LatentPlan t;
+    int rc = plan_latent(a, t);
+    if (rc) return rc;
+    sv::LatentParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (!a->out || !a->len || (a->width > 0 && !a->table)) return SV_EINVAL;
+    if (a->table_stride < 0 || !std::isfinite(a->scale)) return SV_EINVAL;
+    const int32_t heads[3] = {a->B, a->N, a->heads}, nodes[2] = {a->B, a->N}, cache[2] = {a->pages, a->page_size};
+    rc = check_rows(a->q, a->q_stride, heads, 3, 2, p.qs);
+    if (!rc) rc = check_rows(a->rows, a->rows_stride, nodes, 2, 2, p.nws);
+    if (!rc) rc = check_rows(a->cache, a->cache_stride, cache, 2, 2, p.kcs);
+    if (!rc) rc = check_rows(a->out, a->out_stride, heads, 3, 2, p.os);
+    if (rc) return rc;
+    if (expanded(p.os, heads, 3)) return SV_EINVAL;
+    if (misaligned(a->table, 4) || misaligned(a->len, 4) || (a->parent && misaligned(a->parent, 4)) ||
+        (a->n_nodes && misaligned(a->n_nodes, 4)))
+        return SV_EALIGN;
+    if (t.total > 0) {
+        if (!a->workspace) return SV_EINVAL;
+        if (misaligned(a->workspace, 16)) return SV_EALIGN;
+        if (a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < t.total) return SV_ETOOBIG;
+    }
+    p.q = static_cast<const uint8_t*>(a->q);
+    p.nw = static_cast<const uint8_t*>(a->rows);
+    p.kc = static_cast<const uint8_t*>(a->cache);
+    p.out = static_cast<uint8_t*>(a->out);
+    p.table = a->table;
+    p.table_stride = a->table_stride;
+    p.len = a->len;
+    p.parent = a->parent;
+    p.n_nodes = a->n_nodes;
+    p.B = a->B;
+    p.N = a->N;
+    p.H = a->heads;
+    p.C = a->dim;
+    p.dv = a->dim_v;
+    p.pages = a->pages;
+    p.width = a->width;
+    p.ps_shift = __builtin_ctz(static_cast<unsigned>(a->page_size));
+    p.scale2 = score_scale(a->scale);
+    p.flip = a->scale < 0.f ? 1 : 0;
+    p.MT = t.MT;
+    p.clusters = t.clusters;
+    p.merge = t.merge;
+    if (t.merge) {
+        p.start = static_cast<int64_t*>(a->workspace);
+        p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + t.start_bytes);
+    }
+    const int dtype = a->dtype == SV_BF16 ? static_cast<int>(sv::DT_BF16) : sv::kDTypeF16;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    rc = timed_launch(sv::KK_LATENT_ATTN, stream,
+                      [&](const sv::LaunchEvents& ev) { return sv::launch_latent_attn(p, t.s, dtype, stream, ev); });
+    if (rc || !t.merge) return rc;
+    return timed_launch(sv::KK_LATENT_JOIN, stream,
+                        [&](const sv::LaunchEvents& ev) { return sv::launch_latent_join(p, t.s, dtype, stream, ev); });
+}
+
 }  // namespace
 
 extern "C" {
@@ -987,6 +1090,18 @@ int64_t spec_tree_attention_workspace(const sv_tree_attention* args) {
     return entry([&] {
         TreePlan t;
         const int rc = plan_tree(args, t);
+        return rc ? rc : static_cast<int64_t>(t.total);
+    });
+}
+
+int spec_latent_attention(const sv_latent_attention* args, void* stream) {
+    return entry([&] { return latent_attention_impl(args, stream); });
+}
+
+int64_t spec_latent_attention_workspace(const sv_latent_attention* args) {
+    return entry([&] {
+        LatentPlan t;
+        const int rc = plan_latent(args, t);
         return rc ? rc : static_cast<int64_t>(t.total);
     });
 }

@@ -1,0 +1,41 @@
+// Internal structures of the kernels for models with one latent row per token:
+// attention on the rows themselves, products per head, attention of prompts
+// with expanded keys and values.  Not part of the public C ABI.
+#pragma once
+
+#include "sv_tree.h"
+
+namespace sv {
+
+// ---- attention on latent rows ----
+struct LatentParams {
+    const uint8_t *q, *nw, *kc;            // queries, the nodes' own rows, cache rows
+    uint8_t* out;
+    uint32_t qs[3], os[3];                 // strides in 16-byte units: sequence, node, head
+    uint32_t nws[2], kcs[2];               // sequence, node; page, slot
+    const int32_t *table, *len, *parent, *n_nodes;  // parent null: chains; n_nodes may be null
+    int64_t table_stride;
+    int B, N, H, C, dv;
+    int pages, width, ps_shift;            // page size 1 << ps_shift
+    float scale2;                          // |scale| log2(e), a normal number
+    int flip;                              // scale < 0: the queries' signs are flipped
+    int MT;                                // row tiles per sequence
+    int clusters;                          // parts the work is cut into
+    int merge;                             // 0: every sequence is one part
+    int64_t* start;                        // [B + 1] workspace: first tile of each sequence
+    float* part;                           // [clusters, 2, MT, rows, dv template + 2] workspace: partial results
+};
+
+// Rows of a workgroup's tile, and the kernel's row and value widths.
+struct LatentShape {
+    int rows;  // 32, 64 or 128
+    int wide;  // 1: rows up to 576 and values up to 512 elements; 0: 320 and 256
+};
+constexpr int latent_dv(int wide) { return wide ? 512 : 256; }
+
+hipError_t launch_latent_attn(const LatentParams& p, const LatentShape& s, int dtype, hipStream_t st,
+                              const LaunchEvents& ev);
+hipError_t launch_latent_join(const LatentParams& p, const LatentShape& s, int dtype, hipStream_t st,
+                              const LaunchEvents& ev);
+
+}  // namespace sv

@@ -22,6 +22,8 @@ enum TreeKernelKind : int {
     KK_TREE_VERIFY,
     KK_CACHE_PLAN,
     KK_CACHE_COPY,
+    KK_LATENT_ATTN,
+    KK_LATENT_JOIN,
     KK_ALL
 };
 
