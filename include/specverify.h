@@ -635,6 +635,109 @@ int spec_latent_attention(const sv_latent_attention* args, void* stream);
  * at); a negative status for sizes the call refuses. */
 int64_t spec_latent_attention_workspace(const sv_latent_attention* args);
 
+/*
+ * spec_head_product -- a product per head, out[t, h, m] = sum_k x[t, h, k]
+ * w[h, m, k]: queries into the latent space (w: the key weights, transposed
+ * once to [heads, latent, dim_k]) and results out of it (w: the value weights
+ * [heads, dim_v, latent]).  Sums are float32, rounded once.
+ *
+ * dtype          SV_BF16 or SV_F16, of all tensors.
+ * T              tokens, 0 (nothing is done) to 2^24; heads <= 1024; K and M
+ *                multiples of 8, at most 65536; tiles of 128 outputs by 128
+ *                tokens (32 where T <= 32), over the heads, fewer than 2^24 - 8.
+ * x, out         [T, heads, K], [T, heads, M], strides for (token, head); w
+ *                [heads, M, K], strides for (head, row).  The last axis of every
+ *                tensor is contiguous; data and strides are multiples of 16
+ *                bytes.  out must not overlap the inputs, nor its rows each other.
+ *
+ * Errors: SV_EINVAL (NULL, negative stride, out with a stride of 0 along an axis
+ * longer than one), SV_ESHAPE, SV_EDTYPE, SV_EALIGN, SV_EHIP.
+ */
+typedef struct {
+    int32_t dtype;
+    int32_t T, heads, K, M;
+    const void* x;
+    int64_t x_stride[2];
+    const void* w;
+    int64_t w_stride[2];
+    void* out;
+    int64_t out_stride[2];
+} sv_head_product;
+
+int spec_head_product(const sv_head_product* args, void* stream);
+
+/*
+ * spec_latent_prompt -- attention of prompts (the expanded form): keys and values
+ * are made of the cache rows per head, for row s of a sequence
+ *
+ *   k_s = (w_k[h] c_s, e_s),  v_s = w_v[h] c_s,
+ *
+ * c_s the row's first `latent` elements and e_s the dim_p behind them, and a
+ * token at position p attends to rows 0..p:
+ *
+ *   out[t, h] = sum_{s <= p} softmax_s(scale * q[t, h] . k_s) v_s.
+ *
+ * The rows q_start[b] .. q_start[b + 1] of q are the last tokens of sequence b, at
+ * positions len[b] - n .. len[b] - 1; their rows, and those of a prefix before
+ * them, are in the cache.  Keys and values are rounded to the input type,
+ * statistics and other roundings are spec_tree_attention's.
+ *
+ * dtype          SV_BF16 or SV_F16, of all tensors.
+ * T              query tokens, 0 (nothing is done) to 2^24; B <= 65536; heads <= 1024.
+ * dim_k, dim_v   at most 128, dim_p at most 64, latent + dim_p <=
+ *                SPECVERIFY_MAX_LATENT; multiples of 8; dim_p may be 0.
+ * rows           at least the sum of the lengths, at most 2^26: the caller's
+ *                bound, by which the workspace is sized.  The output of a
+ *                sequence that does not fit is NaN.
+ * q, out         [T, heads, dim_k + dim_p], [T, heads, dim_v]; strides for
+ *                (token, head).
+ * cache          [pages, page_size, latent + dim_p]; strides for (page, slot).
+ * w_k, w_v       [heads, dim_k, latent], [heads, dim_v, latent]; strides for
+ *                (head, row).  Data and strides of all these are multiples of
+ *                16 bytes, last axes contiguous.
+ * table, table_stride, len, width, scale  as spec_tree_attention.
+ * q_start        device int32 [B + 1], rising within [0, T]; a sequence whose
+ *                bounds do not rise so has no queries.  Rows of out that belong to
+ *                no sequence are left as they are; a query that sees nothing is zero.
+ * workspace      at least spec_latent_prompt_workspace(args) bytes, aligned to 16.
+ *
+ * What a token does not see (later rows, pages outside the pool) never reaches its
+ * output.  Where it sees infinities or NaN, expanded values beyond the type's range
+ * included, its output is infinite or NaN.  (Launches have fewer than 2^32 threads:
+ * the 128-row tiles of `rows` times the 128-wide tiles of heads * dim_k and of
+ * heads * dim_v, and (T / 128 + min(B, T)) * heads, are below 2^24 - 8.)
+ *
+ * Errors as spec_tree_attention.
+ */
+typedef struct {
+    int32_t dtype;
+    int32_t T, B, heads, latent, dim_k, dim_p, dim_v, rows;
+    const void* q;
+    int64_t q_stride[2];
+    const void* cache;
+    int64_t cache_stride[2];
+    int32_t pages, page_size, width;
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* len;
+    const int32_t* q_start;
+    const void* w_k;
+    int64_t w_k_stride[2];
+    const void* w_v;
+    int64_t w_v_stride[2];
+    float scale;
+    void* out;
+    int64_t out_stride[2];
+    void* workspace;
+    int64_t workspace_bytes;
+} sv_latent_prompt;
+
+int spec_latent_prompt(const sv_latent_prompt* args, void* stream);
+
+/* Bytes of workspace the call needs, from its sizes; a negative status for sizes
+ * the call refuses. */
+int64_t spec_latent_prompt_workspace(const sv_latent_prompt* args);
+
 /* Human-readable text for a status code (for SV_EHIP, the last HIP error). */
 const char* spec_verify_strerror(int status);
 

@@ -26,6 +26,8 @@ Modules:
   produce -- the synthetic draft producer of the two-batch schedule.
   tree    -- the tree round: attention of drafted trees over a paged cache,
              tree verification, commit and fork of cache pages.
+  latent  -- latent rows: attention on a paged cache of rows shared by all
+             heads, products per head, attention of prompts.
 """
 
 from .greedy import GreedyResult, argmax_lowest, greedy_verify, top_k_after_first  # noqa: F401

@@ -47,3 +47,48 @@ def attention(q, cache, table, lens, rows, parent=None, n_nodes=None, *, dim_v, 
             k = np.concatenate([ctx, rows[b, path]])
             out[b, i], spread[b, i], reach[b, i] = _attend(q[b, i], k, k[:, :dim_v], scale)
     return out, spread, reach
+
+
+def head_product(x, w):
+    """out[t, h] = w[h] x[t, h], and sum_k |x| |w| (what a rounding of the sum is worth)."""
+    return np.einsum("thk,hmk->thm", x, w), np.einsum("thk,hmk->thm", np.abs(x), np.abs(w))
+
+
+def prompt(q, cache, table, lens, q_start, w_k, w_v, scale=None):
+    """(out [T, heads, dim_v], spread, reach, loose): as attention, with reach
+    [T, heads, 3] = largest scale * sum |q k|, number of keys, and what float32
+    sums over the latent dimensions and the smallest float16 are worth in a
+    score; loose: the same for the values.  Rows of no sequence are NaN."""
+    T, H, D = q.shape
+    dv, R = w_v.shape[1:]
+    scale = D ** -0.5 if scale is None else scale
+    out, spread = np.full((T, H, dv), np.nan), np.zeros((T, H, dv))
+    reach, loose = np.zeros((T, H, 3)), np.zeros((T, H, dv))
+    for b in range(len(lens)):
+        s, e = int(q_start[b]), int(q_start[b + 1])
+        if not 0 <= s < e <= T:
+            continue
+        length = int(np.clip(lens[b], 0, table.shape[1] * cache.shape[1]))
+        j = np.arange(length)
+        pg = table[b, j // cache.shape[1]] if length else j
+        j = j[(pg >= 0) & (pg < cache.shape[0])]
+        c = cache_rows(cache, table[b], length)
+        for h in range(H):
+            k = np.concatenate([c[:, :R] @ w_k[h].T, c[:, R:]], 1)
+            v = c[:, :R] @ w_v[h].T
+            k_slack = np.concatenate([R * 2.0 ** -23 * (np.abs(c[:, :R]) @ np.abs(w_k[h]).T) + 2.0 ** -25,
+                                      np.zeros((len(c), c.shape[1] - R))], 1)
+            v_slack = R * 2.0 ** -23 * (np.abs(c[:, :R]) @ np.abs(w_v[h]).T) + 2.0 ** -25
+            for t in range(s, e):
+                n = int((j <= length - (e - t)).sum())
+                if n == 0:
+                    out[t, h] = 0.0
+                    continue
+                x = scale * (k[:n] @ q[t, h])
+                with np.errstate(invalid="ignore"):
+                    w = np.exp(x - x.max())
+                    w /= w.sum()
+                out[t, h], spread[t, h], loose[t, h] = w @ v[:n], w @ np.abs(v[:n]), w @ v_slack[:n]
+                a = abs(scale) * np.abs(q[t, h])
+                reach[t, h] = (np.abs(k[:n]) @ a).max(), n, (k_slack[:n] @ a).max()
+    return out, spread, reach, loose

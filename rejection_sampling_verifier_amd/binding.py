@@ -22,13 +22,15 @@ PROBE_POS, PROBE_ROW = 8, 4
 STATUS = {0: "SV_OK", -1: "SV_EINVAL", -2: "SV_ESHAPE", -3: "SV_EDTYPE", -4: "SV_EHIP", -5: "SV_ENOMEM",
           -6: "SV_EALIGN", -7: "SV_ECAPTURE", -8: "SV_ETOOBIG"}
 KERNEL_KINDS = ("stats", "topp", "rows", "smc", "produce", "tree_attention", "tree_join", "verify_clear",
-                "tree_verify", "cache_plan", "cache_copy", "latent_attention", "latent_join")
+                "tree_verify", "cache_plan", "cache_copy", "latent_attention", "latent_join",
+                "head_product", "prompt_plan", "prompt_expand", "prompt_attention")
 
 EXPORTS = ("spec_verify", "spec_verify_noalloc", "spec_verify_probe", "spec_greedy_verify", "spec_hispec_verify", "spec_smc_step",
            "spec_draft_produce",
            "spec_tree_attention", "spec_tree_attention_workspace", "spec_verify_tree", "spec_verify_tree_workspace",
            "spec_cache_commit", "spec_cache_fork", "spec_cache_workspace",
-           "spec_latent_attention", "spec_latent_attention_workspace",
+           "spec_latent_attention", "spec_latent_attention_workspace", "spec_head_product", "spec_latent_prompt",
+           "spec_latent_prompt_workspace",
            "spec_verify_strerror",
            "spec_verify_release",
            "spec_verify_abi_version", "spec_verify_profile_enable", "spec_verify_profile_read",
@@ -673,8 +675,10 @@ def cache_fork(k_cache, v_cache, block_table, seq_len, ancestor, *, out_table=No
 
 # ---- latent rows: one row per token, shared by the heads
 
-# sv_latent_attention's fields in order
+# the fields of sv_latent_attention, sv_head_product and sv_latent_prompt in order
 _PACK_LATENT = struct.Struct("@iiiiiiP3qP2qP2qiii4xPqPPPf4xP3qPq").pack
+_PACK_PRODUCT = struct.Struct("@iiiii4xP2qP2qP2q").pack
+_PACK_PROMPT = struct.Struct("@iiiiiiiii4xP2qP2qiii4xPqPPP2qP2qf4xP2qPq").pack
 _latent = None
 
 
@@ -691,7 +695,8 @@ def _latent_calls():
             return f
 
         _latent = (lib, entry("spec_latent_attention", [blob, vp]),
-                   entry("spec_latent_attention_workspace", [blob], i64))
+                   entry("spec_latent_attention_workspace", [blob], i64), entry("spec_head_product", [blob, vp]),
+                   entry("spec_latent_prompt", [blob, vp]), entry("spec_latent_prompt_workspace", [blob], i64))
     return _latent
 
 
@@ -699,6 +704,13 @@ def _half(t, name):
     if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
         raise ValueError(f"{name}: dtype {t.dtype} is not bfloat16 or float16")
     return t.dtype
+
+
+def _tokens(t, name, shape, dtype, index):
+    """_rows for a tensor that may be empty (whose strides mean nothing)."""
+    if shape[0] == 0 and t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        return (0,) * len(shape)
+    return _rows(t, name, shape, dtype, index)
 
 
 def latent_attention(q, cache, block_table, seq_len, rows, parent=None, n_nodes=None, *, dim_v, scale, out=None,
@@ -749,6 +761,90 @@ def latent_attention(q, cache, block_table, seq_len, rows, parent=None, n_nodes=
                             lambda: size_of(block(0, 0)))
     ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
     _check(lib, call(block(ws.data_ptr() if need else 0, need), _raw_stream(index)))
+    return out
+
+
+def head_product(x, w, *, out=None, stream=None):
+    """out[t, h] = w[h] x[t, h] (spec_head_product): queries into the latent
+    space, results out of it.
+
+    x [T, heads, K], w [heads, M, K]: bfloat16 or float16, last axis contiguous,
+    other strides any multiples of 8 elements.  Returns out [T, heads, M].
+    """
+    lib, _, _, call = _latent_calls()[:4]
+    if x.dim() != 3 or w.dim() != 3:
+        raise ValueError("x must be [T, heads, K] and w [heads, M, K]")
+    dt, index = _half(x, "x"), x.get_device()
+    _no_grad(x, w)
+    (T, heads, K), M = x.shape, w.shape[1]
+    xs = _tokens(x, "x", x.shape, dt, index)
+    ws = _rows(w, "w", (heads, M, K), dt, index)
+    if out is not None:
+        _tokens(out, "out", (T, heads, M), dt, index)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return head_product(x, w, out=out)
+    if out is None:
+        out = x.new_empty((T, heads, M))
+    os = out.stride()
+    _check(lib, call(_PACK_PRODUCT(_DTYPES[dt], T, heads, K, M, x.data_ptr(), xs[0], xs[1], w.data_ptr(), ws[0], ws[1],
+                                   out.data_ptr(), os[0], os[1]), _raw_stream(index)))
+    return out
+
+
+def latent_prompt(q, cache, block_table, seq_len, q_start, w_k, w_v, *, rows, scale=None, out=None, stream=None):
+    """Causal attention of prompts over a paged cache of latent rows, with keys
+    and values expanded per head (spec_latent_prompt).
+
+    q [T, heads, dim_k + dim_p]: rows q_start[b] .. q_start[b + 1] are the last
+    tokens of sequence b, whose rows are in the cache already.  cache [pages,
+    page_size, latent + dim_p], w_k [heads, dim_k, latent], w_v [heads, dim_v,
+    latent]: one dtype, bfloat16 or float16, last axis contiguous, other strides
+    any multiples of 8 elements.  block_table [B, width], seq_len [B], q_start
+    [B + 1]: int32.  rows: at least the sum of the lengths (it sizes the
+    workspace; what does not fit comes out as NaN).  scale None: (dim_k +
+    dim_p) ** -0.5.  Returns out [T, heads, dim_v]; rows of q that belong to no
+    sequence are not written.
+    """
+    lib, _, _, _, call, size_of = _latent_calls()[:6]
+    if q.dim() != 3 or cache.dim() != 3 or w_k.dim() != 3 or w_v.dim() != 3 or seq_len.dim() != 1:
+        raise ValueError("q must be [T, heads, dim], cache [pages, page_size, dim], w_k and w_v [heads, dim, latent] "
+                         "and seq_len [B]")
+    dt, index = _half(q, "q"), q.get_device()
+    _no_grad(q, cache, w_k, w_v)
+    T, heads, dim = q.shape
+    pages, page_size, whole = cache.shape
+    dim_k, latent = w_k.shape[1:]
+    dim_p, dim_v, B = whole - latent, w_v.shape[1], seq_len.shape[0]
+    if dim != dim_k + dim_p:
+        raise ValueError(f"q has {dim} elements a head; w_k and the cache make it {dim_k} + {dim_p}")
+    qs = _tokens(q, "q", q.shape, dt, index)
+    cs = _rows(cache, "cache", cache.shape, dt, index)
+    wks = _rows(w_k, "w_k", (heads, dim_k, latent), dt, index)
+    wvs = _rows(w_v, "w_v", (heads, dim_v, latent), dt, index)
+    tab, tab_stride = _table(block_table, "block_table", B, index)
+    width = block_table.shape[1]
+    ln = _array(seq_len, "seq_len", (B,), index)
+    start = _array(q_start, "q_start", (B + 1,), index)
+    if out is not None:
+        _tokens(out, "out", (T, heads, dim_v), dt, index)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return latent_prompt(q, cache, block_table, seq_len, q_start, w_k, w_v, rows=rows, scale=scale, out=out)
+    if out is None:
+        out = q.new_empty((T, heads, dim_v))
+    os = out.stride()
+
+    def block(ws, need):
+        return _PACK_PROMPT(_DTYPES[dt], T, B, heads, latent, dim_k, dim_p, dim_v, rows, q.data_ptr(), qs[0], qs[1],
+                            cache.data_ptr(), cs[0], cs[1], pages, page_size, width, tab, tab_stride, ln, start,
+                            w_k.data_ptr(), wks[0], wks[1], w_v.data_ptr(), wvs[0], wvs[1],
+                            dim ** -0.5 if scale is None else scale, out.data_ptr(), os[0], os[1], ws, need)
+
+    need = _workspace_bytes(lib, ("prompt", B, T, heads, latent, dim_k, dim_p, dim_v, rows, page_size, width),
+                            lambda: size_of(block(0, 0)))
+    ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    _check(lib, call(block(ws.data_ptr(), need), _raw_stream(index)))
     return out
 
 

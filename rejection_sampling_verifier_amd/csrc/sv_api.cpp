@@ -1013,6 +1013,136 @@ int latent_attention_impl(const sv_latent_attention* a, void* stream_v) {
                         [&](const sv::LaunchEvents& ev) { return sv::launch_latent_join(p, t.s, dtype, stream, ev); });
 }
 
+int half_type(int32_t dtype) { return dtype == SV_BF16 ? static_cast<int>(sv::DT_BF16) : sv::kDTypeF16; }
+
+int head_product_impl(const sv_head_product* a, void* stream_v) {
+    if (!a) return SV_EINVAL;
+    if (a->dtype != SV_BF16 && a->dtype != SV_F16) return SV_EDTYPE;
+    if (a->T < 0 || a->T > 1 << 24 || a->heads < 1 || a->heads > 1024) return SV_ESHAPE;
+    if (a->K < 8 || a->K > 65536 || a->K % 8 || a->M < 8 || a->M > 65536 || a->M % 8) return SV_ESHAPE;
+    sv::ProductParams p;
+    std::memset(&p, 0, sizeof(p));
+    const int32_t tokens[2] = {a->T, a->heads}, rows[2] = {a->heads, a->M};
+    if (a->T > 0) {
+        int rc = check_rows(a->x, a->x_stride, tokens, 2, 2, p.xs);
+        if (!rc) rc = check_rows(a->w, a->w_stride, rows, 2, 2, p.ws);
+        if (!rc) rc = check_rows(a->out, a->out_stride, tokens, 2, 2, p.os);
+        if (rc) return rc;
+        if (expanded(p.os, tokens, 2)) return SV_EINVAL;
+    }
+    p.x = static_cast<const uint8_t*>(a->x);
+    p.w = static_cast<const uint8_t*>(a->w);
+    p.out = static_cast<uint8_t*>(a->out);
+    p.T = a->T;
+    p.H = a->heads;
+    p.M = a->M;
+    p.K = a->K;
+    p.tt = a->T <= 32 ? 32 : 128;
+    // a launch has fewer than 2^32 threads
+    if (static_cast<int64_t>((p.M + 127) / 128) * ((p.T + p.tt - 1) / p.tt) * p.H >= (1ll << 24) - 8) return SV_ESHAPE;
+    if (a->T == 0) return SV_OK;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    return timed_launch(sv::KK_PRODUCT, stream, [&](const sv::LaunchEvents& ev) {
+        return sv::launch_product(p, half_type(a->dtype), stream, ev);
+    });
+}
+
+// The workspace of a prompt call: places, flags, keys, values and second parts of the line.
+struct PromptPlan {
+    size_t odd, there, k, v, pe, total;
+};
+
+int plan_prompt(const sv_latent_prompt* a, PromptPlan& t) {
+    if (!a) return SV_EINVAL;
+    if (a->dtype != SV_BF16 && a->dtype != SV_F16) return SV_EDTYPE;
+    if (a->B < 1 || a->B > 65536 || a->T < 0 || a->T > 1 << 24 || a->heads < 1 || a->heads > 1024) return SV_ESHAPE;
+    if (a->dim_k < 8 || a->dim_k > 128 || a->dim_k % 8 || a->dim_p < 0 || a->dim_p > 64 || a->dim_p % 8 ||
+        a->dim_v < 8 || a->dim_v > 128 || a->dim_v % 8)
+        return SV_ESHAPE;
+    if (a->latent < 8 || a->latent % 8 || a->latent + a->dim_p > SPECVERIFY_MAX_LATENT) return SV_ESHAPE;
+    if (a->pages < 1 || !pow2_page(a->page_size) || a->width < 0) return SV_ESHAPE;
+    if (static_cast<int64_t>(a->width) * a->page_size > (1ll << 28)) return SV_ESHAPE;
+    if (a->rows < 0 || a->rows > 1 << 26) return SV_ESHAPE;
+    // launches have fewer than 2^32 threads
+    const int64_t lines = (static_cast<int64_t>(a->rows) + 127) / 128;
+    const int64_t tiles = a->T / sv::kPromptRows + std::min(a->B, a->T);
+    const int64_t out = (a->heads * a->dim_k + 127) / 128 + (a->heads * a->dim_v + 127) / 128;
+    if (lines * out >= (1ll << 24) - 8 || tiles * a->heads >= (1ll << 24) - 8) return SV_ESHAPE;
+    const size_t rows = static_cast<size_t>(lines) * 128;
+    t.odd = align256((static_cast<size_t>(a->B) + 1) * 2 * sizeof(int64_t));
+    t.there = t.odd + 256;
+    t.k = align256(t.there + rows * sizeof(int32_t));
+    t.v = align256(t.k + static_cast<size_t>(a->heads) * a->rows * a->dim_k * 2);
+    t.pe = align256(t.v + static_cast<size_t>(a->heads) * a->rows * a->dim_v * 2);
+    t.total = align256(t.pe + rows * a->dim_p * 2);
+    return SV_OK;
+}
+
+int latent_prompt_impl(const sv_latent_prompt* a, void* stream_v) {
+    PromptPlan t;
+    int rc = plan_prompt(a, t);
+    if (rc) return rc;
+    if (!a->len || !a->q_start || (a->width > 0 && !a->table)) return SV_EINVAL;
+    if (a->table_stride < 0 || !std::isfinite(a->scale)) return SV_EINVAL;
+    sv::PromptParams p;
+    std::memset(&p, 0, sizeof(p));
+    const int32_t tokens[2] = {a->T, a->heads}, cache[2] = {a->pages, a->page_size}, wk[2] = {a->heads, a->dim_k},
+                  wv[2] = {a->heads, a->dim_v};
+    if (a->T > 0) {
+        rc = check_rows(a->q, a->q_stride, tokens, 2, 2, p.qs);
+        if (!rc) rc = check_rows(a->out, a->out_stride, tokens, 2, 2, p.os);
+        if (!rc && expanded(p.os, tokens, 2)) rc = SV_EINVAL;
+    }
+    if (!rc) rc = check_rows(a->cache, a->cache_stride, cache, 2, 2, p.kcs);
+    if (!rc) rc = check_rows(a->w_k, a->w_k_stride, wk, 2, 2, p.wks);
+    if (!rc) rc = check_rows(a->w_v, a->w_v_stride, wv, 2, 2, p.wvs);
+    if (rc) return rc;
+    if (misaligned(a->table, 4) || misaligned(a->len, 4) || misaligned(a->q_start, 4)) return SV_EALIGN;
+    if (!a->workspace) return SV_EINVAL;
+    if (misaligned(a->workspace, 16)) return SV_EALIGN;
+    if (a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < t.total) return SV_ETOOBIG;
+    if (a->T == 0) return SV_OK;
+    p.q = static_cast<const uint8_t*>(a->q);
+    p.kc = static_cast<const uint8_t*>(a->cache);
+    p.wk = static_cast<const uint8_t*>(a->w_k);
+    p.wv = static_cast<const uint8_t*>(a->w_v);
+    p.out = static_cast<uint8_t*>(a->out);
+    p.table = a->table;
+    p.len = a->len;
+    p.q_start = a->q_start;
+    p.table_stride = a->table_stride;
+    p.T = a->T;
+    p.B = a->B;
+    p.H = a->heads;
+    p.dn = a->dim_k;
+    p.dr = a->dim_p;
+    p.dv = a->dim_v;
+    p.R = a->latent;
+    p.rows = a->rows;
+    p.pages = a->pages;
+    p.width = a->width;
+    p.ps_shift = __builtin_ctz(static_cast<unsigned>(a->page_size));
+    p.scale2 = score_scale(a->scale);
+    p.flip = a->scale < 0.f ? 1 : 0;
+    uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
+    p.plan = reinterpret_cast<int64_t*>(ws);
+    p.odd = reinterpret_cast<int32_t*>(ws + t.odd);
+    p.there = reinterpret_cast<int32_t*>(ws + t.there);
+    p.k = ws + t.k;
+    p.v = ws + t.v;
+    p.pe = ws + t.pe;
+    const int dtype = half_type(a->dtype);
+    const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    rc = timed_launch(sv::KK_PROMPT_PLAN, stream,
+                      [&](const sv::LaunchEvents& ev) { return sv::launch_prompt_plan(p, stream, ev); });
+    if (!rc && a->rows > 0)
+        rc = timed_launch(sv::KK_PROMPT_EXPAND, stream,
+                          [&](const sv::LaunchEvents& ev) { return sv::launch_prompt_expand(p, dtype, stream, ev); });
+    if (rc) return rc;
+    return timed_launch(sv::KK_PROMPT_ATTN, stream,
+                        [&](const sv::LaunchEvents& ev) { return sv::launch_prompt_attn(p, dtype, stream, ev); });
+}
+
 }  // namespace
 
 extern "C" {
@@ -1102,6 +1232,22 @@ int64_t spec_latent_attention_workspace(const sv_latent_attention* args) {
     return entry([&] {
         LatentPlan t;
         const int rc = plan_latent(args, t);
+        return rc ? rc : static_cast<int64_t>(t.total);
+    });
+}
+
+int spec_head_product(const sv_head_product* args, void* stream) {
+    return entry([&] { return head_product_impl(args, stream); });
+}
+
+int spec_latent_prompt(const sv_latent_prompt* args, void* stream) {
+    return entry([&] { return latent_prompt_impl(args, stream); });
+}
+
+int64_t spec_latent_prompt_workspace(const sv_latent_prompt* args) {
+    return entry([&] {
+        PromptPlan t;
+        const int rc = plan_prompt(args, t);
         return rc ? rc : static_cast<int64_t>(t.total);
     });
 }

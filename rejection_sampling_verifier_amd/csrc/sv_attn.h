@@ -113,6 +113,36 @@ __device__ __forceinline__ void to_lds(const uint8_t* src, uint8_t* dst) {
 // in bits 0-3 and 14-15, expcnt 4-6, lgkmcnt 8-11).
 constexpr int kWaitVm0 = 0x0F70;
 
+// The 16-byte chunks of a row are stored at positions XORed with this, so that
+// eight rows at one chunk (the key operand's reads) and four rows at two
+// neighbouring chunks (the transposing reads) lie in different banks.
+__device__ __forceinline__ int swizzle(int row) { return (row & 3) << 1 | (row >> 2 & 1); }
+
+// 16 bytes per lane from base + off to the 1024 at LDS address `dst`.  Assembly,
+// so that the compiler does not wait for these loads at every read of another
+// stage; the kernel waits for them itself (vmcnt).
+__device__ __forceinline__ void load_lds(const uint8_t* base, uint32_t off, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(dst) : "memory");
+}
+__device__ __forceinline__ void load_lds(const uint8_t* from, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(dst) : "memory");
+}
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ v8s lds_read(uint32_t at) {
+    return *reinterpret_cast<__attribute__((address_space(3))) v8s*>(at);
+}
+__device__ __forceinline__ v4s lds_read_tr(uint32_t at) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at));
+}
+
+// Until at most N of the wave's global loads are under way.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 // Byte offsets of row numbers times strides in 16-byte units.
 __device__ __forceinline__ uint64_t units(uint32_t i, uint32_t s) { return (static_cast<uint64_t>(i) * s) << 4; }
 __device__ __forceinline__ uint64_t units(uint32_t i, uint32_t s, uint32_t j, uint32_t r) {

@@ -38,4 +38,39 @@ hipError_t launch_latent_attn(const LatentParams& p, const LatentShape& s, int d
 hipError_t launch_latent_join(const LatentParams& p, const LatentShape& s, int dtype, hipStream_t st,
                               const LaunchEvents& ev);
 
+// ---- products per head ----
+struct ProductParams {
+    const uint8_t *x, *w;          // [T, H, K], [H, M, K]
+    uint8_t* out;                  // [T, H, M]
+    int64_t xs[2], ws[2], os[2];   // strides in 16-byte units: token, head; head, row; token, head
+    int T, H, M, K;
+    int tt;                        // tokens of a workgroup's tile
+};
+hipError_t launch_product(const ProductParams& p, int dtype, hipStream_t st, const LaunchEvents& ev);
+
+// ---- attention of prompts ----
+struct PromptParams {
+    const uint8_t *q, *kc, *wk, *wv;  // [T, H, dn + dr], cache rows, [H, dn, R], [H, dv, R]
+    uint8_t* out;                     // [T, H, dv]
+    int64_t qs[2], os[2];             // strides in 16-byte units: token, head
+    int64_t kcs[2];                   // page, slot
+    int64_t wks[2], wvs[2];           // head, row
+    const int32_t *table, *len, *q_start;
+    int64_t table_stride;
+    int T, B, H, dn, dr, dv, R;
+    int rows;                         // of the line: all sequences' rows one after the other
+    int pages, width, ps_shift;
+    float scale2;
+    int flip;
+    // workspace
+    int64_t* plan;                    // [B + 1] first row of the line, [B + 1] first query tile
+    int32_t* odd;                     // 1: an infinity or NaN among the values
+    int32_t* there;                   // [rows rounded up] 1: the row's page exists
+    uint8_t *k, *v, *pe;              // [H, rows, dn], [H, rows, dv], [rows, dr]
+};
+constexpr int kPromptRows = 128;      // queries of a tile
+hipError_t launch_prompt_plan(const PromptParams& p, hipStream_t st, const LaunchEvents& ev);
+hipError_t launch_prompt_expand(const PromptParams& p, int dtype, hipStream_t st, const LaunchEvents& ev);
+hipError_t launch_prompt_attn(const PromptParams& p, int dtype, hipStream_t st, const LaunchEvents& ev);
+
 }  // namespace sv

@@ -14,30 +14,6 @@
 namespace sv {
 namespace {
 
-// The 16-byte chunks of a row are stored at positions XORed with this, so that
-// eight rows at one chunk (the key operand's reads) and four rows at two
-// neighbouring chunks (the transposing reads) lie in different banks.
-__device__ __forceinline__ int swizzle(int row) { return (row & 3) << 1 | (row >> 2 & 1); }
-
-// 16 bytes per lane from base + off to the 1024 at LDS address `dst`.  Assembly,
-// so that the compiler does not wait for these loads at every read of another
-// stage; the kernel waits for them itself (vmcnt).
-__device__ __forceinline__ void load_lds(const uint8_t* base, uint32_t off, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(dst) : "memory");
-}
-__device__ __forceinline__ void load_lds(const uint8_t* from, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(dst) : "memory");
-}
-
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ v8s lds_read(uint32_t at) {
-    return *reinterpret_cast<__attribute__((address_space(3))) v8s*>(at);
-}
-__device__ __forceinline__ v4s lds_read_tr(uint32_t at) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at));
-}
-
 __device__ __forceinline__ int clamp_len(const LatentParams& p, int len) {
     const int cap = p.width << p.ps_shift;
     return len < 0 ? 0 : len > cap ? cap : len;
@@ -62,11 +38,6 @@ struct LatentLds {
 // Tiles of a sequence: its cache rows, then the tree's.
 __device__ __forceinline__ int tiles_of(const LatentParams& p, int len) {
     return (clamp_len(p, len) + kLatKeys - 1) / kLatKeys + (p.N + kLatKeys - 1) / kLatKeys;
-}
-
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 template <int DT, int DK, int DV, int RB>

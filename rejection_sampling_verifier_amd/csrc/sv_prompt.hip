@@ -1,0 +1,589 @@
+// gfx950 kernels of products per head and of attention for prompts on latent
+// rows, with keys and values expanded per head.
+//
+// For head h, row s of a sequence and query token i at position p_i,
+//
+//   k_s = (w_k c_s, e_s),  v_s = w_v c_s,  c_s the row's first R elements, e_s the rest,
+//   o_i = sum_{s <= p_i} 2^(x_s - m) v_s / sum_{s <= p_i} 2^(x_s - m),  x_s = scale log2(e) q_i.k_s.
+//
+//   k_prompt_plan    the sequences' places in one line of rows, and in one of query tiles;
+//   k_prompt_expand  keys and values of every head for every row of the line;
+//   k_prompt_attn    128 queries of one head against 64 keys at a time.
+
+#include "sv_attn.h"
+#include "sv_latent.h"
+
+namespace sv {
+namespace {
+
+// ---- products: out[t, m] = sum_k x[t, k] w[m, k], 128 outputs m by TT tokens a
+// workgroup, 64 of k at a time.
+//
+// W rows are the matrix instruction's A operand and token rows its B operand,
+// both read 16 bytes a lane from LDS, where the eight chunks of a row's 64
+// elements are XORed with the row number (eight rows on all banks).  A null token
+// row counts as zeros.
+template <int TT>
+struct Tile {
+    static constexpr int kStage = (128 + TT) * 128;
+    static constexpr int WM = TT == 128 ? 2 : 4;             // waves over outputs
+    static constexpr int BM = 128 / WM / 32, BT = TT == 128 ? 2 : 1;  // 32 x 32 blocks of a wave
+    static constexpr int kW = 4, kX = TT / 32;               // wide loads of a wave and stage
+};
+
+template <int DT, int TT>
+__device__ __forceinline__ void product_tile(uint32_t smem_at, const uint8_t* const* wp, const uint8_t* const* xp,
+                                             int K, v16f (*acc)[Tile<TT>::BT]) {
+    using L = Tile<TT>;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hh = lane >> 5, col = lane & 31;
+    const int wm = w % L::WM, wt = w / L::WM;
+    const int chunk = (lane & 7) ^ (lane >> 3);
+    const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero);
+    auto stage = [&](int s, uint32_t at) __attribute__((always_inline)) {
+        const bool in = s * 64 + chunk * 8 < K;
+#pragma unroll
+        for (int i = 0; i < L::kW; ++i)
+            load_lds(in ? wp[i] + s * 128 : zero, smem_at + at + (w * L::kW + i) * 1024);
+#pragma unroll
+        for (int i = 0; i < L::kX; ++i)
+            load_lds(in && xp[i] ? xp[i] + s * 128 : zero, smem_at + at + 16384 + (w * L::kX + i) * 1024);
+    };
+    uint32_t a_rd[4], b_rd[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t c = ((2 * k + hh) ^ (col & 7)) << 4;
+        a_rd[k] = smem_at + (wm * L::BM * 32 + col) * 128 + c;
+        b_rd[k] = smem_at + 16384 + (wt * L::BT * 32 + col) * 128 + c;
+    }
+#pragma unroll
+    for (int a = 0; a < L::BM; ++a)
+#pragma unroll
+        for (int b = 0; b < L::BT; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+    const int S = (K + 63) / 64;
+    stage(0, 0);
+    uint32_t at = 0;
+#pragma unroll 1
+    for (int s = 0; s < S; ++s) {
+        wait_vm<0>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (s + 1 < S) stage(s + 1, L::kStage - at);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v8s a[L::BM], b[L::BT];
+#pragma unroll
+            for (int i = 0; i < L::BM; ++i) a[i] = lds_read(a_rd[k] + at + i * 4096);
+#pragma unroll
+            for (int i = 0; i < L::BT; ++i) b[i] = lds_read(b_rd[k] + at + i * 4096);
+#pragma unroll
+            for (int i = 0; i < L::BM; ++i)
+#pragma unroll
+                for (int j = 0; j < L::BT; ++j) acc[i][j] = mfma<DT>(a[i], b[j], acc[i][j]);
+        }
+        at = L::kStage - at;
+    }
+}
+
+// Neighbouring tasks on one XCD (workgroups go to the eight in turn); -1: none.
+__device__ __forceinline__ int64_t task_of(int64_t tasks) {
+    const int64_t per = (tasks + 7) / 8, t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    return (blockIdx.x >> 3) < per && t < tasks ? t : -1;
+}
+inline int64_t grid_of(int64_t tasks) { return (tasks + 7) / 8 * 8; }
+
+template <int DT, int TT>
+__global__ __launch_bounds__(kThreads, 2) void k_product(ProductParams p) {
+    using L = Tile<TT>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) uint8_t*)smem));
+    const int mt = (p.M + 127) / 128, tt = (p.T + TT - 1) / TT;
+    const int64_t task = task_of(static_cast<int64_t>(mt) * tt * p.H);
+    if (task < 0) return;
+    const int h = static_cast<int>(task / (mt * static_cast<int64_t>(tt)));
+    const int in_head = static_cast<int>(task - h * (mt * static_cast<int64_t>(tt)));
+    const int t0 = in_head / mt * TT, m0 = in_head % mt * 128;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hh = lane >> 5, col = lane & 31, r8 = lane >> 3, chunk = (lane & 7) ^ r8;
+    const uint8_t *wp[L::kW], *xp[L::kX];
+#pragma unroll
+    for (int i = 0; i < L::kW; ++i)
+        wp[i] = p.w + 16 * (h * p.ws[0] + min(m0 + (w * L::kW + i) * 8 + r8, p.M - 1) * p.ws[1] + chunk);
+#pragma unroll
+    for (int i = 0; i < L::kX; ++i)
+        xp[i] = p.x + 16 * (min(t0 + (w * L::kX + i) * 8 + r8, p.T - 1) * p.xs[0] + h * p.xs[1] + chunk);
+    v16f acc[L::BM][L::BT];
+    product_tile<DT, TT>(smem_at, wp, xp, p.K, acc);
+    const int wm = w % L::WM, wt = w / L::WM;
+#pragma unroll
+    for (int b = 0; b < L::BT; ++b) {
+        const int t = t0 + (wt * L::BT + b) * 32 + col;
+        if (t >= p.T) continue;
+        uint8_t* const dst = p.out + 16 * (t * p.os[0] + h * p.os[1]);
+#pragma unroll
+        for (int a = 0; a < L::BM; ++a)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const int m = m0 + (wm * L::BM + a) * 32 + 2 * i + 4 * hh;
+                if (m < p.M)
+                    *reinterpret_cast<v4s*>(dst + 2 * m) =
+                        pack4<DT>(acc[a][b][i], acc[a][b][i + 1], acc[a][b][i + 2], acc[a][b][i + 3]);
+            }
+    }
+}
+
+// ---- prompts
+
+__device__ __forceinline__ int clamp_len(const PromptParams& p, int len) {
+    const int64_t cap = static_cast<int64_t>(p.width) << p.ps_shift;
+    return len < 0 ? 0 : len > cap ? static_cast<int>(cap) : len;
+}
+
+// The last i in [0, n) with at[i] <= x, for rising at.
+__device__ __forceinline__ int last_at(const int64_t* at, int n, int64_t x) {
+    int lo = 0;
+    for (int hi = n; hi - lo > 1;) {
+        const int mid = (lo + hi) >> 1;
+        if (at[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// A sequence's queries: rows [first, first + n) of q; n is 0 where the bounds do not rise within [0, T].
+struct Queries {
+    int first, n;
+};
+__device__ __forceinline__ Queries queries_of(const PromptParams& p, int b) {
+    const int s = p.q_start[b], e = p.q_start[b + 1];
+    return s >= 0 && e > s && e <= p.T ? Queries{s, e - s} : Queries{0, 0};
+}
+
+__global__ __launch_bounds__(1024) void k_prompt_plan(PromptParams p) {
+    __shared__ int64_t s_row[16], s_tile[16];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    int64_t row0 = 0, tile0 = 0;
+    for (int base = 0; base < p.B; base += 1024) {
+        const int b = base + tid;
+        int64_t rows = 0, tiles = 0;
+        if (b < p.B) {
+            rows = clamp_len(p, p.len[b]);
+            tiles = (queries_of(p, b).n + kPromptRows - 1) / kPromptRows;
+        }
+        int64_t r = rows, t = tiles;
+        for (int o = 1; o < 64; o <<= 1) {
+            const int64_t ru = __shfl_up(static_cast<long long>(r), o), tu = __shfl_up(static_cast<long long>(t), o);
+            if (lane >= o) {
+                r += ru;
+                t += tu;
+            }
+        }
+        if (lane == 63) {
+            s_row[w] = r;
+            s_tile[w] = t;
+        }
+        __syncthreads();
+        int64_t ra = 0, ta = 0;
+        for (int i = 0; i < 16; ++i) {
+            if (i < w) {
+                r += s_row[i];
+                t += s_tile[i];
+            }
+            ra += s_row[i];
+            ta += s_tile[i];
+        }
+        if (b < p.B) {
+            p.plan[b] = row0 + r - rows;
+            p.plan[p.B + 1 + b] = tile0 + t - tiles;
+        }
+        row0 += ra;
+        tile0 += ta;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        p.plan[p.B] = row0;
+        p.plan[2 * p.B + 1] = tile0;
+        *p.odd = 0;
+    }
+}
+
+// Keys and values of 128 rows of the line: a product with the rows gathered from
+// their pages.  The first output tile's workgroups also bring the rows' second
+// parts into the line.
+template <int DT>
+__global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
+    using L = Tile<128>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) uint8_t*)smem));
+    const int mk = p.H * p.dn, mv = p.H * p.dv;
+    const int tk = (mk + 127) / 128, tv = (mv + 127) / 128, tr = (p.rows + 127) / 128;
+    const int64_t task = task_of(static_cast<int64_t>(tk + tv) * tr);
+    if (task < 0) return;
+    const int mt = static_cast<int>(task / tr), r0 = static_cast<int>(task - static_cast<int64_t>(mt) * tr) * 128;
+    const int64_t total = p.plan[p.B];
+    if (r0 >= total) return;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hh = lane >> 5, col = lane & 31, r8 = lane >> 3, chunk = (lane & 7) ^ r8;
+    const bool values = mt >= tk;
+    const int m0 = (values ? mt - tk : mt) * 128, M = values ? mv : mk, per = values ? p.dv : p.dn;
+    const uint8_t* const wt0 = values ? p.wv : p.wk;
+    const int64_t* const wst = values ? p.wvs : p.wks;
+    // the row of the line, null where its page does not exist
+    auto row_of = [&](int r) -> const uint8_t* {
+        if (r >= total) return nullptr;
+        const int b = last_at(p.plan, p.B, r);
+        const int j = r - static_cast<int>(p.plan[b]);
+        const int pg = p.table[b * p.table_stride + (j >> p.ps_shift)];
+        if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) return nullptr;
+        return p.kc + 16 * (pg * p.kcs[0] + (j & ((1 << p.ps_shift) - 1)) * p.kcs[1]);
+    };
+    const uint8_t *wp[L::kW], *xp[L::kX];
+#pragma unroll
+    for (int i = 0; i < L::kX; ++i) {
+        const uint8_t* const x = row_of(r0 + (w * L::kX + i) * 8 + r8);
+        xp[i] = x ? x + 16 * chunk : nullptr;
+    }
+#pragma unroll
+    for (int i = 0; i < L::kW; ++i) {
+        const int m = min(m0 + (w * L::kW + i) * 8 + r8, M - 1), h = m / per;
+        wp[i] = wt0 + 16 * (h * wst[0] + (m - h * per) * wst[1] + chunk);
+    }
+    if (mt == 0) {
+        for (int r = threadIdx.x >> 3; r < 128 && r0 + r < total; r += 32) {
+            const uint8_t* const x = row_of(r0 + r);
+            for (int c = lane & 7; c < p.dr / 8; c += 8)
+                *reinterpret_cast<uint4*>(p.pe + (static_cast<int64_t>(r0 + r) * p.dr + 8 * c) * 2) =
+                    x ? *reinterpret_cast<const uint4*>(x + 2 * p.R + 16 * c) : make_uint4(0, 0, 0, 0);
+            if ((lane & 7) == 0) p.there[r0 + r] = x != nullptr;
+        }
+    }
+    v16f acc[L::BM][L::BT];
+    product_tile<DT, 128>(smem_at, wp, xp, p.R, acc);
+    const int wm = w % L::WM, wt = w / L::WM;
+    uint8_t* const to = values ? p.v : p.k;
+    bool bad = false;
+#pragma unroll
+    for (int b = 0; b < L::BT; ++b) {
+        const int r = r0 + (wt * L::BT + b) * 32 + col;
+        if (r >= total || r >= p.rows) continue;
+#pragma unroll
+        for (int a = 0; a < L::BM; ++a)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const int m = m0 + (wm * L::BM + a) * 32 + 2 * i + 4 * hh, h = m / per;
+                if (m >= M) continue;
+                const v4s y = pack4<DT>(acc[a][b][i], acc[a][b][i + 1], acc[a][b][i + 2], acc[a][b][i + 3]);
+                const uint2 u = __builtin_bit_cast(uint2, y);
+                bad |= nonfinite2<DT>(u.x) || nonfinite2<DT>(u.y);
+                *reinterpret_cast<v4s*>(to + 2 * ((static_cast<int64_t>(h) * p.rows + r) * per + m - h * per)) = y;
+            }
+    }
+    if (values && bad) *p.odd = 1;
+}
+
+// 128 queries of one head (32 a wave) against 64 keys at a time, double-buffered.
+template <int DT, int DN, int DR, int DV>
+__global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
+    constexpr int TK = 64;
+    constexpr int DQ = DN + DR, NC = DQ / 8, NV = DV / 8;  // chunks of a key and of a value
+    constexpr int NQ = DQ / 16, ND = DV / 32;
+    constexpr int kKB = DQ * 2, kVB = DV * 2;
+    constexpr int kVAt = TK * kKB, kStage = TK * (kKB + kVB);
+    constexpr int kK = TK * NC / 64 / kWaves, kV = TK * NV / 64 / kWaves;  // wide loads of a wave
+    static_assert(NC % 8 == 0 && NV % 8 == 0, "layout");
+    extern __shared__ __align__(16) uint8_t smem[];  // nothing beside it: two workgroups fill a CU
+    const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) uint8_t*)smem));
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int hh = lane >> 5, col = lane & 31;
+    const int64_t tiles = p.plan[2 * p.B + 1], task = task_of(tiles * p.H);
+    if (task < 0) return;
+    const int h = static_cast<int>(task / tiles);
+    const int64_t tile = tiles - 1 - (task - h * tiles);  // long ones first
+    const int b = last_at(p.plan + p.B + 1, p.B, tile);
+    const int i0 = static_cast<int>(tile - p.plan[p.B + 1 + b]) * kPromptRows;
+    const Queries qs = queries_of(p, b);
+    const int64_t row0 = p.plan[b];
+    const int len = clamp_len(p, p.len[b]);
+    const int mine = i0 + w * 32 + col;  // the lane's query
+    const bool in = mine < qs.n;
+    uint8_t* const dst = p.out + 16 * ((qs.first + mine) * p.os[0] + h * p.os[1]);
+    if (row0 + len > p.rows) {  // the line is too short for this sequence
+        if (in)
+            for (int d = 4 * hh; d < p.dv; d += 8)
+                *reinterpret_cast<v4s*>(dst + 2 * d) = pack4<DT>(NAN, NAN, NAN, NAN);
+        return;
+    }
+    const int shift = len - qs.n;  // position of query 0
+    const int pos = mine + shift;
+    const int low = i0 + w * 32 + shift;  // first and last position of the wave
+    const int high = i0 + w * 32 < qs.n ? min(i0 + w * 32 + 31, qs.n - 1) + shift : -1;
+    const int last = min(i0 + kPromptRows, qs.n) - 1 + shift;  // of the workgroup
+    const int T = last < 0 ? 0 : last / TK + 1;
+
+    // staging: chunk e = 64 i + lane of a tile's keys is chunk e % NC of row e / NC; a key's first
+    // DN / 8 chunks come from the expanded keys, the others from the line's second parts
+    const uint8_t *kp[kK], *vp[kV];
+    uint32_t ks[kK], kr[kK];
+    const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero);
+#pragma unroll
+    for (int i = 0; i < kK; ++i) {
+        const int e = (w * kK + i) * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ (r & 7);
+        kr[i] = r;
+        if (chunk < DN / 8) {
+            const bool there = chunk * 8 < p.dn;
+            kp[i] = there ? p.k + 2 * ((static_cast<int64_t>(h) * p.rows + row0 + r) * p.dn + chunk * 8) : zero;
+            ks[i] = there ? TK * p.dn * 2 : 0;
+        } else {
+            const int c = chunk - DN / 8;
+            const bool there = c * 8 < p.dr;
+            kp[i] = there ? p.pe + 2 * ((row0 + r) * p.dr + c * 8) : zero;
+            ks[i] = there ? TK * p.dr * 2 : 0;
+        }
+    }
+    const int v_row = (w * kV * 64 + lane) / NV;  // of the first load; the next is 64 / NV rows on
+    uint32_t vs[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        const int r = v_row + i * (64 / NV), c = (lane % NV) ^ swizzle(r);
+        const bool there = c * 8 < p.dv;
+        vp[i] = there ? p.v + 2 * ((static_cast<int64_t>(h) * p.rows + row0 + r) * p.dv + c * 8) : zero;
+        vs[i] = there ? TK * p.dv * 2 : 0;
+    }
+    auto stage = [&](int t, uint32_t at) __attribute__((always_inline)) {
+        const bool cut = (t + 1) * TK > len;  // rows past the sequence are staged as zeros
+        const uint32_t to = smem_at + at + w * kK * 1024, tv = smem_at + at + kVAt + w * kV * 1024;
+#pragma unroll
+        for (int i = 0; i < kK; ++i) {
+            const uint8_t* src = kp[i];
+            if (cut && t * TK + static_cast<int>(kr[i]) >= len) src = zero;
+            load_lds(src, to + i * 1024);
+            kp[i] += ks[i];
+        }
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const uint8_t* src = vp[i];
+            if (cut && t * TK + v_row + i * (64 / NV) >= len) src = zero;
+            load_lds(src, tv + i * 1024);
+            vp[i] += vs[i];
+        }
+    };
+    // lane j: whether row j of tile t exists
+    auto there = [&](int t) {
+        const int r = t * TK + lane;
+        return r < len ? p.there[row0 + r] : 0;
+    };
+    uint32_t k_rd[4], v_rd[2];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) k_rd[s] = smem_at + col * kKB + (((2 * s + hh) ^ (col & 7)) << 4);
+    {
+        const int vrow = 4 * hh + ((lane & 15) >> 2);
+        const int c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            v_rd[s] = smem_at + kVAt + vrow * kVB + (((4 * s + c) ^ swizzle(vrow)) << 4) + (lane & 1) * 8;
+    }
+    v8s q[NQ];
+    {
+        const uint8_t* const src = p.q + 16 * ((qs.first + (in ? mine : 0)) * p.qs[0] + h * p.qs[1]);
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) {
+            const int d = s * 16 + hh * 8;
+            const int from = d < DN ? (d < p.dn ? d : -1) : (d - DN < p.dr ? d - DN + p.dn : -1);
+            v8s z = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (in && from >= 0) z = *reinterpret_cast<const v8s*>(src + 2 * from);
+            q[s] = p.flip ? z ^ static_cast<short>(0x8000) : z;
+        }
+    }
+    float mx = -INFINITY, l = 0.f;
+    v16f o[ND];
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
+    const float scale2 = p.scale2;
+    const bool odd = *p.odd != 0;
+    int here = 0, next = 0;
+    if (T > 0) {
+        here = there(0);
+        if (T > 1) next = there(1);
+        stage(0, 0);
+    }
+    uint32_t at = 0;
+#pragma unroll 1
+    for (int t = 0; t < T; ++t) {
+        // this wave's loads of tile t have landed; with the barrier everyone's, and everyone
+        // has read the other stage
+        wait_vm<0>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const uint64_t okm = __ballot(here != 0);
+        here = next;
+        if (t + 1 < T) {
+            stage(t + 1, kStage - at);
+            if (t + 2 < T) next = there(t + 2);
+        }
+        const int kb = t * TK;
+        uint64_t nf = 0;
+        if (odd && kb + TK - 1 > i0 + shift) {
+            // infinities or NaN are about, and some of the queries do not see all of the tile: these
+            // values go out of it (0 times them would reach those queries), and who sees the row gets a
+            // score of NaN.  Every wave looks at all rows; then each clears a part.
+            unsigned long long rows = 0;
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+                for (int i = pass ? w : 0; i < TK * NV / 64; i += pass ? kWaves : 1) {
+                    v8s* const e = reinterpret_cast<v8s*>(smem + at + kVAt + i * 1024 + lane * 16);
+                    const uint4 u = __builtin_bit_cast(uint4, *e);
+                    if (nonfinite2<DT>(u.x) || nonfinite2<DT>(u.y) || nonfinite2<DT>(u.z) || nonfinite2<DT>(u.w)) {
+                        if (pass)
+                            *e = v8s{0, 0, 0, 0, 0, 0, 0, 0};
+                        else
+                            rows |= 1ull << ((i * 64 + lane) / NV);
+                    }
+                }
+                __syncthreads();
+            }
+            for (int s = 32; s; s >>= 1) rows |= __shfl_xor(rows, s);
+            nf = rows;
+        }
+        if (kb <= high) {
+            v16f x[2];
+            float top = -INFINITY;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[ks][i] = 0.f;
+#pragma unroll
+                for (int s = 0; s < NQ; ++s)
+                    x[ks] = mfma<DT>(lds_read(k_rd[s & 3] + at + ks * 32 * kKB + (s >> 2) * 128), q[s], x[ks]);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                if (kb + TK - 1 > low || okm != ~0ull) {
+                    const int key0 = kb + 32 * ks;
+                    const uint32_t see = (static_cast<uint32_t>(okm >> (32 * ks)) & ~bits_from(pos - key0 + 1)) >> 4 * hh;
+                    const uint32_t bad = static_cast<uint32_t>(nf >> (32 * ks)) >> 4 * hh;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t bit = 1u << (8 * (i >> 2) + (i & 3));
+                        x[ks][i] = see & bit ? bad & bit ? __builtin_nanf("") : x[ks][i] : -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, x[ks][i]);
+            }
+            top = scaled(half_max(top), scale2);
+            if (__any(top - mx > kUp<DT> + 8.f)) {
+                const float mn = fmaxf(mx, top - kUp<DT>);
+                const float a = shift_of(mx, mn);
+                l *= a;
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[dt][i] *= a;
+                mx = mn;
+            }
+            const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[ks][i] = __builtin_amdgcn_exp2f(less(scaled(x[ks][i], scale2), ref));
+                    l += x[ks][i];
+                }
+#pragma unroll
+                for (int t2 = 0; t2 < 2; ++t2) {
+                    const v4s lo = pack4<DT>(x[ks][8 * t2], x[ks][8 * t2 + 1], x[ks][8 * t2 + 2], x[ks][8 * t2 + 3]);
+                    const v4s hi =
+                        pack4<DT>(x[ks][8 * t2 + 4], x[ks][8 * t2 + 5], x[ks][8 * t2 + 6], x[ks][8 * t2 + 7]);
+                    const v8s pf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) {
+                        const uint32_t a = v_rd[dt & 1] + at + (ks * 32 + t2 * 16) * kVB + (dt >> 1) * 128;
+                        const v8s vf =
+                            __builtin_shufflevector(lds_read_tr(a), lds_read_tr(a + 8 * kVB), 0, 1, 2, 3, 4, 5, 6, 7);
+                        o[dt] = mfma<DT>(vf, pf, o[dt]);
+                    }
+                }
+            }
+        }
+        at = kStage - at;
+    }
+    l = half_sum(l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // a query that sees nothing: zero
+    if (!in) return;
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const int d = 32 * dt + 2 * i + 4 * hh;
+            if (d < p.dv)
+                *reinterpret_cast<v4s*>(dst + 2 * d) =
+                    pack4<DT>(o[dt][i] * inv, o[dt][i + 1] * inv, o[dt][i + 2] * inv, o[dt][i + 3] * inv);
+        }
+}
+
+template <int DT, int TT>
+hipError_t product_one(const ProductParams& p, hipStream_t st, const LaunchEvents& ev) {
+    const int64_t tasks = static_cast<int64_t>((p.M + 127) / 128) * ((p.T + TT - 1) / TT) * p.H;
+    hipExtLaunchKernelGGL((k_product<DT, TT>), dim3(static_cast<unsigned>(grid_of(tasks))), dim3(kThreads),
+                          2 * Tile<TT>::kStage, st, ev.start, ev.stop, 0, p);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t expand_one(const PromptParams& p, hipStream_t st, const LaunchEvents& ev) {
+    const int64_t tasks =
+        static_cast<int64_t>((p.H * p.dn + 127) / 128 + (p.H * p.dv + 127) / 128) * ((p.rows + 127) / 128);
+    hipExtLaunchKernelGGL((k_prompt_expand<DT>), dim3(static_cast<unsigned>(grid_of(tasks))), dim3(kThreads),
+                          2 * Tile<128>::kStage, st, ev.start, ev.stop, 0, p);
+    return hipGetLastError();
+}
+
+template <int DT, int DN, int DR, int DV>
+hipError_t prompt_one(const PromptParams& p, hipStream_t st, const LaunchEvents& ev) {
+    constexpr int lds = 2 * 64 * (DN + DR + DV) * 2;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(k_prompt_attn<DT, DN, DR, DV>), lds);
+    if (e != hipSuccess) return e;
+    const int64_t tiles = p.T / kPromptRows + (p.B < p.T ? p.B : p.T);  // at most
+    hipExtLaunchKernelGGL((k_prompt_attn<DT, DN, DR, DV>), dim3(static_cast<unsigned>(grid_of(tiles * p.H))),
+                          dim3(kThreads), lds, st, ev.start, ev.stop, 0, p);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t prompt_dims(const PromptParams& p, hipStream_t st, const LaunchEvents& ev) {
+    if (p.dn <= 64 && p.dr <= 64 && p.dv <= 64) return prompt_one<DT, 64, 64, 64>(p, st, ev);
+    if (p.dn <= 96 && p.dr <= 32) return prompt_one<DT, 96, 32, 128>(p, st, ev);
+    return prompt_one<DT, 128, 64, 128>(p, st, ev);
+}
+
+}  // namespace
+
+hipError_t launch_product(const ProductParams& p, int dtype, hipStream_t st, const LaunchEvents& ev) {
+    if (dtype == DT_BF16) return p.tt == 32 ? product_one<DT_BF16, 32>(p, st, ev) : product_one<DT_BF16, 128>(p, st, ev);
+    return p.tt == 32 ? product_one<kDTypeF16, 32>(p, st, ev) : product_one<kDTypeF16, 128>(p, st, ev);
+}
+
+hipError_t launch_prompt_plan(const PromptParams& p, hipStream_t st, const LaunchEvents& ev) {
+    hipExtLaunchKernelGGL(k_prompt_plan, dim3(1), dim3(1024), 0, st, ev.start, ev.stop, 0, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_prompt_expand(const PromptParams& p, int dtype, hipStream_t st, const LaunchEvents& ev) {
+    return dtype == DT_BF16 ? expand_one<DT_BF16>(p, st, ev) : expand_one<kDTypeF16>(p, st, ev);
+}
+
+hipError_t launch_prompt_attn(const PromptParams& p, int dtype, hipStream_t st, const LaunchEvents& ev) {
+    return dtype == DT_BF16 ? prompt_dims<DT_BF16>(p, st, ev) : prompt_dims<kDTypeF16>(p, st, ev);
+}
+
+}  // namespace sv

@@ -24,6 +24,10 @@ enum TreeKernelKind : int {
     KK_CACHE_COPY,
     KK_LATENT_ATTN,
     KK_LATENT_JOIN,
+    KK_PRODUCT,
+    KK_PROMPT_PLAN,
+    KK_PROMPT_EXPAND,
+    KK_PROMPT_ATTN,
     KK_ALL
 };
 
