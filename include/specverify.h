@@ -738,6 +738,123 @@ int spec_latent_prompt(const sv_latent_prompt* args, void* stream);
  * the call refuses. */
 int64_t spec_latent_prompt_workspace(const sv_latent_prompt* args);
 
+/*
+ * spec_cache_reserve -- room for n_new[b] more rows of every sequence (new
+ * requests' prompts, behind a length of 0; the next token of running ones) and
+ * where these rows go.  A partly filled last page is filled up, further pages are
+ * taken lowest free page first, in the order of the sequences; a page is in use
+ * if a live entry of the tables names it.
+ *
+ * table, len     device int32 [B, width] (row stride table_stride) and [B].
+ * n_new          device int32 [B]; a negative count is 0.
+ * pages, page_size, width  the cache's (no tensor is needed); limits as spec_cache_commit's.
+ *                B <= 65534; B * (width / 64 + 1) < 2^31.
+ * rows           the length of the lists below: at least the sum of the counts.
+ * out_table, out_len  as spec_cache_commit's: the new tables, -1 behind the live
+ *                entries, and lengths; they may be table and len themselves.
+ * out_start      device int32 [B + 1]: sequence b's new rows are entries
+ *                out_start[b] .. out_start[b + 1] of the lists.
+ * out_slots, out_position  device int32 [rows]: the new rows' slots, page *
+ *                page_size + place in the page, and their positions in the
+ *                sequence (its old length on); -1 behind the last one.
+ * out_status     device int32 [1]: 0; the number of pages that were lacking; or -1
+ *                when a length, a live page number or `rows` is out of range, a
+ *                table row too short, or a partly filled page that is to be
+ *                appended to is named by another live entry.  Unless 0, tables
+ *                and lengths go out as they came in, out_start is 0 and the lists -1.
+ * workspace      at least spec_cache_reserve_workspace bytes, aligned to 4.
+ *
+ * Outputs must not overlap each other, nor (but for the two that may be) the
+ * inputs.  Errors as spec_cache_commit.
+ */
+int spec_cache_reserve(const int32_t* table, int64_t table_stride, const int32_t* len, const int32_t* n_new, int32_t B,
+                       int32_t width, int32_t pages, int32_t page_size, int32_t rows, int32_t* out_table,
+                       int64_t out_stride, int32_t* out_len, int32_t* out_start, int32_t* out_slots,
+                       int32_t* out_position, int32_t* out_status, void* workspace, int64_t workspace_bytes,
+                       void* stream);
+
+int64_t spec_cache_reserve_workspace(int32_t B, int32_t page_size, int32_t rows);
+
+/*
+ * spec_cache_write -- row t of `a`, and row t of `b` behind it, become the cache row
+ * in slot slots[t]; a slot outside the cache (-1) takes nothing.  For latent rows a
+ * is the latent part and b the part that carries positions; dim_b may be 0 (b is
+ * not looked at).  No two tokens may have the same slot, and a and b must not
+ * overlap the cache.
+ *
+ * cache          [pages, page_size, dim_a + dim_b], strides for (page, slot); a
+ *                [T, dim_a], b [T, dim_b], strides between rows; SV_F32, SV_BF16 or
+ *                SV_F16.  Dimensions (at most 65536), strides and data are multiples of
+ *                16 bytes.  0 <= T <= 2^28.
+ * slots          device int32 [T].
+ *
+ * Errors: SV_EINVAL (NULL, negative stride, a stride of 0 in the cache), SV_ESHAPE,
+ * SV_EDTYPE, SV_EALIGN, SV_EHIP.
+ */
+typedef struct {
+    void* cache;
+    int64_t cache_stride[2];
+    int32_t dtype, pages, page_size;
+    int32_t T, dim_a, dim_b;
+    const void* a;
+    int64_t a_stride;
+    const void* b;
+    int64_t b_stride;
+    const int32_t* slots;
+} sv_cache_rows;
+
+int spec_cache_write(const sv_cache_rows* args, void* stream);
+
+/*
+ * ---- Beam search -----------------------------------------------------------
+ *
+ * spec_beam_select -- the W best continuations of a sequence's W beams.  Beam w's
+ * candidates are the ids v with a logit above -inf, at
+ *
+ *   scores[b, w] + x[v] - log sum_u exp(x[u]),  x = logits[b, w],
+ *
+ * and a finished beam has one, the token `end` at scores[b, w].  The W largest come
+ * out best first, equal ones in the order of w * V + v; between beams the order is
+ * that of the scores in float64, within a beam that of the logits.  A beam whose score is -inf (at the first step all but one),
+ * +inf or NaN, or whose logits hold a NaN, +inf or nothing above -inf, has no
+ * candidates; its logits are not read where the score is -inf or the beam finished.
+ *
+ * logits         [B, W, V] (the descriptor's P = W <= SPECVERIFY_MAX_BEAMS); B * W <=
+ *                65535, V <= 2^24.
+ * scores         device float32 [B, W].
+ * finished       device int32 [B, W], non-zero: finished; or NULL.
+ * end            the token that finishes a beam, or -1 (then finished is NULL).
+ * out_tokens     device int32 [B, W].
+ * out_ancestor   device int32 [B * W]: b * W + the beam continued, as
+ *                spec_cache_fork and spec_beam_reorder take it.
+ * out_scores     device float32 [B, W], rounded once.
+ * out_finished   device int32 [B, W]: 1 where the token is `end` or the beam was finished.
+ *                Where there are fewer candidates than beams: -1, -1, -inf and 0.
+ *                Outputs must not overlap the inputs or each other.
+ * workspace      at least spec_beam_workspace bytes, aligned to 8.
+ *
+ * Errors as spec_verify, SV_ETOOBIG for too small a workspace.
+ */
+#define SPECVERIFY_MAX_BEAMS 64
+int spec_beam_select(const sv_logits* logits, const float* scores, const int32_t* finished, int32_t end,
+                     int32_t* out_tokens, int32_t* out_ancestor, float* out_scores, int32_t* out_finished,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
+int64_t spec_beam_workspace(int32_t B, int32_t W, int32_t V);
+
+/*
+ * spec_beam_reorder -- row k of dst becomes row ancestor[k] of src (a beam's
+ * history, or any state kept by rows; pages follow by spec_cache_fork).  Rows are
+ * row_bytes long, strides are in bytes; an ancestor outside [0, rows) makes row k
+ * of dst zero.  src and dst must not overlap, nor the rows of dst each other;
+ * rows that lie at multiples of 16 bytes are the fastest.  rows <= 65535.
+ *
+ * Errors: SV_EINVAL (NULL, src == dst, a negative stride, rows of dst that overlap),
+ * SV_ESHAPE, SV_EALIGN (ancestor), SV_EHIP.
+ */
+int spec_beam_reorder(const void* src, int64_t src_stride, void* dst, int64_t dst_stride, int64_t row_bytes,
+                      int32_t rows, const int32_t* ancestor, void* stream);
+
 /* Human-readable text for a status code (for SV_EHIP, the last HIP error). */
 const char* spec_verify_strerror(int status);
 

@@ -23,14 +23,16 @@ STATUS = {0: "SV_OK", -1: "SV_EINVAL", -2: "SV_ESHAPE", -3: "SV_EDTYPE", -4: "SV
           -6: "SV_EALIGN", -7: "SV_ECAPTURE", -8: "SV_ETOOBIG"}
 KERNEL_KINDS = ("stats", "topp", "rows", "smc", "produce", "tree_attention", "tree_join", "verify_clear",
                 "tree_verify", "cache_plan", "cache_copy", "latent_attention", "latent_join",
-                "head_product", "prompt_plan", "prompt_expand", "prompt_attention")
+                "head_product", "prompt_plan", "prompt_expand", "prompt_attention", "beam_stats",
+                "beam_select", "beam_reorder", "reserve_plan", "reserve_write", "cache_write")
 
 EXPORTS = ("spec_verify", "spec_verify_noalloc", "spec_verify_probe", "spec_greedy_verify", "spec_hispec_verify", "spec_smc_step",
            "spec_draft_produce",
            "spec_tree_attention", "spec_tree_attention_workspace", "spec_verify_tree", "spec_verify_tree_workspace",
            "spec_cache_commit", "spec_cache_fork", "spec_cache_workspace",
            "spec_latent_attention", "spec_latent_attention_workspace", "spec_head_product", "spec_latent_prompt",
-           "spec_latent_prompt_workspace",
+           "spec_latent_prompt_workspace", "spec_cache_reserve", "spec_cache_reserve_workspace", "spec_cache_write",
+           "spec_beam_select", "spec_beam_workspace", "spec_beam_reorder",
            "spec_verify_strerror",
            "spec_verify_release",
            "spec_verify_abi_version", "spec_verify_profile_enable", "spec_verify_profile_read",
@@ -675,9 +677,10 @@ def cache_fork(k_cache, v_cache, block_table, seq_len, ancestor, *, out_table=No
 
 # ---- latent rows: one row per token, shared by the heads
 
-# the fields of sv_latent_attention, sv_head_product and sv_latent_prompt in order
+# the fields of sv_latent_attention, sv_head_product, sv_cache_rows and sv_latent_prompt in order
 _PACK_LATENT = struct.Struct("@iiiiiiP3qP2qP2qiii4xPqPPPf4xP3qPq").pack
 _PACK_PRODUCT = struct.Struct("@iiiii4xP2qP2qP2q").pack
+_PACK_WRITE = struct.Struct("@P2qiiiiiiPqPqP").pack
 _PACK_PROMPT = struct.Struct("@iiiiiiiii4xP2qP2qiii4xPqPPP2qP2qf4xP2qPq").pack
 _latent = None
 
@@ -687,7 +690,7 @@ def _latent_calls():
     global _latent
     if _latent is None:
         lib = load()
-        vp, blob, i64 = ctypes.c_void_p, ctypes.c_char_p, ctypes.c_int64
+        vp, blob, i32, i64 = ctypes.c_void_p, ctypes.c_char_p, ctypes.c_int32, ctypes.c_int64
 
         def entry(name, args, res=ctypes.c_int):
             f = lib[name]
@@ -696,7 +699,13 @@ def _latent_calls():
 
         _latent = (lib, entry("spec_latent_attention", [blob, vp]),
                    entry("spec_latent_attention_workspace", [blob], i64), entry("spec_head_product", [blob, vp]),
-                   entry("spec_latent_prompt", [blob, vp]), entry("spec_latent_prompt_workspace", [blob], i64))
+                   entry("spec_latent_prompt", [blob, vp]), entry("spec_latent_prompt_workspace", [blob], i64),
+                   entry("spec_cache_reserve", [vp, i64, vp, vp, i32, i32, i32, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp,
+                                                i64, vp]),
+                   entry("spec_cache_reserve_workspace", [i32, i32, i32], i64), entry("spec_cache_write", [blob, vp]),
+                   entry("spec_beam_select", [blob, vp, vp, i32, vp, vp, vp, vp, vp, i64, vp]),
+                   entry("spec_beam_workspace", [i32, i32, i32], i64),
+                   entry("spec_beam_reorder", [vp, i64, vp, i64, i64, i32, vp, vp]))
     return _latent
 
 
@@ -845,6 +854,146 @@ def latent_prompt(q, cache, block_table, seq_len, q_start, w_k, w_v, *, rows, sc
                             lambda: size_of(block(0, 0)))
     ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
     _check(lib, call(block(ws.data_ptr(), need), _raw_stream(index)))
+    return out
+
+
+def cache_reserve(block_table, seq_len, n_new, *, pages, page_size, rows, out_table=None, out_len=None, stream=None):
+    """Room for n_new[b] more rows of every sequence, and where they go
+    (spec_cache_reserve).
+
+    block_table [B, width], seq_len [B], n_new [B]: int32.  pages and page_size:
+    the cache's.  rows: at least the sum of n_new, the length of the lists.
+    Returns (table, length, start [B + 1], slots [rows], position [rows], status
+    [1]), int32; out_table and out_len may be block_table and seq_len themselves.
+    status: 0, the number of pages lacking, or -1; unless 0, nothing is reserved.
+    """
+    lib, call, size_of = _latent_calls()[0], _latent_calls()[6], _latent_calls()[7]
+    index = seq_len.get_device()
+    if seq_len.dim() != 1:
+        raise ValueError("seq_len must be [B]")
+    B = seq_len.shape[0]
+    tab, tab_stride = _table(block_table, "block_table", B, index)
+    width = block_table.shape[1]
+    ln, nn = _array(seq_len, "seq_len", (B,), index), _array(n_new, "n_new", (B,), index)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return cache_reserve(block_table, seq_len, n_new, pages=pages, page_size=page_size, rows=rows,
+                                 out_table=out_table, out_len=out_len)
+    if out_table is None:
+        out_table = seq_len.new_empty((B, width))
+    if out_len is None:
+        out_len = seq_len.new_empty((B,))
+    new, stride = _table(out_table, "out_table", B, index, width)
+    new_len = _array(out_len, "out_len", (B,), index)
+    need = _workspace_bytes(lib, ("reserve", B, page_size, rows), lambda: size_of(B, page_size, rows))
+    # one allocation: the lists and starts, the status and the workspace
+    both = seq_len.new_empty((2 * rows + B + 2 + need // 4,))
+    slots, position, start, status, ws = torch.split(both, (rows, rows, B + 1, 1, need // 4))
+    _check(lib, call(tab, tab_stride, ln, nn, B, width, pages, page_size, rows, new, stride, new_len, start.data_ptr(),
+                     slots.data_ptr(), position.data_ptr(), status.data_ptr(), ws.data_ptr(), need, _raw_stream(index)))
+    return out_table, out_len, start, slots, position, status
+
+
+def cache_write(cache, slots, a, b=None, *, stream=None):
+    """Rows into their slots of a paged cache (spec_cache_write): row t of a, and
+    of b behind it, into slot slots[t], -1 for none.
+
+    cache [pages, page_size, dim] (float32, bfloat16 or float16), written in
+    place; a [T, dim_a] and b [T, dim_b] (None: nothing) of the same dtype with
+    dim_a + dim_b = dim; last axes contiguous, other strides any multiples of 16
+    bytes.  slots [T] int32, no slot twice.
+    """
+    lib, call = _latent_calls()[0], _latent_calls()[8]
+    if cache.dim() != 3 or a.dim() != 2:
+        raise ValueError("cache must be [pages, page_size, dim] and a [T, dim_a]")
+    dt, index = cache.dtype, cache.get_device()
+    if dt not in _DTYPES:
+        raise ValueError(f"cache: dtype {dt} is not float32, bfloat16 or float16")
+    _no_grad(cache, a) if b is None else _no_grad(cache, a, b)
+    pages, page_size, dim = cache.shape
+    T, dim_a = a.shape
+    dim_b = dim - dim_a
+    cs = _rows(cache, "cache", cache.shape, dt, index)
+    st_a = _tokens(a, "a", a.shape, dt, index)
+    if b is None:
+        if dim_b:
+            raise ValueError(f"rows of {dim_a} elements for a cache of {dim}")
+        at_b, st_b = 0, (0,)
+    else:
+        st_b = _tokens(b, "b", (T, dim_b), dt, index)
+        at_b = b.data_ptr()
+    where = _array(slots, "slots", (T,), index)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return cache_write(cache, slots, a, b)
+    _check(lib, call(_PACK_WRITE(cache.data_ptr(), cs[0], cs[1], _DTYPES[dt], pages, page_size, T, dim_a, dim_b,
+                                 a.data_ptr(), st_a[0], at_b, st_b[0], where), _raw_stream(index)))
+
+
+def beam_select(logits, scores, finished=None, *, end=-1, out_tokens=None, out_ancestor=None, out_scores=None,
+                out_finished=None, stream=None):
+    """The W best continuations of every sequence's W beams (spec_beam_select).
+
+    logits [B, W, V]: float32 or bfloat16, V contiguous.  scores [B, W] float32,
+    the beams' running log-probabilities (-inf: no such beam).  finished [B, W]
+    int32 or None; end: the token that finishes a beam, -1 for none.  Returns
+    (tokens [B, W] int32, ancestor [B * W] int32, as cache_fork and beam_reorder
+    take it, scores [B, W] float32, finished [B, W] int32), best first.
+    """
+    lib, call, size_of = _latent_calls()[0], _latent_calls()[9], _latent_calls()[10]
+    desc = _probs(logits, "logits")
+    index = logits.get_device()
+    B, W, V = logits.shape
+    _no_grad(logits, scores)
+    sc = _array(scores, "scores", (B, W), index, _F32)
+    fin = None if finished is None else _array(finished, "finished", (B, W), index)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return beam_select(logits, scores, finished, end=end, out_tokens=out_tokens, out_ancestor=out_ancestor,
+                               out_scores=out_scores, out_finished=out_finished)
+    if out_tokens is None:
+        out_tokens = torch.empty((B, W), dtype=_I32, device=logits.device)
+    if out_ancestor is None:
+        out_ancestor = torch.empty((B * W,), dtype=_I32, device=logits.device)
+    if out_scores is None:
+        out_scores = scores.new_empty((B, W))
+    if out_finished is None:
+        out_finished = torch.empty((B, W), dtype=_I32, device=logits.device)
+    need = _workspace_bytes(lib, ("beam", index, B, W, V), lambda: size_of(B, W, V))
+    ws = torch.empty((need,), dtype=torch.uint8, device=logits.device)
+    _check(lib, call(desc, sc, fin, end, _array(out_tokens, "out_tokens", (B, W), index),
+                     _array(out_ancestor, "out_ancestor", (B * W,), index),
+                     _array(out_scores, "out_scores", (B, W), index, _F32),
+                     _array(out_finished, "out_finished", (B, W), index), ws.data_ptr(), need, _raw_stream(index)))
+    return out_tokens, out_ancestor, out_scores, out_finished
+
+
+def beam_reorder(state, ancestor, *, out=None, stream=None):
+    """Rows of a state in the order of their ancestors (spec_beam_reorder): row k
+    of the result is row ancestor[k] of state, any dtype, [rows, ...], rows
+    contiguous in themselves.  Where ancestor[k] is -1, row k of out is zero.
+    """
+    lib, call = _latent_calls()[0], _latent_calls()[11]
+    index = state.get_device()
+    _no_grad(state)
+    if state.dim() < 1:
+        raise ValueError("state must be [rows, ...]")
+    n = state.shape[0]
+    anc = _array(ancestor, "ancestor", (n,), index)
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return beam_reorder(state, ancestor, out=out)
+    if out is None:
+        out = torch.empty(state.shape, dtype=state.dtype, device=state.device)
+    elif out.shape != state.shape or out.dtype is not state.dtype or out.get_device() != index:
+        raise ValueError(f"out must be {state.dtype} {list(state.shape)} on device {index}")
+    if n == 0:
+        return out
+    if not (state.is_contiguous() or state[0].is_contiguous()) or not (out.is_contiguous() or out[0].is_contiguous()):
+        raise ValueError("rows must be contiguous")
+    size = state.element_size()
+    _check(lib, call(state.data_ptr(), state.stride(0) * size, out.data_ptr(), out.stride(0) * size,
+                     state.numel() // n * size, n, anc, _raw_stream(index)))
     return out
 
 

@@ -16,8 +16,8 @@ LIB = os.path.join(PKG, "libspecverify.so")
 ARCH = "gfx950"
 
 SOURCES = ["sv_kernels.hip", "sv_produce.hip", "sv_tree_attn.hip", "sv_tree_verify.hip", "sv_cache.hip",
-           "sv_latent.hip", "sv_prompt.hip", "sv_api.cpp"]
-DEPS = ["sv_internal.h", "sv_device.h", "sv_tree.h", "sv_attn.h", "sv_latent.h"]
+           "sv_latent.hip", "sv_prompt.hip", "sv_beam.hip", "sv_reserve.hip", "sv_api.cpp"]
+DEPS = ["sv_internal.h", "sv_device.h", "sv_tree.h", "sv_attn.h", "sv_latent.h", "sv_beam.h"]
 
 
 def hipcc():

@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "../../include/specverify.h"
+#include "sv_beam.h"
 #include "sv_internal.h"
 #include "sv_latent.h"
 #include "sv_tree.h"
@@ -1143,6 +1144,174 @@ int latent_prompt_impl(const sv_latent_prompt* a, void* stream_v) {
                         [&](const sv::LaunchEvents& ev) { return sv::launch_prompt_attn(p, dtype, stream, ev); });
 }
 
+static_assert(SPECVERIFY_MAX_BEAMS == sv::kMaxBeams, "beam limit");
+
+// Ids per chunk of a row and chunks: 8192 ids, or 2048 where those would not fill the device.
+int beam_runs(int64_t rows, int V) { return rows * ((V + 8191) / 8192) < 2 * device_cus() ? 1 : 4; }
+
+int64_t beam_workspace(int64_t rows, int W, int V) {
+    const int64_t ids = 2048 * beam_runs(rows, V), chunks = (V + ids - 1) / ids;
+    return align256(rows * chunks * sizeof(sv::BeamChunk)) + rows * chunks * W * sizeof(uint64_t);
+}
+
+int check_beams(int B, int W, int V) {
+    return B < 1 || W < 1 || W > SPECVERIFY_MAX_BEAMS || static_cast<int64_t>(B) * W > 65535 || V < 1 || V > 1 << 24
+               ? SV_ESHAPE
+               : SV_OK;
+}
+
+int beam_select_impl(const sv_logits* l, const float* scores, const int32_t* finished, int32_t end, int32_t* out_tokens,
+                     int32_t* out_ancestor, float* out_scores, int32_t* out_finished, void* ws, int64_t ws_bytes,
+                     void* stream_v) {
+    int rc = check_logits(l);
+    if (rc) return rc;
+    if (!scores || !out_tokens || !out_ancestor || !out_scores || !out_finished || !ws) return SV_EINVAL;
+    if (misaligned(scores, 4) || (finished && misaligned(finished, 4)) || misaligned(out_tokens, 4) ||
+        misaligned(out_ancestor, 4) || misaligned(out_scores, 4) || misaligned(out_finished, 4) || misaligned(ws, 8))
+        return SV_EALIGN;
+    rc = check_beams(l->B, l->P, l->V);
+    if (rc) return rc;
+    if (end < -1 || end >= l->V || (finished && end < 0)) return SV_EINVAL;
+    if (out_scores == scores || (finished && out_finished == finished)) return SV_EINVAL;
+    const int64_t rows = static_cast<int64_t>(l->B) * l->P;
+    if (ws_bytes < beam_workspace(rows, l->P, l->V)) return SV_ETOOBIG;
+    sv::BeamParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.logits = static_cast<const uint8_t*>(l->data);
+    p.sb = l->stride_b;
+    p.sw = l->stride_p;
+    p.scores = scores;
+    p.finished = finished;
+    p.out_tokens = out_tokens;
+    p.out_ancestor = out_ancestor;
+    p.out_finished = out_finished;
+    p.out_scores = out_scores;
+    p.B = l->B;
+    p.W = l->P;
+    p.V = l->V;
+    p.end = end;
+    p.runs = beam_runs(rows, l->V);
+    p.chunks = (l->V + 2048 * p.runs - 1) / (2048 * p.runs);
+    p.rec = static_cast<sv::BeamChunk*>(ws);
+    p.list = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(ws) + align256(rows * p.chunks * sizeof(sv::BeamChunk)));
+    const int dtype = l->dtype == SV_BF16 ? sv::DT_BF16 : sv::DT_F32;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    rc = timed_launch(sv::KK_BEAM_STATS, stream,
+                      [&](const sv::LaunchEvents& ev) { return sv::launch_beam_stats(p, dtype, stream, ev); });
+    if (rc) return rc;
+    return timed_launch(sv::KK_BEAM_SELECT, stream,
+                        [&](const sv::LaunchEvents& ev) { return sv::launch_beam_select(p, dtype, stream, ev); });
+}
+
+int beam_reorder_impl(const void* src, int64_t src_stride, void* dst, int64_t dst_stride, int64_t row_bytes,
+                      int32_t rows, const int32_t* ancestor, void* stream_v) {
+    if (rows < 1 || rows > 65535 || row_bytes < 0 || row_bytes > 1ll << 40) return SV_ESHAPE;
+    if (src_stride < 0 || src_stride > 1ll << 44 || dst_stride > 1ll << 44) return SV_EINVAL;
+    if (rows > 1 && dst_stride < row_bytes) return SV_EINVAL;
+    if (!ancestor || (row_bytes > 0 && (!src || !dst || src == dst))) return SV_EINVAL;
+    if (misaligned(ancestor, 4)) return SV_EALIGN;
+    if (row_bytes == 0) return SV_OK;
+    sv::ReorderParams p;
+    p.src = static_cast<const uint8_t*>(src);
+    p.dst = static_cast<uint8_t*>(dst);
+    p.ancestor = ancestor;
+    p.src_stride = src_stride;
+    p.dst_stride = rows > 1 ? dst_stride : 0;
+    p.bytes = row_bytes;
+    p.rows = rows;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    return timed_launch(sv::KK_BEAM_REORDER, stream,
+                        [&](const sv::LaunchEvents& ev) { return sv::launch_reorder(p, stream, ev); });
+}
+
+int64_t reserve_workspace(int64_t B, int64_t page_size, int64_t rows) {
+    return 4 * (B * sv::kReserveWords + rows / page_size + std::min(B, rows));
+}
+
+int check_reserve(int32_t B, int32_t page_size, int32_t rows) {
+    return B < 1 || B > 65534 || !pow2_page(page_size) || rows < 0 || rows > 1 << 30 ? SV_ESHAPE : SV_OK;
+}
+
+int cache_reserve_impl(const int32_t* table, int64_t table_stride, const int32_t* len, const int32_t* n_new, int32_t B,
+                       int32_t width, int32_t pages, int32_t page_size, int32_t rows, int32_t* out_table,
+                       int64_t out_stride, int32_t* out_len, int32_t* out_start, int32_t* out_slots,
+                       int32_t* out_position, int32_t* out_status, void* ws, int64_t ws_bytes, void* stream_v) {
+    int rc = check_reserve(B, page_size, rows);
+    if (rc) return rc;
+    if (pages < 1 || pages > SPECVERIFY_MAX_PAGES || width < 1 || static_cast<int64_t>(width) * page_size > (1ll << 28) ||
+        B * (static_cast<int64_t>(width) / 64 + 1) >= 1ll << 31)
+        return SV_ESHAPE;
+    if (!table || !len || !n_new || !out_table || !out_len || !out_start || !out_status || !ws ||
+        (rows > 0 && (!out_slots || !out_position)))
+        return SV_EINVAL;
+    if (table_stride < 0 || out_stride < width || (out_table == table && out_stride != table_stride)) return SV_EINVAL;
+    for (const void* q : {static_cast<const void*>(table), static_cast<const void*>(len),
+                          static_cast<const void*>(n_new), static_cast<const void*>(out_table),
+                          static_cast<const void*>(out_len), static_cast<const void*>(out_start),
+                          static_cast<const void*>(out_slots), static_cast<const void*>(out_position),
+                          static_cast<const void*>(out_status), static_cast<const void*>(ws)})
+        if (misaligned(q, 4)) return SV_EALIGN;
+    if (ws_bytes < reserve_workspace(B, page_size, rows)) return SV_ETOOBIG;
+    sv::ReserveParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.table = table;
+    p.len = len;
+    p.n_new = n_new;
+    p.table_stride = table_stride;
+    p.out_stride = out_stride;
+    p.out_table = out_table;
+    p.out_len = out_len;
+    p.start = out_start;
+    p.slots = out_slots;
+    p.position = out_position;
+    p.status = out_status;
+    p.B = B;
+    p.width = width;
+    p.pages = pages;
+    p.ps_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+    p.rows = rows;
+    p.plan = static_cast<int32_t*>(ws);
+    const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    rc = timed_launch(sv::KK_RESERVE_PLAN, stream,
+                      [&](const sv::LaunchEvents& ev) { return sv::launch_reserve_plan(p, stream, ev); });
+    if (rc) return rc;
+    return timed_launch(sv::KK_RESERVE_WRITE, stream,
+                        [&](const sv::LaunchEvents& ev) { return sv::launch_reserve_write(p, stream, ev); });
+}
+
+int cache_write_impl(const sv_cache_rows* a, void* stream_v) {
+    if (!a) return SV_EINVAL;
+    if (a->dtype != SV_F32 && a->dtype != SV_BF16 && a->dtype != SV_F16) return SV_EDTYPE;
+    const int elem = a->dtype == SV_F32 ? 4 : 2;
+    if (a->pages < 1 || a->pages > SPECVERIFY_MAX_PAGES || !pow2_page(a->page_size) || a->T < 0 || a->T > 1 << 28 ||
+        a->dim_a < 1 || a->dim_a > 65536 || a->dim_b < 0 || a->dim_b > 65536)
+        return SV_ESHAPE;
+    if (static_cast<int64_t>(a->dim_a) * elem % 16 || static_cast<int64_t>(a->dim_b) * elem % 16) return SV_EALIGN;
+    if (a->T == 0) return SV_OK;
+    if (!a->slots) return SV_EINVAL;
+    if (misaligned(a->slots, 4)) return SV_EALIGN;
+    sv::WriteParams p;
+    std::memset(&p, 0, sizeof(p));
+    const int32_t cache[2] = {a->pages, a->page_size}, tokens[1] = {a->T};
+    int rc = check_rows(a->cache, a->cache_stride, cache, 2, elem, p.cs);
+    if (!rc && expanded(p.cs, cache, 2)) rc = SV_EINVAL;
+    if (!rc) rc = check_rows(a->a, &a->a_stride, tokens, 1, elem, &p.as);
+    if (!rc && a->dim_b > 0) rc = check_rows(a->b, &a->b_stride, tokens, 1, elem, &p.bs);
+    if (rc) return rc;
+    p.cache = static_cast<uint8_t*>(a->cache);
+    p.a = static_cast<const uint8_t*>(a->a);
+    p.b = static_cast<const uint8_t*>(a->b);
+    p.slots = a->slots;
+    p.T = a->T;
+    p.va = a->dim_a * elem / 16;
+    p.vb = a->dim_b * elem / 16;
+    p.ps_shift = __builtin_ctz(static_cast<unsigned>(a->page_size));
+    p.all = static_cast<int64_t>(a->pages) * a->page_size;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_v);
+    return timed_launch(sv::KK_CACHE_WRITE, stream,
+                        [&](const sv::LaunchEvents& ev) { return sv::launch_cache_write(p, stream, ev); });
+}
+
 }  // namespace
 
 extern "C" {
@@ -1289,6 +1458,50 @@ int spec_cache_fork(const sv_cache* cache, const int32_t* ancestor, int32_t* out
 int64_t spec_cache_workspace(int32_t B, int32_t N, int32_t page_size) {
     if (B < 1 || N < 0 || !pow2_page(page_size)) return SV_ESHAPE;
     return cache_workspace(B, N, page_size);
+}
+
+int spec_beam_select(const sv_logits* logits, const float* scores, const int32_t* finished, int32_t end,
+                     int32_t* out_tokens, int32_t* out_ancestor, float* out_scores, int32_t* out_finished,
+                     void* workspace, int64_t workspace_bytes, void* stream) {
+    return entry([&] {
+        return beam_select_impl(logits, scores, finished, end, out_tokens, out_ancestor, out_scores, out_finished,
+                                workspace, workspace_bytes, stream);
+    });
+}
+
+int64_t spec_beam_workspace(int32_t B, int32_t W, int32_t V) {
+    return entry([&] {
+        const int rc = check_beams(B, W, V);
+        return rc ? rc : beam_workspace(static_cast<int64_t>(B) * W, W, V);
+    });
+}
+
+int spec_beam_reorder(const void* src, int64_t src_stride, void* dst, int64_t dst_stride, int64_t row_bytes,
+                      int32_t rows, const int32_t* ancestor, void* stream) {
+    return entry([&] {
+        return beam_reorder_impl(src, src_stride, dst, dst_stride, row_bytes, rows, ancestor, stream);
+    });
+}
+
+int spec_cache_reserve(const int32_t* table, int64_t table_stride, const int32_t* len, const int32_t* n_new, int32_t B,
+                       int32_t width, int32_t pages, int32_t page_size, int32_t rows, int32_t* out_table,
+                       int64_t out_stride, int32_t* out_len, int32_t* out_start, int32_t* out_slots,
+                       int32_t* out_position, int32_t* out_status, void* workspace, int64_t workspace_bytes,
+                       void* stream) {
+    return entry([&] {
+        return cache_reserve_impl(table, table_stride, len, n_new, B, width, pages, page_size, rows, out_table,
+                                  out_stride, out_len, out_start, out_slots, out_position, out_status, workspace,
+                                  workspace_bytes, stream);
+    });
+}
+
+int64_t spec_cache_reserve_workspace(int32_t B, int32_t page_size, int32_t rows) {
+    const int rc = check_reserve(B, page_size, rows);
+    return rc ? rc : reserve_workspace(B, page_size, rows);
+}
+
+int spec_cache_write(const sv_cache_rows* args, void* stream) {
+    return entry([&] { return cache_write_impl(args, stream); });
 }
 
 const char* spec_verify_strerror(int status) {

@@ -28,6 +28,12 @@ enum TreeKernelKind : int {
     KK_PROMPT_PLAN,
     KK_PROMPT_EXPAND,
     KK_PROMPT_ATTN,
+    KK_BEAM_STATS,
+    KK_BEAM_SELECT,
+    KK_BEAM_REORDER,
+    KK_RESERVE_PLAN,
+    KK_RESERVE_WRITE,
+    KK_CACHE_WRITE,
     KK_ALL
 };
 
