@@ -588,7 +588,7 @@ int64_t spec_cache_workspace(int32_t B, int32_t N, int32_t page_size);
  *
  * dtype          SV_BF16 or SV_F16, of all tensors.
  * B, N           1 <= B <= 65536 sequences, 1 <= N <= 64 nodes.
- * heads          at most 1024; B, rounded up to eights, times N * heads / 128, rounded up, below 2^23.
+ * heads          at most 1024; B, rounded up to eights, times N * heads / 64, rounded up, below 2^23.
  * dim, dim_v     multiples of 8; dim <= SPECVERIFY_MAX_LATENT, dim_v <= dim and 512.
  * q              [B, N, heads, dim]; out [B, N, heads, dim_v]; strides in
  *                elements for (sequence, node, head).
@@ -679,8 +679,9 @@ int spec_head_product(const sv_head_product* args, void* stream);
  *
  * The rows q_start[b] .. q_start[b + 1] of q are the last tokens of sequence b, at
  * positions len[b] - n .. len[b] - 1; their rows, and those of a prefix before
- * them, are in the cache.  Keys and values are rounded to the input type,
- * statistics and other roundings are spec_tree_attention's.
+ * them, are in the cache.  Keys are rounded to the input type; values and weights
+ * to float16's 11 bits in either type, the values times a power of two per head
+ * (chosen by its largest one over the line).  Statistics are float32.
  *
  * dtype          SV_BF16 or SV_F16, of all tensors.
  * T              query tokens, 0 (nothing is done) to 2^24; B <= 65536; heads <= 1024.
@@ -702,7 +703,7 @@ int spec_head_product(const sv_head_product* args, void* stream);
  * workspace      at least spec_latent_prompt_workspace(args) bytes, aligned to 16.
  *
  * What a token does not see (later rows, pages outside the pool) never reaches its
- * output.  Where it sees infinities or NaN, expanded values beyond the type's range
+ * output.  Where it sees infinities or NaN, expanded keys beyond the type's range
  * included, its output is infinite or NaN.  (Launches have fewer than 2^32 threads:
  * the 128-row tiles of `rows` times the 128-wide tiles of heads * dim_k and of
  * heads * dim_v, and (T / 128 + min(B, T)) * heads, are below 2^24 - 8.)

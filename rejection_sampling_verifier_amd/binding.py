@@ -23,7 +23,7 @@ STATUS = {0: "SV_OK", -1: "SV_EINVAL", -2: "SV_ESHAPE", -3: "SV_EDTYPE", -4: "SV
           -6: "SV_EALIGN", -7: "SV_ECAPTURE", -8: "SV_ETOOBIG"}
 KERNEL_KINDS = ("stats", "topp", "rows", "smc", "produce", "tree_attention", "tree_join", "verify_clear",
                 "tree_verify", "cache_plan", "cache_copy", "latent_attention", "latent_join",
-                "head_product", "prompt_plan", "prompt_expand", "prompt_attention", "beam_stats",
+                "head_product", "prompt_plan", "prompt_expand", "prompt_scale", "prompt_attention", "beam_stats",
                 "beam_select", "beam_reorder", "reserve_plan", "reserve_write", "cache_write")
 
 EXPORTS = ("spec_verify", "spec_verify_noalloc", "spec_verify_probe", "spec_greedy_verify", "spec_hispec_verify", "spec_smc_step",

@@ -935,7 +935,7 @@ int plan_latent(const sv_latent_attention* a, LatentPlan& t) {
     if (static_cast<int64_t>(a->width) * a->page_size > (1ll << 28)) return SV_ESHAPE;
     const int rows = a->N * a->heads;
     t.s.wide = a->dim > 320 || a->dim_v > 256;
-    t.s.rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    t.s.rows = rows <= 32 ? 32 : 64;
     t.MT = (rows + t.s.rows - 1) / t.s.rows;
     // a launch has fewer than 2^32 threads
     if ((static_cast<int64_t>(a->B) + 7) / 8 * 8 * t.MT >= 1ll << 23) return SV_ESHAPE;
@@ -1050,7 +1050,7 @@ int head_product_impl(const sv_head_product* a, void* stream_v) {
 
 // The workspace of a prompt call: places, flags, keys, values and second parts of the line.
 struct PromptPlan {
-    size_t odd, there, k, v, pe, total;
+    size_t odd, most, there, k, v, pe, total;
 };
 
 int plan_prompt(const sv_latent_prompt* a, PromptPlan& t) {
@@ -1071,7 +1071,8 @@ int plan_prompt(const sv_latent_prompt* a, PromptPlan& t) {
     if (lines * out >= (1ll << 24) - 8 || tiles * a->heads >= (1ll << 24) - 8) return SV_ESHAPE;
     const size_t rows = static_cast<size_t>(lines) * 128;
     t.odd = align256((static_cast<size_t>(a->B) + 1) * 2 * sizeof(int64_t));
-    t.there = t.odd + 256;
+    t.most = t.odd + 256;
+    t.there = align256(t.most + static_cast<size_t>(a->heads) * sizeof(uint32_t));
     t.k = align256(t.there + rows * sizeof(int32_t));
     t.v = align256(t.k + static_cast<size_t>(a->heads) * a->rows * a->dim_k * 2);
     t.pe = align256(t.v + static_cast<size_t>(a->heads) * a->rows * a->dim_v * 2);
@@ -1128,6 +1129,7 @@ int latent_prompt_impl(const sv_latent_prompt* a, void* stream_v) {
     uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
     p.plan = reinterpret_cast<int64_t*>(ws);
     p.odd = reinterpret_cast<int32_t*>(ws + t.odd);
+    p.most = reinterpret_cast<uint32_t*>(ws + t.most);
     p.there = reinterpret_cast<int32_t*>(ws + t.there);
     p.k = ws + t.k;
     p.v = ws + t.v;
@@ -1136,9 +1138,11 @@ int latent_prompt_impl(const sv_latent_prompt* a, void* stream_v) {
     const hipStream_t stream = static_cast<hipStream_t>(stream_v);
     rc = timed_launch(sv::KK_PROMPT_PLAN, stream,
                       [&](const sv::LaunchEvents& ev) { return sv::launch_prompt_plan(p, stream, ev); });
-    if (!rc && a->rows > 0)
-        rc = timed_launch(sv::KK_PROMPT_EXPAND, stream,
-                          [&](const sv::LaunchEvents& ev) { return sv::launch_prompt_expand(p, dtype, stream, ev); });
+    for (const bool again : {false, true})
+        if (!rc && a->rows > 0)
+            rc = timed_launch(sv::KK_PROMPT_EXPAND + again, stream, [&](const sv::LaunchEvents& ev) {
+                return sv::launch_prompt_expand(p, dtype, again, stream, ev);
+            });
     if (rc) return rc;
     return timed_launch(sv::KK_PROMPT_ATTN, stream,
                         [&](const sv::LaunchEvents& ev) { return sv::launch_prompt_attn(p, dtype, stream, ev); });

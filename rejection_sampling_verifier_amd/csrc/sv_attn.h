@@ -113,18 +113,19 @@ __device__ __forceinline__ void to_lds(const uint8_t* src, uint8_t* dst) {
 // in bits 0-3 and 14-15, expcnt 4-6, lgkmcnt 8-11).
 constexpr int kWaitVm0 = 0x0F70;
 
-// The 16-byte chunks of a row are stored at positions XORed with this, so that
-// eight rows at one chunk (the key operand's reads) and four rows at two
-// neighbouring chunks (the transposing reads) lie in different banks.
-__device__ __forceinline__ int swizzle(int row) { return (row & 3) << 1 | (row >> 2 & 1); }
-
 // 16 bytes per lane from base + off to the 1024 at LDS address `dst`.  Assembly,
 // so that the compiler does not wait for these loads at every read of another
 // stage; the kernel waits for them itself (vmcnt).
+// (base and dst are the same for all lanes, whether the compiler sees it or not.)
 __device__ __forceinline__ void load_lds(const uint8_t* base, uint32_t off, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(dst) : "memory");
+    const uint64_t b = reinterpret_cast<uintptr_t>(base);
+    const uint64_t at = static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32))) << 32 |
+                        static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b)));
+    dst = __builtin_amdgcn_readfirstlane(dst);
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(at), "s"(dst) : "memory");
 }
 __device__ __forceinline__ void load_lds(const uint8_t* from, uint32_t dst) {
+    dst = __builtin_amdgcn_readfirstlane(dst);
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(dst) : "memory");
 }
 
@@ -135,6 +136,20 @@ __device__ __forceinline__ v8s lds_read(uint32_t at) {
 }
 __device__ __forceinline__ v4s lds_read_tr(uint32_t at) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at));
+}
+
+// Orders a block of M matrix instructions and R LDS reads: AHEAD reads first, then
+// the others between the matrix instructions.
+template <int M, int R, int AHEAD>
+__device__ __forceinline__ void reads_ahead() {
+    constexpr int kFirst = AHEAD < R ? AHEAD : R, kRest = R - kFirst, kGap = M / R;
+    __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
+#pragma unroll
+    for (int i = 0; i < kRest; ++i) {
+        if (kGap) __builtin_amdgcn_sched_group_barrier(0x008, kGap, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, M - kRest * kGap, 0);
 }
 
 // Until at most N of the wave's global loads are under way.

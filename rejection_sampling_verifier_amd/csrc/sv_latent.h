@@ -28,7 +28,7 @@ struct LatentParams {
 
 // Rows of a workgroup's tile, and the kernel's row and value widths.
 struct LatentShape {
-    int rows;  // 32, 64 or 128
+    int rows;  // 32 or 64
     int wide;  // 1: rows up to 576 and values up to 512 elements; 0: 320 and 256
 };
 constexpr int latent_dv(int wide) { return wide ? 512 : 256; }
@@ -65,12 +65,13 @@ struct PromptParams {
     // workspace
     int64_t* plan;                    // [B + 1] first row of the line, [B + 1] first query tile
     int32_t* odd;                     // 1: an infinity or NaN among the values
+    uint32_t* most;                   // [H] bits of the largest value's size
     int32_t* there;                   // [rows rounded up] 1: the row's page exists
     uint8_t *k, *v, *pe;              // [H, rows, dn], [H, rows, dv], [rows, dr]
 };
 constexpr int kPromptRows = 128;      // queries of a tile
 hipError_t launch_prompt_plan(const PromptParams& p, hipStream_t st, const LaunchEvents& ev);
-hipError_t launch_prompt_expand(const PromptParams& p, int dtype, hipStream_t st, const LaunchEvents& ev);
+hipError_t launch_prompt_expand(const PromptParams& p, int dtype, bool again, hipStream_t st, const LaunchEvents& ev);
 hipError_t launch_prompt_attn(const PromptParams& p, int dtype, hipStream_t st, const LaunchEvents& ev);
 
 }  // namespace sv

@@ -19,25 +19,61 @@ __device__ __forceinline__ int clamp_len(const LatentParams& p, int len) {
     return len < 0 ? 0 : len > cap ? cap : len;
 }
 
+// The 16-byte chunks of a row are stored at positions XORed with this.  A wide LDS
+// read takes 16 lanes at a time (0-3, 12-15, 20-23, 24-27 and so on) over 64
+// banks, in which rows of 1152 or 640 bytes alternate between two halves: the key
+// operand's 16 lanes (rows 0-3 and 12-15 at one chunk, 4-11 at its neighbour) and
+// the transposing read's 32 (four rows at four chunks) then meet no bank twice.
+// With row & 7, XORed as usual, the products of scores were as long again.
+__device__ __forceinline__ int swizzle(int row) {
+    return (row >> 1 & 1) << 2 | ((row >> 2 ^ row >> 3) & 1) << 1 | (row >> 3 & 1);
+}
+
 constexpr int kLatThreads = 512, kLatWaves = 8;
 constexpr int kLatKeys = 32;  // keys of a tile
+constexpr int kLatRing = 4;   // tiles in LDS: one for the values, one for the scores, two under way
 
-// What a kernel of RB rows and DK elements a row keeps in LDS: a ring of tiles,
-// the partial scores that two waves exchange, the weights.
+// LDS of a kernel of RB rows and DK elements a row: the ring, two tiles' weights.
 template <int DK, int RB>
 struct LatentLds {
     static constexpr int kStage = kLatKeys * DK * 2;
-    static constexpr int kX = RB / 32 * 2 * 4096;  // two waves per 32 rows
     static constexpr int kP = RB * kLatKeys * 2;
-    static constexpr int kFit = ((160 << 10) - 4096 - kX - kP) / kStage;
-    static constexpr int kRing = kFit > 4 ? 4 : kFit;
-    static constexpr int kX0 = kRing * kStage, kP0 = kX0 + kX, kAll = kP0 + kP;
-    static_assert(kRing >= 3, "tiles under way");
+    static constexpr int kP0 = kLatRing * kStage, kAll = kP0 + 2 * kP;
 };
 
 // Tiles of a sequence: its cache rows, then the tree's.
 __device__ __forceinline__ int tiles_of(const LatentParams& p, int len) {
     return (clamp_len(p, len) + kLatKeys - 1) / kLatKeys + (p.N + kLatKeys - 1) / kLatKeys;
+}
+
+typedef __attribute__((address_space(3))) v4s lds_v4s_t;
+typedef const __attribute__((address_space(4))) int32_t const_i32;
+
+// Everyone's LDS writes are seen, and everyone is here.
+__device__ __forceinline__ void meet() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// The value in all four quarter-waves: of the lanes with the same lane & 15.
+__device__ __forceinline__ float quarter_max(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float quarter_sum(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+template <int DT>
+__device__ __forceinline__ v4f mfma16(v8s a, v8s b, v4f c) {
+    if constexpr (DT == DT_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0,
+                                                       0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0,
+                                                      0);
 }
 
 template <int DT, int DK, int DV, int RB>
@@ -46,26 +82,28 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
     constexpr int TK = kLatKeys;
     constexpr int NC = DK / 8;                // 16-byte chunks per row
     constexpr int NL = TK * NC / 64;          // wide loads of a tile
-    constexpr int kMost = (NL + kLatWaves - 1) / kLatWaves, kLeast = NL / kLatWaves;  // of a wave
-    constexpr int NQ = DK / 32;               // matrix steps of half a row
-    constexpr int RG = RB / 32;               // groups of 32 rows
-    constexpr int CB = DV / 32 / kLatWaves;   // blocks of 32 values a wave sums
+    constexpr int kLoads = NL / 4;            // of a value wave
+    constexpr int NQ = DK / 32;               // matrix steps of a row
+    constexpr int NB = RB / 32;               // blocks of 16 rows a score wave has
+    constexpr int RG = RB / 32;               // blocks of 32 rows a value wave has
+    constexpr int CB = DV / 32 / 4;           // and of 32 values
     constexpr int kRowB = DK * 2;
     constexpr int kRec = RB * (DV + 2);       // floats of a partial result
-    static_assert(NC % 8 == 0 && NL * 64 == TK * NC && CB >= 1, "layout");
+    static_assert(NC % 8 == 0 && NL * 64 == TK * NC && NL % 4 == 0 && CB >= 1, "layout");
 
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s_a[RB], s_m[RB], s_l[2][RB];
-    __shared__ int s_move[2];
+    __shared__ int s_raise[2];
+    __shared__ uint32_t s_ok[kLatRing];       // rows of the tiles that exist
     __shared__ int64_t s_sum[kLatWaves];
     __shared__ int32_t s_scan[kLatWaves];
     __shared__ int s_b;
     __shared__ int64_t s_before;
-    __shared__ unsigned long long s_nf;
+    __shared__ unsigned int s_nf;
 
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int hh = lane >> 5, col = lane & 31;
-    const int rg = w >> 1, kh = w & 1;        // scores: the wave's rows and half of their elements
+    const bool scores = w < 4;                // the others sum values
+    const int wv = w & 3;
     int c, m;
     if (p.MT == 1) {
         c = blockIdx.x;
@@ -129,41 +167,33 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
         before = s_before;
     }
 
+    if (tid < 2) s_raise[tid] = 0;
     const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) uint8_t*)smem));
-    // Staging: wide load i = w + 8 k of a tile fills 1024 bytes; lane l's 16 are chunk position
-    // (64 i + l) % NC of row (64 i + l) / NC.  Eight rows are NC / 8 loads.
-    uint32_t off[kMost];
-#pragma unroll
-    for (int k = 0; k < kMost; ++k) {
-        const int e = (w + 8 * k) * 64 + lane, r = e / NC;
-        off[k] = static_cast<uint32_t>(units(r & 7, p.kcs[1], (e - r * NC) ^ swizzle(r), 1));
-    }
-    const int mine = w < NL - kLeast * kLatWaves ? kLeast + 1 : kLeast;  // loads of this wave
+    // Staging, by the value waves: wide load i = wv + 4 k of a tile fills 1024 bytes; lane l's 16 are
+    // chunk position (64 i + l) % NC of row (64 i + l) / NC.  Eight rows are NC / 8 loads.
+    // chunks past the row's elements are zeros that nothing overwrites
+    if (p.C < DK)
+        for (int i = tid; i < kLatRing * Lds::kStage / 16; i += kLatThreads)
+            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    meet();
     // eight whole rows on one page: a scalar address and these
-    const bool by_eights = p.C == DK && p.ps_shift >= 3 && p.kcs[1] < (1u << 25);
-    // reading, within a stage: keys 16 bytes a lane (four chunks, the next are 128 bytes on), values transposed
-    uint32_t k_rd[4], v_rd[CB];
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-        k_rd[s] = smem_at + col * kRowB + (((kh * (NC / 2) + 2 * s + hh) ^ swizzle(col)) << 4);
-    {
-        const int vrow = 4 * hh + ((lane & 15) >> 2);
-        const int low = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);  // chunk of the four of 32 dimensions
-#pragma unroll
-        for (int s = 0; s < CB; ++s)
-            v_rd[s] = smem_at + vrow * kRowB + (((4 * (w * CB + s) + low) ^ swizzle(vrow)) << 4) + (lane & 1) * 8;
-    }
-    const uint32_t x_at = smem_at + Lds::kX0 + lane * 16;              // + 4096 per wave, 1024 per four sums
-    const int p_xor = (col >> 1) & 3;                                  // weights: [row][4 chunks], 8 rows on all banks
-    const uint32_t p_at = smem_at + Lds::kP0 + col * 64;
-    const float scale2 = p.scale2;
+    const bool by_eights = p.ps_shift >= 3 && p.kcs[1] < (1u << 25);
     const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero);
     const int ps_mask = (1 << p.ps_shift) - 1;
     const int tree_tiles = (p.N + TK - 1) / TK;
+    const uint32_t p_at = smem_at + Lds::kP0;  // weights: 64 bytes a row, its four chunks so that eight rows use all banks
+    // score wave wv: 16 keys (kh) against RB / 2 rows (from 16 NB rq on); lane & 15 is a key, then a row
+    const int kh = wv & 1, rq = wv >> 1;
+    int step = 0;  // of the workgroup, over all its sequences
 
     int64_t f = f0;
     while (f < f1) {
+        // the lane's number, anew for every sequence: what is made of it would otherwise be kept in
+        // registers over the whole kernel, and the loops' spilled
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int c16 = lane & 15, g4 = lane >> 4, hh = lane >> 5, col = lane & 31;
         const int len = clamp_len(p, p.len[b]);
         const int cache = (len + TK - 1) / TK, T = cache + tree_tiles;
         const int t0 = static_cast<int>(f - before);
@@ -175,274 +205,398 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
             n = n < 0 ? 0 : n > p.N ? p.N : n;
         }
         const int rows = n * p.H;
-        v16f o[RG][CB];
+        const bool any = m * RB < rows;
+        const int32_t* const tab = p.table + b * p.table_stride;
+        const uint8_t* const nwb = p.nw + units(b, p.nws[0]);
+        // The pages of a whole tile of cache rows, eight rows each on one: scalar loads, which do not
+        // queue behind the rows under way.  -1: not such a tile.
+        struct Pages {
+            int at[4];
+        };
+        auto pages_of = [&](int t) {
+            Pages r;
+            const bool fit = by_eights && t < t1 && (t + 1) * TK <= len;
 #pragma unroll
-        for (int r = 0; r < RG; ++r)
+            for (int g = 0; g < 4; ++g)
+                r.at[g] = fit ? *(const_i32*)(tab + ((t * TK + 8 * g) >> p.ps_shift)) : -1;
+            return r;
+        };
+        uint32_t off[kLoads], padded = 0;
+        if (!scores) {
 #pragma unroll
-            for (int s = 0; s < CB; ++s)
+            for (int k = 0; k < kLoads; ++k) {
+                const int e = (wv + 4 * k) * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ swizzle(r);
+                off[k] = static_cast<uint32_t>(units(r & 7, p.kcs[1], chunk, 1));
+                if (chunk * 8 >= p.C) padded |= 1u << k;
+            }
+        }
+        // starts staging tile t and says which of its rows exist (the others are staged as zeros)
+        auto stage = [&](int t, const Pages& pg) {
+            const bool tree = t >= cache;
+            const int first = (tree ? t - cache : t) * TK;
+            const int slot = (t - t0) % kLatRing;
+            const uint32_t to = smem_at + slot * Lds::kStage + wv * 1024;
+            const uint32_t most = static_cast<uint32_t>(p.pages);
+            if (static_cast<uint32_t>(pg.at[0]) < most && static_cast<uint32_t>(pg.at[1]) < most &&
+                static_cast<uint32_t>(pg.at[2]) < most && static_cast<uint32_t>(pg.at[3]) < most) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[r][s][i] = 0.f;
-
-        if (m * RB < rows) {
-            const int my_row = m * RB + rg * 32 + col;  // of the scores
-            const bool active = rg < RG && m * RB + rg * 32 < rows;
-            const int32_t* const tab = p.table + b * p.table_stride;
-            const uint8_t* const nwb = p.nw + units(b, p.nws[0]);
-            float mx = -INFINITY, l = 0.f;
-            // lane j: the page of row j of tile t
-            auto page = [&](int t) {
-                int pg = -1;
-                if (t < cache) {
-                    const int key = t * TK + col;
-                    if (key < len) pg = tab[key >> p.ps_shift];
+                for (int k = 0; k < kLoads; ++k) {
+                    const int g = (wv + 4 * k) / (NC / 8);
+                    const int pg8 = g < 2 ? (g ? pg.at[1] : pg.at[0]) : (g == 2 ? pg.at[2] : pg.at[3]);
+                    const uint8_t* const base = p.kc + units(pg8, p.kcs[0], (first + 8 * g) & ps_mask, p.kcs[1]);
+                    if (!(padded >> k & 1)) load_lds(base, off[k], to + k * 4096);
                 }
-                return pg;
-            };
-            // starts staging tile t; returns the rows that exist (the others are staged as zeros)
-            auto stage = [&](int t, int pg, uint32_t at) {
-                const bool tree = t >= cache;
-                const int first = (tree ? t - cache : t) * TK;
-                const uint32_t okm = static_cast<uint32_t>(
-                    tree ? __ballot(first + col < n)
-                         : __ballot(static_cast<uint32_t>(pg) < static_cast<uint32_t>(p.pages)));
-                const uint32_t to = smem_at + at + w * 1024;
-                if (!tree && okm == ~0u && by_eights) {
-#pragma unroll
-                    for (int k = 0; k < kMost; ++k) {
-                        if (k == kLeast && mine == kLeast) break;
-                        const int g = (w + 8 * k) / (NC / 8) * 8;
-                        const uint32_t pg8 = __builtin_amdgcn_readlane(pg, g);
-                        load_lds(p.kc + units(pg8, p.kcs[0], (first + g) & ps_mask, p.kcs[1]), off[k], to + k * 8192);
-                    }
-                } else {
+                if (wv == 0 && lane == 0) s_ok[slot] = ~0u;
+                return;
+            }
+            int pl = -1;  // lane j: the page of row j
+            if (!tree && first + col < len) pl = tab[(first + col) >> p.ps_shift];
+            const uint32_t okm = static_cast<uint32_t>(tree ? __ballot(first + col < n)
+                                                            : __ballot(static_cast<uint32_t>(pl) < most));
 #pragma unroll 1
-                    for (int k = 0; k < mine; ++k) {
-                        const int e = (w + 8 * k) * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ swizzle(r);
-                        const uint32_t pg_of = __shfl(pg, r);
-                        const uint8_t* const src =
-                            tree ? nwb + units(first + r, p.nws[1], chunk, 1)
-                                 : p.kc + units(pg_of, p.kcs[0], (first + r) & ps_mask, p.kcs[1]) + 16 * chunk;
-                        load_lds((okm >> r & 1) && chunk * 8 < p.C ? src : zero, to + k * 8192);
+            for (int k = 0; k < kLoads; ++k) {
+                const int e = (wv + 4 * k) * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ swizzle(r);
+                const uint32_t pg_of = __shfl(pl, r);
+                const uint8_t* const src =
+                    tree ? nwb + units(first + r, p.nws[1], chunk, 1)
+                         : p.kc + units(pg_of, p.kcs[0], (first + r) & ps_mask, p.kcs[1]) + 16 * chunk;
+                load_lds((okm >> r & 1) && chunk * 8 < p.C ? src : zero, to + k * 4096);
+            }
+            if (wv == 0 && lane == 0) s_ok[slot] = okm;
+        };
+        // Step t: tile t is there, the weights of tile t - 1 too; tile t + 2 is sent for.  Both kinds of
+        // waves go through the same barriers.
+        Pages pg;
+        auto begin = [&] {
+            stage(t0, pages_of(t0));
+            if (t0 + 1 < t1) stage(t0 + 1, pages_of(t0 + 1));
+            pg = pages_of(t0 + 2);
+        };
+        auto arrive = [&](int t) {
+            // this wave's loads of tile t have landed, the next tile's stay under way
+            if (t + 1 < t1)
+                wait_vm<kLoads>();
+            else
+                wait_vm<0>();
+            meet();
+            if (t + 2 < t1) stage(t + 2, pg);
+            pg = pages_of(t + 3);
+        };
+        // Rows of the tree in tile t that hold infinities or NaN among their values: these values go out
+        // of the tile (0 times them would reach the nodes that do not see the row), and whoever sees the
+        // row gets a score of NaN instead.
+        auto cleaned = [&](int t) {
+            uint32_t nf = 0;
+            if (!scores) {
+                const uint32_t at = ((t - t0) % kLatRing) * Lds::kStage;
+#pragma unroll 1
+                for (int k = 0; k < kLoads; ++k) {
+                    const int e = (wv + 4 * k) * 64 + lane, r = e / NC;
+                    if (((e - r * NC) ^ swizzle(r)) * 8 >= p.dv) continue;
+                    v8s* const y = reinterpret_cast<v8s*>(smem + at + (wv + 4 * k) * 1024 + lane * 16);
+                    const uint4 u = __builtin_bit_cast(uint4, *y);
+                    if (nonfinite2<DT>(u.x) || nonfinite2<DT>(u.y) || nonfinite2<DT>(u.z) || nonfinite2<DT>(u.w)) {
+                        nf |= 1u << r;
+                        *y = v8s{0, 0, 0, 0, 0, 0, 0, 0};
                     }
                 }
-                return okm;
-            };
+            }
+            if (tid == 0) s_nf = 0;
+            meet();
+            if (nf) atomicOr(&s_nf, nf);
+            meet();
+            return s_nf;
+        };
 
-            // queries: the B operand, resident; a negative scale is moved into their sign
-            v8s q[NQ];
-            const int node = my_row < rows ? my_row / p.H : 0;
-            {
-                const uint8_t* const src = p.q + units(b, p.qs[0], node, p.qs[1]) +
-                                           units(my_row < rows ? my_row - node * p.H : 0, p.qs[2]);
+        if (any && scores) {
+            // ---- scores and weights, ahead of the value waves where both want the matrix unit: the sums of
+            // the tile before then run under the exponentials
+            __builtin_amdgcn_s_setprio(2);
+            const bool active = m * RB + 16 * NB * rq < rows;
+            int my_row[NB];
+            v8s q[NB][NQ];
+            uint64_t set[NB];
+            uint64_t all = 0;
+            if (t1 > cache && p.parent) all = ancestors(p.parent + static_cast<int64_t>(b) * p.N, n, lane, 0);
+            const float scale2 = p.scale2;
+#pragma unroll
+            for (int r = 0; r < NB; ++r) {
+                my_row[r] = m * RB + 16 * (NB * rq + r) + c16;
+                const bool in = my_row[r] < rows;
+                const int node = in ? my_row[r] / p.H : 0;
+                set[r] = p.parent ? __shfl(static_cast<unsigned long long>(all), node) : (2ull << node) - 1;
+                // queries: the B operand, resident; a negative scale is moved into their sign
+                const uint8_t* const src =
+                    p.q + units(b, p.qs[0], node, p.qs[1]) + units(in ? my_row[r] - node * p.H : 0, p.qs[2]);
 #pragma unroll
                 for (int s = 0; s < NQ; ++s) {
-                    const int d = kh * (DK / 2) + s * 16 + hh * 8;
+                    const int d = s * 32 + g4 * 8;
                     v8s z = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (active && my_row < rows && d < p.C) z = *reinterpret_cast<const v8s*>(src + 2 * d);
-                    q[s] = p.flip ? z ^ static_cast<short>(0x8000) : z;
+                    if (in && d < p.C) z = *reinterpret_cast<const v8s*>(src + 2 * d);
+                    q[r][s] = p.flip ? z ^ static_cast<short>(0x8000) : z;
                 }
             }
-            uint64_t set = 0;  // the nodes the row sees
-            if (t1 > cache) {
-                if (p.parent)
-                    set = __shfl(static_cast<unsigned long long>(
-                                     ancestors(p.parent + static_cast<int64_t>(b) * p.N, n, lane, 0)),
-                                 node);
-                else
-                    set = (2ull << node) - 1;
-            }
-
-            // the ring: tiles t .. t + kRing - 2 are under way or there
-            constexpr int kAhead = Lds::kRing - 1;
-            uint32_t okm[kAhead];
+            const int key = 16 * kh + c16;
+            uint32_t k_rd[2];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                okm[k] = 0;
-                if (t0 + k < t1) okm[k] = stage(t0 + k, page(t0 + k), k * Lds::kStage);
+            for (int s = 0; s < 2; ++s) k_rd[s] = smem_at + key * kRowB + (((4 * s + g4) ^ swizzle(key)) << 4);
+            // the lane's four weights of a row: keys 16 kh + 4 g4 + 0..3 go where the value waves'
+            // operand has them, 16 kh + (0..3, 8..11 | 4..7, 12..15)
+            uint32_t p_wr[NB];
+#pragma unroll
+            for (int r = 0; r < NB; ++r) {
+                const int lr = 16 * (NB * rq + r) + c16;
+                p_wr[r] = p_at + lr * 64 + (((2 * kh + (g4 & 1)) ^ ((lr >> 2) & 3)) << 4) + (g4 >> 1) * 8;
             }
-            int pg = t0 + kAhead < t1 ? page(t0 + kAhead) : -1;
-            uint32_t at = 0, to = kAhead * Lds::kStage;
+            float mx[NB], l[NB], l_old[NB];
+            v4f x[NB];
+#pragma unroll
+            for (int r = 0; r < NB; ++r) {
+                mx[r] = -INFINITY;
+                l[r] = l_old[r] = 0.f;
+                x[r] = v4f{0.f, 0.f, 0.f, 0.f};
+            }
+            // weights of the scores in x relative to the reference, into buffer `at`
+            auto weigh = [&](int at) {
+#pragma unroll
+                for (int r = 0; r < NB; ++r) {
+                    const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
+                    float y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[i] = __builtin_amdgcn_exp2f(less(x[r][i], ref));
+                        l[r] += y[i];
+                    }
+                    *reinterpret_cast<lds_v4s_t*>(p_wr[r] + at * Lds::kP) = pack4<DT>(y[0], y[1], y[2], y[3]);
+                }
+            };
 #pragma unroll 1
-            for (int t = t0; t < t1; ++t) {
+            for (int t = t0; t <= t1; ++t, ++step) {
+                meet();
+                const int raised = s_raise[(step - 1) & 1];
+                const uint32_t ok = s_ok[(t - t0) % kLatRing];
                 const bool tree = t >= cache;
-                // this wave's loads of tile t have landed (later tiles' stay under way); with the
-                // barrier everyone's, and everyone is done with the tile before it
-                if (t + kAhead - 1 < t1) {
-                    if (mine > kLeast)
-                        wait_vm<(kAhead - 1) * kMost>();
-                    else
-                        wait_vm<(kAhead - 1) * kLeast>();
-                } else {
-                    wait_vm<0>();
-                }
-                __builtin_amdgcn_s_barrier();
-                asm volatile("" ::: "memory");
-                __builtin_amdgcn_sched_barrier(0);
-                const uint32_t ok = okm[0];
+                const uint32_t at = ((t - t0) % kLatRing) * Lds::kStage;
+                // the keys' operands a few steps at a time, those of the next two parts on their way meanwhile
+                constexpr int kPart = NQ % 3 ? 2 : 3, kParts = NQ / kPart;
+                static_assert(kParts * kPart == NQ && kParts >= 3, "steps");
+                v8s kf[3][kPart];
+                auto fetch = [&](int part) __attribute__((always_inline)) {
 #pragma unroll
-                for (int k = 0; k + 1 < kAhead; ++k) okm[k] = okm[k + 1];
-                if (t + kAhead < t1) {
-                    okm[kAhead - 1] = stage(t + kAhead, pg, to);
-                    if (t + kAhead + 1 < t1) pg = page(t + kAhead + 1);
+                    for (int j = 0; j < kPart; ++j) {
+                        const int s = part * kPart + j;
+                        kf[part % 3][j] = lds_read(k_rd[s & 1] + at + (s >> 1) * 128);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                };
+                if (t > t0 && __builtin_amdgcn_readfirstlane(raised) == step) {
+                    // a row of tile t - 1 is too far above its reference: a new one, from both waves that
+                    // share the row, and the weights once more
+                    float top[NB];
+                    if (active) {
+#pragma unroll
+                        for (int r = 0; r < NB; ++r) {
+                            top[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+                            top[r] = quarter_max(top[r]);
+                            if (g4 == 0) s_l[kh][16 * (NB * rq + r) + c16] = top[r];
+                        }
+                    }
+                    meet();
+                    if (active) {
+#pragma unroll
+                        for (int r = 0; r < NB; ++r) {
+                            const int lr = 16 * (NB * rq + r) + c16;
+                            const float mn = fmaxf(mx[r], fmaxf(top[r], s_l[kh ^ 1][lr]) - kUp<DT>);
+                            const float a = shift_of(mx[r], mn);
+                            if (g4 == 0 && kh == 0) s_a[lr] = a;
+                            mx[r] = mn;
+                            l[r] = l_old[r] * a;
+                        }
+                        weigh((step - 1) & 1);
+                    }
+                    meet();
                 }
-                uint32_t nf = 0;  // rows of the tree that hold infinities or NaN among their values
-                if (tree) {
-                    // these go out of the tile (0 times them would reach the nodes that do not see
-                    // the row); whoever sees the row gets a score of NaN instead
+                if (t == t1) continue;
+                uint32_t nf = 0;
+                if (tree) nf = cleaned(t);
+                if (active) {
+                    v4f x2[NB];  // even and odd steps apart: the chains of sums are half as long
+#pragma unroll
+                    for (int r = 0; r < NB; ++r) x[r] = x2[r] = v4f{0.f, 0.f, 0.f, 0.f};
+                    __builtin_amdgcn_sched_barrier(0);
+                    fetch(0);
+                    fetch(1);
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part) {
+                        if (part + 2 < kParts) fetch(part + 2);
+#pragma unroll
+                        for (int j = 0; j < kPart; ++j) {
+                            const int s = part * kPart + j;
+#pragma unroll
+                            for (int r = 0; r < NB; ++r) {
+                                v4f& sum = s & 1 ? x2[r] : x[r];
+                                sum = mfma16<DT>(kf[part % 3][j], q[r][s], sum);
+                            }
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    bool raise = false;
+#pragma unroll
+                    for (int r = 0; r < NB; ++r) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[r][i] = scaled(x[r][i] + x2[r][i], scale2);
+                    }
+                    if (tree || __builtin_amdgcn_readfirstlane(ok) != ~0u) {
+                        const int at4 = 16 * kh + 4 * g4;
+#pragma unroll
+                        for (int r = 0; r < NB; ++r) {
+                            uint32_t see = ok;
+                            if (tree) see &= static_cast<uint32_t>(set[r] >> (t - cache) * TK);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                x[r][i] = see >> (at4 + i) & 1 ? nf >> (at4 + i) & 1 ? __builtin_nanf("") : x[r][i]
+                                                               : -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < NB; ++r) {
+                        const float top = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+                        raise |= top - mx[r] > kUp<DT> + 8.f;
+                        l_old[r] = l[r];
+                    }
+                    if (__any(raise) && lane == 0) s_raise[step & 1] = step + 1;
+                    weigh(step & 1);
+                }
+            }
+            if (active) {
+#pragma unroll
+                for (int r = 0; r < NB; ++r) {
+                    const int lr = 16 * (NB * rq + r) + c16;
+                    const float sum = quarter_sum(l[r]);
+                    if (g4 == 0) {
+                        s_l[kh][lr] = sum;
+                        if (kh == 0) s_m[lr] = mx[r];
+                    }
+                }
+            }
+            meet();
+        } else {
+            // ---- sums of values
+            v16f o[RG][CB];
+#pragma unroll
+            for (int r = 0; r < RG; ++r)
+#pragma unroll
+                for (int s = 0; s < CB; ++s)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[r][s][i] = 0.f;
+            if (any) {
+                uint32_t v_rd[2][2];  // odd and even blocks of 32 values; the first rows and eight rows on
+                const int vrow = 4 * hh + ((lane & 15) >> 2);
+                const int low = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);  // chunk of the four of 32 dimensions
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        v_rd[s][j] = smem_at + (vrow + 8 * j) * kRowB +
+                                     (((4 * ((wv * CB + s) & 1) + low) ^ swizzle(vrow + 8 * j)) << 4) + (lane & 1) * 8 +
+                                     ((wv * CB + s) >> 1) * 128;
+                const uint32_t p_rd = p_at + col * 64;
+                const int p_xor = (col >> 2) & 3;
+                begin();
 #pragma unroll 1
-                    for (int k = 0; k < mine; ++k) {
-                        const int e = (w + 8 * k) * 64 + lane, r = e / NC;
-                        if (((e - r * NC) ^ swizzle(r)) * 8 >= p.dv) continue;
-                        v8s* const y = reinterpret_cast<v8s*>(smem + at + (w + 8 * k) * 1024 + lane * 16);
-                        const uint4 u = __builtin_bit_cast(uint4, *y);
-                        if (nonfinite2<DT>(u.x) || nonfinite2<DT>(u.y) || nonfinite2<DT>(u.z) || nonfinite2<DT>(u.w)) {
-                            nf |= 1u << r;
-                            *y = v8s{0, 0, 0, 0, 0, 0, 0, 0};
+                for (int t = t0; t <= t1; ++t, ++step) {
+                    arrive(t);
+                    const int raised = s_raise[(step - 1) & 1];
+                    if (t > t0 && __builtin_amdgcn_readfirstlane(raised) == step) {
+                        meet();
+                        meet();
+#pragma unroll
+                        for (int r = 0; r < RG; ++r) {
+                            const float a = s_a[r * 32 + col];
+#pragma unroll
+                            for (int s = 0; s < CB; ++s)
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[r][s][i] *= a;
                         }
                     }
-                    if (tid == 0) s_nf = 0;
-                    __syncthreads();
-                    if (nf) atomicOr(&s_nf, static_cast<unsigned long long>(nf));
-                    __syncthreads();
-                    nf = static_cast<uint32_t>(s_nf);
-                }
-                v16f x;
-                if (active) {
+                    if (t < t1 && t >= cache) cleaned(t);
+                    if (t > t0) {
+                        const uint32_t at = ((t - 1 - t0) % kLatRing) * Lds::kStage;
+                        const uint32_t pa = p_rd + ((step - 1) & 1) * Lds::kP;
+                        // operands of 16 keys, then those of the other 16 on their way meanwhile
+                        v8s pf[2][RG], vf[2][CB];
+                        auto fetch = [&](int t2) __attribute__((always_inline)) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+                            for (int r = 0; r < RG; ++r)
+                                pf[t2][r] = lds_read(pa + r * 2048 + (((2 * t2 + hh) ^ p_xor) << 4));
 #pragma unroll
-                    for (int s = 0; s < NQ; ++s) x = mfma<DT>(lds_read(k_rd[s & 3] + at + (s >> 2) * 128), q[s], x);
+                            for (int s = 0; s < CB; ++s) {
+                                const uint32_t a = at + t2 * 16 * kRowB + (s >> 1) * 128;
+                                vf[t2][s] = __builtin_shufflevector(lds_read_tr(v_rd[s & 1][0] + a),
+                                                                    lds_read_tr(v_rd[s & 1][1] + a), 0, 1, 2, 3, 4, 5, 6, 7);
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                        };
+                        __builtin_amdgcn_sched_barrier(0);
+                        fetch(0);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        *reinterpret_cast<__attribute__((address_space(3))) v4f*>(x_at + w * 4096 + g * 1024) =
-                            v4f{x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
-                }
-                if (tid == 0) s_move[t & 1] = 0;
-                __syncthreads();
-                if (active) {
+                        for (int t2 = 0; t2 < 2; ++t2) {
+                            if (t2 == 0) fetch(1);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const v4f y = *reinterpret_cast<__attribute__((address_space(3))) v4f*>(
-                            x_at + (w ^ 1) * 4096 + g * 1024);
+                            for (int s = 0; s < CB; ++s)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) x[4 * g + i] += y[i];
-                    }
-                    if (tree || ok != ~0u) {
-                        uint32_t see = ok;
-                        if (tree) see &= static_cast<uint32_t>(set >> (t - cache) * TK);
-                        const uint32_t bad = nf >> 4 * hh;
-                        see >>= 4 * hh;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint32_t bit = 1u << (8 * (i >> 2) + (i & 3));
-                            x[i] = see & bit ? bad & bit ? __builtin_nanf("") : x[i] : -INFINITY;
+                                for (int r = 0; r < RG; ++r) o[r][s] = mfma<DT>(vf[t2][s], pf[t2][r], o[r][s]);
+                            __builtin_amdgcn_sched_barrier(0);
                         }
                     }
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) top = fmaxf(top, x[i]);
-                    top = scaled(half_max(top), scale2);
-                    if (__any(top - mx > kUp<DT> + 8.f)) {
-                        const float mn = fmaxf(mx, top - kUp<DT>);
-                        const float a = shift_of(mx, mn);
-                        l *= a;
-                        mx = mn;
-                        // the sums of all waves move along; the other groups' rows stay
-                        s_a[rg * 32 + col] = a;
-                        if (lane == 0) atomicOr(&s_move[t & 1], 1 << rg);
-                    }
-                    const float ref = mx == -INFINITY ? 0.f : mx;
-                    float y[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        y[i] = __builtin_amdgcn_exp2f(less(scaled(kh ? x[8 + i] : x[i], scale2), ref));
-                        l += y[i];
-                    }
-                    const v4s lo = pack4<DT>(y[0], y[1], y[2], y[3]), hi = pack4<DT>(y[4], y[5], y[6], y[7]);
-                    *reinterpret_cast<__attribute__((address_space(3))) v8s*>(
-                        p_at + rg * 2048 + (((2 * kh + hh) ^ p_xor) << 4)) =
-                        __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                 }
-                __syncthreads();
-                const int move = s_move[t & 1];
-                if (move) {
+                meet();  // the sums of the weights are there
+            }
+            // dimensions 32 (wv CB + s) + 8 g + 4 hh + 0..3 of row 32 r + col
+            if (!scores) {
 #pragma unroll
-                    for (int r = 0; r < RG; ++r) {
-                        if (!(move >> r & 1)) continue;
-                        const float a = s_a[r * 32 + col];
+                for (int r = 0; r < RG; ++r) {
+                    const int lr = r * 32 + col, row = m * RB + lr;
+                    const bool in = row < rows;
+                    const float l = in ? s_l[0][lr] + s_l[1][lr] : 1.f;
+                    if (whole) {
+                        if (row >= p.N * p.H) continue;
+                        const int node = row / p.H;
+                        const float inv = 1.f / l;
+                        uint8_t* const dst = p.out + units(b, p.os[0], node, p.os[1]) + units(row - node * p.H, p.os[2]);
 #pragma unroll
                         for (int s = 0; s < CB; ++s)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[r][s][i] *= a;
+                            for (int i = 0; i < 16; i += 4) {
+                                const int d = 32 * (wv * CB + s) + 2 * i + 4 * hh;
+                                const v16f& y = o[r][s];
+                                if (d < p.dv)  // an absent node's row is zero
+                                    *reinterpret_cast<v4s*>(dst + 2 * d) =
+                                        in ? pack4<DT>(y[i] * inv, y[i + 1] * inv, y[i + 2] * inv, y[i + 3] * inv)
+                                           : v4s{0, 0, 0, 0};
+                            }
+                    } else if (in) {
+                        float* const rec =
+                            p.part + ((static_cast<int64_t>(c) * 2 + (f == f0 ? 0 : 1)) * p.MT + m) * kRec;
+#pragma unroll
+                        for (int s = 0; s < CB; ++s)
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4) {
+                                const int d = 32 * (wv * CB + s) + 2 * i + 4 * hh;
+                                const v16f& y = o[r][s];
+                                if (d < p.dv)
+                                    *reinterpret_cast<float4*>(rec + lr * DV + d) =
+                                        make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                            }
+                        if (hh == 0 && wv == 0) {
+                            rec[RB * DV + lr] = s_m[lr];
+                            rec[RB * DV + RB + lr] = l;
+                        }
                     }
-                }
-#pragma unroll
-                for (int t2 = 0; t2 < 2; ++t2) {
-                    v8s pf[RG];
-#pragma unroll
-                    for (int r = 0; r < RG; ++r) pf[r] = lds_read(p_at + r * 2048 + (((2 * t2 + hh) ^ p_xor) << 4));
-#pragma unroll
-                    for (int s = 0; s < CB; ++s) {
-                        const uint32_t a = v_rd[s] + at + t2 * 16 * kRowB;
-                        const v8s vf =
-                            __builtin_shufflevector(lds_read_tr(a), lds_read_tr(a + 8 * kRowB), 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-                        for (int r = 0; r < RG; ++r) o[r][s] = mfma<DT>(vf, pf[r], o[r][s]);
-                    }
-                }
-                at = at + Lds::kStage == Lds::kX0 ? 0 : at + Lds::kStage;
-                to = to + Lds::kStage == Lds::kX0 ? 0 : to + Lds::kStage;
-            }
-            if (active) {
-                l = half_sum(l);
-                if (hh == 0) {
-                    s_l[kh][rg * 32 + col] = l;
-                    if (kh == 0) s_m[rg * 32 + col] = mx;
-                }
-            }
-            __syncthreads();
-        }
-
-        // dimensions 32 (w CB + s) + 8 g + 4 hh + 0..3 of row 32 r + col
-#pragma unroll
-        for (int r = 0; r < RG; ++r) {
-            const int lr = r * 32 + col, row = m * RB + lr;
-            const bool in = row < rows;
-            const float l = in ? s_l[0][lr] + s_l[1][lr] : 1.f;
-            if (whole) {
-                if (row >= p.N * p.H) continue;
-                const int node = row / p.H;
-                const float inv = 1.f / l;
-                uint8_t* const dst = p.out + units(b, p.os[0], node, p.os[1]) + units(row - node * p.H, p.os[2]);
-#pragma unroll
-                for (int s = 0; s < CB; ++s)
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const int d = 32 * (w * CB + s) + 2 * i + 4 * hh;
-                        const v16f& y = o[r][s];
-                        if (d < p.dv)  // an absent node's row is zero
-                            *reinterpret_cast<v4s*>(dst + 2 * d) =
-                                in ? pack4<DT>(y[i] * inv, y[i + 1] * inv, y[i + 2] * inv, y[i + 3] * inv)
-                                   : v4s{0, 0, 0, 0};
-                    }
-            } else if (in) {
-                float* const rec = p.part + ((static_cast<int64_t>(c) * 2 + (f == f0 ? 0 : 1)) * p.MT + m) * kRec;
-#pragma unroll
-                for (int s = 0; s < CB; ++s)
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const int d = 32 * (w * CB + s) + 2 * i + 4 * hh;
-                        const v16f& y = o[r][s];
-                        if (d < p.dv)
-                            *reinterpret_cast<float4*>(rec + lr * DV + d) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-                    }
-                if (hh == 0 && w == 0) {
-                    rec[RB * DV + lr] = s_m[lr];
-                    rec[RB * DV + RB + lr] = l;
                 }
             }
         }
-        __syncthreads();  // the stages and sums are free again
+        meet();  // the stages and sums are free again
         f += t1 - t0;
         if (t1 == T && f < f1) {
             before += T;
@@ -454,7 +608,9 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
 // Joins the partial results of the sequences that were divided: o = sum_c
 // 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over the parts in order.  A workgroup
 // takes one query row; DV / 4 threads are a team that takes four dimensions
-// each, and the teams share the row's parts.
+// each, and the teams share the row's parts.  Where sequences have few parts a
+// wave takes a row instead: no barriers, half the time (sequences of two to
+// three parts 19 us with a workgroup each).
 template <int DT, int DV, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_latent_join(LatentParams p, int RB) {
     constexpr int TEAM = DV / 4, TEAMS = THREADS / TEAM;
@@ -530,6 +686,87 @@ __global__ __launch_bounds__(THREADS) void k_latent_join(LatentParams p, int RB)
     *reinterpret_cast<v4s*>(p.out + units(b, p.os[0], node, p.os[1]) + units(head, p.os[2]) + 2 * d) = res;
 }
 
+template <int DT, int DV>
+__global__ __launch_bounds__(256) void k_latent_join_few(LatentParams p, int RB) {
+    constexpr int kD = DV / 256;  // groups of four dimensions a lane has
+    const int b = blockIdx.x, lane = threadIdx.x & 63;
+    const int row = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t first = p.start[b], T = p.start[b + 1] - first;
+    const Cut cut(p.clusters, p.start[p.B]);
+    const int c0 = cut.of(first), c1 = cut.of(first + T - 1);
+    if (c0 == c1 || row >= p.N * p.H) return;
+    int n = p.N;
+    if (p.n_nodes) {
+        n = p.n_nodes[b];
+        n = n < 0 ? 0 : n > p.N ? p.N : n;
+    }
+    const int node = row / p.H, head = row - node * p.H;
+    v4s res[kD];
+#pragma unroll
+    for (int k = 0; k < kD; ++k) res[k] = v4s{0, 0, 0, 0};
+    if (node < n) {
+        const int m = row / RB, r = row - m * RB;
+        const int64_t rec = RB * (DV + 2);
+        // the first part's record is its second one unless the part begins here
+        const int slot0 = cut.start(c0) == first ? 0 : 1;
+        auto at = [&](int c) { return p.part + ((static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * p.MT + m) * rec; };
+        float mx = -INFINITY, l = 0.f;
+        float4 o[kD];
+#pragma unroll
+        for (int k = 0; k < kD; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kFlight = 4;
+        for (int c = c0; c <= c1; c += kFlight) {
+            float mc[kFlight], lc[kFlight];
+            float4 v[kFlight][kD];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const float* const q = at(min(c + i, c1));
+                mc[i] = c + i <= c1 ? q[RB * DV + r] : -INFINITY;
+                lc[i] = q[RB * DV + RB + r];
+#pragma unroll
+                for (int k = 0; k < kD; ++k) {
+                    const int d = k * 256 + lane * 4;
+                    v[i][k] = d < p.dv && c + i <= c1 ? *reinterpret_cast<const float4*>(q + r * DV + d)
+                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+            float mn = mx;
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) mn = fmaxf(mn, mc[i]);
+            const float a = shift_of(mx, mn);
+            l *= a;
+#pragma unroll
+            for (int k = 0; k < kD; ++k) {
+                o[k].x *= a;
+                o[k].y *= a;
+                o[k].z *= a;
+                o[k].w *= a;
+            }
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                if (c + i > c1) break;
+                const float e = shift_of(mc[i], mn);
+                l += e * lc[i];
+#pragma unroll
+                for (int k = 0; k < kD; ++k) {
+                    o[k].x += e * v[i][k].x;
+                    o[k].y += e * v[i][k].y;
+                    o[k].z += e * v[i][k].z;
+                    o[k].w += e * v[i][k].w;
+                }
+            }
+            mx = mn;
+        }
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int k = 0; k < kD; ++k) res[k] = pack4<DT>(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv);
+    }
+    uint8_t* const dst = p.out + units(b, p.os[0], node, p.os[1]) + units(head, p.os[2]);
+#pragma unroll
+    for (int k = 0; k < kD; ++k)
+        if (k * 256 + lane * 4 < p.dv) *reinterpret_cast<v4s*>(dst + 2 * (k * 256 + lane * 4)) = res[k];
+}
+
 template <int DT, int DK, int DV, int RB>
 hipError_t attn_one(const LatentParams& p, hipStream_t st, const LaunchEvents& ev) {
     constexpr int lds = LatentLds<DK, RB>::kAll;
@@ -543,13 +780,16 @@ hipError_t attn_one(const LatentParams& p, hipStream_t st, const LaunchEvents& e
 
 template <int DT, int DK, int DV>
 hipError_t attn_rows(const LatentParams& p, int rows, hipStream_t st, const LaunchEvents& ev) {
-    if (rows == 32) return attn_one<DT, DK, DV, 32>(p, st, ev);
-    if (rows == 64) return attn_one<DT, DK, DV, 64>(p, st, ev);
-    return attn_one<DT, DK, DV, 128>(p, st, ev);
+    return rows == 32 ? attn_one<DT, DK, DV, 32>(p, st, ev) : attn_one<DT, DK, DV, 64>(p, st, ev);
 }
 
 template <int DT, int DV>
 hipError_t join_one(const LatentParams& p, const LatentShape& s, hipStream_t st, const LaunchEvents& ev) {
+    if (p.clusters <= 8 * p.B) {  // parts per sequence
+        hipExtLaunchKernelGGL((k_latent_join_few<DT, DV>), dim3(p.B, (p.N * p.H + 3) / 4), dim3(256), 0, st, ev.start,
+                              ev.stop, 0, p, s.rows);
+        return hipGetLastError();
+    }
     const dim3 grid(p.B, p.N * p.H);
     hipExtLaunchKernelGGL((k_latent_join<DT, DV, 256>), grid, dim3(256), 0, st, ev.start, ev.stop, 0, p, s.rows);
     return hipGetLastError();

@@ -7,8 +7,14 @@
 //   o_i = sum_{s <= p_i} 2^(x_s - m) v_s / sum_{s <= p_i} 2^(x_s - m),  x_s = scale log2(e) q_i.k_s.
 //
 //   k_prompt_plan    the sequences' places in one line of rows, and in one of query tiles;
-//   k_prompt_expand  keys and values of every head for every row of the line;
+//   k_prompt_expand  keys and values of every head for every row of the line, and again
+//                    the values of heads whose largest one float16 does not hold well;
 //   k_prompt_attn    128 queries of one head against 64 keys at a time.
+//
+// Keys are rounded to the input type, as their queries are in it.  Values and
+// weights meet in float16 whatever the input type, each head's values times a
+// power of two taken from its largest one: with both in bfloat16 the outputs'
+// error was 1.65 times that of the output's own rounding, with float16 @ times.
 
 #include "sv_attn.h"
 #include "sv_latent.h"
@@ -21,7 +27,9 @@ namespace {
 //
 // W rows are the matrix instruction's A operand and token rows its B operand,
 // both read 16 bytes a lane from LDS, where the eight chunks of a row's 64
-// elements are XORed with the row number (eight rows on all banks).  A null token
+// elements are XORed with half the row number: a read takes 16 lanes at a time
+// (0-3, 12-15, 20-23, 24-27 and so on) over 64 banks, rows alternate between two
+// halves of them, and these lanes' even rows have the eight halves 0-7.  A null token
 // row counts as zeros.
 template <int TT>
 struct Tile {
@@ -31,6 +39,9 @@ struct Tile {
     static constexpr int kW = 4, kX = TT / 32;               // wide loads of a wave and stage
 };
 
+// The chunk that lane `lane` of wide load `idx` of eight rows stages.
+__device__ __forceinline__ int product_chunk(int lane, int idx) { return (lane & 7) ^ ((idx & 1) << 2 | lane >> 4); }
+
 template <int DT, int TT>
 __device__ __forceinline__ void product_tile(uint32_t smem_at, const uint8_t* const* wp, const uint8_t* const* xp,
                                              int K, v16f (*acc)[Tile<TT>::BT]) {
@@ -38,21 +49,21 @@ __device__ __forceinline__ void product_tile(uint32_t smem_at, const uint8_t* co
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int hh = lane >> 5, col = lane & 31;
     const int wm = w % L::WM, wt = w / L::WM;
-    const int chunk = (lane & 7) ^ (lane >> 3);
     const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero);
     auto stage = [&](int s, uint32_t at) __attribute__((always_inline)) {
-        const bool in = s * 64 + chunk * 8 < K;
 #pragma unroll
         for (int i = 0; i < L::kW; ++i)
-            load_lds(in ? wp[i] + s * 128 : zero, smem_at + at + (w * L::kW + i) * 1024);
+            load_lds(s * 64 + product_chunk(lane, w * L::kW + i) * 8 < K ? wp[i] + s * 128 : zero,
+                     smem_at + at + (w * L::kW + i) * 1024);
 #pragma unroll
         for (int i = 0; i < L::kX; ++i)
-            load_lds(in && xp[i] ? xp[i] + s * 128 : zero, smem_at + at + 16384 + (w * L::kX + i) * 1024);
+            load_lds(s * 64 + product_chunk(lane, w * L::kX + i) * 8 < K && xp[i] ? xp[i] + s * 128 : zero,
+                     smem_at + at + 16384 + (w * L::kX + i) * 1024);
     };
     uint32_t a_rd[4], b_rd[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const uint32_t c = ((2 * k + hh) ^ (col & 7)) << 4;
+        const uint32_t c = ((2 * k + hh) ^ (col >> 1 & 7)) << 4;
         a_rd[k] = smem_at + (wm * L::BM * 32 + col) * 128 + c;
         b_rd[k] = smem_at + 16384 + (wt * L::BT * 32 + col) * 128 + c;
     }
@@ -107,14 +118,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(ProductParams p) {
     const int in_head = static_cast<int>(task - h * (mt * static_cast<int64_t>(tt)));
     const int t0 = in_head / mt * TT, m0 = in_head % mt * 128;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int hh = lane >> 5, col = lane & 31, r8 = lane >> 3, chunk = (lane & 7) ^ r8;
+    const int hh = lane >> 5, col = lane & 31, r8 = lane >> 3;
     const uint8_t *wp[L::kW], *xp[L::kX];
 #pragma unroll
     for (int i = 0; i < L::kW; ++i)
-        wp[i] = p.w + 16 * (h * p.ws[0] + min(m0 + (w * L::kW + i) * 8 + r8, p.M - 1) * p.ws[1] + chunk);
+        wp[i] = p.w + 16 * (h * p.ws[0] + min(m0 + (w * L::kW + i) * 8 + r8, p.M - 1) * p.ws[1] +
+                            product_chunk(lane, w * L::kW + i));
 #pragma unroll
     for (int i = 0; i < L::kX; ++i)
-        xp[i] = p.x + 16 * (min(t0 + (w * L::kX + i) * 8 + r8, p.T - 1) * p.xs[0] + h * p.xs[1] + chunk);
+        xp[i] = p.x + 16 * (min(t0 + (w * L::kX + i) * 8 + r8, p.T - 1) * p.xs[0] + h * p.xs[1] +
+                            product_chunk(lane, w * L::kX + i));
     v16f acc[L::BM][L::BT];
     product_tile<DT, TT>(smem_at, wp, xp, p.K, acc);
     const int wm = w % L::WM, wt = w / L::WM;
@@ -140,6 +153,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(ProductParams p) {
 __device__ __forceinline__ int clamp_len(const PromptParams& p, int len) {
     const int64_t cap = static_cast<int64_t>(p.width) << p.ps_shift;
     return len < 0 ? 0 : len > cap ? static_cast<int>(cap) : len;
+}
+
+// The power of two a head's values are stored times, by the bits of the largest one's
+// size: 1 where float16 holds them at its full precision, with room for a hundredth
+// of it.  The largest becomes 2^14 to 2^15 otherwise.
+__device__ __forceinline__ float value_scale(uint32_t most) {
+    const float m = __uint_as_float(most);
+    if (most == 0 || (m >= 0x1p-4f && m < 0x1p15f)) return 1.f;
+    const int e = static_cast<int>(most >> 23) - 127;  // denormal sizes: -127
+    return __uint_as_float(static_cast<uint32_t>(127 + min(14 - e, 120)) << 23);
 }
 
 // The last i in [0, n) with at[i] <= x, for rising at.
@@ -210,27 +233,33 @@ __global__ __launch_bounds__(1024) void k_prompt_plan(PromptParams p) {
         p.plan[2 * p.B + 1] = tile0;
         *p.odd = 0;
     }
+    for (int h = tid; h < p.H; h += 1024) p.most[h] = 0;
 }
 
 // Keys and values of 128 rows of the line: a product with the rows gathered from
 // their pages.  The first output tile's workgroups also bring the rows' second
-// parts into the line.
-template <int DT>
+// parts into the line.  AGAIN: the values of heads that need a scale.
+template <int DT, bool AGAIN>
 __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
     using L = Tile<128>;
     extern __shared__ __align__(16) uint8_t smem[];
     const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) uint8_t*)smem));
     const int mk = p.H * p.dn, mv = p.H * p.dv;
-    const int tk = (mk + 127) / 128, tv = (mv + 127) / 128, tr = (p.rows + 127) / 128;
+    const int tk = AGAIN ? 0 : (mk + 127) / 128, tv = (mv + 127) / 128, tr = (p.rows + 127) / 128;
     const int64_t task = task_of(static_cast<int64_t>(tk + tv) * tr);
     if (task < 0) return;
     const int mt = static_cast<int>(task / tr), r0 = static_cast<int>(task - static_cast<int64_t>(mt) * tr) * 128;
     const int64_t total = p.plan[p.B];
     if (r0 >= total) return;
+    if (AGAIN) {
+        bool any = false;
+        for (int h = mt * 128 / p.dv; h <= min(mt * 128 + 127, mv - 1) / p.dv; ++h) any |= value_scale(p.most[h]) != 1.f;
+        if (!any) return;
+    }
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int hh = lane >> 5, col = lane & 31, r8 = lane >> 3, chunk = (lane & 7) ^ r8;
-    const bool values = mt >= tk;
+    const int hh = lane >> 5, col = lane & 31, r8 = lane >> 3;
+    const bool values = AGAIN || mt >= tk;
     const int m0 = (values ? mt - tk : mt) * 128, M = values ? mv : mk, per = values ? p.dv : p.dn;
     const uint8_t* const wt0 = values ? p.wv : p.wk;
     const int64_t* const wst = values ? p.wvs : p.wks;
@@ -247,14 +276,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
 #pragma unroll
     for (int i = 0; i < L::kX; ++i) {
         const uint8_t* const x = row_of(r0 + (w * L::kX + i) * 8 + r8);
-        xp[i] = x ? x + 16 * chunk : nullptr;
+        xp[i] = x ? x + 16 * product_chunk(lane, w * L::kX + i) : nullptr;
     }
 #pragma unroll
     for (int i = 0; i < L::kW; ++i) {
         const int m = min(m0 + (w * L::kW + i) * 8 + r8, M - 1), h = m / per;
-        wp[i] = wt0 + 16 * (h * wst[0] + (m - h * per) * wst[1] + chunk);
+        wp[i] = wt0 + 16 * (h * wst[0] + (m - h * per) * wst[1] + product_chunk(lane, w * L::kW + i));
     }
-    if (mt == 0) {
+    if (!AGAIN && mt == 0) {
         for (int r = threadIdx.x >> 3; r < 128 && r0 + r < total; r += 32) {
             const uint8_t* const x = row_of(r0 + r);
             for (int c = lane & 7; c < p.dr / 8; c += 8)
@@ -266,25 +295,68 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
     v16f acc[L::BM][L::BT];
     product_tile<DT, 128>(smem_at, wp, xp, p.R, acc);
     const int wm = w % L::WM, wt = w / L::WM;
-    uint8_t* const to = values ? p.v : p.k;
-    bool bad = false;
+    if (!values) {
 #pragma unroll
-    for (int b = 0; b < L::BT; ++b) {
-        const int r = r0 + (wt * L::BT + b) * 32 + col;
-        if (r >= total || r >= p.rows) continue;
+        for (int b = 0; b < L::BT; ++b) {
+            const int r = r0 + (wt * L::BT + b) * 32 + col;
+            if (r >= total || r >= p.rows) continue;
 #pragma unroll
-        for (int a = 0; a < L::BM; ++a)
+            for (int a = 0; a < L::BM; ++a)
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const int m = m0 + (wm * L::BM + a) * 32 + 2 * i + 4 * hh, h = m / per;
-                if (m >= M) continue;
-                const v4s y = pack4<DT>(acc[a][b][i], acc[a][b][i + 1], acc[a][b][i + 2], acc[a][b][i + 3]);
-                const uint2 u = __builtin_bit_cast(uint2, y);
-                bad |= nonfinite2<DT>(u.x) || nonfinite2<DT>(u.y);
-                *reinterpret_cast<v4s*>(to + 2 * ((static_cast<int64_t>(h) * p.rows + r) * per + m - h * per)) = y;
-            }
+                for (int i = 0; i < 16; i += 4) {
+                    const int m = m0 + (wm * L::BM + a) * 32 + 2 * i + 4 * hh, h = m / per;
+                    if (m < M)
+                        *reinterpret_cast<v4s*>(p.k + 2 * ((static_cast<int64_t>(h) * p.rows + r) * per + m - h * per)) =
+                            pack4<DT>(acc[a][b][i], acc[a][b][i + 1], acc[a][b][i + 2], acc[a][b][i + 3]);
+                }
+        }
+        return;
     }
-    if (values && bad) *p.odd = 1;
+    // a wave's eight neighbouring outputs are of one head
+    uint32_t most = 0;
+    int of = -1;
+    bool odd = false;
+    auto tell = [&] {
+        for (int s = 32; s; s >>= 1) most = max(most, static_cast<uint32_t>(__shfl_xor(most, s)));
+        // most waves find a larger one there: 4000 atomics on one line cost 20 us
+        if (lane == 0 && of >= 0 &&
+            most > __hip_atomic_load(p.most + of, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+            atomicMax(p.most + of, most);
+        most = 0;
+    };
+#pragma unroll
+    for (int a = 0; a < L::BM; ++a)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const int m8 = m0 + (wm * L::BM + a) * 32 + 2 * i, m = m8 + 4 * hh, h = m8 / per;
+            if (m8 >= M) continue;
+            if (!AGAIN && h != of) {
+                if (of >= 0) tell();
+                of = h;
+            }
+            const float scale = AGAIN ? value_scale(p.most[h]) : 1.f;
+#pragma unroll
+            for (int b = 0; b < L::BT; ++b) {
+                const int r = r0 + (wt * L::BT + b) * 32 + col;
+                if (r >= total || r >= p.rows) continue;
+                float y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    y[j] = acc[a][b][i + j] * scale;
+                    const uint32_t size = __float_as_uint(acc[a][b][i + j]) & 0x7FFFFFFFu;
+                    if (size >= 0x7F800000u)
+                        odd = true;
+                    else
+                        most = max(most, size);
+                }
+                *reinterpret_cast<v4s*>(p.v + 2 * ((static_cast<int64_t>(h) * p.rows + r) * per + m - h * per)) =
+                    pack4<kDTypeF16>(y[0], y[1], y[2], y[3]);
+            }
+        }
+    if (!AGAIN) {
+        tell();
+        if (odd) *p.odd = 1;
+    }
 }
 
 // 128 queries of one head (32 a wave) against 64 keys at a time, double-buffered.
@@ -297,6 +369,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
     constexpr int kVAt = TK * kKB, kStage = TK * (kKB + kVB);
     constexpr int kK = TK * NC / 64 / kWaves, kV = TK * NV / 64 / kWaves;  // wide loads of a wave
     static_assert(NC % 8 == 0 && NV % 8 == 0, "layout");
+    // positions of a row's chunks, so that no bank is met twice in a wide read (above: rows of 256 bytes
+    // fill all 64 banks, others alternate) or a transposing one (four rows at four chunks)
+    auto k_swizzle = [](int r) { return kKB % 256 ? r >> 1 & 7 : r & 15; };
+    auto v_swizzle = [](int r) { return kVB % 256 ? (r >> 1 & 1) << 2 : (r & 3) << 2; };
+    constexpr int KR = kKB % 256 ? 4 : 8;  // addresses of a key's operands; the next ones are KR * 32 bytes on
     extern __shared__ __align__(16) uint8_t smem[];  // nothing beside it: two workgroups fill a CU
     const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) uint8_t*)smem));
@@ -334,7 +411,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
     const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero);
 #pragma unroll
     for (int i = 0; i < kK; ++i) {
-        const int e = (w * kK + i) * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ (r & 7);
+        const int e = (w * kK + i) * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ k_swizzle(r);
         kr[i] = r;
         if (chunk < DN / 8) {
             const bool there = chunk * 8 < p.dn;
@@ -351,7 +428,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
     uint32_t vs[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-        const int r = v_row + i * (64 / NV), c = (lane % NV) ^ swizzle(r);
+        const int r = v_row + i * (64 / NV), c = (lane % NV) ^ v_swizzle(r);
         const bool there = c * 8 < p.dv;
         vp[i] = there ? p.v + 2 * ((static_cast<int64_t>(h) * p.rows + row0 + r) * p.dv + c * 8) : zero;
         vs[i] = there ? TK * p.dv * 2 : 0;
@@ -379,15 +456,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
         const int r = t * TK + lane;
         return r < len ? p.there[row0 + r] : 0;
     };
-    uint32_t k_rd[4], v_rd[2];
+    uint32_t k_rd[KR], v_rd[ND];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) k_rd[s] = smem_at + col * kKB + (((2 * s + hh) ^ (col & 7)) << 4);
+    for (int s = 0; s < KR; ++s) k_rd[s] = smem_at + col * kKB + (((2 * s + hh) ^ k_swizzle(col)) << 4);
     {
         const int vrow = 4 * hh + ((lane & 15) >> 2);
         const int c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-            v_rd[s] = smem_at + kVAt + vrow * kVB + (((4 * s + c) ^ swizzle(vrow)) << 4) + (lane & 1) * 8;
+        for (int dt = 0; dt < ND; ++dt)
+            v_rd[dt] = smem_at + kVAt + vrow * kVB + (((4 * dt + c) ^ v_swizzle(vrow)) << 4) + (lane & 1) * 8;
     }
     v8s q[NQ];
     {
@@ -442,7 +519,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
                 for (int i = pass ? w : 0; i < TK * NV / 64; i += pass ? kWaves : 1) {
                     v8s* const e = reinterpret_cast<v8s*>(smem + at + kVAt + i * 1024 + lane * 16);
                     const uint4 u = __builtin_bit_cast(uint4, *e);
-                    if (nonfinite2<DT>(u.x) || nonfinite2<DT>(u.y) || nonfinite2<DT>(u.z) || nonfinite2<DT>(u.w)) {
+                    if (nonfinite2<kDTypeF16>(u.x) || nonfinite2<kDTypeF16>(u.y) || nonfinite2<kDTypeF16>(u.z) || nonfinite2<kDTypeF16>(u.w)) {
                         if (pass)
                             *e = v8s{0, 0, 0, 0, 0, 0, 0, 0};
                         else
@@ -463,7 +540,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
                 for (int i = 0; i < 16; ++i) x[ks][i] = 0.f;
 #pragma unroll
                 for (int s = 0; s < NQ; ++s)
-                    x[ks] = mfma<DT>(lds_read(k_rd[s & 3] + at + ks * 32 * kKB + (s >> 2) * 128), q[s], x[ks]);
+                    x[ks] = mfma<DT>(lds_read(k_rd[s % KR] + at + ks * 32 * kKB + s / KR * (KR * 32)), q[s], x[ks]);
             }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -481,8 +558,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
                 for (int i = 0; i < 16; ++i) top = fmaxf(top, x[ks][i]);
             }
             top = scaled(half_max(top), scale2);
-            if (__any(top - mx > kUp<DT> + 8.f)) {
-                const float mn = fmaxf(mx, top - kUp<DT>);
+            if (__any(top - mx > kUp<kDTypeF16> + 8.f)) {
+                const float mn = fmaxf(mx, top - kUp<kDTypeF16>);
                 const float a = shift_of(mx, mn);
                 l *= a;
 #pragma unroll
@@ -501,16 +578,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
                 }
 #pragma unroll
                 for (int t2 = 0; t2 < 2; ++t2) {
-                    const v4s lo = pack4<DT>(x[ks][8 * t2], x[ks][8 * t2 + 1], x[ks][8 * t2 + 2], x[ks][8 * t2 + 3]);
+                    const v4s lo = pack4<kDTypeF16>(x[ks][8 * t2], x[ks][8 * t2 + 1], x[ks][8 * t2 + 2], x[ks][8 * t2 + 3]);
                     const v4s hi =
-                        pack4<DT>(x[ks][8 * t2 + 4], x[ks][8 * t2 + 5], x[ks][8 * t2 + 6], x[ks][8 * t2 + 7]);
+                        pack4<kDTypeF16>(x[ks][8 * t2 + 4], x[ks][8 * t2 + 5], x[ks][8 * t2 + 6], x[ks][8 * t2 + 7]);
                     const v8s pf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
                     for (int dt = 0; dt < ND; ++dt) {
-                        const uint32_t a = v_rd[dt & 1] + at + (ks * 32 + t2 * 16) * kVB + (dt >> 1) * 128;
+                        const uint32_t a = v_rd[dt] + at + (ks * 32 + t2 * 16) * kVB;
                         const v8s vf =
                             __builtin_shufflevector(lds_read_tr(a), lds_read_tr(a + 8 * kVB), 0, 1, 2, 3, 4, 5, 6, 7);
-                        o[dt] = mfma<DT>(vf, pf, o[dt]);
+                        o[dt] = mfma<kDTypeF16>(vf, pf, o[dt]);
                     }
                 }
             }
@@ -518,7 +595,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
         at = kStage - at;
     }
     l = half_sum(l);
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // a query that sees nothing: zero
+    const float inv = l == 0.f ? 0.f : 1.f / l / value_scale(p.most[h]);  // a query that sees nothing: zero
     if (!in) return;
 #pragma unroll
     for (int dt = 0; dt < ND; ++dt)
@@ -539,11 +616,11 @@ hipError_t product_one(const ProductParams& p, hipStream_t st, const LaunchEvent
     return hipGetLastError();
 }
 
-template <int DT>
+template <int DT, bool AGAIN>
 hipError_t expand_one(const PromptParams& p, hipStream_t st, const LaunchEvents& ev) {
-    const int64_t tasks =
-        static_cast<int64_t>((p.H * p.dn + 127) / 128 + (p.H * p.dv + 127) / 128) * ((p.rows + 127) / 128);
-    hipExtLaunchKernelGGL((k_prompt_expand<DT>), dim3(static_cast<unsigned>(grid_of(tasks))), dim3(kThreads),
+    const int64_t tasks = static_cast<int64_t>((AGAIN ? 0 : (p.H * p.dn + 127) / 128) + (p.H * p.dv + 127) / 128) *
+                          ((p.rows + 127) / 128);
+    hipExtLaunchKernelGGL((k_prompt_expand<DT, AGAIN>), dim3(static_cast<unsigned>(grid_of(tasks))), dim3(kThreads),
                           2 * Tile<128>::kStage, st, ev.start, ev.stop, 0, p);
     return hipGetLastError();
 }
@@ -578,8 +655,9 @@ hipError_t launch_prompt_plan(const PromptParams& p, hipStream_t st, const Launc
     return hipGetLastError();
 }
 
-hipError_t launch_prompt_expand(const PromptParams& p, int dtype, hipStream_t st, const LaunchEvents& ev) {
-    return dtype == DT_BF16 ? expand_one<DT_BF16>(p, st, ev) : expand_one<kDTypeF16>(p, st, ev);
+hipError_t launch_prompt_expand(const PromptParams& p, int dtype, bool again, hipStream_t st, const LaunchEvents& ev) {
+    if (again) return dtype == DT_BF16 ? expand_one<DT_BF16, true>(p, st, ev) : expand_one<kDTypeF16, true>(p, st, ev);
+    return dtype == DT_BF16 ? expand_one<DT_BF16, false>(p, st, ev) : expand_one<kDTypeF16, false>(p, st, ev);
 }
 
 hipError_t launch_prompt_attn(const PromptParams& p, int dtype, hipStream_t st, const LaunchEvents& ev) {

@@ -27,6 +27,7 @@ enum TreeKernelKind : int {
     KK_PRODUCT,
     KK_PROMPT_PLAN,
     KK_PROMPT_EXPAND,
+    KK_PROMPT_SCALE,
     KK_PROMPT_ATTN,
     KK_BEAM_STATS,
     KK_BEAM_SELECT,
