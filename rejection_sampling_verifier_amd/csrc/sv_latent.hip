@@ -81,20 +81,19 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
     using Lds = LatentLds<DK, RB>;
     constexpr int TK = kLatKeys;
     constexpr int NC = DK / 8;                // 16-byte chunks per row
-    constexpr int NL = TK * NC / 64;          // wide loads of a tile
-    constexpr int kLoads = NL / 4;            // of a value wave
+    constexpr int kLoads = NC / 8;            // wide loads of a value wave and tile
     constexpr int NQ = DK / 32;               // matrix steps of a row
     constexpr int NB = RB / 32;               // blocks of 16 rows a score wave has
     constexpr int RG = RB / 32;               // blocks of 32 rows a value wave has
     constexpr int CB = DV / 32 / 4;           // and of 32 values
     constexpr int kRowB = DK * 2;
     constexpr int kRec = RB * (DV + 2);       // floats of a partial result
-    static_assert(NC % 8 == 0 && NL * 64 == TK * NC && NL % 4 == 0 && CB >= 1, "layout");
+    static_assert(NC % 8 == 0 && TK == 32 && CB >= 1, "layout");
 
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s_a[RB], s_m[RB], s_l[2][RB];
     __shared__ int s_raise[2];
-    __shared__ uint32_t s_ok[kLatRing];       // rows of the tiles that exist
+    __shared__ __align__(4) uint8_t s_ok[kLatRing][4];  // rows of the tiles that exist
     __shared__ int64_t s_sum[kLatWaves];
     __shared__ int32_t s_scan[kLatWaves];
     __shared__ int s_b;
@@ -170,8 +169,8 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
     if (tid < 2) s_raise[tid] = 0;
     const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) uint8_t*)smem));
-    // Staging, by the value waves: wide load i = wv + 4 k of a tile fills 1024 bytes; lane l's 16 are
-    // chunk position (64 i + l) % NC of row (64 i + l) / NC.  Eight rows are NC / 8 loads.
+    // Staging, by the value waves, eight rows each: wide load k fills 1024 bytes; lane l's 16 are chunk
+    // position (64 k + l) % NC of row (64 k + l) / NC.
     // chunks past the row's elements are zeros that nothing overwrites
     if (p.C < DK)
         for (int i = tid; i < kLatRing * Lds::kStage / 16; i += kLatThreads)
@@ -208,69 +207,64 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
         const bool any = m * RB < rows;
         const int32_t* const tab = p.table + b * p.table_stride;
         const uint8_t* const nwb = p.nw + units(b, p.nws[0]);
-        // The pages of a whole tile of cache rows, eight rows each on one: scalar loads, which do not
-        // queue behind the rows under way.  -1: not such a tile.
-        struct Pages {
-            int at[4];
-        };
-        auto pages_of = [&](int t) {
-            Pages r;
-            const bool fit = by_eights && t < t1 && (t + 1) * TK <= len;
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                r.at[g] = fit ? *(const_i32*)(tab + ((t * TK + 8 * g) >> p.ps_shift)) : -1;
-            return r;
-        };
         uint32_t off[kLoads], padded = 0;
         if (!scores) {
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
-                const int e = (wv + 4 * k) * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ swizzle(r);
-                off[k] = static_cast<uint32_t>(units(r & 7, p.kcs[1], chunk, 1));
+                const int e = k * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ swizzle(8 * wv + r);
+                off[k] = static_cast<uint32_t>(units(r, p.kcs[1], chunk, 1));
                 if (chunk * 8 >= p.C) padded |= 1u << k;
             }
         }
-        // starts staging tile t and says which of its rows exist (the others are staged as zeros)
-        auto stage = [&](int t, const Pages& pg) {
+        // The page of the wave's eight rows of tile t, where these are whole cache rows on one page: a
+        // scalar load, which does not queue behind the rows under way.  -1: not so.
+        auto page_of = [&](int t) {
+            const int key = t * TK + 8 * wv;
+            return by_eights && t < t1 && key + 8 <= len ? *(const_i32*)(tab + (key >> p.ps_shift)) : -1;
+        };
+        // starts staging the wave's rows of tile t and says which exist (the others are staged as zeros)
+        auto stage = [&](int t, int pg) {
             const bool tree = t >= cache;
-            const int first = (tree ? t - cache : t) * TK;
-            const int slot = (t - t0) % kLatRing;
-            const uint32_t to = smem_at + slot * Lds::kStage + wv * 1024;
+            const int first = (tree ? t - cache : t) * TK + 8 * wv, slot = (t - t0) % kLatRing;
+            const uint32_t to = smem_at + slot * Lds::kStage + wv * (kLoads * 1024);
             const uint32_t most = static_cast<uint32_t>(p.pages);
-            if (static_cast<uint32_t>(pg.at[0]) < most && static_cast<uint32_t>(pg.at[1]) < most &&
-                static_cast<uint32_t>(pg.at[2]) < most && static_cast<uint32_t>(pg.at[3]) < most) {
+            if (static_cast<uint32_t>(pg) < most) {
+                const uint8_t* const base = p.kc + units(pg, p.kcs[0], first & ps_mask, p.kcs[1]);
+                if (p.C == DK) {
 #pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    const int g = (wv + 4 * k) / (NC / 8);
-                    const int pg8 = g < 2 ? (g ? pg.at[1] : pg.at[0]) : (g == 2 ? pg.at[2] : pg.at[3]);
-                    const uint8_t* const base = p.kc + units(pg8, p.kcs[0], (first + 8 * g) & ps_mask, p.kcs[1]);
-                    if (!(padded >> k & 1)) load_lds(base, off[k], to + k * 4096);
+                    for (int k = 0; k < kLoads; ++k) load_lds(base, off[k], to + k * 1024);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kLoads; ++k)
+                        if (!(padded >> k & 1)) load_lds(base, off[k], to + k * 1024);
                 }
-                if (wv == 0 && lane == 0) s_ok[slot] = ~0u;
+                if (lane == 0) s_ok[slot][wv] = 0xFF;
                 return;
             }
-            int pl = -1;  // lane j: the page of row j
-            if (!tree && first + col < len) pl = tab[(first + col) >> p.ps_shift];
-            const uint32_t okm = static_cast<uint32_t>(tree ? __ballot(first + col < n)
-                                                            : __ballot(static_cast<uint32_t>(pl) < most));
+            const int row = first + (lane & 7);  // lane j: whether row j exists, its page
+            int pl = -1;
+            if (!tree && row < len) pl = tab[row >> p.ps_shift];
+            const uint32_t okm =
+                static_cast<uint32_t>(tree ? __ballot(row < n) : __ballot(static_cast<uint32_t>(pl) < most)) & 0xFFu;
 #pragma unroll 1
             for (int k = 0; k < kLoads; ++k) {
-                const int e = (wv + 4 * k) * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ swizzle(r);
+                const int e = k * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ swizzle(8 * wv + r);
                 const uint32_t pg_of = __shfl(pl, r);
                 const uint8_t* const src =
                     tree ? nwb + units(first + r, p.nws[1], chunk, 1)
                          : p.kc + units(pg_of, p.kcs[0], (first + r) & ps_mask, p.kcs[1]) + 16 * chunk;
-                load_lds((okm >> r & 1) && chunk * 8 < p.C ? src : zero, to + k * 4096);
+                load_lds((okm >> r & 1) && chunk * 8 < p.C ? src : zero, to + k * 1024);
             }
-            if (wv == 0 && lane == 0) s_ok[slot] = okm;
+            if (lane == 0) s_ok[slot][wv] = static_cast<uint8_t>(okm);
         };
         // Step t: tile t is there, the weights of tile t - 1 too; tile t + 2 is sent for.  Both kinds of
         // waves go through the same barriers.
-        Pages pg;
+        int pg = -1;
         auto begin = [&] {
-            stage(t0, pages_of(t0));
-            if (t0 + 1 < t1) stage(t0 + 1, pages_of(t0 + 1));
-            pg = pages_of(t0 + 2);
+            const int p0 = page_of(t0), p1 = page_of(t0 + 1);
+            pg = page_of(t0 + 2);
+            stage(t0, p0);
+            if (t0 + 1 < t1) stage(t0 + 1, p1);
         };
         auto arrive = [&](int t) {
             // this wave's loads of tile t have landed, the next tile's stay under way
@@ -280,7 +274,7 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
                 wait_vm<0>();
             meet();
             if (t + 2 < t1) stage(t + 2, pg);
-            pg = pages_of(t + 3);
+            pg = page_of(t + 3);
         };
         // Rows of the tree in tile t that hold infinities or NaN among their values: these values go out
         // of the tile (0 times them would reach the nodes that do not see the row), and whoever sees the
@@ -291,12 +285,12 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
                 const uint32_t at = ((t - t0) % kLatRing) * Lds::kStage;
 #pragma unroll 1
                 for (int k = 0; k < kLoads; ++k) {
-                    const int e = (wv + 4 * k) * 64 + lane, r = e / NC;
-                    if (((e - r * NC) ^ swizzle(r)) * 8 >= p.dv) continue;
-                    v8s* const y = reinterpret_cast<v8s*>(smem + at + (wv + 4 * k) * 1024 + lane * 16);
+                    const int e = k * 64 + lane, r = e / NC;
+                    if (((e - r * NC) ^ swizzle(8 * wv + r)) * 8 >= p.dv) continue;
+                    v8s* const y = reinterpret_cast<v8s*>(smem + at + (wv * kLoads + k) * 1024 + lane * 16);
                     const uint4 u = __builtin_bit_cast(uint4, *y);
                     if (nonfinite2<DT>(u.x) || nonfinite2<DT>(u.y) || nonfinite2<DT>(u.z) || nonfinite2<DT>(u.w)) {
-                        nf |= 1u << r;
+                        nf |= 1u << (8 * wv + r);
                         *y = v8s{0, 0, 0, 0, 0, 0, 0, 0};
                     }
                 }
@@ -374,7 +368,7 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
             for (int t = t0; t <= t1; ++t, ++step) {
                 meet();
                 const int raised = s_raise[(step - 1) & 1];
-                const uint32_t ok = s_ok[(t - t0) % kLatRing];
+                const uint32_t ok = *reinterpret_cast<const uint32_t*>(s_ok[(t - t0) % kLatRing]);
                 const bool tree = t >= cache;
                 const uint32_t at = ((t - t0) % kLatRing) * Lds::kStage;
                 // the keys' operands a few steps at a time, those of the next two parts on their way meanwhile
