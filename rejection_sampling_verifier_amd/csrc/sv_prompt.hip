@@ -359,21 +359,36 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
     }
 }
 
-// 128 queries of one head (32 a wave) against 64 keys at a time, double-buffered.
+// Where chunk c of row r of a tile lies in LDS, rows of PITCH bytes: c XORed with this, so
+// that the 16 lanes of a wide read (rows 0-3, 12-15, 20-23, 24-27 and so on) meet no bank twice.
+template <int PITCH>
+__device__ __forceinline__ int row_swizzle(int r) {
+    return PITCH == 256 ? r & 15 : PITCH == 128 ? r >> 1 & 7 : r >> 2 & 3;
+}
+
+// A part of a tile's rows, W elements each: staging and the operands' addresses.
+template <int W>
+struct Rows {
+    static constexpr int kPitch = 2 * W, kChunks = W / 8;
+    static constexpr int kLoads = 64 * kChunks / 64 / kWaves;                      // wide loads of a wave
+    static constexpr int kAddr = kPitch == 256 ? 8 : kPitch == 128 ? 4 : 2;         // addresses of the operands
+    static_assert(kPitch == 256 || kPitch == 192 || kPitch == 128 || kPitch == 64, "layout");
+};
+
+// 128 queries of one head (32 a wave) against 64 keys at a time, double-buffered:
+// two workgroups fill a CU's LDS and take turns at its matrix units.  A tile's
+// operands are read from LDS some steps before they are needed.
 template <int DT, int DN, int DR, int DV>
 __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
+    using KN = Rows<DN>;
+    using KR = Rows<DR>;
+    using VR = Rows<DV>;
     constexpr int TK = 64;
-    constexpr int DQ = DN + DR, NC = DQ / 8, NV = DV / 8;  // chunks of a key and of a value
-    constexpr int NQ = DQ / 16, ND = DV / 32;
-    constexpr int kKB = DQ * 2, kVB = DV * 2;
-    constexpr int kVAt = TK * kKB, kStage = TK * (kKB + kVB);
-    constexpr int kK = TK * NC / 64 / kWaves, kV = TK * NV / 64 / kWaves;  // wide loads of a wave
-    static_assert(NC % 8 == 0 && NV % 8 == 0, "layout");
-    // positions of a row's chunks, so that no bank is met twice in a wide read (above: rows of 256 bytes
-    // fill all 64 banks, others alternate) or a transposing one (four rows at four chunks)
-    auto k_swizzle = [](int r) { return kKB % 256 ? r >> 1 & 7 : r & 15; };
-    auto v_swizzle = [](int r) { return kVB % 256 ? (r >> 1 & 1) << 2 : (r & 3) << 2; };
-    constexpr int KR = kKB % 256 ? 4 : 8;  // addresses of a key's operands; the next ones are KR * 32 bytes on
+    constexpr int kRAt = TK * KN::kPitch, kVAt = kRAt + TK * KR::kPitch, kStage = kVAt + TK * VR::kPitch;
+    constexpr int SN = DN / 16, SR = DR / 16, NQ = SN + SR, ND = DV / 32;
+    // the transposing read takes four rows at four chunks
+    auto v_swizzle = [](int r) { return VR::kPitch == 256 ? (r & 3) << 2 : (r >> 1 & 1) << 2; };
+    static_assert(VR::kPitch == 256 || VR::kPitch == 128, "layout");
     extern __shared__ __align__(16) uint8_t smem[];  // nothing beside it: two workgroups fill a CU
     const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) uint8_t*)smem));
@@ -404,67 +419,82 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
     const int last = min(i0 + kPromptRows, qs.n) - 1 + shift;  // of the workgroup
     const int T = last < 0 ? 0 : last / TK + 1;
 
-    // staging: chunk e = 64 i + lane of a tile's keys is chunk e % NC of row e / NC; a key's first
-    // DN / 8 chunks come from the expanded keys, the others from the line's second parts
-    const uint8_t *kp[kK], *vp[kV];
-    uint32_t ks[kK], kr[kK];
+    // Staging: chunk e = 64 i + lane of a part of the tile is chunk e % kChunks of row e / kChunks; `off` is
+    // where it comes from, relative to the tile's first row.  Dimensions past the head's are zeros in LDS
+    // that nothing overwrites.
+    uint32_t off_n[KN::kLoads], off_r[KR::kLoads], off_v[VR::kLoads], pad = 0;
+    const bool padded = p.dn < DN || p.dr < DR || p.dv < DV;
+    auto row_n = [&](int i) { return ((w * KN::kLoads + i) * 64 + lane) / KN::kChunks; };
+    auto row_r = [&](int i) { return ((w * KR::kLoads + i) * 64 + lane) / KR::kChunks; };
+    auto row_v = [&](int i) { return ((w * VR::kLoads + i) * 64 + lane) / VR::kChunks; };
+#pragma unroll
+    for (int i = 0; i < KN::kLoads; ++i) {
+        const int r = row_n(i), c = ((w * KN::kLoads + i) * 64 + lane) % KN::kChunks ^ row_swizzle<KN::kPitch>(r);
+        off_n[i] = 2 * (r * p.dn + 8 * c);
+        if (8 * c >= p.dn) pad |= 1u << i;
+    }
+#pragma unroll
+    for (int i = 0; i < KR::kLoads; ++i) {
+        const int r = row_r(i), c = ((w * KR::kLoads + i) * 64 + lane) % KR::kChunks ^ row_swizzle<KR::kPitch>(r);
+        off_r[i] = 2 * (r * p.dr + 8 * c);
+        if (8 * c >= p.dr) pad |= 1u << (8 + i);
+    }
+#pragma unroll
+    for (int i = 0; i < VR::kLoads; ++i) {
+        const int r = row_v(i), c = ((w * VR::kLoads + i) * 64 + lane) % VR::kChunks ^ v_swizzle(r);
+        off_v[i] = 2 * (r * p.dv + 8 * c);
+        if (8 * c >= p.dv) pad |= 1u << (16 + i);
+    }
     const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero);
-#pragma unroll
-    for (int i = 0; i < kK; ++i) {
-        const int e = (w * kK + i) * 64 + lane, r = e / NC, chunk = (e - r * NC) ^ k_swizzle(r);
-        kr[i] = r;
-        if (chunk < DN / 8) {
-            const bool there = chunk * 8 < p.dn;
-            kp[i] = there ? p.k + 2 * ((static_cast<int64_t>(h) * p.rows + row0 + r) * p.dn + chunk * 8) : zero;
-            ks[i] = there ? TK * p.dn * 2 : 0;
-        } else {
-            const int c = chunk - DN / 8;
-            const bool there = c * 8 < p.dr;
-            kp[i] = there ? p.pe + 2 * ((row0 + r) * p.dr + c * 8) : zero;
-            ks[i] = there ? TK * p.dr * 2 : 0;
-        }
-    }
-    const int v_row = (w * kV * 64 + lane) / NV;  // of the first load; the next is 64 / NV rows on
-    uint32_t vs[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int r = v_row + i * (64 / NV), c = (lane % NV) ^ v_swizzle(r);
-        const bool there = c * 8 < p.dv;
-        vp[i] = there ? p.v + 2 * ((static_cast<int64_t>(h) * p.rows + row0 + r) * p.dv + c * 8) : zero;
-        vs[i] = there ? TK * p.dv * 2 : 0;
-    }
+    const uint8_t* kb_n = p.k + 2 * (static_cast<int64_t>(h) * p.rows + row0) * p.dn;
+    const uint8_t* kb_r = p.pe + 2 * row0 * p.dr;
+    const uint8_t* kb_v = p.v + 2 * (static_cast<int64_t>(h) * p.rows + row0) * p.dv;
     auto stage = [&](int t, uint32_t at) __attribute__((always_inline)) {
-        const bool cut = (t + 1) * TK > len;  // rows past the sequence are staged as zeros
-        const uint32_t to = smem_at + at + w * kK * 1024, tv = smem_at + at + kVAt + w * kV * 1024;
+        const uint32_t to = smem_at + at;
+        const uint32_t to_n = to + w * KN::kLoads * 1024, to_r = to + kRAt + w * KR::kLoads * 1024,
+                       to_v = to + kVAt + w * VR::kLoads * 1024;
+        if ((t + 1) * TK <= len && !padded) {
 #pragma unroll
-        for (int i = 0; i < kK; ++i) {
-            const uint8_t* src = kp[i];
-            if (cut && t * TK + static_cast<int>(kr[i]) >= len) src = zero;
-            load_lds(src, to + i * 1024);
-            kp[i] += ks[i];
-        }
+            for (int i = 0; i < KN::kLoads; ++i) load_lds(kb_n, off_n[i], to_n + i * 1024);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const uint8_t* src = vp[i];
-            if (cut && t * TK + v_row + i * (64 / NV) >= len) src = zero;
-            load_lds(src, tv + i * 1024);
-            vp[i] += vs[i];
+            for (int i = 0; i < KR::kLoads; ++i) load_lds(kb_r, off_r[i], to_r + i * 1024);
+#pragma unroll
+            for (int i = 0; i < VR::kLoads; ++i) load_lds(kb_v, off_v[i], to_v + i * 1024);
+        } else {  // rows past the sequence are staged as zeros
+            const int left = len - t * TK;
+#pragma unroll
+            for (int i = 0; i < KN::kLoads; ++i)
+                if (!(pad >> i & 1)) load_lds(row_n(i) < left ? kb_n + off_n[i] : zero, to_n + i * 1024);
+#pragma unroll
+            for (int i = 0; i < KR::kLoads; ++i)
+                if (!(pad >> (8 + i) & 1)) load_lds(row_r(i) < left ? kb_r + off_r[i] : zero, to_r + i * 1024);
+#pragma unroll
+            for (int i = 0; i < VR::kLoads; ++i)
+                if (!(pad >> (16 + i) & 1)) load_lds(row_v(i) < left ? kb_v + off_v[i] : zero, to_v + i * 1024);
         }
+        kb_n += 2 * TK * p.dn;
+        kb_r += 2 * TK * p.dr;
+        kb_v += 2 * TK * p.dv;
     };
     // lane j: whether row j of tile t exists
     auto there = [&](int t) {
         const int r = t * TK + lane;
         return r < len ? p.there[row0 + r] : 0;
     };
-    uint32_t k_rd[KR], v_rd[ND];
+    // operands: step s of a key's first part is at rd[s % kAddr], s / kAddr times 32 kAddr bytes on
+    uint32_t n_rd[KN::kAddr], r_rd[KR::kAddr], v_rd[ND];
 #pragma unroll
-    for (int s = 0; s < KR; ++s) k_rd[s] = smem_at + col * kKB + (((2 * s + hh) ^ k_swizzle(col)) << 4);
+    for (int s = 0; s < KN::kAddr; ++s)
+        n_rd[s] = smem_at + col * KN::kPitch + (((2 * s + hh) ^ row_swizzle<KN::kPitch>(col)) << 4);
+#pragma unroll
+    for (int s = 0; s < KR::kAddr; ++s)
+        r_rd[s] = smem_at + kRAt + col * KR::kPitch + (((2 * s + hh) ^ row_swizzle<KR::kPitch>(col)) << 4);
     {
         const int vrow = 4 * hh + ((lane & 15) >> 2);
         const int c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt)
-            v_rd[dt] = smem_at + kVAt + vrow * kVB + (((4 * dt + c) ^ v_swizzle(vrow)) << 4) + (lane & 1) * 8;
+            v_rd[dt] = smem_at + kVAt + vrow * VR::kPitch + (((4 * dt + c) ^ v_swizzle(vrow)) << 4) + (lane & 1) * 8;
     }
     v8s q[NQ];
     {
@@ -486,6 +516,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
         for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
     const float scale2 = p.scale2;
     const bool odd = *p.odd != 0;
+    if (padded) {
+        for (int i = tid; i < 2 * kStage / 16; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
     int here = 0, next = 0;
     if (T > 0) {
         here = there(0);
@@ -516,14 +550,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
 #pragma unroll 1
             for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
-                for (int i = pass ? w : 0; i < TK * NV / 64; i += pass ? kWaves : 1) {
+                for (int i = pass ? w : 0; i < VR::kLoads * kWaves; i += pass ? kWaves : 1) {
                     v8s* const e = reinterpret_cast<v8s*>(smem + at + kVAt + i * 1024 + lane * 16);
                     const uint4 u = __builtin_bit_cast(uint4, *e);
-                    if (nonfinite2<kDTypeF16>(u.x) || nonfinite2<kDTypeF16>(u.y) || nonfinite2<kDTypeF16>(u.z) || nonfinite2<kDTypeF16>(u.w)) {
+                    if (nonfinite2<kDTypeF16>(u.x) || nonfinite2<kDTypeF16>(u.y) || nonfinite2<kDTypeF16>(u.z) ||
+                        nonfinite2<kDTypeF16>(u.w)) {
                         if (pass)
                             *e = v8s{0, 0, 0, 0, 0, 0, 0, 0};
                         else
-                            rows |= 1ull << ((i * 64 + lane) / NV);
+                            rows |= 1ull << ((i * 64 + lane) / VR::kChunks);
                     }
                 }
                 __syncthreads();
@@ -533,15 +568,51 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
         }
         if (kb <= high) {
             v16f x[2];
-            float top = -INFINITY;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
+            for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[ks][i] = 0.f;
+            // four steps' operands at a time, those of the next two parts on their way meanwhile
+            constexpr int kPart = 4, kParts = 2 * NQ / kPart;
+            static_assert(kPart * kParts == 2 * NQ, "steps");
+            v8s kf[3][kPart];
+            auto fetch = [&](int part) __attribute__((always_inline)) {
 #pragma unroll
-                for (int s = 0; s < NQ; ++s)
-                    x[ks] = mfma<DT>(lds_read(k_rd[s % KR] + at + ks * 32 * kKB + s / KR * (KR * 32)), q[s], x[ks]);
+                for (int j = 0; j < kPart; ++j) {
+                    const int ks = (part * kPart + j) / NQ, s = (part * kPart + j) % NQ;
+                    kf[part % 3][j] =
+                        s < SN ? lds_read(n_rd[s % KN::kAddr] + at + ks * 32 * KN::kPitch + s / KN::kAddr * (32 * KN::kAddr))
+                               : lds_read(r_rd[(s - SN) % KR::kAddr] + at + ks * 32 * KR::kPitch +
+                                          (s - SN) / KR::kAddr * (32 * KR::kAddr));
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(0);
+            fetch(1);
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+                if (part + 2 < kParts) fetch(part + 2);
+#pragma unroll
+                for (int j = 0; j < kPart; ++j) {
+                    const int ks = (part * kPart + j) / NQ, s = (part * kPart + j) % NQ;
+                    x[ks] = mfma<DT>(kf[part % 3][j], q[s], x[ks]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
+            // values of 16 keys, those of the next 16 on their way meanwhile
+            v8s vf[2][ND];
+            auto values = [&](int step) __attribute__((always_inline)) {
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) {
+                    const uint32_t a = v_rd[dt] + at + step * 16 * VR::kPitch;
+                    vf[step & 1][dt] =
+                        __builtin_shufflevector(lds_read_tr(a), lds_read_tr(a + 8 * VR::kPitch), 0, 1, 2, 3, 4, 5, 6, 7);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            values(0);
+            float top = -INFINITY;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 if (kb + TK - 1 > low || okm != ~0ull) {
@@ -570,26 +641,19 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
             }
             const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
+            for (int step = 0; step < 4; ++step) {
+                const int ks = step >> 1, t2 = step & 1;
+                if (step + 1 < 4) values(step + 1);
+                float y[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    x[ks][i] = __builtin_amdgcn_exp2f(less(scaled(x[ks][i], scale2), ref));
-                    l += x[ks][i];
+                for (int i = 0; i < 8; ++i) {
+                    y[i] = __builtin_amdgcn_exp2f(less(scaled(x[ks][8 * t2 + i], scale2), ref));
+                    l += y[i];
                 }
+                const v4s lo = pack4<kDTypeF16>(y[0], y[1], y[2], y[3]), hi = pack4<kDTypeF16>(y[4], y[5], y[6], y[7]);
+                const v8s pf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-                for (int t2 = 0; t2 < 2; ++t2) {
-                    const v4s lo = pack4<kDTypeF16>(x[ks][8 * t2], x[ks][8 * t2 + 1], x[ks][8 * t2 + 2], x[ks][8 * t2 + 3]);
-                    const v4s hi =
-                        pack4<kDTypeF16>(x[ks][8 * t2 + 4], x[ks][8 * t2 + 5], x[ks][8 * t2 + 6], x[ks][8 * t2 + 7]);
-                    const v8s pf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-                    for (int dt = 0; dt < ND; ++dt) {
-                        const uint32_t a = v_rd[dt] + at + (ks * 32 + t2 * 16) * kVB;
-                        const v8s vf =
-                            __builtin_shufflevector(lds_read_tr(a), lds_read_tr(a + 8 * kVB), 0, 1, 2, 3, 4, 5, 6, 7);
-                        o[dt] = mfma<kDTypeF16>(vf, pf, o[dt]);
-                    }
-                }
+                for (int dt = 0; dt < ND; ++dt) o[dt] = mfma<kDTypeF16>(vf[step & 1][dt], pf, o[dt]);
             }
         }
         at = kStage - at;
