@@ -1072,7 +1072,7 @@ int plan_prompt(const sv_latent_prompt* a, PromptPlan& t) {
     const size_t rows = static_cast<size_t>(lines) * 128;
     t.odd = align256((static_cast<size_t>(a->B) + 1) * 2 * sizeof(int64_t));
     t.most = t.odd + 256;
-    t.there = align256(t.most + static_cast<size_t>(a->heads) * sizeof(uint32_t));
+    t.there = align256(t.most + static_cast<size_t>(a->heads) * sv::kMostStride * sizeof(uint32_t));
     t.k = align256(t.there + rows * sizeof(int32_t));
     t.v = align256(t.k + static_cast<size_t>(a->heads) * a->rows * a->dim_k * 2);
     t.pe = align256(t.v + static_cast<size_t>(a->heads) * a->rows * a->dim_v * 2);

@@ -28,7 +28,7 @@ namespace sv {
 namespace {
 
 constexpr uint32_t kLowest = 0x007FFFFFu;  // order key of -inf: such ids are no candidates
-constexpr int kListed = 1024;              // candidates a workgroup ranks at most in one go
+constexpr int kListed = 1024;              // candidates a chunk's workgroup ranks at most in one go
 
 // Relative error of a chunk's sum: the exponential's argument is taken exactly and
 // split into its integer and a fraction of two roundings of 2^-25, 2^f has an
@@ -177,6 +177,7 @@ __global__ __launch_bounds__(kThreads) void k_beam_stats(BeamParams p) {
             __syncthreads();
         }
     }
+    if (tid >= listed && tid < p.W) out[tid] = 0;  // no candidate
     if (tid == 0) {
         const double all = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
         p.rec[static_cast<int64_t>(r) * p.chunks + chunk] =
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(kThreads) void k_beam_stats(BeamParams p) {
     }
 }
 
-constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
+constexpr int kSelThreads = 512, kSelWaves = kSelThreads / 64;
 
 __device__ __forceinline__ uint64_t score_key(double s) {
     const uint64_t u = __double_as_longlong(s + 0.0);
@@ -208,13 +209,23 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
     __shared__ double s_log[kMaxBeams];   // logarithm of the sum relative to the largest; NaN: the beam gives nothing
     __shared__ float s_top[kMaxBeams];
     __shared__ double s_tau[kSelWaves], s_part[kSelWaves];
-    __shared__ Cand s_list[kListed], s_best[kSelWaves];
+    __shared__ Cand s_list[kSelThreads], s_best[kSelWaves];
     __shared__ int s_n, s_near;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, b = blockIdx.x;
     const int W = p.W, per_row = p.chunks * W;
     const float* const scores = p.scores + b * W;
     const int32_t* const done = p.finished ? p.finished + b * W : nullptr;
     const double nan = __builtin_nan("");
+    // up to kKept of the lists' entries a thread, on their way while the sums are joined
+    constexpr int kKept = 8;
+    const int lists = W * per_row, total = lists + (done ? W : 0);
+    const uint64_t* const list = p.list + static_cast<int64_t>(b) * W * per_row;
+    uint64_t entry[kKept];
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int c = tid + k * kSelThreads;
+        entry[k] = c < lists ? list[c] : 0;
+    }
     for (int i = w; i < W; i += kSelWaves) {
         double log_sum = nan;
         float top = -SV_INF;
@@ -239,35 +250,37 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
     }
     __syncthreads();
 
-    // candidate c of the lists, and behind them one for every finished beam
-    const int lists = W * per_row, total = lists + (done ? W : 0);
-    auto candidate = [&](int c) {
+    // candidate c of the lists, and behind them one for every finished beam.  (What a row that is not
+    // asked for has in its lists is not looked at: it may be left from another call.)
+    auto candidate = [&](int c, uint64_t e) {
         Cand y{nan, 0.0, ~0u};
         if (c >= lists) {
             const int i = c - lists;
-            if (done[i] && scores[i] > -SV_INF && scores[i] < SV_INF)
+            if (c < total && done[i] && scores[i] > -SV_INF && scores[i] < SV_INF)
                 y = Cand{static_cast<double>(scores[i]), 0.0, static_cast<uint32_t>(i) * p.V + p.end};
             return y;
         }
-        const int i = c / per_row, at = c - i * per_row, chunk = at / W;
-        if (s_log[i] != s_log[i]) return y;
-        const int64_t place = static_cast<int64_t>(b * W + i) * p.chunks + chunk;
-        if (at - chunk * W >= p.rec[place].n) return y;
-        const uint64_t e = p.list[place * W + at - chunk * W];
+        const int i = c / per_row;
+        if (s_log[i] != s_log[i] || e == 0) return y;
         y.flat = static_cast<uint32_t>(i) * p.V + ~static_cast<uint32_t>(e);
         y.d = static_cast<double>(key_value(static_cast<uint32_t>(e >> 32))) - s_top[i];
         y.s = scores[i] + (y.d - s_log[i]);
         return y;
+    };
+    // all of the thread's candidates: those at hand, then the others
+    auto each = [&](auto&& use) {
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) use(candidate(tid + k * kSelThreads, entry[k]));
+        for (int c = tid + kKept * kSelThreads; c < total; c += kSelThreads) use(candidate(c, c < lists ? list[c] : 0));
     };
 
     for (int round = 0;; ++round) {  // the second with float64 sums
         if (tid == 0) s_n = s_near = 0;
         // a bound that W candidates of one wave's lanes reach
         double best = -__builtin_huge_val();
-        for (int c = tid; c < total; c += kSelThreads) {
-            const double s = candidate(c).s;
-            if (s > best) best = s;
-        }
+        each([&](const Cand& y) {
+            if (y.s > best) best = y.s;
+        });
         {
             uint64_t x = score_key(best);
 #pragma unroll
@@ -285,13 +298,12 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
         double tau = s_tau[0];
         for (int i = 1; i < kSelWaves; ++i) tau = fmax(tau, s_tau[i]);
         if (round == 0) tau -= kBand;
-        for (int c = tid; c < total; c += kSelThreads) {
-            const Cand y = candidate(c);
+        each([&](const Cand& y) {
             if (y.s >= tau) {
                 const int at = atomicAdd(&s_n, 1);
-                if (at < kListed) s_list[at] = y;
+                if (at < kSelThreads) s_list[at] = y;
             }
-        }
+        });
         __syncthreads();
         const int n = s_n;
         auto put = [&](int rank, const Cand& y) {
@@ -302,7 +314,7 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
             p.out_finished[at] = (done && done[i]) || v == p.end;
         };
         bool again = round == 0;
-        if (n <= kListed) {
+        if (n <= kSelThreads) {
             Cand me{};
             int rank = W;
             if (tid < n) {
@@ -332,10 +344,9 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
             Cand last{};
             for (int i = 0; i < W; ++i) {
                 Cand top{nan, 0.0, ~0u};
-                for (int c = tid; c < total; c += kSelThreads) {
-                    const Cand y = candidate(c);
+                each([&](const Cand& y) {
                     if (y.s == y.s && (i == 0 || before(last, y)) && (top.s != top.s || before(y, top))) top = y;
-                }
+                });
                 for (int o = 32; o; o >>= 1) {
                     const Cand y{__shfl_xor(top.s, o), __shfl_xor(top.d, o), __shfl_xor(top.flat, o)};
                     if (y.s == y.s && (top.s != top.s || before(y, top))) top = y;

@@ -65,10 +65,11 @@ struct PromptParams {
     // workspace
     int64_t* plan;                    // [B + 1] first row of the line, [B + 1] first query tile
     int32_t* odd;                     // 1: an infinity or NaN among the values
-    uint32_t* most;                   // [H] bits of the largest value's size
+    uint32_t* most;                   // [H, kMostStride] bits of the largest value's size
     int32_t* there;                   // [rows rounded up] 1: the row's page exists
     uint8_t *k, *v, *pe;              // [H, rows, dn], [H, rows, dv], [rows, dr]
 };
+constexpr int kMostStride = 16;       // words: a line of the L2 a head
 constexpr int kPromptRows = 128;      // queries of a tile
 hipError_t launch_prompt_plan(const PromptParams& p, hipStream_t st, const LaunchEvents& ev);
 hipError_t launch_prompt_expand(const PromptParams& p, int dtype, bool again, hipStream_t st, const LaunchEvents& ev);

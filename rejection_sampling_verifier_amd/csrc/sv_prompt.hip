@@ -233,7 +233,7 @@ __global__ __launch_bounds__(1024) void k_prompt_plan(PromptParams p) {
         p.plan[2 * p.B + 1] = tile0;
         *p.odd = 0;
     }
-    for (int h = tid; h < p.H; h += 1024) p.most[h] = 0;
+    for (int h = tid; h < p.H; h += 1024) p.most[h * kMostStride] = 0;
 }
 
 // Keys and values of 128 rows of the line: a product with the rows gathered from
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
     if (r0 >= total) return;
     if (AGAIN) {
         bool any = false;
-        for (int h = mt * 128 / p.dv; h <= min(mt * 128 + 127, mv - 1) / p.dv; ++h) any |= value_scale(p.most[h]) != 1.f;
+        for (int h = mt * 128 / p.dv; h <= min(mt * 128 + 127, mv - 1) / p.dv; ++h) any |= value_scale(p.most[h * kMostStride]) != 1.f;
         if (!any) return;
     }
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -318,10 +318,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
     bool odd = false;
     auto tell = [&] {
         for (int s = 32; s; s >>= 1) most = max(most, static_cast<uint32_t>(__shfl_xor(most, s)));
-        // most waves find a larger one there: 4000 atomics on one line cost 20 us
+        // most waves find a larger one there: 4000 atomics on one line cost 20 us (hence a line a head, too)
         if (lane == 0 && of >= 0 &&
-            most > __hip_atomic_load(p.most + of, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
-            atomicMax(p.most + of, most);
+            most > __hip_atomic_load(p.most + of * kMostStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+            atomicMax(p.most + of * kMostStride, most);
         most = 0;
     };
 #pragma unroll
@@ -334,7 +334,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
                 if (of >= 0) tell();
                 of = h;
             }
-            const float scale = AGAIN ? value_scale(p.most[h]) : 1.f;
+            const float scale = AGAIN ? value_scale(p.most[h * kMostStride]) : 1.f;
 #pragma unroll
             for (int b = 0; b < L::BT; ++b) {
                 const int r = r0 + (wt * L::BT + b) * 32 + col;
@@ -659,7 +659,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
         at = kStage - at;
     }
     l = half_sum(l);
-    const float inv = l == 0.f ? 0.f : 1.f / l / value_scale(p.most[h]);  // a query that sees nothing: zero
+    const float inv = l == 0.f ? 0.f : 1.f / l / value_scale(p.most[h * kMostStride]);  // a query that sees nothing: zero
     if (!in) return;
 #pragma unroll
     for (int dt = 0; dt < ND; ++dt)
