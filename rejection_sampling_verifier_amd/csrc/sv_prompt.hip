@@ -82,17 +82,25 @@ __device__ __forceinline__ void product_tile(uint32_t smem_at, const uint8_t* co
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (s + 1 < S) stage(s + 1, L::kStage - at);
+        // the next step's operands are on their way while a step's are multiplied
+        v8s a[2][L::BM], b[2][L::BT];
+        auto fetch = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < L::BM; ++i) a[k & 1][i] = lds_read(a_rd[k] + at + i * 4096);
+#pragma unroll
+            for (int i = 0; i < L::BT; ++i) b[k & 1][i] = lds_read(b_rd[k] + at + i * 4096);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            v8s a[L::BM], b[L::BT];
-#pragma unroll
-            for (int i = 0; i < L::BM; ++i) a[i] = lds_read(a_rd[k] + at + i * 4096);
-#pragma unroll
-            for (int i = 0; i < L::BT; ++i) b[i] = lds_read(b_rd[k] + at + i * 4096);
+            if (k < 3) fetch(k + 1);
 #pragma unroll
             for (int i = 0; i < L::BM; ++i)
 #pragma unroll
-                for (int j = 0; j < L::BT; ++j) acc[i][j] = mfma<DT>(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < L::BT; ++j) acc[i][j] = mfma<DT>(a[k & 1][i], b[k & 1][j], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
         at = L::kStage - at;
     }
@@ -249,7 +257,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
     const int tk = AGAIN ? 0 : (mk + 127) / 128, tv = (mv + 127) / 128, tr = (p.rows + 127) / 128;
     const int64_t task = task_of(static_cast<int64_t>(tk + tv) * tr);
     if (task < 0) return;
-    const int mt = static_cast<int>(task / tr), r0 = static_cast<int>(task - static_cast<int64_t>(mt) * tr) * 128;
+    // eight row tiles against all outputs, then the next eight: the workgroups an XCD has at a time
+    // share about eight tiles of rows and eight of weights, which its L2 holds
+    const int rg = static_cast<int>(task / (8 * (tk + tv))), in_rg = static_cast<int>(task - rg * 8ll * (tk + tv));
+    const int wide = min(8, tr - 8 * rg), mt = in_rg / wide, r0 = (8 * rg + in_rg - mt * wide) * 128;
     const int64_t total = p.plan[p.B];
     if (r0 >= total) return;
     if (AGAIN) {
