@@ -1126,6 +1126,7 @@ int latent_prompt_impl(const sv_latent_prompt* a, void* stream_v) {
     p.ps_shift = __builtin_ctz(static_cast<unsigned>(a->page_size));
     p.scale2 = score_scale(a->scale);
     p.flip = a->scale < 0.f ? 1 : 0;
+    p.cus = device_cus();
     uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
     p.plan = reinterpret_cast<int64_t*>(ws);
     p.odd = reinterpret_cast<int32_t*>(ws + t.odd);

@@ -62,9 +62,10 @@ struct PromptParams {
     int pages, width, ps_shift;
     float scale2;
     int flip;
+    int cus;                          // of the device
     // workspace
     int64_t* plan;                    // [B + 1] first row of the line, [B + 1] first query tile
-    int32_t* odd;                     // 1: an infinity or NaN among the values
+    int32_t* odd;                     // bit 0: an infinity or NaN among the values; 1: a row whose page does not exist
     uint32_t* most;                   // [H, kMostStride] bits of the largest value's size
     int32_t* there;                   // [rows rounded up] 1: the row's page exists
     uint8_t *k, *v, *pe;              // [H, rows, dn], [H, rows, dv], [rows, dr]

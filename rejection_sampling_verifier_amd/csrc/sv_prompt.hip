@@ -300,7 +300,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
             for (int c = lane & 7; c < p.dr / 8; c += 8)
                 *reinterpret_cast<uint4*>(p.pe + (static_cast<int64_t>(r0 + r) * p.dr + 8 * c) * 2) =
                     x ? *reinterpret_cast<const uint4*>(x + 2 * p.R + 16 * c) : make_uint4(0, 0, 0, 0);
-            if ((lane & 7) == 0) p.there[r0 + r] = x != nullptr;
+            if ((lane & 7) == 0) {
+                p.there[r0 + r] = x != nullptr;
+                if (!x) atomicOr(p.odd, 2);
+            }
         }
     }
     v16f acc[L::BM][L::BT];
@@ -366,7 +369,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
         }
     if (!AGAIN) {
         tell();
-        if (odd) *p.odd = 1;
+        if (odd) atomicOr(p.odd, 1);
     }
 }
 
@@ -386,10 +389,11 @@ struct Rows {
     static_assert(kPitch == 256 || kPitch == 192 || kPitch == 128 || kPitch == 64, "layout");
 };
 
-// 128 queries of one head (32 a wave) against 64 keys at a time, double-buffered:
-// two workgroups fill a CU's LDS and take turns at its matrix units.  A tile's
-// operands are read from LDS some steps before they are needed.
-template <int DT, int DN, int DR, int DV>
+// 128 queries of one head (32 a wave) against 64 keys at a time, in a ring of RING
+// tiles: with two, two workgroups fill a CU's LDS and take turns at its matrix
+// units; where there are not that many, each has more tiles on their way.  A
+// tile's operands are read from LDS some steps before they are needed.
+template <int DT, int DN, int DR, int DV, int RING>
 __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
     using KN = Rows<DN>;
     using KR = Rows<DR>;
@@ -431,9 +435,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
     const int T = last < 0 ? 0 : last / TK + 1;
 
     // Staging: chunk e = 64 i + lane of a part of the tile is chunk e % kChunks of row e / kChunks; `off` is
-    // where it comes from, relative to the tile's first row.  Dimensions past the head's are zeros in LDS
-    // that nothing overwrites.
+    // where it comes from, relative to the tile's first row.  Dimensions past the head's are zeros.
     uint32_t off_n[KN::kLoads], off_r[KR::kLoads], off_v[VR::kLoads], pad = 0;
+    constexpr int kPer = KN::kLoads + KR::kLoads + VR::kLoads;
     const bool padded = p.dn < DN || p.dr < DR || p.dv < DV;
     auto row_n = [&](int i) { return ((w * KN::kLoads + i) * 64 + lane) / KN::kChunks; };
     auto row_r = [&](int i) { return ((w * KR::kLoads + i) * 64 + lane) / KR::kChunks; };
@@ -471,17 +475,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
             for (int i = 0; i < KR::kLoads; ++i) load_lds(kb_r, off_r[i], to_r + i * 1024);
 #pragma unroll
             for (int i = 0; i < VR::kLoads; ++i) load_lds(kb_v, off_v[i], to_v + i * 1024);
-        } else {  // rows past the sequence are staged as zeros
+        } else {  // rows past the sequence are zeros, too
             const int left = len - t * TK;
 #pragma unroll
             for (int i = 0; i < KN::kLoads; ++i)
-                if (!(pad >> i & 1)) load_lds(row_n(i) < left ? kb_n + off_n[i] : zero, to_n + i * 1024);
+                load_lds(!(pad >> i & 1) && row_n(i) < left ? kb_n + off_n[i] : zero, to_n + i * 1024);
 #pragma unroll
             for (int i = 0; i < KR::kLoads; ++i)
-                if (!(pad >> (8 + i) & 1)) load_lds(row_r(i) < left ? kb_r + off_r[i] : zero, to_r + i * 1024);
+                load_lds(!(pad >> (8 + i) & 1) && row_r(i) < left ? kb_r + off_r[i] : zero, to_r + i * 1024);
 #pragma unroll
             for (int i = 0; i < VR::kLoads; ++i)
-                if (!(pad >> (16 + i) & 1)) load_lds(row_v(i) < left ? kb_v + off_v[i] : zero, to_v + i * 1024);
+                load_lds(!(pad >> (16 + i) & 1) && row_v(i) < left ? kb_v + off_v[i] : zero, to_v + i * 1024);
         }
         kb_n += 2 * TK * p.dn;
         kb_r += 2 * TK * p.dr;
@@ -526,31 +530,24 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
     const float scale2 = p.scale2;
-    const bool odd = *p.odd != 0;
-    if (padded) {
-        for (int i = tid; i < 2 * kStage / 16; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-    }
-    int here = 0, next = 0;
-    if (T > 0) {
-        here = there(0);
-        if (T > 1) next = there(1);
-        stage(0, 0);
-    }
-    uint32_t at = 0;
+    const bool odd = *p.odd & 1, gaps = *p.odd & 2;
+    constexpr int kAhead = RING - 1;
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t)
+        if (t < T) stage(t, t * kStage);
+    uint32_t at = 0, to = kAhead * kStage;
 #pragma unroll 1
     for (int t = 0; t < T; ++t) {
-        // this wave's loads of tile t have landed; with the barrier everyone's, and everyone
-        // has read the other stage
-        wait_vm<0>();
+        // this wave's loads of tile t have landed (later tiles' stay under way); with the barrier
+        // everyone's, and everyone is done with the tile before it
+        if (t + kAhead <= T)
+            wait_vm<(kAhead - 1) * kPer>();
+        else
+            wait_vm<0>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        const uint64_t okm = __ballot(here != 0);
-        here = next;
-        if (t + 1 < T) {
-            stage(t + 1, kStage - at);
-            if (t + 2 < T) next = there(t + 2);
-        }
+        const uint64_t okm = gaps ? __ballot(there(t) != 0) : ~0ull;
+        if (t + kAhead < T) stage(t + kAhead, to);
         const int kb = t * TK;
         uint64_t nf = 0;
         if (odd && kb + TK - 1 > i0 + shift) {
@@ -667,7 +664,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
                 for (int dt = 0; dt < ND; ++dt) o[dt] = mfma<kDTypeF16>(vf[step & 1][dt], pf, o[dt]);
             }
         }
-        at = kStage - at;
+        at = at == kAhead * kStage ? 0 : at + kStage;
+        to = to == kAhead * kStage ? 0 : to + kStage;
     }
     l = half_sum(l);
     const float inv = l == 0.f ? 0.f : 1.f / l / value_scale(p.most[h * kMostStride]);  // a query that sees nothing: zero
@@ -700,15 +698,22 @@ hipError_t expand_one(const PromptParams& p, hipStream_t st, const LaunchEvents&
     return hipGetLastError();
 }
 
-template <int DT, int DN, int DR, int DV>
-hipError_t prompt_one(const PromptParams& p, hipStream_t st, const LaunchEvents& ev) {
-    constexpr int lds = 2 * 64 * (DN + DR + DV) * 2;
-    const hipError_t e = allow_lds(reinterpret_cast<const void*>(k_prompt_attn<DT, DN, DR, DV>), lds);
+template <int DT, int DN, int DR, int DV, int RING>
+hipError_t prompt_ring(const PromptParams& p, int64_t tasks, hipStream_t st, const LaunchEvents& ev) {
+    constexpr int lds = RING * 64 * (DN + DR + DV) * 2;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(k_prompt_attn<DT, DN, DR, DV, RING>), lds);
     if (e != hipSuccess) return e;
-    const int64_t tiles = p.T / kPromptRows + (p.B < p.T ? p.B : p.T);  // at most
-    hipExtLaunchKernelGGL((k_prompt_attn<DT, DN, DR, DV>), dim3(static_cast<unsigned>(grid_of(tiles * p.H))),
+    hipExtLaunchKernelGGL((k_prompt_attn<DT, DN, DR, DV, RING>), dim3(static_cast<unsigned>(grid_of(tasks))),
                           dim3(kThreads), lds, st, ev.start, ev.stop, 0, p);
     return hipGetLastError();
+}
+
+template <int DT, int DN, int DR, int DV>
+hipError_t prompt_one(const PromptParams& p, hipStream_t st, const LaunchEvents& ev) {
+    const int64_t tasks = (p.T / kPromptRows + static_cast<int64_t>(p.B < p.T ? p.B : p.T)) * p.H;  // at most
+    constexpr int kDeep = 64 * (DN + DR + DV) * 2 * 4 < (160 << 10) ? 4 : 3;
+    return tasks <= p.cus ? prompt_ring<DT, DN, DR, DV, kDeep>(p, tasks, st, ev)
+                          : prompt_ring<DT, DN, DR, DV, 2>(p, tasks, st, ev);
 }
 
 template <int DT>
