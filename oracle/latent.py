@@ -84,8 +84,8 @@ def prompt(q, cache, table, lens, q_start, w_k, w_v, scale=None):
                 if n == 0:
                     out[t, h] = 0.0
                     continue
-                x = scale * (k[:n] @ q[t, h])
                 with np.errstate(invalid="ignore"):
+                    x = scale * (k[:n] @ q[t, h])
                     w = np.exp(x - x.max())
                     w /= w.sum()
                 out[t, h], spread[t, h], loose[t, h] = w @ v[:n], w @ np.abs(v[:n]), w @ v_slack[:n]

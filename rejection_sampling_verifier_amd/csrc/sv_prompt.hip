@@ -421,7 +421,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
     const int mine = i0 + w * 32 + col;  // the lane's query
     const bool in = mine < qs.n;
     uint8_t* const dst = p.out + 16 * ((qs.first + mine) * p.os[0] + h * p.os[1]);
-    if (row0 + len > p.rows) {  // the line is too short for this sequence
+    if (len > 0 && row0 + len > p.rows) {  // the line is too short for this sequence
         if (in)
             for (int d = 4 * hh; d < p.dv; d += 8)
                 *reinterpret_cast<v4s*>(dst + 2 * d) = pack4<DT>(NAN, NAN, NAN, NAN);
