@@ -680,8 +680,10 @@ int spec_head_product(const sv_head_product* args, void* stream);
  * The rows q_start[b] .. q_start[b + 1] of q are the last tokens of sequence b, at
  * positions len[b] - n .. len[b] - 1; their rows, and those of a prefix before
  * them, are in the cache.  Keys are rounded to the input type; values and weights
- * to float16's 11 bits in either type, the values times a power of two per head
- * (chosen by its largest one over the line).  Statistics are float32.
+ * to float16's 11 bits in either type, the values times a power of two per head,
+ * chosen by its largest finite one over all sequences' rows (a value's error is
+ * half a step, or 2^-21 of that largest one where this is more).  Statistics are
+ * float32.
  *
  * dtype          SV_BF16 or SV_F16, of all tensors.
  * T              query tokens, 0 (nothing is done) to 2^24; B <= 65536; heads <= 1024.

@@ -283,6 +283,22 @@ def test_later_rows_do_not_reach_earlier_tokens(bad, p):
     assert out[:p].isfinite().all() and not out[p:150].isfinite().any() and out[150:].isfinite().all()
 
 
+@pytest.mark.parametrize("row", [0, 5, 60, 70])
+def test_value_beyond_float32_of_one_row(row):
+    """A row whose keys are finite and one of whose values is not: every token that
+    sees it, wherever it lies in a tile of queries."""
+    s = pro.make((200,), (200,), H=2, dims=(64, 32, 64, 128), poison=False)
+    s["cache"][..., 7] = 0.0
+    s["w_k"][:, :, 7] = 0.0
+    s["w_v"][:, :, 7] = 0.0
+    s["w_v"][1, 3, 7] = 3e38
+    want = pro.call(s)
+    at(s, 0, row)[7] = 3e38
+    out = pro.call(s)
+    assert same(out[:, 0], want[:, 0]) and same(out[:row], want[:row])
+    assert not out[row:, 1, 3].isfinite().any()
+
+
 def test_missing_pages_of_prompts():
     s = pro.make((200, 90, 40), (200, 30, 40), H=2, dims=(64, 32, 64, 128), extra=2)
     pages = s["cache"].shape[0]
