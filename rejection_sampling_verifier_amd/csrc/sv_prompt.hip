@@ -393,8 +393,8 @@ struct Rows {
 // tiles: with two, two workgroups fill a CU's LDS and take turns at its matrix
 // units; where there are not that many, each has more tiles on their way.  A
 // tile's operands are read from LDS some steps before they are needed.
-template <int DT, int DN, int DR, int DV, int RING>
-__global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
+template <int DT, int DN, int DR, int DV, int RING, int GROUPS>
+__global__ __launch_bounds__(GROUPS * kThreads, 2) void k_prompt_attn(PromptParams p) {
     using KN = Rows<DN>;
     using KR = Rows<DR>;
     using VR = Rows<DV>;
@@ -407,7 +407,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
     extern __shared__ __align__(16) uint8_t smem[];  // nothing beside it: two workgroups fill a CU
     const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) uint8_t*)smem));
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, w8 = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int w = w8 & 3, group = GROUPS > 1 ? w8 >> 2 : 0;
     const int hh = lane >> 5, col = lane & 31;
     const int64_t tiles = p.plan[2 * p.B + 1], task = task_of(tiles * p.H);
     if (task < 0) return;
@@ -422,7 +423,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
     const bool in = mine < qs.n;
     uint8_t* const dst = p.out + 16 * ((qs.first + mine) * p.os[0] + h * p.os[1]);
     if (len > 0 && row0 + len > p.rows) {  // the line is too short for this sequence
-        if (in)
+        if (in && !group)
             for (int d = 4 * hh; d < p.dv; d += 8)
                 *reinterpret_cast<v4s*>(dst + 2 * d) = pack4<DT>(NAN, NAN, NAN, NAN);
         return;
@@ -432,7 +433,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
     const int low = i0 + w * 32 + shift;  // first and last position of the wave
     const int high = i0 + w * 32 < qs.n ? min(i0 + w * 32 + 31, qs.n - 1) + shift : -1;
     const int last = min(i0 + kPromptRows, qs.n) - 1 + shift;  // of the workgroup
-    const int T = last < 0 ? 0 : last / TK + 1;
+    const int all = last < 0 ? 0 : last / TK + 1, steps = (all + GROUPS - 1) / GROUPS;
+    const int T = (all + GROUPS - 1 - group) / GROUPS;  // this group's tiles: group, group + GROUPS, ...
+    const uint32_t ring = group * RING * kStage;
 
     // Staging: chunk e = 64 i + lane of a part of the tile is chunk e % kChunks of row e / kChunks; `off` is
     // where it comes from, relative to the tile's first row.  Dimensions past the head's are zeros.
@@ -461,11 +464,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
         if (8 * c >= p.dv) pad |= 1u << (16 + i);
     }
     const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&kZero);
-    const uint8_t* kb_n = p.k + 2 * (static_cast<int64_t>(h) * p.rows + row0) * p.dn;
-    const uint8_t* kb_r = p.pe + 2 * row0 * p.dr;
-    const uint8_t* kb_v = p.v + 2 * (static_cast<int64_t>(h) * p.rows + row0) * p.dv;
-    auto stage = [&](int t, uint32_t at) __attribute__((always_inline)) {
-        const uint32_t to = smem_at + at;
+    const uint8_t* kb_n = p.k + 2 * (static_cast<int64_t>(h) * p.rows + row0 + group * TK) * p.dn;
+    const uint8_t* kb_r = p.pe + 2 * (row0 + group * TK) * p.dr;
+    const uint8_t* kb_v = p.v + 2 * (static_cast<int64_t>(h) * p.rows + row0 + group * TK) * p.dv;
+    auto stage = [&](int s, uint32_t at) __attribute__((always_inline)) {
+        const int t = s * GROUPS + group;
+        const uint32_t to = smem_at + ring + at;
         const uint32_t to_n = to + w * KN::kLoads * 1024, to_r = to + kRAt + w * KR::kLoads * 1024,
                        to_v = to + kVAt + w * VR::kLoads * 1024;
         if ((t + 1) * TK <= len && !padded) {
@@ -487,29 +491,29 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
             for (int i = 0; i < VR::kLoads; ++i)
                 load_lds(!(pad >> (16 + i) & 1) && row_v(i) < left ? kb_v + off_v[i] : zero, to_v + i * 1024);
         }
-        kb_n += 2 * TK * p.dn;
-        kb_r += 2 * TK * p.dr;
-        kb_v += 2 * TK * p.dv;
+        kb_n += GROUPS * 2 * TK * p.dn;
+        kb_r += GROUPS * 2 * TK * p.dr;
+        kb_v += GROUPS * 2 * TK * p.dv;
     };
-    // lane j: whether row j of tile t exists
-    auto there = [&](int t) {
-        const int r = t * TK + lane;
+    // lane j: whether row kb + j exists
+    auto there = [&](int kb) {
+        const int r = kb + lane;
         return r < len ? p.there[row0 + r] : 0;
     };
     // operands: step s of a key's first part is at rd[s % kAddr], s / kAddr times 32 kAddr bytes on
     uint32_t n_rd[KN::kAddr], r_rd[KR::kAddr], v_rd[ND];
 #pragma unroll
     for (int s = 0; s < KN::kAddr; ++s)
-        n_rd[s] = smem_at + col * KN::kPitch + (((2 * s + hh) ^ row_swizzle<KN::kPitch>(col)) << 4);
+        n_rd[s] = smem_at + ring + col * KN::kPitch + (((2 * s + hh) ^ row_swizzle<KN::kPitch>(col)) << 4);
 #pragma unroll
     for (int s = 0; s < KR::kAddr; ++s)
-        r_rd[s] = smem_at + kRAt + col * KR::kPitch + (((2 * s + hh) ^ row_swizzle<KR::kPitch>(col)) << 4);
+        r_rd[s] = smem_at + ring + kRAt + col * KR::kPitch + (((2 * s + hh) ^ row_swizzle<KR::kPitch>(col)) << 4);
     {
         const int vrow = 4 * hh + ((lane & 15) >> 2);
         const int c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt)
-            v_rd[dt] = smem_at + kVAt + vrow * VR::kPitch + (((4 * dt + c) ^ v_swizzle(vrow)) << 4) + (lane & 1) * 8;
+            v_rd[dt] = smem_at + ring + kVAt + vrow * VR::kPitch + (((4 * dt + c) ^ v_swizzle(vrow)) << 4) + (lane & 1) * 8;
     }
     v8s q[NQ];
     {
@@ -537,7 +541,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
         if (t < T) stage(t, t * kStage);
     uint32_t at = 0, to = kAhead * kStage;
 #pragma unroll 1
-    for (int t = 0; t < T; ++t) {
+    for (int t = 0; t < steps; ++t) {
         // this wave's loads of tile t have landed (later tiles' stay under way); with the barrier
         // everyone's, and everyone is done with the tile before it
         if (t + kAhead <= T)
@@ -546,11 +550,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
             wait_vm<0>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        const uint64_t okm = gaps ? __ballot(there(t) != 0) : ~0ull;
+        const int kb = (t * GROUPS + group) * TK;
+        const uint64_t okm = gaps ? __ballot(there(kb) != 0) : ~0ull;
         if (t + kAhead < T) stage(t + kAhead, to);
-        const int kb = t * TK;
         uint64_t nf = 0;
-        if (odd && kb + TK - 1 > i0 + shift) {
+        if (odd && ((t + 1) * GROUPS) * TK - 1 > i0 + shift) {
             // infinities or NaN are about, and some of the queries do not see all of the tile: these
             // values go out of it (0 times them would reach those queries), and who sees the row gets a
             // score of NaN.  Every wave looks at all rows; then each clears a part.
@@ -559,7 +563,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
             for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
                 for (int i = pass ? w : 0; i < VR::kLoads * kWaves; i += pass ? kWaves : 1) {
-                    v8s* const e = reinterpret_cast<v8s*>(smem + at + kVAt + i * 1024 + lane * 16);
+                    v8s* const e = reinterpret_cast<v8s*>(smem + ring + at + kVAt + i * 1024 + lane * 16);
                     const uint4 u = __builtin_bit_cast(uint4, *e);
                     if (nonfinite2<kDTypeF16>(u.x) || nonfinite2<kDTypeF16>(u.y) || nonfinite2<kDTypeF16>(u.z) ||
                         nonfinite2<kDTypeF16>(u.w)) {
@@ -667,6 +671,29 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_attn(PromptParams p) {
         at = at == kAhead * kStage ? 0 : at + kStage;
         to = to == kAhead * kStage ? 0 : to + kStage;
     }
+    if (GROUPS > 1) {
+        // the second group's sums through LDS, taken over by the first: 32 queries of each wave by
+        // DV values, the shift and the weights' sum
+        __syncthreads();
+        float* const part = reinterpret_cast<float*>(smem) + w * (16 * ND + 2) * 64 + lane;
+        if (group) {
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) part[(dt * 16 + i) * 64] = o[dt][i];
+            part[16 * ND * 64] = mx;
+            part[(16 * ND + 1) * 64] = l;
+        }
+        __syncthreads();
+        if (group) return;
+        const float other = part[16 * ND * 64], top = fmaxf(mx, other);
+        const float a = shift_of(mx, top), c = shift_of(other, top);
+        l = l * a + part[(16 * ND + 1) * 64] * c;
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[dt][i] = o[dt][i] * a + part[(dt * 16 + i) * 64] * c;
+    }
     l = half_sum(l);
     const float inv = l == 0.f ? 0.f : 1.f / l / value_scale(p.most[h * kMostStride]);  // a query that sees nothing: zero
     if (!in) return;
@@ -698,22 +725,23 @@ hipError_t expand_one(const PromptParams& p, hipStream_t st, const LaunchEvents&
     return hipGetLastError();
 }
 
-template <int DT, int DN, int DR, int DV, int RING>
+template <int DT, int DN, int DR, int DV, int RING, int GROUPS>
 hipError_t prompt_ring(const PromptParams& p, int64_t tasks, hipStream_t st, const LaunchEvents& ev) {
-    constexpr int lds = RING * 64 * (DN + DR + DV) * 2;
-    const hipError_t e = allow_lds(reinterpret_cast<const void*>(k_prompt_attn<DT, DN, DR, DV, RING>), lds);
+    constexpr int lds = GROUPS * RING * 64 * (DN + DR + DV) * 2;
+    static_assert(lds <= 160 << 10 && (GROUPS == 1 || lds >= kWaves * (DV / 2 + 2) * 64 * 4), "LDS");
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(k_prompt_attn<DT, DN, DR, DV, RING, GROUPS>), lds);
     if (e != hipSuccess) return e;
-    hipExtLaunchKernelGGL((k_prompt_attn<DT, DN, DR, DV, RING>), dim3(static_cast<unsigned>(grid_of(tasks))),
-                          dim3(kThreads), lds, st, ev.start, ev.stop, 0, p);
+    hipExtLaunchKernelGGL((k_prompt_attn<DT, DN, DR, DV, RING, GROUPS>), dim3(static_cast<unsigned>(grid_of(tasks))),
+                          dim3(GROUPS * kThreads), lds, st, ev.start, ev.stop, 0, p);
     return hipGetLastError();
 }
 
 template <int DT, int DN, int DR, int DV>
 hipError_t prompt_one(const PromptParams& p, hipStream_t st, const LaunchEvents& ev) {
     const int64_t tasks = (p.T / kPromptRows + static_cast<int64_t>(p.B < p.T ? p.B : p.T)) * p.H;  // at most
-    constexpr int kDeep = 64 * (DN + DR + DV) * 2 * 4 < (160 << 10) ? 4 : 3;
-    return tasks <= p.cus ? prompt_ring<DT, DN, DR, DV, kDeep>(p, tasks, st, ev)
-                          : prompt_ring<DT, DN, DR, DV, 2>(p, tasks, st, ev);
+    constexpr int kDeep = 2 * 3 * 64 * (DN + DR + DV) * 2 <= (160 << 10) ? 3 : 2;
+    return tasks <= p.cus ? prompt_ring<DT, DN, DR, DV, kDeep, 2>(p, tasks, st, ev)
+                          : prompt_ring<DT, DN, DR, DV, 2, 1>(p, tasks, st, ev);
 }
 
 template <int DT>
