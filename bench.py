@@ -883,6 +883,127 @@ def tree_bench(args, binding, torch, dev):
 
 
 # ---------------------------------------------------------------------------
+# --beams: a step of beam decoding with latent attention
+# ---------------------------------------------------------------------------
+BEAMS = dict(B=8, W=4, layers=2, heads=128, dim_k=128, dim_p=64, dim_v=128, latent=512, page=64, length=4096, prompt=1024)
+
+
+def beam_bench(args, binding, torch, dev):
+    """A step: rows reserved for every beam's token; in every layer queries into
+    the latent space, attention on the rows, results out of it, the new rows
+    written; then the selection, the fork of the pages and the histories.  Every
+    step starts from the same tables and lengths.  Beside it the attention of a
+    batch of prompts in one layer."""
+    import numpy as np
+
+    from rejection_sampling_verifier_amd import workloads
+
+    c = BEAMS
+    B, W, L, H, R, DP, DK, DV, ps, V = (c["B"], c["W"], c["layers"], c["heads"], c["latent"], c["dim_p"], c["dim_k"],
+                                        c["dim_v"], c["page"], workloads.V_LLAMA3)
+    n, C = B * W, R + DP
+    rng = np.random.default_rng(12)
+    gen = torch.Generator(device=dev).manual_seed(12)
+    print(f"[bench] generating the beam step: {B} requests of {W} beams, {L} layers", file=sys.stderr, flush=True)
+    lens_h = np.repeat(rng.integers(c["length"] // 2, c["length"] + 1, B), W).astype(np.int32)
+    blocks = -(-lens_h // ps)
+    width, pages = int(blocks.max()) + 2, int(blocks.sum()) + 3 * n
+    perm, at = rng.permutation(pages), 0
+    table_h = np.full((n, width), -1, np.int32)
+    for b in range(n):
+        table_h[b, :blocks[b]] = perm[at:at + blocks[b]]
+        at += blocks[b]
+
+    def rows(*s, by=1.0):
+        return (torch.randn(s, generator=gen, device=dev) * by).to(torch.bfloat16)
+
+    cache = rows(L, pages, ps, C)
+    q, latent, turned = rows(L, n, H, DK + DP), rows(L, n, R), rows(L, n, DP)
+    w_k, w_v = rows(L, H, DK, R, by=R ** -0.5), rows(L, H, DV, R, by=R ** -0.5)
+    w_in = w_k.transpose(2, 3).contiguous()
+    table, lens = (torch.from_numpy(a).to(dev) for a in (table_h, lens_h))
+    ones = torch.ones((n,), dtype=torch.int32, device=dev)
+    logits = rows(B, W, V, by=2.0)
+    scores = -torch.rand((B, W), generator=gen, device=dev).sort(-1)[0]
+    history = torch.zeros((n, c["length"]), dtype=torch.int32, device=dev)
+    # the fork takes a row's halves, as it would keys and values
+    k, v = cache[..., None, :C // 2], cache[..., None, C // 2:]
+    absorbed = torch.cat((rows(L, n, H, R), q[..., DK:]), -1)[:, :, None]
+    own = torch.cat((latent, turned), -1)[:, :, None]
+    scale = (DK + DP) ** -0.5
+    stream = torch.cuda.current_stream(dev)
+    last = {}
+
+    def step(i):
+        t, m, _, slots, _, last["reserved"] = binding.cache_reserve(table, lens, ones, pages=pages, page_size=ps, rows=n)
+        for j in range(L):
+            binding.head_product(q[j][..., :DK], w_in[j], out=absorbed[j, :, 0, :, :R])
+            mid = binding.latent_attention(absorbed[j], cache[j], table, lens, own[j], dim_v=R, scale=scale)
+            last["out"] = binding.head_product(mid[:, 0], w_v[j])
+            binding.cache_write(cache[j], slots, latent[j], turned[j])
+        anc = binding.beam_select(logits, scores)[1]
+        last["status"] = binding.cache_fork(k, v, t, m, anc)[2]
+        binding.beam_reorder(history, anc)
+
+    T = 4 * c["prompt"]
+    start = torch.arange(0, T + 1, c["prompt"], dtype=torch.int32, device=dev)
+    first, four = torch.full((4,), c["prompt"], dtype=torch.int32, device=dev), table[::W][:4].contiguous()
+    pq = rows(T, H, DK + DP)
+
+    def prompt(i):
+        last["out"] = binding.latent_prompt(pq, cache[0], four, first, start, w_k[0], w_v[0], rows=T)
+
+    def timed(fn, steps):
+        for i in range(min(args.warmup, steps)):
+            fn(i)
+        torch.cuda.synchronize()
+        e0, e1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        e0.record(stream)
+        for i in range(steps):
+            fn(i)
+        e1.record(stream)
+        torch.cuda.synchronize()
+        ms = e0.elapsed_time(e1) / steps
+        binding.profile_read()
+        binding.profile_enable(True)
+        for i in range(steps):
+            fn(i)
+        torch.cuda.synchronize()
+        binding.profile_enable(False)
+        return ms, {kind: round(x[0] / x[1] * 1e3, 3) for kind, x in binding.profile_read().items() if x[1]}
+
+    ms_step, us = timed(step, args.steps)
+    assert int(last["reserved"]) == 0 and int(last["status"]) == 0
+    prompt_ms, prompt_us = timed(prompt, max(1, args.steps // 10))
+    cache_bytes = 2 * int(lens_h.sum()) * C
+    print(f"[bench] beam step {args.steps} steps: {ms_step * 1e3:.2f} us/step, prompts {prompt_ms * 1e3:.2f} us; kernels "
+          f"{us}", file=sys.stderr, flush=True)
+    line = {
+        "metric": "beam step: beams' tokens attended and selected/sec at B=8,W=4,V=128256",
+        "value": round(n / (ms_step / 1e3), 1),
+        "unit": "tokens/s",
+        "n_gpus": 1,
+        "steps": args.steps,
+        "warmup": args.warmup,
+        "ms_per_step": round(ms_step, 6),
+        "higher_is_better": True,
+        "scaling": "weak",
+        "vs_baseline": None,
+        "dtype": "bf16",
+        "data": "synthetic",
+        "config": {"workload": f"beam step B={B} W={W} {L} layers {H} heads on rows of {R} + {DP}, "
+                               f"{int(lens_h.min())}..{int(lens_h.max())} cached rows, V={V} bf16 logits",
+                   "cache_bytes_per_layer": cache_bytes,
+                   "attention_GBps": round(cache_bytes / (us["latent_attention"] / 1e6) / 1e9, 1),
+                   "attention_TFLOPs": round(2 * int(lens_h.sum()) * H * (C + R) / us["latent_attention"] / 1e6, 1)},
+        "kernels_us": us,
+        "prompts": {"tokens": T, "us_per_call": round(prompt_ms * 1e3, 3), "kernels_us": prompt_us},
+        "per_call": per_call_distribution(torch, stream, step, args.steps),
+    }
+    print(json.dumps(line), flush=True)
+
+
+# ---------------------------------------------------------------------------
 # GPU timing
 # ---------------------------------------------------------------------------
 def main():
@@ -905,6 +1026,10 @@ def main():
     ap.add_argument("--tree", action="store_true",
                     help="time a round of drafted trees over a paged cache: spec_tree_attention per layer, "
                          "spec_verify_tree, spec_cache_commit; and spec_cache_fork")
+    ap.add_argument("--beams", action="store_true",
+                    help="time a step of beam decoding on a cache of latent rows: spec_cache_reserve, per layer "
+                         "spec_head_product, spec_latent_attention and spec_cache_write, then spec_beam_select, "
+                         "spec_cache_fork and spec_beam_reorder; and spec_latent_prompt")
     ap.add_argument("--smc", action="store_true",
                     help="time the SMC-SD step (spec_smc_step) on the same inputs instead of the verify step")
     ap.add_argument("--calibrate", action="store_true",
@@ -932,6 +1057,9 @@ def main():
         return
     if args.tree:
         tree_bench(args, binding, torch, dev)
+        return
+    if args.beams:
+        beam_bench(args, binding, torch, dev)
         return
 
     print(f"[bench] generating {N_SETS} input sets of workload {args.workload}", file=sys.stderr, flush=True)

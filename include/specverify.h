@@ -874,8 +874,11 @@ int spec_verify_abi_version(void);
  * the n kernel kinds (0 statistics pass, 1 nucleus selection, 2 row pass:
  * decision and resample, or the SMC particle pass, 3 SMC resampling, 4 the
  * synthetic draft producer, 5 tree attention, 6 its join, 7 the clearing of tree
- * verification's workspace, 8 tree verification, 9 cache plan, 10 cache copies), the
- * summed duration in milliseconds and the number of launches since the last
+ * verification's workspace, 8 tree verification, 9 cache plan, 10 cache copies, 11
+ * latent attention, 12 its join, 13 products per head, 14 the prompts' places, 15
+ * their keys and values, 16 the values' second writing, 17 the prompts' attention,
+ * 18 beam statistics, 19 beam selection, 20 reordered rows, 21 reservation plan, 22
+ * its outputs, 23 rows into their slots), the summed duration in milliseconds and the number of launches since the last
  * read; it returns the number of kinds written.  Host arrays ms[n],
  * launches[n]. */
 int spec_verify_profile_enable(int enable);
