@@ -106,6 +106,26 @@ __device__ __forceinline__ void product_tile(uint32_t smem_at, const uint8_t* co
     }
 }
 
+// Results leave through LDS, so that a row's are stored together: 16 bytes at a time straight
+// from the registers, twice 8 neighbouring lanes' worth, cost more than the product (@).  Where
+// outputs m .. m + 3 of row r lie there: a row's 16 chunks XORed with its number, and a chunk's
+// halves with its fifth bit, so that 32 rows' writes meet no bank twice.
+__device__ __forceinline__ int out_at(int r, int m) {
+    return r * 256 + ((m >> 3 ^ (r & 15)) << 4) + ((m >> 2 ^ r >> 4) & 1) * 8;
+}
+
+// store(r, m, x): eight outputs from m on, a multiple of 8, of row r.
+template <int TT, class F>
+__device__ __forceinline__ void store_rows(const uint8_t* smem, F&& store) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TT * 16 / kThreads; ++i) {
+        const int e = i * kThreads + threadIdx.x, r = e >> 4, m = (e & 15) * 8;
+        const uint4 x = *reinterpret_cast<const uint4*>(smem + (out_at(r, m) & ~15));
+        store(r, m, r & 16 ? make_uint4(x.z, x.w, x.x, x.y) : x);
+    }
+}
+
 // Neighbouring tasks on one XCD (workgroups go to the eight in turn); -1: none.
 __device__ __forceinline__ int64_t task_of(int64_t tasks) {
     const int64_t per = (tasks + 7) / 8, t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
@@ -139,21 +159,19 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(ProductParams p) {
     v16f acc[L::BM][L::BT];
     product_tile<DT, TT>(smem_at, wp, xp, p.K, acc);
     const int wm = w % L::WM, wt = w / L::WM;
+    __syncthreads();
 #pragma unroll
-    for (int b = 0; b < L::BT; ++b) {
-        const int t = t0 + (wt * L::BT + b) * 32 + col;
-        if (t >= p.T) continue;
-        uint8_t* const dst = p.out + 16 * (t * p.os[0] + h * p.os[1]);
+    for (int b = 0; b < L::BT; ++b)
 #pragma unroll
         for (int a = 0; a < L::BM; ++a)
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const int m = m0 + (wm * L::BM + a) * 32 + 2 * i + 4 * hh;
-                if (m < p.M)
-                    *reinterpret_cast<v4s*>(dst + 2 * m) =
-                        pack4<DT>(acc[a][b][i], acc[a][b][i + 1], acc[a][b][i + 2], acc[a][b][i + 3]);
-            }
-    }
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<v4s*>(smem + out_at((wt * L::BT + b) * 32 + col, (wm * L::BM + a) * 32 + 2 * i + 4 * hh)) =
+                    pack4<DT>(acc[a][b][i], acc[a][b][i + 1], acc[a][b][i + 2], acc[a][b][i + 3]);
+    store_rows<TT>(smem, [&](int r, int m, uint4 x) {
+        if (t0 + r < p.T && m0 + m < p.M)
+            *reinterpret_cast<uint4*>(p.out + 16 * ((t0 + r) * p.os[0] + h * p.os[1]) + 2 * (m0 + m)) = x;
+    });
 }
 
 // ---- prompts
@@ -309,21 +327,25 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
     v16f acc[L::BM][L::BT];
     product_tile<DT, 128>(smem_at, wp, xp, p.R, acc);
     const int wm = w % L::WM, wt = w / L::WM;
+    auto store = [&](uint8_t* to) {
+        store_rows<128>(smem, [&](int r, int m, uint4 x) {
+            const int h = (m0 + m) / per;
+            if (r0 + r < total && r0 + r < p.rows && m0 + m < M)
+                *reinterpret_cast<uint4*>(to + 2 * ((static_cast<int64_t>(h) * p.rows + r0 + r) * per + m0 + m - h * per)) = x;
+        });
+    };
+    __syncthreads();
     if (!values) {
 #pragma unroll
-        for (int b = 0; b < L::BT; ++b) {
-            const int r = r0 + (wt * L::BT + b) * 32 + col;
-            if (r >= total || r >= p.rows) continue;
+        for (int b = 0; b < L::BT; ++b)
 #pragma unroll
             for (int a = 0; a < L::BM; ++a)
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const int m = m0 + (wm * L::BM + a) * 32 + 2 * i + 4 * hh, h = m / per;
-                    if (m < M)
-                        *reinterpret_cast<v4s*>(p.k + 2 * ((static_cast<int64_t>(h) * p.rows + r) * per + m - h * per)) =
-                            pack4<DT>(acc[a][b][i], acc[a][b][i + 1], acc[a][b][i + 2], acc[a][b][i + 3]);
-                }
-        }
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<v4s*>(smem + out_at((wt * L::BT + b) * 32 + col,
+                                                          (wm * L::BM + a) * 32 + 2 * i + 4 * hh)) =
+                        pack4<DT>(acc[a][b][i], acc[a][b][i + 1], acc[a][b][i + 2], acc[a][b][i + 3]);
+        store(p.k);
         return;
     }
     // a wave's eight neighbouring outputs are of one head
@@ -342,7 +364,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
     for (int a = 0; a < L::BM; ++a)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-            const int m8 = m0 + (wm * L::BM + a) * 32 + 2 * i, m = m8 + 4 * hh, h = m8 / per;
+            const int m8 = m0 + (wm * L::BM + a) * 32 + 2 * i, h = m8 / per;
             if (m8 >= M) continue;
             if (!AGAIN && h != of) {
                 if (of >= 0) tell();
@@ -363,14 +385,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
                     else
                         most = max(most, size);
                 }
-                *reinterpret_cast<v4s*>(p.v + 2 * ((static_cast<int64_t>(h) * p.rows + r) * per + m - h * per)) =
-                    pack4<kDTypeF16>(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<v4s*>(smem + out_at(r - r0, m8 - m0 + 4 * hh)) = pack4<kDTypeF16>(y[0], y[1], y[2], y[3]);
             }
         }
     if (!AGAIN) {
         tell();
         if (odd) atomicOr(p.odd, 1);
     }
+    store(p.v);
 }
 
 // Where chunk c of row r of a tile lies in LDS, rows of PITCH bytes: c XORed with this, so
