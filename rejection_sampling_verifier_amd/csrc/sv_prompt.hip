@@ -31,21 +31,21 @@ namespace {
 // (0-3, 12-15, 20-23, 24-27 and so on) over 64 banks, rows alternate between two
 // halves of them, and these lanes' even rows have the eight halves 0-7.  A null token
 // row counts as zeros.
-template <int TT>
+template <int TM, int TT>
 struct Tile {
-    static constexpr int kStage = (128 + TT) * 128;
-    static constexpr int WM = TT == 128 ? 2 : 4;             // waves over outputs
-    static constexpr int BM = 128 / WM / 32, BT = TT == 128 ? 2 : 1;  // 32 x 32 blocks of a wave
-    static constexpr int kW = 4, kX = TT / 32;               // wide loads of a wave and stage
+    static constexpr int kWaves = TM == 256 ? 8 : 4, kThreads = 64 * kWaves;
+    static constexpr int kXAt = TM * 128, kStage = (TM + TT) * 128;
+    static constexpr int WM = TT == 32 ? 4 : 2;                                   // waves over outputs
+    static constexpr int BM = TM / WM / 32, BT = TT / (kWaves / WM) / 32;         // 32 x 32 blocks of a wave
+    static constexpr int kW = TM / 8 / kWaves, kX = TT / 8 / kWaves;              // wide loads of a wave and stage
 };
 
 // The chunk that lane `lane` of wide load `idx` of eight rows stages.
 __device__ __forceinline__ int product_chunk(int lane, int idx) { return (lane & 7) ^ ((idx & 1) << 2 | lane >> 4); }
 
-template <int DT, int TT>
+template <int DT, class L>
 __device__ __forceinline__ void product_tile(uint32_t smem_at, const uint8_t* const* wp, const uint8_t* const* xp,
-                                             int K, v16f (*acc)[Tile<TT>::BT]) {
-    using L = Tile<TT>;
+                                             int K, v16f (*acc)[L::BT]) {
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int hh = lane >> 5, col = lane & 31;
     const int wm = w % L::WM, wt = w / L::WM;
@@ -58,14 +58,14 @@ __device__ __forceinline__ void product_tile(uint32_t smem_at, const uint8_t* co
 #pragma unroll
         for (int i = 0; i < L::kX; ++i)
             load_lds(s * 64 + product_chunk(lane, w * L::kX + i) * 8 < K && xp[i] ? xp[i] + s * 128 : zero,
-                     smem_at + at + 16384 + (w * L::kX + i) * 1024);
+                     smem_at + at + L::kXAt + (w * L::kX + i) * 1024);
     };
     uint32_t a_rd[4], b_rd[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const uint32_t c = ((2 * k + hh) ^ (col >> 1 & 7)) << 4;
         a_rd[k] = smem_at + (wm * L::BM * 32 + col) * 128 + c;
-        b_rd[k] = smem_at + 16384 + (wt * L::BT * 32 + col) * 128 + c;
+        b_rd[k] = smem_at + L::kXAt + (wt * L::BT * 32 + col) * 128 + c;
     }
 #pragma unroll
     for (int a = 0; a < L::BM; ++a)
@@ -106,22 +106,24 @@ __device__ __forceinline__ void product_tile(uint32_t smem_at, const uint8_t* co
     }
 }
 
-// Results leave through LDS, so that a row's are stored together: 16 bytes at a time straight
-// from the registers, twice 8 neighbouring lanes' worth, cost more than the product (@).  Where
-// outputs m .. m + 3 of row r lie there: a row's 16 chunks XORed with its number, and a chunk's
+// Results leave through LDS, so that a row's are stored together (16 bytes of a row at a time,
+// straight from the registers: 46 us for 42 where 1024 tokens of 128 heads leave the latent
+// space).  Where outputs m .. m + 3 of row r lie there: a row's 16 chunks XORed with its number, and a chunk's
 // halves with its fifth bit, so that 32 rows' writes meet no bank twice.
+template <int TM>
 __device__ __forceinline__ int out_at(int r, int m) {
-    return r * 256 + ((m >> 3 ^ (r & 15)) << 4) + ((m >> 2 ^ r >> 4) & 1) * 8;
+    return r * (2 * TM) + ((m >> 3 ^ (r & 15)) << 4) + ((m >> 2 ^ r >> 4) & 1) * 8;
 }
 
 // store(r, m, x): eight outputs from m on, a multiple of 8, of row r.
-template <int TT, class F>
+template <int TM, int TT, class F>
 __device__ __forceinline__ void store_rows(const uint8_t* smem, F&& store) {
+    constexpr int kRow = TM / 8, kThreads = Tile<TM, TT>::kThreads;  // chunks of a row
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < TT * 16 / kThreads; ++i) {
-        const int e = i * kThreads + threadIdx.x, r = e >> 4, m = (e & 15) * 8;
-        const uint4 x = *reinterpret_cast<const uint4*>(smem + (out_at(r, m) & ~15));
+    for (int i = 0; i < TT * kRow / kThreads; ++i) {
+        const int e = i * kThreads + threadIdx.x, r = e / kRow, m = e % kRow * 8;
+        const uint4 x = *reinterpret_cast<const uint4*>(smem + (out_at<TM>(r, m) & ~15));
         store(r, m, r & 16 ? make_uint4(x.z, x.w, x.x, x.y) : x);
     }
 }
@@ -135,7 +137,7 @@ inline int64_t grid_of(int64_t tasks) { return (tasks + 7) / 8 * 8; }
 
 template <int DT, int TT>
 __global__ __launch_bounds__(kThreads, 2) void k_product(ProductParams p) {
-    using L = Tile<TT>;
+    using L = Tile<128, TT>;
     extern __shared__ __align__(16) uint8_t smem[];
     const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) uint8_t*)smem));
@@ -157,7 +159,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(ProductParams p) {
         xp[i] = p.x + 16 * (min(t0 + (w * L::kX + i) * 8 + r8, p.T - 1) * p.xs[0] + h * p.xs[1] +
                             product_chunk(lane, w * L::kX + i));
     v16f acc[L::BM][L::BT];
-    product_tile<DT, TT>(smem_at, wp, xp, p.K, acc);
+    product_tile<DT, L>(smem_at, wp, xp, p.K, acc);
     const int wm = w % L::WM, wt = w / L::WM;
     __syncthreads();
 #pragma unroll
@@ -166,9 +168,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(ProductParams p) {
         for (int a = 0; a < L::BM; ++a)
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<v4s*>(smem + out_at((wt * L::BT + b) * 32 + col, (wm * L::BM + a) * 32 + 2 * i + 4 * hh)) =
+                *reinterpret_cast<v4s*>(smem + out_at<128>((wt * L::BT + b) * 32 + col, (wm * L::BM + a) * 32 + 2 * i + 4 * hh)) =
                     pack4<DT>(acc[a][b][i], acc[a][b][i + 1], acc[a][b][i + 2], acc[a][b][i + 3]);
-    store_rows<TT>(smem, [&](int r, int m, uint4 x) {
+    store_rows<128, TT>(smem, [&](int r, int m, uint4 x) {
         if (t0 + r < p.T && m0 + m < p.M)
             *reinterpret_cast<uint4*>(p.out + 16 * ((t0 + r) * p.os[0] + h * p.os[1]) + 2 * (m0 + m)) = x;
     });
@@ -265,31 +267,34 @@ __global__ __launch_bounds__(1024) void k_prompt_plan(PromptParams p) {
 // Keys and values of 128 rows of the line: a product with the rows gathered from
 // their pages.  The first output tile's workgroups also bring the rows' second
 // parts into the line.  AGAIN: the values of heads that need a scale.
-template <int DT, bool AGAIN>
-__global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
-    using L = Tile<128>;
+template <int DT, int TT, bool AGAIN>
+__global__ __launch_bounds__(TT == 256 ? 512 : 256, 2) void k_prompt_expand(PromptParams p) {
+    using L = Tile<TT, TT>;
     extern __shared__ __align__(16) uint8_t smem[];
     const uint32_t smem_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) uint8_t*)smem));
     const int mk = p.H * p.dn, mv = p.H * p.dv;
-    const int tk = AGAIN ? 0 : (mk + 127) / 128, tv = (mv + 127) / 128, tr = (p.rows + 127) / 128;
+    const int tk = AGAIN ? 0 : (mk + TT - 1) / TT, tv = (mv + TT - 1) / TT, tr = (p.rows + TT - 1) / TT;
     const int64_t task = task_of(static_cast<int64_t>(tk + tv) * tr);
     if (task < 0) return;
-    // eight row tiles against all outputs, then the next eight: the workgroups an XCD has at a time
-    // share about eight tiles of rows and eight of weights, which its L2 holds
-    const int rg = static_cast<int>(task / (8 * (tk + tv))), in_rg = static_cast<int>(task - rg * 8ll * (tk + tv));
-    const int wide = min(8, tr - 8 * rg), mt = in_rg / wide, r0 = (8 * rg + in_rg - mt * wide) * 128;
+    // 1024 rows against all outputs, then the next: the workgroups that an XCD has at a time share
+    // about that many rows and 1024 outputs' weights, which its L2 holds
+    constexpr int kGroup = 1024 / TT;
+    const int rg = static_cast<int>(task / (kGroup * (tk + tv)));
+    const int in_rg = static_cast<int>(task - rg * static_cast<int64_t>(kGroup) * (tk + tv));
+    const int wide = min(kGroup, tr - kGroup * rg), mt = in_rg / wide, r0 = (kGroup * rg + in_rg - mt * wide) * TT;
     const int64_t total = p.plan[p.B];
     if (r0 >= total) return;
     if (AGAIN) {
         bool any = false;
-        for (int h = mt * 128 / p.dv; h <= min(mt * 128 + 127, mv - 1) / p.dv; ++h) any |= value_scale(p.most[h * kMostStride]) != 1.f;
+        for (int h = mt * TT / p.dv; h <= min(mt * TT + TT - 1, mv - 1) / p.dv; ++h)
+            any |= value_scale(p.most[h * kMostStride]) != 1.f;
         if (!any) return;
     }
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int hh = lane >> 5, col = lane & 31, r8 = lane >> 3;
     const bool values = AGAIN || mt >= tk;
-    const int m0 = (values ? mt - tk : mt) * 128, M = values ? mv : mk, per = values ? p.dv : p.dn;
+    const int m0 = (values ? mt - tk : mt) * TT, M = values ? mv : mk, per = values ? p.dv : p.dn;
     const uint8_t* const wt0 = values ? p.wv : p.wk;
     const int64_t* const wst = values ? p.wvs : p.wks;
     // the row of the line, null where its page does not exist
@@ -313,7 +318,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
         wp[i] = wt0 + 16 * (h * wst[0] + (m - h * per) * wst[1] + product_chunk(lane, w * L::kW + i));
     }
     if (!AGAIN && mt == 0) {
-        for (int r = threadIdx.x >> 3; r < 128 && r0 + r < total; r += 32) {
+        for (int r = threadIdx.x >> 3; r < TT && r0 + r < total && r0 + r < p.rows; r += L::kThreads / 8) {
             const uint8_t* const x = row_of(r0 + r);
             for (int c = lane & 7; c < p.dr / 8; c += 8)
                 *reinterpret_cast<uint4*>(p.pe + (static_cast<int64_t>(r0 + r) * p.dr + 8 * c) * 2) =
@@ -325,10 +330,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
         }
     }
     v16f acc[L::BM][L::BT];
-    product_tile<DT, 128>(smem_at, wp, xp, p.R, acc);
+    product_tile<DT, L>(smem_at, wp, xp, p.R, acc);
     const int wm = w % L::WM, wt = w / L::WM;
     auto store = [&](uint8_t* to) {
-        store_rows<128>(smem, [&](int r, int m, uint4 x) {
+        store_rows<TT, TT>(smem, [&](int r, int m, uint4 x) {
             const int h = (m0 + m) / per;
             if (r0 + r < total && r0 + r < p.rows && m0 + m < M)
                 *reinterpret_cast<uint4*>(to + 2 * ((static_cast<int64_t>(h) * p.rows + r0 + r) * per + m0 + m - h * per)) = x;
@@ -342,7 +347,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
             for (int a = 0; a < L::BM; ++a)
 #pragma unroll
                 for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<v4s*>(smem + out_at((wt * L::BT + b) * 32 + col,
+                    *reinterpret_cast<v4s*>(smem + out_at<TT>((wt * L::BT + b) * 32 + col,
                                                           (wm * L::BM + a) * 32 + 2 * i + 4 * hh)) =
                         pack4<DT>(acc[a][b][i], acc[a][b][i + 1], acc[a][b][i + 2], acc[a][b][i + 3]);
         store(p.k);
@@ -385,7 +390,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt_expand(PromptParams p) {
                     else
                         most = max(most, size);
                 }
-                *reinterpret_cast<v4s*>(smem + out_at(r - r0, m8 - m0 + 4 * hh)) = pack4<kDTypeF16>(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<v4s*>(smem + out_at<TT>(r - r0, m8 - m0 + 4 * hh)) = pack4<kDTypeF16>(y[0], y[1], y[2], y[3]);
             }
         }
     if (!AGAIN) {
@@ -734,17 +739,35 @@ template <int DT, int TT>
 hipError_t product_one(const ProductParams& p, hipStream_t st, const LaunchEvents& ev) {
     const int64_t tasks = static_cast<int64_t>((p.M + 127) / 128) * ((p.T + TT - 1) / TT) * p.H;
     hipExtLaunchKernelGGL((k_product<DT, TT>), dim3(static_cast<unsigned>(grid_of(tasks))), dim3(kThreads),
-                          2 * Tile<TT>::kStage, st, ev.start, ev.stop, 0, p);
+                          2 * Tile<128, TT>::kStage, st, ev.start, ev.stop, 0, p);
     return hipGetLastError();
 }
 
-template <int DT, bool AGAIN>
+// Tiles of tt outputs by tt rows (again: of the values alone).
+int64_t expand_tasks(const PromptParams& p, int tt, bool again) {
+    return static_cast<int64_t>((again ? 0 : (p.H * p.dn + tt - 1) / tt) + (p.H * p.dv + tt - 1) / tt) *
+           ((p.rows + tt - 1) / tt);
+}
+
+template <int DT, int TT, bool AGAIN>
 hipError_t expand_one(const PromptParams& p, hipStream_t st, const LaunchEvents& ev) {
-    const int64_t tasks = static_cast<int64_t>((AGAIN ? 0 : (p.H * p.dn + 127) / 128) + (p.H * p.dv + 127) / 128) *
-                          ((p.rows + 127) / 128);
-    hipExtLaunchKernelGGL((k_prompt_expand<DT, AGAIN>), dim3(static_cast<unsigned>(grid_of(tasks))), dim3(kThreads),
-                          2 * Tile<128>::kStage, st, ev.start, ev.stop, 0, p);
+    using L = Tile<TT, TT>;
+    const int64_t tasks = expand_tasks(p, TT, AGAIN);
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(k_prompt_expand<DT, TT, AGAIN>), 2 * L::kStage);
+    if (e != hipSuccess) return e;
+    hipExtLaunchKernelGGL((k_prompt_expand<DT, TT, AGAIN>), dim3(static_cast<unsigned>(grid_of(tasks))),
+                          dim3(L::kThreads), 2 * L::kStage, st, ev.start, ev.stop, 0, p);
     return hipGetLastError();
+}
+
+// The large tile (one workgroup of eight waves a CU) reads and stages half as much per product:
+// 1376 of them 140 us for 163 with four times as many small ones, 128 heads on 4096 rows 235 for
+// 308; but 294, one round and a bit, 35 us for 32.
+template <int DT>
+hipError_t expand_tile(const PromptParams& p, bool again, hipStream_t st, const LaunchEvents& ev) {
+    if (again) return expand_one<DT, 128, true>(p, st, ev);
+    return expand_tasks(p, 256, false) > 2 * p.cus ? expand_one<DT, 256, false>(p, st, ev)
+                                                   : expand_one<DT, 128, false>(p, st, ev);
 }
 
 template <int DT, int DN, int DR, int DV, int RING, int GROUPS>
@@ -786,8 +809,7 @@ hipError_t launch_prompt_plan(const PromptParams& p, hipStream_t st, const Launc
 }
 
 hipError_t launch_prompt_expand(const PromptParams& p, int dtype, bool again, hipStream_t st, const LaunchEvents& ev) {
-    if (again) return dtype == DT_BF16 ? expand_one<DT_BF16, true>(p, st, ev) : expand_one<kDTypeF16, true>(p, st, ev);
-    return dtype == DT_BF16 ? expand_one<DT_BF16, false>(p, st, ev) : expand_one<kDTypeF16, false>(p, st, ev);
+    return dtype == DT_BF16 ? expand_tile<DT_BF16>(p, again, st, ev) : expand_tile<kDTypeF16>(p, again, st, ev);
 }
 
 hipError_t launch_prompt_attn(const PromptParams& p, int dtype, hipStream_t st, const LaunchEvents& ev) {

@@ -299,6 +299,14 @@ def test_value_beyond_float32_of_one_row(row):
     assert not out[row:, 1, 3].isfinite().any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_many_heads_on_many_rows(dtype):
+    """Keys and values of 130 heads for 2200 rows: more large tiles than the device holds twice."""
+    s = pro.make((700, 3, 1497), (9, 3, 5), H=130, dims=(64, 32, 72, 136), dtype=dtype)
+    s["w_v"][7] *= 1e-3
+    pro.check(s, f"130 heads {dtype}")
+
+
 def test_missing_pages_of_prompts():
     s = pro.make((200, 90, 40), (200, 30, 40), H=2, dims=(64, 32, 64, 128), extra=2)
     pages = s["cache"].shape[0]
