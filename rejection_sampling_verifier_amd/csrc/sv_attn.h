@@ -138,20 +138,6 @@ __device__ __forceinline__ v4s lds_read_tr(uint32_t at) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(at));
 }
 
-// Orders a block of M matrix instructions and R LDS reads: AHEAD reads first, then
-// the others between the matrix instructions.
-template <int M, int R, int AHEAD>
-__device__ __forceinline__ void reads_ahead() {
-    constexpr int kFirst = AHEAD < R ? AHEAD : R, kRest = R - kFirst, kGap = M / R;
-    __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
-#pragma unroll
-    for (int i = 0; i < kRest; ++i) {
-        if (kGap) __builtin_amdgcn_sched_group_barrier(0x008, kGap, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, M - kRest * kGap, 0);
-}
-
 // Until at most N of the wave's global loads are under way.
 template <int N>
 __device__ __forceinline__ void wait_vm() {

@@ -11,6 +11,14 @@
 //                    the values of heads whose largest one float16 does not hold well;
 //   k_prompt_attn    128 queries of one head against 64 keys at a time.
 //
+// Expanding costs latent / (dim_k + dim_p + dim_v) as much again per query and key as
+// attending, once per row; attending on the rows themselves would cost 3.4 times the
+// products per query (latent 512, dim_k 128, dim_p 64, dim_v 128).  Four prompts of at
+// most 4096 tokens, 32 heads: 140 us expanding (92 GFLOP and 180 MB of results), 430 us
+// attending (316 GFLOP, 735 TFLOP/s); the softmax between the two products (37 % of a
+// SIMD's cycles) does not overlap with them (40 %) as much as two workgroups a CU
+// would allow.
+//
 // Keys are rounded to the input type, as their queries are in it.  Values and
 // weights meet in float16 whatever the input type, each head's values times a
 // power of two taken from its largest one: with both in bfloat16 the outputs'
@@ -418,8 +426,9 @@ struct Rows {
 
 // 128 queries of one head (32 a wave) against 64 keys at a time, in a ring of RING
 // tiles: with two, two workgroups fill a CU's LDS and take turns at its matrix
-// units; where there are not that many, each has more tiles on their way.  A
-// tile's operands are read from LDS some steps before they are needed.
+// units.  Where there are not that many, a workgroup has two GROUPS of four waves
+// that take the tiles in turn, each with a ring of its own, and add up at the end.
+// A tile's operands are read from LDS some steps before they are needed.
 template <int DT, int DN, int DR, int DV, int RING, int GROUPS>
 __global__ __launch_bounds__(GROUPS * kThreads, 2) void k_prompt_attn(PromptParams p) {
     using KN = Rows<DN>;
@@ -784,6 +793,8 @@ hipError_t prompt_ring(const PromptParams& p, int64_t tasks, hipStream_t st, con
 template <int DT, int DN, int DR, int DV>
 hipError_t prompt_one(const PromptParams& p, hipStream_t st, const LaunchEvents& ev) {
     const int64_t tasks = (p.T / kPromptRows + static_cast<int64_t>(p.B < p.T ? p.B : p.T)) * p.H;  // at most
+    // Two groups where there are no more workgroups than CUs: 150 of them 63 us for 83.  With 2600
+    // the join at the end and the common barrier cost more than they give (469 us for 430).
     constexpr int kDeep = 2 * 3 * 64 * (DN + DR + DV) * 2 <= (160 << 10) ? 3 : 2;
     return tasks <= p.cus ? prompt_ring<DT, DN, DR, DV, kDeep, 2>(p, tasks, st, ev)
                           : prompt_ring<DT, DN, DR, DV, 2, 1>(p, tasks, st, ev);
