@@ -700,8 +700,9 @@ int spec_head_product(const sv_head_product* args, void* stream);
  *                16 bytes, last axes contiguous.
  * table, table_stride, len, width, scale  as spec_tree_attention.
  * q_start        device int32 [B + 1], rising within [0, T]; a sequence whose
- *                bounds do not rise so has no queries.  Rows of out that belong to
- *                no sequence are left as they are; a query that sees nothing is zero.
+ *                bounds do not rise so has no queries (no two sequences may share
+ *                rows of q).  Rows of out that belong to no sequence are left as they
+ *                are; a query that sees nothing is zero.
  * workspace      at least spec_latent_prompt_workspace(args) bytes, aligned to 16.
  *
  * What a token does not see (later rows, pages outside the pool) never reaches its

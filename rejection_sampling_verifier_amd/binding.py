@@ -715,6 +715,13 @@ def _half(t, name):
     return t.dtype
 
 
+def _int32(x, name):
+    """An argument that ctypes would cut to 32 bits."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name}: {x} is out of range")
+    return x
+
+
 def _tokens(t, name, shape, dtype, index):
     """_rows for a tensor that may be empty (whose strides mean nothing)."""
     if shape[0] == 0 and t.dtype is dtype and t.shape == shape and t.get_device() == index:
@@ -827,6 +834,7 @@ def latent_prompt(q, cache, block_table, seq_len, q_start, w_k, w_v, *, rows, sc
     dim_p, dim_v, B = whole - latent, w_v.shape[1], seq_len.shape[0]
     if dim != dim_k + dim_p:
         raise ValueError(f"q has {dim} elements a head; w_k and the cache make it {dim_k} + {dim_p}")
+    _int32(rows, "rows")
     qs = _tokens(q, "q", q.shape, dt, index)
     cs = _rows(cache, "cache", cache.shape, dt, index)
     wks = _rows(w_k, "w_k", (heads, dim_k, latent), dt, index)
@@ -871,6 +879,8 @@ def cache_reserve(block_table, seq_len, n_new, *, pages, page_size, rows, out_ta
     index = seq_len.get_device()
     if seq_len.dim() != 1:
         raise ValueError("seq_len must be [B]")
+    for x, name in ((pages, "pages"), (page_size, "page_size"), (rows, "rows")):
+        _int32(x, name)
     B = seq_len.shape[0]
     tab, tab_stride = _table(block_table, "block_table", B, index)
     width = block_table.shape[1]
@@ -944,6 +954,7 @@ def beam_select(logits, scores, finished=None, *, end=-1, out_tokens=None, out_a
     desc = _probs(logits, "logits")
     index = logits.get_device()
     B, W, V = logits.shape
+    _int32(end, "end")
     _no_grad(logits, scores)
     sc = _array(scores, "scores", (B, W), index, _F32)
     fin = None if finished is None else _array(finished, "finished", (B, W), index)

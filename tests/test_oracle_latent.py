@@ -402,16 +402,17 @@ def test_binding_refuses_before_the_library():
                  w_v=z(4, 8, 32), rows=30),
             [("q", z(9, 4, 32)), ("q", z(9, 3, 24)), ("q", z(9, 4, 24).float()), ("cache", z(10, 16, 48)),
              ("w_k", z(4, 24, 32)), ("w_v", z(4, 8, 24)), ("w_v", z(5, 8, 32)), ("q_start", i(2)),
-             ("q_start", i(3).long()), ("seq_len", i(2, 1)), ("out", z(9, 4, 16))])
+             ("q_start", i(3).long()), ("seq_len", i(2, 1)), ("out", z(9, 4, 16)), ("rows", 1 << 32)])
     refuses(binding.cache_write, dict(cache=z(10, 16, 40), slots=i(5), a=z(5, 32), b=z(5, 8)),
             [("a", z(5, 24)), ("a", z(4, 32)), ("a", z(5, 32).half()), ("b", z(5, 16)), ("b", None), ("slots", i(4)),
              ("slots", i(5).long()), ("cache", z(16, 40)), ("cache", z(10, 16, 40).long())])
     refuses(binding.cache_reserve,
             dict(block_table=i(2, 5), seq_len=i(2), n_new=i(2), pages=10, page_size=16, rows=30),
-            [("block_table", i(3, 5)), ("seq_len", i(2).long()), ("n_new", i(3)), ("seq_len", i(2, 1))])
+            [("block_table", i(3, 5)), ("seq_len", i(2).long()), ("n_new", i(3)), ("seq_len", i(2, 1)), ("rows", (1 << 32) + 30),
+             ("pages", (1 << 32) + 10), ("page_size", (1 << 32) + 16)])
     refuses(binding.beam_select, dict(logits=torch.zeros(2, 4, 50), scores=torch.zeros(2, 4)),
             [("logits", torch.zeros(2, 4, 50).half()), ("logits", torch.zeros(4, 50)), ("scores", torch.zeros(2, 3)),
-             ("scores", torch.zeros(2, 4).double()), ("finished", torch.zeros(2, 4)), ("scores", torch.zeros(2, 4, 1))])
+             ("scores", torch.zeros(2, 4).double()), ("finished", torch.zeros(2, 4)), ("scores", torch.zeros(2, 4, 1)), ("end", (1 << 32) + 3)])
     refuses(binding.beam_reorder, dict(state=i(8, 3), ancestor=i(8)),
             [("ancestor", i(7)), ("ancestor", i(8).long()), ("out", i(8, 4)), ("out", i(8, 3).long()),
              ("state", torch.zeros(8, 3, requires_grad=True)), ("state", i(3, 8, 4).transpose(0, 2))])
