@@ -28,6 +28,7 @@ Modules:
              tree verification, commit and fork of cache pages.
   latent  -- latent rows: attention on a paged cache of rows shared by all
              heads, products per head, attention of prompts.
+  beam    -- one step of beam selection, and the reservation of cache rows.
 """
 
 from .greedy import GreedyResult, argmax_lowest, greedy_verify, top_k_after_first  # noqa: F401
