@@ -770,8 +770,8 @@ hipError_t expand_one(const PromptParams& p, hipStream_t st, const LaunchEvents&
 }
 
 // The large tile (one workgroup of eight waves a CU) reads and stages half as much per product:
-// 1376 of them 140 us for 163 with four times as many small ones, 128 heads on 4096 rows 235 for
-// 308; but 294, one round and a bit, 35 us for 32.
+// 1376 of them 140 us for 163 with four times as many small ones, 128 heads on 4096 rows 215 to 235
+// for 308; but 294, one round and a bit, 35 us for 32.
 template <int DT>
 hipError_t expand_tile(const PromptParams& p, bool again, hipStream_t st, const LaunchEvents& ev) {
     if (again) return expand_one<DT, 128, true>(p, st, ev);
