@@ -24,7 +24,7 @@
 // Weights are rounded once, to the input type.
 //
 // What bounds it: 64 new tokens of 128 heads over at most 4096 rows (207 MB, 46
-// GFLOP) take 94 us and 10 for the join, 32 trees of 16 nodes and 16 heads over at most 8192
+// GFLOP) take 90 us and 10 for the join, 32 trees of 16 nodes and 16 heads over at most 8192
 // (202 MB, 71 GFLOP) 135 and 10: 480 to 520 TFLOP/s.  A workgroup's start, first tile,
 // last tile and results are about 24 us; a tile of 64 rows is 0.9 us, of which the scores'
 // chain (products, maximum, exponentials, weights to LDS) is 0.5 and the products
@@ -192,10 +192,6 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
         (__attribute__((address_space(3))) uint8_t*)smem));
     // Staging, by the value waves, eight rows each: wide load k fills 1024 bytes; lane l's 16 are chunk
     // position (64 k + l) % NC of row (64 k + l) / NC.
-    // chunks past the row's elements are zeros that nothing overwrites
-    if (p.C < DK)
-        for (int i = tid; i < kLatRing * Lds::kStage / 16; i += kLatThreads)
-            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     meet();
     // eight whole rows on one page: a scalar address and these
     const bool by_eights = p.ps_shift >= 3 && p.kcs[1] < (1u << 25);
@@ -255,11 +251,10 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
 #pragma unroll
                     for (int k = 0; k < kLoads; ++k) load_lds(base, off[k], to + k * 1024);
                 } else {
-                    // every load still goes out, as the waits count on: any 64 neighbouring chunks hold one
-                    // of a row's own (the wide rows have 33 of 72 at least, the others come round in 40)
+                    // chunks past the row's elements are zeros
 #pragma unroll
                     for (int k = 0; k < kLoads; ++k)
-                        if (!(padded >> k & 1)) load_lds(base, off[k], to + k * 1024);
+                        load_lds(padded >> k & 1 ? zero : base + off[k], to + k * 1024);
                 }
                 if (lane == 0) s_ok[slot][wv] = 0xFF;
                 return;
@@ -569,48 +564,55 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
                 }
                 meet();  // the sums of the weights are there
             }
-            // dimensions 32 (wv CB + s) + 8 g + 4 hh + 0..3 of row 32 r + col
-            if (!scores) {
+            // The results go through the ring, which nobody reads any more, so that rows leave whole:
+            // dimensions 32 (wv CB + s) + 8 g + 4 hh + 0..3 of row 32 r + col, four floats in a place
+            // XORed with the row (16 rows' writes at a time meet no bank twice)
+            if (any && !scores) {
 #pragma unroll
-                for (int r = 0; r < RG; ++r) {
-                    const int lr = r * 32 + col, row = m * RB + lr;
-                    const bool in = row < rows;
-                    const float l = in ? s_l[0][lr] + s_l[1][lr] : 1.f;
-                    if (whole) {
-                        if (row >= p.N * p.H) continue;
-                        const int node = row / p.H;
-                        const float inv = 1.f / l;
-                        uint8_t* const dst = p.out + units(b, p.os[0], node, p.os[1]) + units(row - node * p.H, p.os[2]);
+                for (int r = 0; r < RG; ++r)
 #pragma unroll
-                        for (int s = 0; s < CB; ++s)
+                    for (int s = 0; s < CB; ++s)
 #pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                const int d = 32 * (wv * CB + s) + 2 * i + 4 * hh;
-                                const v16f& y = o[r][s];
-                                if (d < p.dv)  // an absent node's row is zero
-                                    *reinterpret_cast<v4s*>(dst + 2 * d) =
-                                        in ? pack4<DT>(y[i] * inv, y[i + 1] * inv, y[i + 2] * inv, y[i + 3] * inv)
-                                           : v4s{0, 0, 0, 0};
-                            }
-                    } else if (in) {
-                        float* const rec =
-                            p.part + ((static_cast<int64_t>(c) * 2 + (f == f0 ? 0 : 1)) * p.MT + m) * kRec;
-#pragma unroll
-                        for (int s = 0; s < CB; ++s)
-#pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                const int d = 32 * (wv * CB + s) + 2 * i + 4 * hh;
-                                const v16f& y = o[r][s];
-                                if (d < p.dv)
-                                    *reinterpret_cast<float4*>(rec + lr * DV + d) =
-                                        make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-                            }
-                        if (hh == 0 && wv == 0) {
-                            rec[RB * DV + lr] = s_m[lr];
-                            rec[RB * DV + RB + lr] = l;
+                        for (int i = 0; i < 16; i += 4) {
+                            const int lr = r * 32 + col, d4 = (32 * (wv * CB + s) + 2 * i + 4 * hh) / 4;
+                            const v16f& y = o[r][s];
+                            *reinterpret_cast<float4*>(smem + lr * (DV * 4) + ((d4 ^ (lr & 15)) << 4)) =
+                                make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
                         }
-                    }
+            }
+        }
+        meet();
+        auto sums = [&](int lr, int d4) {
+            return *reinterpret_cast<const float4*>(smem + lr * (DV * 4) + ((d4 ^ (lr & 15)) << 4));
+        };
+        if (whole) {
+#pragma unroll 1
+            for (int e = tid; e < RB * (DV / 8); e += kLatThreads) {
+                const int lr = e / (DV / 8), d = (e - lr * (DV / 8)) * 8, row = m * RB + lr;
+                if (row >= p.N * p.H || d >= p.dv) continue;
+                const int node = row / p.H;
+                uint8_t* const dst = p.out + units(b, p.os[0], node, p.os[1]) + units(row - node * p.H, p.os[2]) + 2 * d;
+                v8s y = {0, 0, 0, 0, 0, 0, 0, 0};  // an absent node's row
+                if (row < rows) {
+                    const float inv = 1.f / (s_l[0][lr] + s_l[1][lr]);
+                    const float4 lo = sums(lr, d / 4), hi = sums(lr, d / 4 + 1);
+                    y = __builtin_shufflevector(pack4<DT>(lo.x * inv, lo.y * inv, lo.z * inv, lo.w * inv),
+                                                pack4<DT>(hi.x * inv, hi.y * inv, hi.z * inv, hi.w * inv), 0, 1, 2, 3,
+                                                4, 5, 6, 7);
                 }
+                *reinterpret_cast<v8s*>(dst) = y;
+            }
+        } else if (any) {
+            float* const rec = p.part + ((static_cast<int64_t>(c) * 2 + (f == f0 ? 0 : 1)) * p.MT + m) * kRec;
+            const int last = min(RB, rows - m * RB);
+#pragma unroll 4
+            for (int e = tid; e < last * (DV / 4); e += kLatThreads) {
+                const int lr = e / (DV / 4), d4 = e - lr * (DV / 4);
+                if (4 * d4 < p.dv) *reinterpret_cast<float4*>(rec + lr * DV + 4 * d4) = sums(lr, d4);
+            }
+            if (tid < last) {
+                rec[RB * DV + tid] = s_m[tid];
+                rec[RB * DV + RB + tid] = s_l[0][tid] + s_l[1][tid];
             }
         }
         meet();  // the stages and sums are free again
