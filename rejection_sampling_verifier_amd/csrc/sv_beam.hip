@@ -365,6 +365,7 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
             }
         }
         if (!again) return;
+        __syncthreads();  // everyone has read s_near, also where no row is left to be summed (all beams finished)
         // float64 sums of the rows that take part
         for (int i = 0; i < W; ++i) {
             if (s_log[i] != s_log[i]) continue;
