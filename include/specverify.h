@@ -818,10 +818,12 @@ int spec_cache_write(const sv_cache_rows* args, void* stream);
  *   scores[b, w] + x[v] - log sum_u exp(x[u]),  x = logits[b, w],
  *
  * and a finished beam has one, the token `end` at scores[b, w].  The W largest come
- * out best first, equal ones in the order of w * V + v; between beams the order is
- * that of the scores in float64, within a beam that of the logits.  A beam whose score is -inf (at the first step all but one),
- * +inf or NaN, or whose logits hold a NaN, +inf or nothing above -inf, has no
- * candidates; its logits are not read where the score is -inf or the beam finished.
+ * out best first: by the scores in float64, equal ones by beam, then within a beam by
+ * logit (also where float64 scores cannot tell two apart), then by id; with equal
+ * logits that is the order of w * V + v.  A beam whose score is -inf (at the first
+ * step all but one), +inf or NaN, or whose logits hold a NaN, +inf or nothing above
+ * -inf, has no candidates; its logits are not read where the score is -inf or the
+ * beam finished.
  *
  * logits         [B, W, V] (the descriptor's P = W <= SPECVERIFY_MAX_BEAMS); B * W <=
  *                65535, V <= 2^24.

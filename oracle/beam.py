@@ -18,13 +18,14 @@ def log_softmax(x):
 def beam_select(logits, scores, finished=None, end=-1):
     """logits [B, W, V] float64, scores [B, W]; returns (tokens, ancestor,
     scores, finished, margin): margin [B] is the smallest distance between two
-    different beams' candidates that decides something.  A beam's own ids come in
-    the order of their logits, also where float64 cannot tell their scores apart."""
+    different beams' candidates that decides something.  Equal scores come in the
+    order of the beams, a beam's own ids in that of their logits (also where float64
+    cannot tell their scores apart), then of their numbers."""
     B, W, V = logits.shape
     tokens, anc = np.full((B, W), -1, np.int32), np.full(B * W, -1, np.int32)
     out, fin, margin = np.full((B, W), -np.inf), np.zeros((B, W), np.int32), np.full(B, np.inf)
     for b in range(B):
-        s, d = np.full((W, V), -np.inf), np.zeros((W, V))
+        s, logit = np.full((W, V), -np.inf), np.zeros((W, V))
         for w in range(W):
             base = float(scores[b, w])
             if not np.isfinite(base):
@@ -36,11 +37,12 @@ def beam_select(logits, scores, finished=None, end=-1):
             if np.isnan(x).any() or x.max() == np.inf or x.max() == -np.inf:
                 continue
             with np.errstate(divide="ignore"):
-                s[w] = base + log_softmax(x)
+                s[w] = (base + (x - x.max())) - np.log(np.exp(x - x.max()).sum())
             s[w][x == -np.inf] = -np.inf
-            d[w] = x - x.max()
+            logit[w] = x
         flat = s.reshape(-1)
-        order = np.lexsort((np.arange(W * V), -d.reshape(-1), -flat))
+        at = np.arange(W * V)
+        order = np.lexsort((at, -logit.reshape(-1), at // V, -flat))
         order = order[flat[order] > -np.inf]
         for k, c in enumerate(order[:W]):
             w, v = divmod(int(c), V)

@@ -196,16 +196,17 @@ __device__ __forceinline__ uint64_t score_key(double s) {
     return u >> 63 ? ~u : u | 1ull << 63;
 }
 
-// A candidate: its score (NaN: none), its logit's distance from the row's largest, w V + v.
-// Of equal scores the smaller distance is first (only ids of one beam have equal
-// scores and different distances, where float64 cannot tell their scores apart),
-// then the smaller number.
+// A candidate: its score (NaN: none), its beam, its logit's order key and its id.
+// Of equal scores the lower beam's is first; within a beam the larger logit (also
+// where float64 cannot tell the scores apart), then the lower id.
 struct Cand {
-    double s, d;
-    uint32_t flat;
+    double s;
+    uint32_t beam, key, id;
 };
 __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
-    return a.s > b.s || (a.s == b.s && (a.d > b.d || (a.d == b.d && a.flat < b.flat)));
+    if (a.s != b.s) return a.s > b.s;
+    if (a.beam != b.beam) return a.beam < b.beam;
+    return a.key > b.key || (a.key == b.key && a.id < b.id);
 }
 
 template <int DT>
@@ -257,18 +258,21 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
     // candidate c of the lists, and behind them one for every finished beam.  (What a row that is not
     // asked for has in its lists is not looked at: it may be left from another call.)
     auto candidate = [&](int c, uint64_t e) {
-        Cand y{nan, 0.0, ~0u};
+        Cand y{nan, 0u, 0u, 0u};
         if (c >= lists) {
             const int i = c - lists;
             if (c < total && done[i] && scores[i] > -SV_INF && scores[i] < SV_INF)
-                y = Cand{static_cast<double>(scores[i]), 0.0, static_cast<uint32_t>(i) * p.V + p.end};
+                y = Cand{static_cast<double>(scores[i]), static_cast<uint32_t>(i), 0u, static_cast<uint32_t>(p.end)};
             return y;
         }
         const int i = c / per_row;
         if (s_log[i] != s_log[i] || e == 0) return y;
-        y.flat = static_cast<uint32_t>(i) * p.V + ~static_cast<uint32_t>(e);
-        y.d = static_cast<double>(key_value(static_cast<uint32_t>(e >> 32))) - s_top[i];
-        y.s = scores[i] + (y.d - s_log[i]);
+        y.beam = i;
+        y.key = static_cast<uint32_t>(e >> 32);
+        y.id = ~static_cast<uint32_t>(e);
+        // the logarithm last: what is before it is exact for numbers of ordinary sizes, and beams of equal
+        // rows tie wherever their sums of score and logit do
+        y.s = (scores[i] + (static_cast<double>(key_value(y.key)) - s_top[i])) - s_log[i];
         return y;
     };
     // all of the thread's candidates: those at hand, then the others
@@ -311,7 +315,7 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
         __syncthreads();
         const int n = s_n;
         auto put = [&](int rank, const Cand& y) {
-            const int i = y.flat / p.V, v = y.flat - i * p.V, at = b * W + rank;
+            const int i = y.beam, v = y.id, at = b * W + rank;
             p.out_tokens[at] = v;
             p.out_ancestor[at] = b * W + i;
             p.out_scores[at] = static_cast<float>(y.s);
@@ -323,13 +327,12 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
             int rank = W;
             if (tid < n) {
                 me = s_list[tid];
-                const uint32_t beam = me.flat / p.V;
                 rank = 0;
                 bool near = false;
                 for (int j = 0; j < n; ++j) {
                     const Cand y = s_list[j];
                     rank += before(y, me);
-                    near |= fabs(y.s - me.s) <= kBand && y.flat / p.V != beam;
+                    near |= fabs(y.s - me.s) <= kBand && y.beam != me.beam;
                 }
                 if (rank < W && near) s_near = 1;
             }
@@ -347,12 +350,13 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
         } else if (!again) {  // many equal scores: one after the other
             Cand last{};
             for (int i = 0; i < W; ++i) {
-                Cand top{nan, 0.0, ~0u};
+                Cand top{nan, 0u, 0u, 0u};
                 each([&](const Cand& y) {
                     if (y.s == y.s && (i == 0 || before(last, y)) && (top.s != top.s || before(y, top))) top = y;
                 });
                 for (int o = 32; o; o >>= 1) {
-                    const Cand y{__shfl_xor(top.s, o), __shfl_xor(top.d, o), __shfl_xor(top.flat, o)};
+                    const Cand y{__shfl_xor(top.s, o), __shfl_xor(top.beam, o), __shfl_xor(top.key, o),
+                                 __shfl_xor(top.id, o)};
                     if (y.s == y.s && (top.s != top.s || before(y, top))) top = y;
                 }
                 if (lane == 0) s_best[w] = top;

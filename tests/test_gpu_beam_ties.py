@@ -6,7 +6,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import beam as ref
 from rejection_sampling_verifier_amd import binding
+from test_oracle_beam_ties import in_whole_numbers
 from tree_helpers import dev
 
 pytestmark = pytest.mark.gpu
@@ -71,3 +73,55 @@ def test_finished_beams_beside_beams_without_candidates(bad):
             assert rows(got, b, W)[:2] == want
         assert (got[0][:, 2:] == -1).all() and (got[1].view(B, W)[:, 2:] == -1).all()
         assert (got[2][:, 2:] == -INF).all() and (got[3][:, 2:] == 0).all()
+
+
+# ---- equal scores of different beams
+
+def order_of(got, b, W):
+    return [r[:2] for r in rows(got, b, W)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_the_lower_beam_comes_first(dtype):
+    logits = torch.full((1, 2, 9), -1.0, dtype=dtype, device="cuda")
+    logits[..., 0] = 0.0
+    got = binding.beam_select(logits, torch.tensor([[-1.0, -2.0]], device="cuda"))
+    assert order_of(got, 0, 2) == [(0, 0), (1, 0)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("W,V,levels", [(4, 50, 10), (8, 3000, 40), (16, 20000, 60), (8, 20000, 2)])
+def test_shared_rows_of_whole_numbers(dtype, W, V, levels):
+    """Beams of one row each with scores that are whole numbers apart: many candidates are equal, from a few
+    to more than a workgroup ranks at once."""
+    rng = np.random.default_rng(V + levels)
+    B = 12
+    x = np.stack([np.maximum(-rng.permutation(V), -levels) for _ in range(B)])
+    scores = rng.integers(-6, 0, (B, W))
+    logits = dev(np.repeat(x[:, None], W, 1).astype(np.float32), dtype)
+    got = binding.beam_select(logits, dev(scores.astype(np.float32)))
+    host = ref.beam_select(logits.double().cpu().numpy(), scores.astype(np.float64))
+    for b in range(B):
+        want = in_whole_numbers(x[b], scores[b], W)
+        assert order_of(got, b, W) == want, b
+        assert list(zip(host[0][b].tolist(), (host[1].reshape(-1, W)[b] - b * W).tolist())) == want, b
+
+
+@pytest.mark.parametrize("finished_first", [True, False])
+def test_finished_beside_live(finished_first):
+    """A live beam with one id left has it at its own score."""
+    logits = torch.full((1, 2, 5), -INF, device="cuda")
+    logits[..., 3] = 4.0
+    scores = torch.full((1, 2), -2.0, device="cuda")
+    done = torch.tensor([[1, 0]] if finished_first else [[0, 1]], dtype=torch.int32, device="cuda")
+    got = binding.beam_select(logits, scores, done, end=1)
+    want = [(1, 0, -2.0, 1), (3, 1, -2.0, 0)] if finished_first else [(3, 0, -2.0, 0), (1, 1, -2.0, 1)]
+    assert rows(got, 0, 2) == want
+
+
+def test_logits_decide_within_a_beam():
+    """1e-30 and 0 are equal beside a largest logit of 5, as scores; -0 and 0 are equal logits."""
+    logits = torch.full((1, 4, 20), -INF, device="cuda")
+    logits[0, 0, [2, 5, 10, 11]] = torch.tensor([5.0, -0.0, 1e-30, 0.0], device="cuda")
+    got = binding.beam_select(logits, torch.tensor([[-1.0, -INF, -INF, -INF]], device="cuda"))
+    assert order_of(got, 0, 4) == [(2, 0), (10, 0), (5, 0), (11, 0)]
