@@ -833,7 +833,10 @@ int spec_cache_write(const sv_cache_rows* args, void* stream);
  * out_tokens     device int32 [B, W].
  * out_ancestor   device int32 [B * W]: b * W + the beam continued, as
  *                spec_cache_fork and spec_beam_reorder take it.
- * out_scores     device float32 [B, W], rounded once.
+ * out_scores     device float32 [B, W], rounded once.  The logarithm is off by at most
+ *                2^-20 of the share of probability that the ids beside the beam's
+ *                first one have (by a float64 rounding where two beams' candidates are
+ *                close, as these sums are taken again).
  * out_finished   device int32 [B, W]: 1 where the token is `end` or the beam was finished.
  *                Where there are fewer candidates than beams: -1, -1, -inf and 0.
  *                Outputs must not overlap the inputs or each other.

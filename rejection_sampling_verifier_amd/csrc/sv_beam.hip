@@ -34,11 +34,15 @@ namespace {
 constexpr uint32_t kLowest = 0x007FFFFFu;  // order key of -inf: such ids are no candidates
 constexpr int kListed = 1024;              // candidates a chunk's workgroup ranks at most in one go
 
-// Relative error of a chunk's sum: the exponential's argument is taken exactly and
-// split into its integer and a fraction of two roundings of 2^-25, 2^f has an
-// error of 2^-23 relative, eight terms are summed in float32 (seven times 2^-24),
-// the rest in float64: below 2^-20.  The distance of two rows' candidates is off
-// by twice that at most; the band is twice as wide again.
+// Relative error of an exponential below the row's largest: the argument is taken
+// exactly (between bfloat16 numbers with an error of 2^-21 up to 16 below the largest,
+// 2^-20 up to 32) and split into its integer and a fraction of two roundings of 2^-25,
+// and 2^f has an error of 2^-23: below 2^-20, but for terms further than 32 below,
+// which make 2^-39 at most of any sum's error.  The largest is exactly 1, and sums are
+// float64 (in float32, eight terms at a time, what the other ids have beside one with
+// 1 - 1e-7 of the probability was lost in part or whole).  So a row's logarithm is off
+// by 2^-20 of the share that its other ids have; the distance of two rows' candidates
+// by twice that at most, and the band is twice as wide again.
 constexpr double kBand = 0x1p-18;
 
 // 16 bytes at any element's address.
@@ -71,7 +75,7 @@ __device__ __forceinline__ float exp_of(float x, float top) {
     const float d = x - top;
     const float n = __builtin_rintf(d * kHi);
     float f = fmaf(d, kLo, fmaf(d, kHi, -n));
-    if (DT == DT_F32) {  // what the difference's rounding left (a bfloat16's is exact where it counts)
+    if (DT == DT_F32) {  // what the difference's rounding left (bfloat16: 8 to 13 % of the kernel's time for it)
         const float y = x - d;
         f = fmaf((x - (d + y)) + (y - top), kHi, f);
     }
@@ -133,10 +137,9 @@ __global__ __launch_bounds__(kThreads) void k_beam_stats(BeamParams p) {
     double sum = 0.0;
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
-        float s = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            s += exp_of<DT>(x[k][i], top);
+            sum += exp_of<DT>(x[k][i], top);
             const uint32_t key = order_key(x[k][i]);
             if (key >= tau) {
                 const int at = atomicAdd(&s_n, 1);
@@ -144,7 +147,6 @@ __global__ __launch_bounds__(kThreads) void k_beam_stats(BeamParams p) {
                     s_list[at] = static_cast<uint64_t>(key) << 32 | ~static_cast<uint32_t>(id0 + k * kThreads * 8 + i);
             }
         }
-        sum += s;
     }
     for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
     if (lane == 0) s_sum[w] = sum;

@@ -125,3 +125,28 @@ def test_logits_decide_within_a_beam():
     logits[0, 0, [2, 5, 10, 11]] = torch.tensor([5.0, -0.0, 1e-30, 0.0], device="cuda")
     got = binding.beam_select(logits, torch.tensor([[-1.0, -INF, -INF, -INF]], device="cuda"))
     assert order_of(got, 0, 4) == [(2, 0), (10, 0), (5, 0), (11, 0)]
+
+
+# ---- the scores themselves
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V", [2, 8, 2049, 40001])
+@pytest.mark.parametrize("gap", [1, 6, 17, 25, 30])
+def test_scores_of_confident_rows(dtype, V, gap):
+    """One id has nearly all of the probability: what the others have is kept.  The bound: each of their
+    exponentials is off by 2^-20 relative at most, which moves the logarithm by that much of their share;
+    float64 sums and logarithms (2^-50); half a step of float32."""
+    rng = np.random.default_rng(gap)
+    B = 3
+    x = rng.standard_normal((B, 1, V)) * 0.25 - gap
+    x[np.arange(B), 0, rng.integers(0, V, B)] = 0.125
+    logits = dev(x, dtype)
+    got = binding.beam_select(logits, torch.zeros((B, 1), device="cuda"))
+    y = logits.double().cpu().numpy()[:, 0]
+    top = y.max(-1)
+    rest = np.exp(y - top[:, None])
+    rest[np.arange(B), y.argmax(-1)] = 0.0
+    rest = rest.sum(-1)
+    want = -np.log1p(rest)
+    err = np.abs(got[2].double().cpu().numpy()[:, 0] - want)
+    assert (err <= 2.0 ** -20 * rest / (1 + rest) + 2.0 ** -50 + 2.0 ** -24 * np.abs(want)).all(), (err, want)
