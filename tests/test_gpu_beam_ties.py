@@ -150,3 +150,31 @@ def test_scores_of_confident_rows(dtype, V, gap):
     want = -np.log1p(rest)
     err = np.abs(got[2].double().cpu().numpy()[:, 0] - want)
     assert (err <= 2.0 ** -20 * rest / (1 + rest) + 2.0 ** -50 + 2.0 ** -24 * np.abs(want)).all(), (err, want)
+
+
+# ---- nearer than float32 exponentials tell
+
+@pytest.mark.parametrize("seed", range(3))
+def test_scores_apart_by_less_than_the_exponentials_error(seed):
+    """Two beams whose rows differ by a few float32 steps everywhere, with the same largest logit and score: their best candidates are apart
+    by their logarithms' difference alone, set to 4e-11 by a logit of little mass.  Half of the time the second
+    beam is the better one."""
+    rng = np.random.default_rng(seed)
+    B, V = 48, 30011
+    x = (rng.standard_normal((B, 1, V)) * 2 * (1 + 1e-6 * rng.standard_normal((B, 2, V)))).astype(np.float32)
+    x[:, :, 0] = 3.0
+    x[:, :, 5] = 12.0  # far above the others, so that the best candidates of both are this id
+    want = 4e-11 * np.where(rng.random(B) < 0.5, 1, -1)
+    for b in range(B):
+        for _ in range(3):  # Newton's steps on row 1's first logit
+            lse = [np.log(np.exp(x[b, w].astype(np.float64) - 12.0).sum()) for w in range(2)]
+            p = np.exp(float(x[b, 1, 0]) - 12.0 - lse[1])
+            x[b, 1, 0] = np.float32(x[b, 1, 0] + np.log1p((lse[0] - want[b] - lse[1]) / p))
+    scores = np.full((B, 2), -3.0, np.float32)
+    tokens, anc, out, _, margin = ref.beam_select(x.astype(np.float64), scores.astype(np.float64))
+    assert (tokens == 5).all() and (margin > 1e-11).all() and (margin < 1e-10).all(), margin
+    assert 8 < (anc.reshape(B, 2)[:, 0] % 2).sum() < 40
+    got = binding.beam_select(dev(x), dev(scores))
+    np.testing.assert_array_equal(got[0].cpu().numpy(), tokens)
+    np.testing.assert_array_equal(got[1].cpu().numpy(), anc)
+    assert (np.abs(got[2].double().cpu().numpy() - out) <= 2.0 ** -24 * np.abs(out) + 2.0 ** -45).all()
