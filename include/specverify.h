@@ -680,10 +680,11 @@ int spec_head_product(const sv_head_product* args, void* stream);
  * The rows q_start[b] .. q_start[b + 1] of q are the last tokens of sequence b, at
  * positions len[b] - n .. len[b] - 1; their rows, and those of a prefix before
  * them, are in the cache.  Keys are rounded to the input type; values and weights
- * to float16's 11 bits in either type, the values times a power of two per head,
- * chosen by its largest finite one over all sequences' rows (a value's error is
- * half a step, or 2^-21 of that largest one where this is more).  Statistics are
- * float32.
+ * to float16's 11 bits in either type.  A row's values (per head) are kept times a
+ * power of two where the largest finite one lies outside [2^-14, 2^11): a value's
+ * error is half a step, or 2^-15 of that largest one where this is more.  Weights
+ * are relative to the largest product of weight and power of two that the token sees
+ * (those below 2^-32 of it are lost).  Statistics are float32.
  *
  * dtype          SV_BF16 or SV_F16, of all tensors.
  * T              query tokens, 0 (nothing is done) to 2^24; B <= 65536; heads <= 1024.
@@ -705,11 +706,11 @@ int spec_head_product(const sv_head_product* args, void* stream);
  *                are; a query that sees nothing is zero.
  * workspace      at least spec_latent_prompt_workspace(args) bytes, aligned to 16.
  *
- * What a token does not see (later rows, pages outside the pool) never reaches its
- * output.  Where it sees infinities or NaN, expanded keys beyond the type's range
- * included, its output is infinite or NaN.  (Launches have fewer than 2^32 threads:
- * the 128-row tiles of `rows` times the 128-wide tiles of heads * dim_k and of
- * heads * dim_v, and (T / 128 + min(B, T)) * heads, are below 2^24 - 8.)
+ * What a token does not see (later rows, other sequences, pages outside the pool)
+ * never reaches its output.  Where it sees infinities or NaN, expanded keys beyond
+ * the type's range included, its output is infinite or NaN.  (Launches have fewer
+ * than 2^32 threads: the 128-row tiles of `rows` times the 128-wide tiles of heads *
+ * dim_k and of heads * dim_v, and (T / 128 + min(B, T)) * heads, are below 2^24 - 8.)
  *
  * Errors as spec_tree_attention.
  */
@@ -882,11 +883,11 @@ int spec_verify_abi_version(void);
  * synthetic draft producer, 5 tree attention, 6 its join, 7 the clearing of tree
  * verification's workspace, 8 tree verification, 9 cache plan, 10 cache copies, 11
  * latent attention, 12 its join, 13 products per head, 14 the prompts' places, 15
- * their keys and values, 16 the values' second writing, 17 the prompts' attention,
- * 18 beam statistics, 19 beam selection, 20 reordered rows, 21 reservation plan, 22
- * its outputs, 23 rows into their slots), the summed duration in milliseconds and the number of launches since the last
- * read; it returns the number of kinds written.  Host arrays ms[n],
- * launches[n]. */
+ * their keys and values, 16 their rows' powers of two and the values of such rows
+ * once more, 17 the prompts' attention, 18 beam statistics, 19 beam selection, 20
+ * reordered rows, 21 reservation plan, 22 its outputs, 23 rows into their slots), the
+ * summed duration in milliseconds and the number of launches since the last read; it
+ * returns the number of kinds written.  Host arrays ms[n], launches[n]. */
 int spec_verify_profile_enable(int enable);
 int spec_verify_profile_read(double* ms, int64_t* launches, int n);
 

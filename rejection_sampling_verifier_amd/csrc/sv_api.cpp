@@ -1053,7 +1053,7 @@ int head_product_impl(const sv_head_product* a, void* stream_v) {
 
 // The workspace of a prompt call: places, flags, keys, values and second parts of the line.
 struct PromptPlan {
-    size_t odd, most, there, k, v, pe, total;
+    size_t odd, sizes, power, there, k, v, pe, total;
 };
 
 int plan_prompt(const sv_latent_prompt* a, PromptPlan& t) {
@@ -1074,8 +1074,9 @@ int plan_prompt(const sv_latent_prompt* a, PromptPlan& t) {
     if (lines * out >= (1ll << 24) - 8 || tiles * a->heads >= (1ll << 24) - 8) return SV_ESHAPE;
     const size_t rows = static_cast<size_t>(lines) * 128;
     t.odd = align256((static_cast<size_t>(a->B) + 1) * 2 * sizeof(int64_t));
-    t.most = t.odd + 256;
-    t.there = align256(t.most + static_cast<size_t>(a->heads) * sv::kMostStride * sizeof(uint32_t));
+    t.sizes = t.odd + 256;
+    t.power = align256(t.sizes + static_cast<size_t>(a->heads) * a->rows * sv::kSizeParts * sizeof(int16_t));
+    t.there = align256(t.power + static_cast<size_t>(a->heads) * a->rows * sizeof(int16_t));
     t.k = align256(t.there + rows * sizeof(int32_t));
     t.v = align256(t.k + static_cast<size_t>(a->heads) * a->rows * a->dim_k * 2);
     t.pe = align256(t.v + static_cast<size_t>(a->heads) * a->rows * a->dim_v * 2);
@@ -1133,7 +1134,8 @@ int latent_prompt_impl(const sv_latent_prompt* a, void* stream_v) {
     uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
     p.plan = reinterpret_cast<int64_t*>(ws);
     p.odd = reinterpret_cast<int32_t*>(ws + t.odd);
-    p.most = reinterpret_cast<uint32_t*>(ws + t.most);
+    p.sizes = reinterpret_cast<int16_t*>(ws + t.sizes);
+    p.power = reinterpret_cast<int16_t*>(ws + t.power);
     p.there = reinterpret_cast<int32_t*>(ws + t.there);
     p.k = ws + t.k;
     p.v = ws + t.v;

@@ -65,12 +65,15 @@ struct PromptParams {
     int cus;                          // of the device
     // workspace
     int64_t* plan;                    // [B + 1] first row of the line, [B + 1] first query tile
-    int32_t* odd;                     // bit 0: an infinity or NaN among the values; 1: a row whose page does not exist
-    uint32_t* most;                   // [H, kMostStride] bits of the largest value's size
+    int32_t* odd;                     // bit 0: an infinity or NaN among the values; 1: a row whose page does not exist;
+                                      // 2: a row whose values have a power of two of their own
+    int16_t* sizes;                   // [H, kSizeParts, rows] exponent of the largest value in a part of a row
+    int16_t* power;                   // [H, rows] the row's power of two
     int32_t* there;                   // [rows rounded up] 1: the row's page exists
     uint8_t *k, *v, *pe;              // [H, rows, dn], [H, rows, dv], [rows, dr]
+    int part;                         // outputs of a part: those a wave of the expansion has, 64 or 128
 };
-constexpr int kMostStride = 16;       // words: a line of the L2 a head
+constexpr int kSizeParts = 3;         // a head's values lie in that many parts at most
 constexpr int kPromptRows = 128;      // queries of a tile
 hipError_t launch_prompt_plan(const PromptParams& p, hipStream_t st, const LaunchEvents& ev);
 hipError_t launch_prompt_expand(const PromptParams& p, int dtype, bool again, hipStream_t st, const LaunchEvents& ev);

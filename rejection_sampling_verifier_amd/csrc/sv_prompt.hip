@@ -8,21 +8,28 @@
 //
 //   k_prompt_plan    the sequences' places in one line of rows, and in one of query tiles;
 //   k_prompt_expand  keys and values of every head for every row of the line, and again
-//                    the values of heads whose largest one float16 does not hold well;
+//                    the values of rows whose largest one float16 does not hold well;
 //   k_prompt_attn    128 queries of one head against 64 keys at a time.
 //
 // Expanding costs latent / (dim_k + dim_p + dim_v) as much again per query and key as
 // attending, once per row; attending on the rows themselves would cost 3.4 times the
 // products per query (latent 512, dim_k 128, dim_p 64, dim_v 128).  Four prompts of at
-// most 4096 tokens, 32 heads: 140 us expanding (92 GFLOP and 180 MB of results), 430 us
-// attending (316 GFLOP, 735 TFLOP/s); the softmax between the two products (37 % of a
+// most 4096 tokens, 32 heads: 140 us expanding (92 GFLOP and 180 MB of results), 420 us
+// attending (316 GFLOP, 750 TFLOP/s); the softmax between the two products (37 % of a
 // SIMD's cycles) does not overlap with them (40 %) as much as two workgroups a CU
 // would allow.
 //
 // Keys are rounded to the input type, as their queries are in it.  Values and
-// weights meet in float16 whatever the input type, each head's values times a
-// power of two taken from its largest one: with both in bfloat16 the outputs'
+// weights meet in float16 whatever the input type: with both in bfloat16 the outputs'
 // error was 1.65 times that of the output's own rounding, with float16 1.18 times.
+// float16 ends at 2^16 and its full precision at 2^-14, so a row whose values are very
+// large or very small has a power of two of its own (per head): v = u 2^(e - 4), with
+// e = 0 where the largest lies in [2^-14, 2^11).  Its weight is multiplied by 2^e,
+//
+//   o = sum_s 2^(x_s + e_s - r) u_s,   l = sum_s 2^(x_s - m),
+//
+// with a reference r of the products' own: what a token sees decides its r, and no row
+// that it does not see can push its values out of float16's range.
 
 #include "sv_attn.h"
 #include "sv_latent.h"
@@ -191,14 +198,19 @@ __device__ __forceinline__ int clamp_len(const PromptParams& p, int len) {
     return len < 0 ? 0 : len > cap ? static_cast<int>(cap) : len;
 }
 
-// The power of two a head's values are stored times, by the bits of the largest one's
-// size: 1 where float16 holds them at its full precision, with room for a hundredth
-// of it.  The largest becomes 2^14 to 2^15 otherwise.
-__device__ __forceinline__ float value_scale(uint32_t most) {
-    const float m = __uint_as_float(most);
-    if (most == 0 || (m >= 0x1p-4f && m < 0x1p15f)) return 1.f;
-    const int e = static_cast<int>(most >> 23) - 127;  // denormal sizes: -127
-    return __uint_as_float(static_cast<uint32_t>(127 + min(14 - e, 120)) << 23);
+// Values are stored times 2^kLift 2^-e: in the middle of float16's range, the size of a
+// row's largest one in [2^kLow, 2^kHigh) with e = 0, else brought to 2^14..2^15.
+constexpr int kLift = 4, kLow = -14, kHigh = 11;
+constexpr int kNone = -32768;  // the exponent of rows without any value but zeros: their weights count for nothing
+
+// e of row r of the line, from the parts of head h's values.
+__device__ __forceinline__ int power_of(const PromptParams& p, int h, int r) {
+    const int parts = (h * p.dv + p.dv - 1) / p.part - h * p.dv / p.part + 1;
+    int top = kNone;
+    for (int i = 0; i < parts; ++i)
+        top = max(top, static_cast<int>(p.sizes[(static_cast<int64_t>(h) * kSizeParts + i) * p.rows + r]));
+    if (top == kNone) return p.there[r] ? kNone : 0;  // nobody sees a row whose page does not exist
+    return top >= kLow && top < kHigh ? 0 : top - (kHigh - 1);
 }
 
 // The last i in [0, n) with at[i] <= x, for rising at.
@@ -269,12 +281,12 @@ __global__ __launch_bounds__(1024) void k_prompt_plan(PromptParams p) {
         p.plan[2 * p.B + 1] = tile0;
         *p.odd = 0;
     }
-    for (int h = tid; h < p.H; h += 1024) p.most[h * kMostStride] = 0;
 }
 
-// Keys and values of 128 rows of the line: a product with the rows gathered from
+// Keys and values of TT rows of the line: a product with the rows gathered from
 // their pages.  The first output tile's workgroups also bring the rows' second
-// parts into the line.  AGAIN: the values of heads that need a scale.
+// parts into the line.  AGAIN: the rows' powers of two are found from the sizes that the
+// first launch left, and values of tiles where one is not 1 are made and stored again.
 template <int DT, int TT, bool AGAIN>
 __global__ __launch_bounds__(TT == 256 ? 512 : 256, 2) void k_prompt_expand(PromptParams p) {
     using L = Tile<TT, TT>;
@@ -294,10 +306,19 @@ __global__ __launch_bounds__(TT == 256 ? 512 : 256, 2) void k_prompt_expand(Prom
     const int64_t total = p.plan[p.B];
     if (r0 >= total) return;
     if (AGAIN) {
-        bool any = false;
-        for (int h = mt * TT / p.dv; h <= min(mt * TT + TT - 1, mv - 1) / p.dv; ++h)
-            any |= value_scale(p.most[h * kMostStride]) != 1.f;
-        if (!any) return;
+        const int h0 = mt * TT / p.dv, heads = min(mt * TT + TT - 1, mv - 1) / p.dv - h0 + 1;
+        int found = 0;  // bit 0: a power that is not 1; 1: one that changes values
+        for (int i = threadIdx.x; i < heads * TT; i += L::kThreads) {
+            const int h = h0 + i / TT, r = r0 + i % TT;
+            if (r >= total || r >= p.rows) continue;
+            const int e = power_of(p, h, r);
+            if (h * p.dv >= mt * TT) p.power[static_cast<int64_t>(h) * p.rows + r] = static_cast<int16_t>(e);
+            found |= e == 0 ? 0 : e == kNone ? 1 : 3;
+        }
+        if (__any(found) && (threadIdx.x & 63) == 0 &&
+            !(__hip_atomic_load(p.odd, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) & 4))
+            atomicOr(p.odd, 4);
+        if (!__syncthreads_or(found & 2)) return;
     }
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int hh = lane >> 5, col = lane & 31, r8 = lane >> 3;
@@ -362,16 +383,21 @@ __global__ __launch_bounds__(TT == 256 ? 512 : 256, 2) void k_prompt_expand(Prom
         return;
     }
     // a wave's eight neighbouring outputs are of one head
-    uint32_t most = 0;
+    uint32_t most[L::BT] = {};
     int of = -1;
     bool odd = false;
+    const int part = (m0 + wm * L::BM * 32) / (L::BM * 32);  // the wave's, of all heads' values
     auto tell = [&] {
-        for (int s = 32; s; s >>= 1) most = max(most, static_cast<uint32_t>(__shfl_xor(most, s)));
-        // most waves find a larger one there: 4000 atomics on one line cost 20 us (hence a line a head, too)
-        if (lane == 0 && of >= 0 &&
-            most > __hip_atomic_load(p.most + of * kMostStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
-            atomicMax(p.most + of * kMostStride, most);
-        most = 0;
+#pragma unroll
+        for (int b = 0; b < L::BT; ++b) {
+            const auto both = __builtin_amdgcn_permlane32_swap(most[b], most[b], false, false);
+            const uint32_t top = max(both[0], both[1]);
+            const int r = r0 + (wt * L::BT + b) * 32 + col;
+            if (hh == 0 && r < total && r < p.rows)
+                p.sizes[(static_cast<int64_t>(of) * kSizeParts + part - of * p.dv / (L::BM * 32)) * p.rows + r] =
+                    static_cast<int16_t>(top == 0 ? kNone : static_cast<int>(top >> 23) - 127);  // denormal: -127
+            most[b] = 0;
+        }
     };
 #pragma unroll
     for (int a = 0; a < L::BM; ++a)
@@ -383,26 +409,26 @@ __global__ __launch_bounds__(TT == 256 ? 512 : 256, 2) void k_prompt_expand(Prom
                 if (of >= 0) tell();
                 of = h;
             }
-            const float scale = AGAIN ? value_scale(p.most[h * kMostStride]) : 1.f;
 #pragma unroll
             for (int b = 0; b < L::BT; ++b) {
                 const int r = r0 + (wt * L::BT + b) * 32 + col;
                 if (r >= total || r >= p.rows) continue;
+                const int up = AGAIN ? kLift - power_of(p, h, r) : kLift;
                 float y[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    y[j] = acc[a][b][i + j] * scale;
+                    y[j] = AGAIN ? ldexpf(acc[a][b][i + j], up) : acc[a][b][i + j] * (1 << kLift);
                     const uint32_t size = __float_as_uint(acc[a][b][i + j]) & 0x7FFFFFFFu;
                     if (size >= 0x7F800000u)
                         odd = true;
                     else
-                        most = max(most, size);
+                        most[b] = max(most[b], size);
                 }
                 *reinterpret_cast<v4s*>(smem + out_at<TT>(r - r0, m8 - m0 + 4 * hh)) = pack4<kDTypeF16>(y[0], y[1], y[2], y[3]);
             }
         }
     if (!AGAIN) {
-        tell();
+        if (of >= 0) tell();
         if (odd) atomicOr(p.odd, 1);
     }
     store(p.v);
@@ -429,8 +455,14 @@ struct Rows {
 // units.  Where there are not that many, a workgroup has two GROUPS of four waves
 // that take the tiles in turn, each with a ring of its own, and add up at the end.
 // A tile's operands are read from LDS some steps before they are needed.
-template <int DT, int DN, int DR, int DV, int RING, int GROUPS>
-__global__ __launch_bounds__(GROUPS * kThreads, 2) void k_prompt_attn(PromptParams p) {
+//
+// POWERS: some rows of the line have a power of two of their own.  The products'
+// reference is then mx + ko, with ko = 0 until a query sees such a row; ko is kept
+// apart, as scores may be so large that float32 holds no power of two beside them.
+// The same arithmetic as without for queries that see none, and a loop of its own: with
+// one for both, the registers of the usual case would be spilled.
+template <int DT, int DN, int DR, int DV, int RING, int GROUPS, bool POWERS>
+__device__ __forceinline__ void prompt_attend(const PromptParams& p) {
     using KN = Rows<DN>;
     using KR = Rows<DR>;
     using VR = Rows<DV>;
@@ -563,13 +595,15 @@ __global__ __launch_bounds__(GROUPS * kThreads, 2) void k_prompt_attn(PromptPara
             q[s] = p.flip ? z ^ static_cast<short>(0x8000) : z;
         }
     }
-    float mx = -INFINITY, l = 0.f;
+    float mx = -INFINITY, l = 0.f, ko = 0.f;
+    bool apart = false;  // the query has seen a row with a power of its own
     v16f o[ND];
 #pragma unroll
     for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
     const float scale2 = p.scale2;
+    constexpr float kRaise = kUp<kDTypeF16> + 8.f;
     const bool odd = *p.odd & 1, gaps = *p.odd & 2;
     constexpr int kAhead = RING - 1;
 #pragma unroll
@@ -588,6 +622,8 @@ __global__ __launch_bounds__(GROUPS * kThreads, 2) void k_prompt_attn(PromptPara
         asm volatile("" ::: "memory");
         const int kb = (t * GROUPS + group) * TK;
         const uint64_t okm = gaps ? __ballot(there(kb) != 0) : ~0ull;
+        const int power = POWERS && kb + lane < len
+                              ? p.power[static_cast<int64_t>(h) * p.rows + row0 + kb + lane] : 0;  // of row kb + lane
         if (t + kAhead < T) stage(t + kAhead, to);
         uint64_t nf = 0;
         if (odd && ((t + 1) * GROUPS) * TK - 1 > i0 + shift) {
@@ -677,17 +713,59 @@ __global__ __launch_bounds__(GROUPS * kThreads, 2) void k_prompt_attn(PromptPara
                 for (int i = 0; i < 16; ++i) top = fmaxf(top, x[ks][i]);
             }
             top = scaled(half_max(top), scale2);
-            if (__any(top - mx > kUp<kDTypeF16> + 8.f)) {
-                const float mn = fmaxf(mx, top - kUp<kDTypeF16>);
-                const float a = shift_of(mx, mn);
-                l *= a;
+            float by = scale2, ref = 0.f, sum = l;  // the exponents of the weights are x by - ref
+            bool whole = true;                      // the weights are those of the sum, too
+            if (POWERS) {
+                const uint64_t own = __ballot(power != 0);
+                if (own) {
+                    const uint32_t lo = static_cast<uint32_t>(own & okm) & ~bits_from(pos - kb + 1);
+                    const uint32_t hi = static_cast<uint32_t>((own & okm) >> 32) & ~bits_from(pos - kb - 31);
+                    apart |= (lo | hi) != 0;
+                }
+                if (__any(apart)) {
+                    whole = false;
+                    by = 1.f;
+                    const float was = mx;
+                    if (top - mx > kRaise) mx = fmaxf(mx, top - kUp<kDTypeF16>);
+                    const float m = mx == -INFINITY ? 0.f : mx, a = shift_of(was, mx);
+                    sum *= a;
+                    float high = -INFINITY;
 #pragma unroll
-                for (int dt = 0; dt < ND; ++dt)
+                    for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[dt][i] *= a;
-                mx = mn;
+                        for (int i = 0; i < 16; ++i) {
+                            const float y = less(scaled(x[ks][i], scale2), m);
+                            sum += __builtin_amdgcn_exp2f(y);
+                            x[ks][i] = y + static_cast<float>(__shfl(power, 32 * ks + 8 * (i >> 2) + (i & 3) + 4 * hh));
+                            high = fmaxf(high, x[ks][i]);
+                        }
+                    high = half_max(high);
+                    float f = a;  // what the products so far are multiplied by
+                    if (apart) {
+                        const float k = was == -INFINITY ? -INFINITY : was == mx ? ko : ko + (was - mx);
+                        ko = high - k > kRaise ? fmaxf(k, high - kUp<kDTypeF16>) : k;
+                        f = shift_of(k, ko);
+                        ref = ko == -INFINITY ? 0.f : ko;
+                    }
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[dt][i] *= f;
+                }
             }
-            const float ref = mx == -INFINITY ? 0.f : mx;
+            if (whole) {
+                if (__any(top - mx > kRaise)) {
+                    const float was = mx;
+                    if (top - mx > kRaise) mx = fmaxf(mx, top - kUp<kDTypeF16>);
+                    const float a = shift_of(was, mx);
+                    sum *= a;
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[dt][i] *= a;
+                }
+                ref = mx == -INFINITY ? 0.f : mx;
+            }
 #pragma unroll
             for (int step = 0; step < 4; ++step) {
                 const int ks = step >> 1, t2 = step & 1;
@@ -695,23 +773,24 @@ __global__ __launch_bounds__(GROUPS * kThreads, 2) void k_prompt_attn(PromptPara
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    y[i] = __builtin_amdgcn_exp2f(less(scaled(x[ks][8 * t2 + i], scale2), ref));
-                    l += y[i];
+                    y[i] = __builtin_amdgcn_exp2f(less(scaled(x[ks][8 * t2 + i], by), ref));
+                    if (!POWERS || whole) sum += y[i];
                 }
                 const v4s lo = pack4<kDTypeF16>(y[0], y[1], y[2], y[3]), hi = pack4<kDTypeF16>(y[4], y[5], y[6], y[7]);
                 const v8s pf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
                 for (int dt = 0; dt < ND; ++dt) o[dt] = mfma<kDTypeF16>(vf[step & 1][dt], pf, o[dt]);
             }
+            l = sum;
         }
         at = at == kAhead * kStage ? 0 : at + kStage;
         to = to == kAhead * kStage ? 0 : to + kStage;
     }
     if (GROUPS > 1) {
         // the second group's sums through LDS, taken over by the first: 32 queries of each wave by
-        // DV values, the shift and the weights' sum
+        // DV values, the reference and the weights' sum, the products' reference
         __syncthreads();
-        float* const part = reinterpret_cast<float*>(smem) + w * (16 * ND + 2) * 64 + lane;
+        float* const part = reinterpret_cast<float*>(smem) + w * (16 * ND + 3) * 64 + lane;
         if (group) {
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt)
@@ -719,29 +798,54 @@ __global__ __launch_bounds__(GROUPS * kThreads, 2) void k_prompt_attn(PromptPara
                 for (int i = 0; i < 16; ++i) part[(dt * 16 + i) * 64] = o[dt][i];
             part[16 * ND * 64] = mx;
             part[(16 * ND + 1) * 64] = l;
+            if (POWERS) part[(16 * ND + 2) * 64] = ko;
         }
         __syncthreads();
         if (group) return;
         const float other = part[16 * ND * 64], top = fmaxf(mx, other);
-        const float a = shift_of(mx, top), c = shift_of(other, top);
+        float a = shift_of(mx, top), c = shift_of(other, top);
         l = l * a + part[(16 * ND + 1) * 64] * c;
+        if (POWERS) {
+            const float theirs = part[(16 * ND + 2) * 64];
+            const float k = mx == -INFINITY ? -INFINITY : mx == top ? ko : ko + (mx - top);
+            const float j = other == -INFINITY ? -INFINITY : other == top ? theirs : theirs + (other - top);
+            ko = fmaxf(k, j);
+            a = shift_of(k, ko);
+            c = shift_of(j, ko);
+        }
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[dt][i] = o[dt][i] * a + part[(dt * 16 + i) * 64] * c;
     }
     l = half_sum(l);
-    const float inv = l == 0.f ? 0.f : 1.f / l / value_scale(p.most[h * kMostStride]);  // a query that sees nothing: zero
+    const float inv = l == 0.f ? 0.f : 1.f / l / (1 << kLift);  // a query that sees nothing: zero
     if (!in) return;
+    // 2^ko in two steps: the first may leave float32's range where the product does not
+    ko = fminf(fmaxf(ko, -1000.f), 1000.f);
+    const int up = static_cast<int>(__builtin_rintf(ko));
+    const float rest = POWERS ? __builtin_amdgcn_exp2f(ko - up) : 1.f;
 #pragma unroll
     for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
             const int d = 32 * dt + 2 * i + 4 * hh;
-            if (d < p.dv)
-                *reinterpret_cast<v4s*>(dst + 2 * d) =
-                    pack4<DT>(o[dt][i] * inv, o[dt][i + 1] * inv, o[dt][i + 2] * inv, o[dt][i + 3] * inv);
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[j] = o[dt][i + j] * inv;
+                if (POWERS) y[j] = ldexpf(y[j] * rest, up);
+            }
+            if (d < p.dv) *reinterpret_cast<v4s*>(dst + 2 * d) = pack4<DT>(y[0], y[1], y[2], y[3]);
         }
+}
+
+template <int DT, int DN, int DR, int DV, int RING, int GROUPS>
+__global__ __launch_bounds__(GROUPS * kThreads, 2) void k_prompt_attn(PromptParams p) {
+    if (*p.odd & 4)
+        prompt_attend<DT, DN, DR, DV, RING, GROUPS, true>(p);
+    else
+        prompt_attend<DT, DN, DR, DV, RING, GROUPS, false>(p);
 }
 
 template <int DT, int TT>
@@ -774,15 +878,19 @@ hipError_t expand_one(const PromptParams& p, hipStream_t st, const LaunchEvents&
 // for 308; but 294, one round and a bit, 35 us for 32.
 template <int DT>
 hipError_t expand_tile(const PromptParams& p, bool again, hipStream_t st, const LaunchEvents& ev) {
-    if (again) return expand_one<DT, 128, true>(p, st, ev);
-    return expand_tasks(p, 256, false) > 2 * p.cus ? expand_one<DT, 256, false>(p, st, ev)
-                                                   : expand_one<DT, 128, false>(p, st, ev);
+    const bool large = expand_tasks(p, 256, false) > 2 * p.cus;
+    if (again) {
+        PromptParams q = p;
+        q.part = large ? 128 : 64;
+        return expand_one<DT, 128, true>(q, st, ev);
+    }
+    return large ? expand_one<DT, 256, false>(p, st, ev) : expand_one<DT, 128, false>(p, st, ev);
 }
 
 template <int DT, int DN, int DR, int DV, int RING, int GROUPS>
 hipError_t prompt_ring(const PromptParams& p, int64_t tasks, hipStream_t st, const LaunchEvents& ev) {
     constexpr int lds = GROUPS * RING * 64 * (DN + DR + DV) * 2;
-    static_assert(lds <= 160 << 10 && (GROUPS == 1 || lds >= kWaves * (DV / 2 + 2) * 64 * 4), "LDS");
+    static_assert(lds <= 160 << 10 && (GROUPS == 1 || lds >= kWaves * (DV / 2 + 3) * 64 * 4), "LDS");
     const hipError_t e = allow_lds(reinterpret_cast<const void*>(k_prompt_attn<DT, DN, DR, DV, RING, GROUPS>), lds);
     if (e != hipSuccess) return e;
     hipExtLaunchKernelGGL((k_prompt_attn<DT, DN, DR, DV, RING, GROUPS>), dim3(static_cast<unsigned>(grid_of(tasks))),
