@@ -989,6 +989,9 @@ def beam_reorder(state, ancestor, *, out=None, stream=None):
     _no_grad(state)
     if state.dim() < 1:
         raise ValueError("state must be [rows, ...]")
+    for t in (state,) if out is None else (state, out):
+        if t.is_conj() or t.is_neg():
+            raise ValueError("lazily conjugated or negated: resolve it first")
     n = state.shape[0]
     anc = _array(ancestor, "ancestor", (n,), index)
     if _elsewhere(index, stream):
