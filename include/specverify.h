@@ -704,7 +704,9 @@ int spec_head_product(const sv_head_product* args, void* stream);
  *                bounds do not rise so has no queries (no two sequences may share
  *                rows of q).  Rows of out that belong to no sequence are left as they
  *                are; a query that sees nothing is zero.
- * workspace      at least spec_latent_prompt_workspace(args) bytes, aligned to 16.
+ * workspace      at least spec_latent_prompt_workspace(args) bytes, aligned to 16:
+ *                about 2 heads rows (dim_k + dim_v), as the keys and values of all
+ *                rows, the prefixes' too, are made by every call.
  *
  * What a token does not see (later rows, other sequences, pages outside the pool)
  * never reaches its output.  Where it sees infinities or NaN, expanded keys beyond

@@ -935,8 +935,8 @@ int plan_latent(const sv_latent_attention* a, LatentPlan& t) {
     if (static_cast<int64_t>(a->width) * a->page_size > (1ll << 28)) return SV_ESHAPE;
     const int rows = a->N * a->heads;
     t.s.wide = a->dim > 320 || a->dim_v > 256;
-    // 64 rows share a tile's staging where there are that many (64 x 128: 94 us for 122 with 32; 32 x 256:
-    // 137 for 192); up to 32 half the products would be of nothing
+    // 64 rows share a tile's staging where there are that many (64 x 128: 90 us for 121 with 32; 32 x 256:
+    // 136 for 190); up to 32 half the products would be of nothing
     t.s.rows = rows <= 32 ? 32 : 64;
     t.MT = (rows + t.s.rows - 1) / t.s.rows;
     // a launch has fewer than 2^32 threads

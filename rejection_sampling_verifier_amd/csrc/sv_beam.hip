@@ -4,24 +4,27 @@
 //
 //   s(w, v) = score_w + x_wv - log sum_u e^(x_wu)
 //
-// the W largest, equal ones in the order of w V + v; a finished beam has one
-// candidate, the end token at its own score.
+// the W largest, equal ones in the order of the beams, then of logits and ids; a
+// finished beam has one candidate, the end token at its own score.
 //
 //   k_beam_stats   a chunk of a row: its maximum, the sum of its exponentials and
 //                  its W largest logits;
 //   k_beam_select  a sequence: the rows' logarithms of sums, then the W best.
 //
 // Within a row the order is that of the logits, exact in any arithmetic.  Between
-// rows it depends on the logarithms, which come from float32 exponentials with a
-// relative error of kBand / 2 at most; where two rows' candidates are closer than
-// kBand and that decides, the sequence's sums are taken again in float64.
+// rows it depends on the logarithms, which come from float32 exponentials (kBand);
+// where two rows' candidates are closer than kBand and that decides, the sequence's
+// sums are taken again in float64.  So they are where more than kSelThreads candidates
+// reach the selection's bound, with ties or without: see there.
 //
 // Chunks are cut by id, never by alignment, and sums have a fixed order: equal
 // rows give equal sums wherever they lie.
 //
-// What bounds it: 32 sequences of 8 beams over 128256 float32 ids (131 MB) take 34 us of
-// statistics (the reads alone 27, 4.9 TB/s) and 15 of selection; one sequence of 4
-// beams 4.4 and 9.5, a chain of dependent steps in one workgroup.
+// What bounds it: 32 sequences of 8 beams over 128256 float32 ids (131 MB) take 35 us of
+// statistics (the reads alone 27, 4.9 TB/s) and 15.5 of selection; one sequence of 4
+// beams 4.7 and 9.6, a chain of dependent steps in one workgroup.  Made for few beams:
+// one sequence of 12, 16, 24, 32 and 64 takes 29, 81, 1350, 2700 and 8750 us of
+// selection, eight of them over 32000 ids 20, 23, 29, 740 and 2300.
 
 #include <hip/hip_ext.h>
 
@@ -286,7 +289,10 @@ __global__ __launch_bounds__(kSelThreads) void k_beam_select(BeamParams p) {
 
     for (int round = 0;; ++round) {  // the second with float64 sums
         if (tid == 0) s_n = s_near = 0;
-        // a bound that W candidates of one wave's lanes reach
+        // A bound that W candidates of one wave's lanes reach: close for few beams.  Lists are sorted and
+        // W long, so for 32 and 64 beams a lane has the same rank of every list, and the bound is the
+        // largest candidate of about rank W / 2 or W - 1: thousands reach it, and then the sums are
+        // taken again and the winners found one after the other.
         double best = -__builtin_huge_val();
         each([&](const Cand& y) {
             if (y.s > best) best = y.s;

@@ -18,7 +18,8 @@
 // the scores and weights of a tile (16 x 16 x 32 products, 16 keys by half the rows
 // each), four stage tiles and sum a quarter of the values each (32 x 32 x 16).  A
 // ring of four tiles in LDS and two of weights keep them one tile apart, with one
-// barrier a tile.  With every wave doing both, the sums spilled (64 trees 281 us).
+// barrier a tile.  With every wave doing both, the sums spilled (32 trees 281 us,
+// 64 tokens 205).
 // Rows come by loads that write LDS directly, two tiles ahead; page numbers by
 // scalar loads, as the compiler's own vector loads would wait for all of these.
 // Weights are rounded once, to the input type.
