@@ -682,9 +682,9 @@ int spec_head_product(const sv_head_product* args, void* stream);
  * them, are in the cache.  Keys are rounded to the input type; values and weights
  * to float16's 11 bits in either type.  A row's values (per head) are kept times a
  * power of two where the largest finite one lies outside [2^-14, 2^11): a value's
- * error is half a step, or 2^-15 of that largest one where this is more.  Weights
- * are relative to the largest product of weight and power of two that the token sees
- * (those below 2^-32 of it are lost).  Statistics are float32.
+ * error is half a step, or 2^-15 of that largest one where this is more; that of a
+ * weight times its row's power, half a step or 2^-32 of the largest such product that
+ * the token sees.  Statistics are float32.
  *
  * dtype          SV_BF16 or SV_F16, of all tensors.
  * T              query tokens, 0 (nothing is done) to 2^24; B <= 65536; heads <= 1024.

@@ -51,11 +51,13 @@ def resize(s, b, rng, lo, hi):
         values_of(s, b, j).mul_(2.0 ** int(rng.integers(lo, hi + 1)))
 
 
-# (lens, new), heads, dims: few and many query tiles; both tiles of the expansion; heads that end inside a tile
+# (lens, new), heads, dims: few and many query tiles; both tiles of the expansion; heads whose values lie in one to
+# three of the parts that their sizes are found in
 SHAPES = [((150, 61), (150, 20), 2, (64, 32, 64, 128)), ((300, 41), (300, 41), 3, (128, 64, 128, 512)),
           ((200, 90), (70, 90), 5, (80, 32, 72, 256)), ((400, 100), (400, 100), 70, (64, 32, 64, 128)),
           ((700, 3, 1497), (9, 3, 5), 130, (64, 32, 72, 136)), ((140,), (140,), 7, (96, 64, 96, 384)),
-          ((130, 70), (130, 70), 30, (8, 8, 8, 16))]
+          ((130, 70), (130, 70), 30, (8, 8, 8, 16)), ((200, 90), (200, 90), 80, (128, 64, 128, 512)),
+          ((200, 90), (200, 90), 80, (80, 32, 120, 256)), ((700, 1503), (5, 9), 130, (64, 32, 104, 136))]
 
 
 @pytest.mark.parametrize("dtype,lo,hi", [(BF16, -40, 40), (BF16, -100, -60), (FP16, -10, 10)])
