@@ -419,7 +419,9 @@ __global__ __launch_bounds__(kLatThreads, 2) void k_latent_attn(LatentParams p) 
 #pragma unroll
                         for (int r = 0; r < NB; ++r) {
                             const int lr = 16 * (NB * rq + r) + c16;
-                            const float mn = fmaxf(mx[r], fmaxf(top[r], s_l[kh ^ 1][lr]) - kUp<DT>);
+                            // a row by its own scores alone: what other rows see leaves its bits as they are
+                            const float high = fmaxf(top[r], s_l[kh ^ 1][lr]);
+                            const float mn = high - mx[r] > kUp<DT> + 8.f ? fmaxf(mx[r], high - kUp<DT>) : mx[r];
                             const float a = shift_of(mx[r], mn);
                             if (g4 == 0 && kh == 0) s_a[lr] = a;
                             mx[r] = mn;
